@@ -83,6 +83,7 @@ typedef struct pkv_dims {
 #define PKV_DEV_BAD_BLOCK_ID    0x2  /* a block id the context needs is outside [0, num_blocks) */
 #define PKV_DEV_TIMEOUT         0x4  /* a shared-memory copy did not complete in time */
 #define PKV_DEV_BAD_PREFIX      0x8  /* cascade: a table does not start with the shared prefix */
+#define PKV_DEV_BAD_POSITION    0x10 /* rotate-and-append: a position outside the cos/sin table */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* pkv_status_string(pkv_status status);
@@ -126,6 +127,83 @@ pkv_status pkv_append_bf16(const void* k, const void* v, void* k_cache, void* v_
 pkv_status pkv_append_int8(const void* k, const void* v, int8_t* k_cache, int8_t* v_cache,
                            float* k_scale, float* v_scale, const int64_t* slot_mapping,
                            int32_t num_tokens, const pkv_dims* dims, pkv_stream_t stream);
+
+/* Norms and position rotation of pkv_rotate_append_*. Strides are elements between the
+ * rows of consecutive tokens (multiples of 8, at least heads * head_dim: q, k and v may be
+ * parts of one fused projection's output); the rows of a token's heads are contiguous. */
+typedef struct pkv_rotary {
+  const float* cos_sin;        /* device [num_positions, rotary_dim] fp32: the rotary_dim / 2
+                                  cosines of the position's angles, then their sines */
+  const void* q_norm;          /* device [head_dim] bf16 norm weight of q rows; NULL: no norm */
+  const void* k_norm;          /* the same for k rows */
+  int64_t out_stride, q_stride, k_stride, v_stride;
+  int32_t num_positions;
+  int32_t rotary_dim;          /* rotated elements of a row: a multiple of 16, at most head_dim */
+  int32_t interleaved;         /* 0: element i turns with i + rotary_dim / 2; else 2i with 2i + 1 */
+  float eps;                   /* added to the mean square of a normed row */
+} pkv_rotary;
+
+/*
+ * pkv_rotate_append_bf16 -- the norm of each head's q and k row, the rotation of its
+ * position, and the write of K and V into their cache slots, in one pass over the new
+ * tokens: what a decode step or a prefill chunk does before pkv_append_* and pkv_decode_*.
+ * For a row x of q or k of a token at position n (fp32 arithmetic):
+ *   y = x * rsqrt(mean(x^2) + eps) * w          (y = x without a norm weight)
+ *   (y_a, y_b) := (y_a cos_i - y_b sin_i, y_b cos_i + y_a sin_i), i < rotary_dim / 2,
+ * with a, b the pair's elements and cos_i, sin_i row n of the table. q rows leave in q_out
+ * (bf16); k rows go to their slot (bf16, one rounding); v rows are copied there unchanged.
+ *   q, q_out      [num_tokens, Hq, D] bf16; q_out may be q (same stride), else must not
+ *                 overlap an input.
+ *   k, v          [num_tokens, Hkv, D] bf16.
+ *   positions     [num_tokens] int64. A position outside [0, num_positions) gives a zero
+ *                 q row and writes no K or V; it is flagged PKV_DEV_BAD_POSITION in the
+ *                 optional device int32 *status.
+ *   slot_mapping  as for pkv_append_bf16 (a skipped token's q row is still written).
+ * num_tokens == 0 is a no-op returning PKV_OK.
+ */
+pkv_status pkv_rotate_append_bf16(void* q_out, const void* q, const void* k, const void* v,
+                                  const int64_t* positions, const pkv_rotary* rotary,
+                                  void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                  int32_t num_tokens, const pkv_dims* dims, int32_t* status,
+                                  pkv_stream_t stream);
+
+/*
+ * pkv_rotate_append_q8 -- pkv_rotate_append_bf16 into a one-byte cache: rows are quantised
+ * as pkv_append_int8 / pkv_append_fp8 do, k from its fp32 row (not rounded to bf16 before).
+ *   kv_dtype   PKV_KV_INT8, PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2 (else PKV_ERR_DTYPE).
+ */
+pkv_status pkv_rotate_append_q8(void* q_out, const void* q, const void* k, const void* v,
+                                const int64_t* positions, const pkv_rotary* rotary,
+                                void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                const int64_t* slot_mapping, int32_t num_tokens,
+                                pkv_kv_dtype kv_dtype, const pkv_dims* dims, int32_t* status,
+                                pkv_stream_t stream);
+
+/*
+ * pkv_gather_tokens -- cached rows read back as dense bf16 rows, sequence by sequence (for
+ * a dense attention over a cached prefix, or a move to another layout): row
+ * out_offsets[s] + i of out_k / out_v is token token_starts[s] + i of sequence s, for
+ * i < out_offsets[s + 1] - out_offsets[s]; a one-byte row is decode(code) * scale in fp32,
+ * rounded once to bf16; bf16 rows are copied bit for bit.
+ *   out_k, out_v   [num_out_tokens, Hkv, D] bf16; rows at or past out_offsets[num_seqs] are
+ *                  left as they were.
+ *   token_starts   [num_seqs] int32, or NULL for all zero.
+ *   out_offsets    [num_seqs + 1] int32, non-negative, never falling, at most
+ *                  num_out_tokens (device memory; flagged PKV_DEV_BAD_CONTEXT_LEN
+ *                  otherwise, and then any row may be written, but none outside the
+ *                  buffers).
+ *   status         optional device int32. A token outside its table row
+ *                  (PKV_DEV_BAD_CONTEXT_LEN) and a block id outside the pool
+ *                  (PKV_DEV_BAD_BLOCK_ID) give a zero row, flagged here.
+ * dims.num_q_heads is not used (any multiple of num_kv_heads). num_out_tokens == 0 is a
+ * no-op returning PKV_OK.
+ */
+pkv_status pkv_gather_tokens(void* out_k, void* out_v, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale,
+                             const int32_t* block_tables, const int32_t* token_starts,
+                             const int32_t* out_offsets, int32_t num_out_tokens,
+                             pkv_kv_dtype kv_dtype, const pkv_dims* dims, int32_t* status,
+                             pkv_stream_t stream);
 
 /*
  * pkv_decode_workspace_bytes -- size of the device workspace that pkv_decode_bf16 /
@@ -197,6 +275,45 @@ pkv_status pkv_decode_fp8(void* out, const void* q, const uint8_t* k_cache,
                           const int32_t* block_tables, const int32_t* context_lens, float scale,
                           pkv_kv_dtype fp8_format, const pkv_dims* dims, void* workspace,
                           size_t workspace_bytes, int32_t* status, pkv_stream_t stream);
+
+/*
+ * pkv_decode_diff_bf16 -- single-token differential attention over the same cache: heads go
+ * in pairs (2j, 2j + 1) and a pair's result is the difference of its two softmax maps over
+ * both heads' values. With g = Hq / Hkv, query pair j reads KV pair p = j / g, and
+ * V' = [V of head 2p | V of head 2p + 1] (2 D wide):
+ *   A_m = softmax(scale * K_{2p+m} q[s, 2j + m]),  m = 0, 1
+ *   o = A_0 V' - lam[j] * A_1 V'
+ *   out[s, j] = out_scale * o * rsqrt(mean(o^2) + eps) * norm_weight
+ *               (out_scale * o without a norm weight).
+ * fp32 accumulation and statistics, bf16 output.
+ *   q             [num_seqs, Hq, D] bf16; Hq and Hkv even (else PKV_ERR_SHAPE).
+ *   out           [num_seqs, Hq / 2, 2 D] bf16.
+ *   lam           [Hq / 2] fp32, device.
+ *   norm_weight   [2 D] bf16, device; NULL: no norm (eps is then not used).
+ *   workspace     at least pkv_decode_diff_workspace_bytes() bytes; otherwise as for
+ *                 pkv_decode_bf16, like status, empty sequences and unused table entries.
+ */
+pkv_status pkv_decode_diff_workspace_bytes(const pkv_dims* dims, pkv_kv_dtype kv_dtype,
+                                           size_t* bytes);
+pkv_status pkv_decode_diff_bf16(void* out, const void* q, const void* k_cache,
+                                const void* v_cache, const int32_t* block_tables,
+                                const int32_t* context_lens, const float* lam,
+                                const void* norm_weight, float eps, float out_scale, float scale,
+                                const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                                int32_t* status, pkv_stream_t stream);
+
+/*
+ * pkv_decode_diff_q8 -- pkv_decode_diff_bf16 over a one-byte cache (kv_dtype PKV_KV_INT8,
+ * PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2, else PKV_ERR_DTYPE), with the arithmetic and the
+ * limits on V scales of pkv_decode_int8 / pkv_decode_fp8.
+ */
+pkv_status pkv_decode_diff_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              const float* lam, const void* norm_weight, float eps,
+                              float out_scale, float scale, pkv_kv_dtype kv_dtype,
+                              const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                              int32_t* status, pkv_stream_t stream);
 
 /*
  * Whole-block moves ("块管理器：分页如何运作", chenk.top page). One block of the cache

@@ -24,8 +24,9 @@ Sources (the pages the method is taken from):
 Every function here is pinned against the pages' worked examples, closed forms,
 invariants, independent implementations and brute force -- ``tests/test_oracle_pins.py``
 (paging, decode, INT8), ``tests/test_oracle_fp8_pins.py``, ``tests/test_oracle_multi_pins.py``
-and ``tests/test_oracle_block_pins.py`` (copy-on-write and swap); none is marked
-"parity unpinned".
+``tests/test_oracle_block_pins.py`` (copy-on-write and swap) and
+``tests/test_oracle_diff_pins.py`` (norm and rotation, differential attention); none is
+marked "parity unpinned".
 """
 
 from .paged_attention import (  # noqa: F401
@@ -53,4 +54,6 @@ from .paged_attention import (  # noqa: F401
     copy_blocks,
     swap_out_blocks,
     swap_in_blocks,
+    norm_rotate_row,
+    decode_attention_diff,
 )

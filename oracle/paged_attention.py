@@ -472,3 +472,58 @@ def swap_in_blocks(cache, host, block_ids):
     for i, b in enumerate(ids):
         out[b] = host[i]
     return out
+
+
+# ---------------------------------------------------------------------------
+# Norm and rotation of new rows, rows read back, differential attention: the neighbours
+# of append and decode (no counterpart on the pages; the formulas are in the functions).
+# ---------------------------------------------------------------------------
+
+def norm_rotate_row(x, weight, cos, sin, eps, interleaved=False):
+    """One head's row [D] normed and rotated, float64.
+
+    ``y = x / sqrt(mean(x^2) + eps) * weight`` (``weight`` None: y = x); then pair i, of
+    len(cos), is turned by its angle: elements (i, i + len(cos)), or (2i, 2i + 1)
+    interleaved. Elements past the pairs stay y.
+    """
+    y = np.array(x, dtype=np.float64)
+    if weight is not None:
+        y = y / np.sqrt(np.mean(y * y) + eps) * np.asarray(weight, dtype=np.float64)
+    n = len(cos)
+    out = y.copy()
+    for i in range(n):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+        c, s = float(cos[i]), float(sin[i])
+        out[a] = y[a] * c - y[b] * s
+        out[b] = y[b] * c + y[a] * s
+    return out
+
+
+def decode_attention_diff(q, keys, values, lam, scale, norm_weight=None, eps=0.0, out_scale=1.0):
+    """Differential attention of one sequence, float64.
+
+    ``q``: [Hq, D]; ``keys``, ``values``: Hkv arrays [L, D] of its cached rows (as
+    gather_sequence gives them). Query pair j (heads 2j, 2j + 1) reads KV pair p = j // g:
+    out[j] = A_0 V' - lam[j] A_1 V' with A_m = softmax(scale K_{2p+m} q_{2j+m}) and V' the
+    pair's value rows side by side; with ``norm_weight`` out is divided by the root of its
+    mean square plus ``eps`` and multiplied by the weight; then by ``out_scale``. Returns
+    ([Hq / 2, 2 D], maps [Hq / 2, 2, L]).
+    """
+    q = np.asarray(q, dtype=np.float64)
+    Hq, D = q.shape
+    g = Hq // len(keys)
+    L = keys[0].shape[0]
+    out, maps = np.zeros((Hq // 2, 2 * D)), np.zeros((Hq // 2, 2, L))
+    if L == 0:
+        return out, maps
+    for j in range(Hq // 2):
+        p = j // g
+        wide = np.concatenate([values[2 * p], values[2 * p + 1]], axis=1)
+        for m in range(2):
+            o, maps[j, m] = attend_one_head(q[2 * j + m], keys[2 * p + m], wide, scale)
+            out[j] = out[j] + o if m == 0 else out[j] - float(lam[j]) * o
+        if norm_weight is not None:
+            out[j] = out[j] / np.sqrt(np.mean(out[j] ** 2) + eps) * np.asarray(norm_weight,
+                                                                               dtype=np.float64)
+        out[j] *= out_scale
+    return out, maps

@@ -13,6 +13,8 @@ _API = (
     "paged_decode_attention_multi_q8", "paged_decode_attention_cascade_q8",
     "cascade_q8_workspace_bytes",
     "cascade_workspace_bytes", "multi_workspace_bytes", "multi_q8_workspace_bytes",
+    "paged_kv_rotate_append", "paged_kv_rotate_append_q8", "paged_kv_gather",
+    "paged_decode_attention_diff", "paged_decode_attention_diff_q8", "diff_workspace_bytes",
     "copy_blocks", "swap_out", "swap_in",
     "decode_workspace_bytes", "library_path", "load_library", "PagedKVError",
     "Status", "Dims",

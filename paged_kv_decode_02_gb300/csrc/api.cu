@@ -32,6 +32,14 @@ constexpr int kTcHeadCost = 2;
 // cascade decode: the prefix kernel runs on about 1/kCascadePrefixShare of the SMs
 constexpr int kCascadePrefixShare = 3;
 
+// CODE_* of a KV dtype; -1: bf16
+int code_of(int kvt) {
+  return kvt == PKV_KV_INT8 ? CODE_I8
+         : kvt == PKV_KV_FP8_E4M3 ? CODE_E4M3
+         : kvt == PKV_KV_FP8_E5M2 ? CODE_E5M2
+                                  : -1;
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -79,14 +87,38 @@ bool make_cache_map(CUtensorMap* map, const void* base, bool int8, int D, long l
   return r == CUDA_SUCCESS;
 }
 
+// 4-D map over a cache for the differential decode: (swizzle span of a row, token in
+// block, block and head, span of the row); a box is `box` tokens of two heads, whole rows.
+bool make_pair_map(CUtensorMap* map, const void* base, bool q8, int D, long long heads, int BS,
+                   int box_tokens) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int elt = q8 ? 1 : 2;
+  const int row_bytes = D * elt;
+  const int seg = row_bytes >= 128 ? 128 : 64;
+  const int halves = row_bytes / seg;
+  cuuint64_t dims[4] = {cuuint64_t(seg / elt), cuuint64_t(BS), cuuint64_t(heads),
+                        cuuint64_t(halves)};
+  cuuint64_t strides[3] = {cuuint64_t(row_bytes), cuuint64_t(row_bytes) * BS, cuuint64_t(seg)};
+  cuuint32_t box[4] = {cuuint32_t(seg / elt), cuuint32_t(box_tokens), 2u, cuuint32_t(halves)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             seg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Encoded descriptors of recently used caches (the descriptor only depends on the
 // base address and the shape, so a decode loop over the same cache re-uses it).
 struct MapKey {
   const void* base;
   long long rows;
   int D, BS, q8;
+  int pair_box;  // > 0: a map of head pairs with boxes of that many tokens
   bool operator==(const MapKey& o) const {
-    return base == o.base && rows == o.rows && D == o.D && BS == o.BS && q8 == o.q8;
+    return base == o.base && rows == o.rows && D == o.D && BS == o.BS && q8 == o.q8 &&
+           pair_box == o.pair_box;
   }
 };
 constexpr int kMapCache = 16;
@@ -95,20 +127,33 @@ MapKey g_map_keys[kMapCache];
 CUtensorMap g_maps[kMapCache];
 int g_map_count = 0, g_map_next = 0;
 
-bool cache_map(CUtensorMap* map, const void* base, bool q8, int D, long long rows, int BS) {
-  const MapKey key{base, rows, D, BS, q8 ? 1 : 0};
+bool cached_map(CUtensorMap* map, const MapKey& key) {
   std::lock_guard<std::mutex> lock(g_map_mu);
   for (int i = 0; i < g_map_count; ++i)
     if (g_map_keys[i] == key) {
       *map = g_maps[i];
       return true;
     }
-  if (!make_cache_map(map, base, q8, D, rows, BS)) return false;
+  const bool made = key.pair_box > 0 ? make_pair_map(map, key.base, key.q8 != 0, key.D, key.rows,
+                                                     key.BS, key.pair_box)
+                                     : make_cache_map(map, key.base, key.q8 != 0, key.D, key.rows,
+                                                      key.BS);
+  if (!made) return false;
   g_map_keys[g_map_next] = key;
   g_maps[g_map_next] = *map;
   g_map_next = (g_map_next + 1) % kMapCache;
   if (g_map_count < kMapCache) ++g_map_count;
   return true;
+}
+
+bool cache_map(CUtensorMap* map, const void* base, bool q8, int D, long long rows, int BS) {
+  return cached_map(map, MapKey{base, rows, D, BS, q8 ? 1 : 0, 0});
+}
+
+// rows: blocks x heads
+bool pair_map(CUtensorMap* map, const void* base, bool q8, int D, long long rows, int BS,
+              int box_tokens) {
+  return cached_map(map, MapKey{base, rows, D, BS, q8 ? 1 : 0, box_tokens});
 }
 
 // ---------------------------------------------------------------------------
@@ -594,6 +639,207 @@ pkv_status check_append(const void* k, const void* v, const void* kc, const void
   return PKV_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Rotate-and-append
+// ---------------------------------------------------------------------------
+pkv_status run_rotate(int kvt, void* out, const void* q, const void* k, const void* v,
+                      const int64_t* positions, const pkv_rotary* ro, void* k_cache,
+                      void* v_cache, float* k_scale, float* v_scale, const int64_t* slots,
+                      int32_t T, const pkv_dims* d, int32_t* status, cudaStream_t stream) {
+  pkv_status st = check_dims(d);
+  if (st != PKV_OK) return st;
+  if (!ro) return PKV_ERR_NULL;
+  if (T < 0 || ro->num_positions <= 0) return PKV_ERR_SHAPE;
+  if (ro->rotary_dim <= 0 || ro->rotary_dim > d->head_dim) return PKV_ERR_SHAPE;
+  if (ro->rotary_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  const int64_t strides[4] = {ro->out_stride, ro->q_stride, ro->k_stride, ro->v_stride};
+  for (int i = 0; i < 4; ++i) {
+    const int heads = i < 2 ? d->num_q_heads : d->num_kv_heads;
+    if (T > 1 && strides[i] < (int64_t)heads * d->head_dim) return PKV_ERR_SHAPE;
+    if (strides[i] % 8 != 0) return PKV_ERR_ALIGNMENT;
+  }
+  if (T == 0) return PKV_OK;
+  if (!out || !q || !k || !v || !positions || !ro->cos_sin || !k_cache || !v_cache || !slots)
+    return PKV_ERR_NULL;
+  const bool q8 = kvt != PKV_KV_BF16;
+  if (q8 && (!k_scale || !v_scale)) return PKV_ERR_NULL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+      !aligned16(ro->cos_sin) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (ro->q_norm && !aligned16(ro->q_norm)) || (ro->k_norm && !aligned16(ro->k_norm)))
+    return PKV_ERR_ALIGNMENT;
+  RotateParams p{};
+  p.out = out;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_norm = ro->q_norm;
+  p.k_norm = ro->k_norm;
+  p.cos_sin = ro->cos_sin;
+  p.positions = positions;
+  p.slots = slots;
+  p.kc = static_cast<uint8_t*>(k_cache);
+  p.vc = static_cast<uint8_t*>(v_cache);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.status = status;
+  p.out_stride = ro->out_stride;
+  p.q_stride = ro->q_stride;
+  p.k_stride = ro->k_stride;
+  p.v_stride = ro->v_stride;
+  p.T = T;
+  p.Hq = d->num_q_heads;
+  p.Hkv = d->num_kv_heads;
+  p.BS = d->block_size;
+  p.NB = d->num_blocks;
+  p.P = ro->num_positions;
+  p.R = ro->rotary_dim;
+  p.interleaved = ro->interleaved ? 1 : 0;
+  p.eps = ro->eps;
+  return launch_rotate_append(code_of(kvt), d->head_dim, p, stream) == cudaSuccess ? PKV_OK
+                                                                                  : PKV_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Differential decode
+// ---------------------------------------------------------------------------
+struct DiffPlan {
+  DiffKernelInfo k;
+  int gs, nsg, G;
+  size_t smem, off_ml, off_o, ws_bytes;
+};
+
+pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
+  pkv_status st = check_dims(d);
+  if (st != PKV_OK) return st;
+  if (d->num_q_heads % 2 != 0 || d->num_kv_heads % 2 != 0) return PKV_ERR_SHAPE;
+  if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
+  struct Key {
+    pkv_dims d;
+    int kvt, device;
+  };
+  static std::mutex mu;
+  static Key keys[kPlanCache];
+  static DiffPlan plans[kPlanCache];
+  static int count = 0, next = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+  Key key;
+  std::memset(&key, 0, sizeof(key));
+  key.d = *d;
+  key.kvt = kvt;
+  key.device = dev;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < count; ++i)
+    if (std::memcmp(&keys[i], &key, sizeof(key)) == 0) {
+      *out = plans[i];
+      return PKV_OK;
+    }
+  DiffPlan P{};
+  const bool found = kvt == PKV_KV_BF16   ? select_diff_bf16(d->head_dim, d->block_size, &P.k)
+                     : kvt == PKV_KV_INT8 ? select_diff_int8(d->head_dim, d->block_size, &P.k)
+                     : kvt == PKV_KV_FP8_E4M3
+                         ? select_diff_e4m3(d->head_dim, d->block_size, &P.k)
+                         : select_diff_e5m2(d->head_dim, d->block_size, &P.k);
+  if (!found) return PKV_ERR_UNSUPPORTED;
+  // up to 8 query pairs (16 rows of the MMA) per work unit, as evenly as they go
+  const int g = d->num_q_heads / d->num_kv_heads;
+  P.nsg = (g + 7) / 8;
+  P.gs = (g + P.nsg - 1) / P.nsg;
+  int sms = 0, per_sm = 0, optin = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, P.k.fn) != cudaSuccess) return PKV_ERR_CUDA;
+  const size_t max_dyn = size_t(optin) - fa.sharedSizeBytes;
+  P.smem = size_t(P.k.smem) + align_up(size_t(d->num_seqs + 1) * 4, 16);
+  if (P.smem > max_dyn) return PKV_ERR_UNSUPPORTED;  // batch too large for one CTA's table
+  if (cudaFuncSetAttribute(P.k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(max_dyn)) !=
+      cudaSuccess)
+    return PKV_ERR_CUDA;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, P.k.fn, P.k.threads, P.smem) !=
+          cudaSuccess ||
+      per_sm <= 0)
+    return PKV_ERR_CUDA;
+  P.G = sms * per_sm;
+  // workspace: [prefix (B + 1) int32][records' (m, l), 2 per CTA][records' o]
+  const size_t rows = size_t(2) * P.G * 2 * P.gs;
+  P.off_ml = align_up(size_t(d->num_seqs + 1) * 4, 256);
+  P.off_o = align_up(P.off_ml + rows * 8, 256);
+  P.ws_bytes = align_up(P.off_o + rows * 2 * d->head_dim * 4, 256);
+  keys[next] = key;
+  plans[next] = P;
+  next = (next + 1) % kPlanCache;
+  if (count < kPlanCache) ++count;
+  *out = P;
+  return PKV_OK;
+}
+
+pkv_status run_diff(int kvt, void* out, const void* q, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                    const int32_t* context_lens, const float* lam, const void* norm_weight,
+                    float eps, float out_scale, float scale, const pkv_dims* d, void* workspace,
+                    size_t workspace_bytes, int32_t* status, cudaStream_t stream) {
+  pkv_status st = check_dims(d);
+  if (st != PKV_OK) return st;
+  if (d->num_q_heads % 2 != 0 || d->num_kv_heads % 2 != 0) return PKV_ERR_SHAPE;
+  if (d->num_seqs == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !lam)
+    return PKV_ERR_NULL;
+  const bool q8 = kvt != PKV_KV_BF16;
+  if (q8 && (!k_scale || !v_scale)) return PKV_ERR_NULL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (q8 && (!aligned16(k_scale) || !aligned16(v_scale))) ||
+      (norm_weight && !aligned16(norm_weight)))
+    return PKV_ERR_ALIGNMENT;
+  DiffPlan P;
+  st = make_diff_plan(d, kvt, &P);
+  if (st != PKV_OK) return st;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < P.ws_bytes)
+    return PKV_ERR_WORKSPACE;
+  const long long heads = (long long)d->num_blocks * d->num_kv_heads;
+  CUtensorMap tmk, tmv;
+  if (!pair_map(&tmk, k_cache, q8, d->head_dim, heads, d->block_size, P.k.box) ||
+      !pair_map(&tmv, v_cache, q8, d->head_dim, heads, d->block_size, P.k.box))
+    return PKV_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  DiffParams p{};
+  p.q = q;
+  p.out = out;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.lam = lam;
+  p.norm_w = norm_weight;
+  p.part_o = reinterpret_cast<float*>(ws + P.off_o);
+  p.part_ml = reinterpret_cast<float*>(ws + P.off_ml);
+  p.prefix = reinterpret_cast<int32_t*>(ws);
+  p.status = status;
+  p.B = d->num_seqs;
+  p.P = d->num_kv_heads / 2;
+  p.MBS = d->max_blocks_per_seq;
+  p.NB = d->num_blocks;
+  p.BS = d->block_size;
+  p.g = d->num_q_heads / d->num_kv_heads;
+  p.gs = P.gs;
+  p.nsg = P.nsg;
+  p.G = P.G;
+  p.D = d->head_dim;
+  p.item = P.k.item;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.eps = eps;
+  p.out_scale = out_scale;
+  p.timeout_ns = kTimeoutNs;
+  void* args[] = {&tmk, &tmv, &p};
+  if (launch_pdl(P.k.fn, dim3(P.G), dim3(P.k.threads), args, P.smem, stream) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  launch_diff_merge(p, stream);
+  if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
+  return PKV_OK;
+}
+
 }  // namespace
 
 pkv_status decode_bf16_fixed_counters(void* out, const void* q, const void* k_cache,
@@ -885,6 +1131,102 @@ pkv_status pkv_decode_multi_q8(void* out, const void* q, const void* k_cache,
   return run_decode(kv_dtype, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
                     context_lens, scale, dims, workspace, workspace_bytes, status,
                     reinterpret_cast<cudaStream_t>(stream), q_len);
+}
+
+pkv_status pkv_rotate_append_bf16(void* q_out, const void* q, const void* k, const void* v,
+                                  const int64_t* positions, const pkv_rotary* rotary,
+                                  void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                                  int32_t num_tokens, const pkv_dims* dims, int32_t* status,
+                                  pkv_stream_t stream) {
+  return run_rotate(PKV_KV_BF16, q_out, q, k, v, positions, rotary, k_cache, v_cache, nullptr,
+                    nullptr, slot_mapping, num_tokens, dims, status,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_rotate_append_q8(void* q_out, const void* q, const void* k, const void* v,
+                                const int64_t* positions, const pkv_rotary* rotary,
+                                void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                const int64_t* slot_mapping, int32_t num_tokens,
+                                pkv_kv_dtype kv_dtype, const pkv_dims* dims, int32_t* status,
+                                pkv_stream_t stream) {
+  if (code_of(kv_dtype) < 0) return PKV_ERR_DTYPE;
+  return run_rotate(kv_dtype, q_out, q, k, v, positions, rotary, k_cache, v_cache, k_scale,
+                    v_scale, slot_mapping, num_tokens, dims, status,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_gather_tokens(void* out_k, void* out_v, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale,
+                             const int32_t* block_tables, const int32_t* token_starts,
+                             const int32_t* out_offsets, int32_t num_out_tokens,
+                             pkv_kv_dtype kv_dtype, const pkv_dims* dims, int32_t* status,
+                             pkv_stream_t stream) {
+  pkv_status st = check_dims(dims);
+  if (st != PKV_OK) return st;
+  if (kv_dtype < PKV_KV_BF16 || kv_dtype > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
+  if (num_out_tokens < 0) return PKV_ERR_SHAPE;
+  if (num_out_tokens == 0 || dims->num_seqs == 0) return PKV_OK;
+  if (!out_k || !out_v || !k_cache || !v_cache || !block_tables || !out_offsets)
+    return PKV_ERR_NULL;
+  const bool q8 = kv_dtype != PKV_KV_BF16;
+  if (q8 && (!k_scale || !v_scale)) return PKV_ERR_NULL;
+  if (!aligned16(out_k) || !aligned16(out_v) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PKV_ERR_ALIGNMENT;
+  GatherParams p{};
+  p.ok = out_k;
+  p.ov = out_v;
+  p.kc = static_cast<const uint8_t*>(k_cache);
+  p.vc = static_cast<const uint8_t*>(v_cache);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.block_tables = block_tables;
+  p.starts = token_starts;
+  p.offsets = out_offsets;
+  p.status = status;
+  p.B = dims->num_seqs;
+  p.Hkv = dims->num_kv_heads;
+  p.BS = dims->block_size;
+  p.NB = dims->num_blocks;
+  p.MBS = dims->max_blocks_per_seq;
+  p.N = num_out_tokens;
+  return launch_gather(code_of(kv_dtype), dims->head_dim, p,
+                       reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_decode_diff_workspace_bytes(const pkv_dims* dims, pkv_kv_dtype kv_dtype,
+                                           size_t* bytes) {
+  if (!bytes) return PKV_ERR_NULL;
+  DiffPlan P;
+  pkv_status st = make_diff_plan(dims, kv_dtype, &P);
+  if (st != PKV_OK) return st;
+  *bytes = P.ws_bytes;
+  return PKV_OK;
+}
+
+pkv_status pkv_decode_diff_bf16(void* out, const void* q, const void* k_cache,
+                                const void* v_cache, const int32_t* block_tables,
+                                const int32_t* context_lens, const float* lam,
+                                const void* norm_weight, float eps, float out_scale, float scale,
+                                const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                                int32_t* status, pkv_stream_t stream) {
+  return run_diff(PKV_KV_BF16, out, q, k_cache, v_cache, nullptr, nullptr, block_tables,
+                  context_lens, lam, norm_weight, eps, out_scale, scale, dims, workspace,
+                  workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+pkv_status pkv_decode_diff_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              const float* lam, const void* norm_weight, float eps,
+                              float out_scale, float scale, pkv_kv_dtype kv_dtype,
+                              const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                              int32_t* status, pkv_stream_t stream) {
+  if (code_of(kv_dtype) < 0) return PKV_ERR_DTYPE;
+  return run_diff(kv_dtype, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                  context_lens, lam, norm_weight, eps, out_scale, scale, dims, workspace,
+                  workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, float* k_scale, float* v_scale,

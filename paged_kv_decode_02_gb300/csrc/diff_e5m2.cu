@@ -1,0 +1,10 @@
+// diff_e5m2.cu -- differential decode over E5M2 caches.
+#include "decode_diff.cuh"
+
+namespace pkv {
+
+bool select_diff_e5m2(int D, int BS, DiffKernelInfo* info) {
+  return select_diff_q8<CODE_E5M2>(D, BS, info);
+}
+
+}  // namespace pkv

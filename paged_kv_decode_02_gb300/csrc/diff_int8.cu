@@ -1,0 +1,10 @@
+// diff_int8.cu -- differential decode over INT8 caches.
+#include "decode_diff.cuh"
+
+namespace pkv {
+
+bool select_diff_int8(int D, int BS, DiffKernelInfo* info) {
+  return select_diff_q8<CODE_I8>(D, BS, info);
+}
+
+}  // namespace pkv

@@ -1,0 +1,140 @@
+// gather.cu -- cached rows read back: the tokens of each sequence, in order, as dense bf16
+// rows (one-byte codes times their row's scale, rounded once).
+//
+// Row out_offsets[s] + i of the output is token starts[s] + i of sequence s, reached
+// through the block table ("分页注意力", chenk.top page). A copy, bound by memory. A CTA
+// takes 2^tile_log2 consecutive output tokens of K or of V (blockIdx.y): its first threads
+// find each token's sequence by bisection of the offsets and its cache row through the
+// table, then all threads move rows, 8 elements each (a 16-byte store), with several loads
+// in flight. Rows of one head and consecutive tokens are neighbours in the cache, rows of
+// one token neighbours in the output, so both sides move whole rows of D elements.
+#include "common.cuh"
+#include "decode.cuh"
+#include "internal.h"
+
+namespace pkv {
+
+namespace {
+constexpr int kGatherThreads = 256;
+constexpr int kGatherUnroll = 4;
+constexpr int kGatherMaxLog2 = 5;  // at most 32 tokens per CTA
+}  // namespace
+
+template <int D, int CODE>
+__global__ void __launch_bounds__(kGatherThreads) paged_kv_gather_kernel(const GatherParams p) {
+  constexpr int CPR = D / 8;                   // 8-element chunks per row
+  constexpr int RPS = kGatherThreads / CPR;    // rows per step of the CTA
+  __shared__ long long s_row[1 << kGatherMaxLog2];  // cache row of head 0; -1: zeros, -2: none
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  const int tid = threadIdx.x;
+  const int tokens = 1 << p.tile_log2;
+  const long long n0 = (long long)blockIdx.x << p.tile_log2;
+  if (tid < tokens) {
+    const long long n = n0 + tid;
+    long long row = -2;
+    if (n < p.N) {
+      int lo = 0, hi = p.B;  // the last sequence whose offset is at most n
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.offsets + mid) <= n) lo = mid; else hi = mid;
+      }
+      const int o0 = __ldg(p.offsets + lo), o1 = __ldg(p.offsets + lo + 1);
+      if (o0 <= n && n < o1) {
+        const long long tok = (p.starts ? (long long)__ldg(p.starts + lo) : 0ll) + (n - o0);
+        int flag = 0;
+        row = -1;
+        if (tok < 0 || tok >= (long long)p.MBS * p.BS) {
+          flag = PKV_DEV_BAD_CONTEXT_LEN;
+        } else {
+          const int id = __ldg(p.block_tables + size_t(lo) * p.MBS + tok / p.BS);
+          if (id < 0 || id >= p.NB) flag = PKV_DEV_BAD_BLOCK_ID;
+          else row = (long long)id * p.Hkv * p.BS + tok % p.BS;
+        }
+        if (flag && p.status) atomicOr(p.status, flag);
+      }
+    }
+    s_row[tid] = row;
+  }
+  // the offsets themselves: 0 <= offsets[0], never falling, at most N
+  if (p.status && blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int s = tid; s < p.B; s += kGatherThreads) {
+      const int o0 = __ldg(p.offsets + s), o1 = __ldg(p.offsets + s + 1);
+      if (o0 < 0 || o1 < o0 || o1 > p.N) atomicOr(p.status, PKV_DEV_BAD_CONTEXT_LEN);
+    }
+  }
+  __syncthreads();
+  const bool isv = blockIdx.y != 0;
+  const uint8_t* cache = isv ? p.vc : p.kc;
+  const float* scale = isv ? p.vs : p.ks;
+  uint4* out = static_cast<uint4*>(isv ? p.ov : p.ok);
+  const int c = tid % CPR;
+  const int rows = p.Hkv << p.tile_log2;  // row i: head i >> tile_log2, token i & (tokens - 1)
+  for (int i0 = tid / CPR; i0 < rows; i0 += RPS * kGatherUnroll) {
+    uint4 raw[kGatherUnroll];
+    float sc[kGatherUnroll];
+    long long src[kGatherUnroll];
+#pragma unroll
+    for (int k = 0; k < kGatherUnroll; ++k) {
+      const int i = i0 + k * RPS;
+      const long long r = i < rows ? s_row[i & (tokens - 1)] : -2;
+      src[k] = r < 0 ? r : r + (long long)(i >> p.tile_log2) * p.BS;
+      raw[k] = make_uint4(0u, 0u, 0u, 0u);
+      sc[k] = 0.f;
+      if (src[k] >= 0) {
+        if constexpr (CODE < 0) {
+          raw[k] = __ldg(reinterpret_cast<const uint4*>(cache) + src[k] * CPR + c);
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(cache) + src[k] * CPR + c);
+          raw[k].x = v.x;
+          raw[k].y = v.y;
+          sc[k] = __ldg(scale + src[k]);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kGatherUnroll; ++k) {
+      if (src[k] == -2) continue;
+      const int i = i0 + k * RPS;
+      uint4 v = raw[k];
+      if constexpr (CODE >= 0) {
+        using Codec = Code8<CODE>;
+        const uint32_t w[2] = {Codec::pre(raw[k].x), Codec::pre(raw[k].y)};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 a = unpack_f16x2(Codec::lo(w[e])), b = unpack_f16x2(Codec::hi(w[e]));
+          o[2 * e] = pack_bf16x2(a.x * sc[k], a.y * sc[k]);
+          o[2 * e + 1] = pack_bf16x2(b.x * sc[k], b.y * sc[k]);
+        }
+        v = src[k] < 0 ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      const long long n = n0 + (i & (tokens - 1));
+      out[(n * p.Hkv + (i >> p.tile_log2)) * CPR + c] = v;
+    }
+  }
+}
+
+cudaError_t launch_gather(int code, int D, const GatherParams& p, cudaStream_t stream) {
+  if (p.N <= 0) return cudaSuccess;
+  const void* fn = nullptr;
+#define PKV_GATHER(DD, CC) \
+  if (D == DD && code == CC) fn = reinterpret_cast<const void*>(&paged_kv_gather_kernel<DD, CC>);
+  PKV_GATHER(128, -1)
+  PKV_GATHER(64, -1)
+  PKV_GATHER(128, CODE_I8)
+  PKV_GATHER(64, CODE_I8)
+  PKV_GATHER(128, CODE_E4M3)
+  PKV_GATHER(64, CODE_E4M3)
+  PKV_GATHER(128, CODE_E5M2)
+  PKV_GATHER(64, CODE_E5M2)
+#undef PKV_GATHER
+  if (!fn) return cudaErrorInvalidValue;
+  GatherParams copy = p;
+  copy.tile_log2 = 4;
+  const long long tiles = ((long long)p.N + (1 << copy.tile_log2) - 1) >> copy.tile_log2;
+  void* args[] = {&copy};
+  return launch_pdl(fn, dim3(unsigned(tiles), 2), dim3(kGatherThreads), args, 0, stream);
+}
+
+}  // namespace pkv

@@ -205,6 +205,84 @@ pkv_status decode_bf16_fixed_counters(void* out, const void* q, const void* k_ca
                                       size_t counter_words, int32_t* status,
                                       cudaStream_t stream);
 
+// Parameters of rotate-and-append (rotate.cu): T tokens' q, k and v rows; strides in
+// elements between tokens.
+struct RotateParams {
+  void* out;                   // [T, Hq, D] bf16 (may be q)
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_norm;          // [D] bf16, or NULL
+  const void* k_norm;
+  const float* cos_sin;        // [P, R] fp32: R / 2 cosines, then R / 2 sines
+  const int64_t* positions;    // [T]
+  const int64_t* slots;        // [T]
+  uint8_t* kc;
+  uint8_t* vc;
+  float* ks;                   // one-byte caches only
+  float* vs;
+  int32_t* status;
+  long long out_stride, q_stride, k_stride, v_stride;
+  int T, Hq, Hkv, BS, NB, P, R, interleaved;
+  float eps;
+};
+// code: CODE_I8, CODE_E4M3 or CODE_E5M2; -1: bf16 cache
+cudaError_t launch_rotate_append(int code, int D, const RotateParams& p, cudaStream_t stream);
+
+// Parameters of the gather of cached rows (gather.cu).
+struct GatherParams {
+  void* ok;                    // [N, Hkv, D] bf16
+  void* ov;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const float* ks;             // one-byte caches only
+  const float* vs;
+  const int32_t* block_tables;
+  const int32_t* starts;       // [B] first token of each sequence, or NULL: 0
+  const int32_t* offsets;      // [B + 1]
+  int32_t* status;
+  int B, Hkv, BS, NB, MBS, N;
+  int tile_log2;               // tokens per CTA, log2
+};
+// code as for launch_rotate_append
+cudaError_t launch_gather(int code, int D, const GatherParams& p, cudaStream_t stream);
+
+// Parameters of the differential decode (decode_diff.cuh, diff_merge.cu).
+struct DiffParams {
+  const void* q;               // [B, Hq, D] bf16
+  void* out;                   // [B, Hq / 2, 2 D] bf16
+  const float* k_scale;        // [NB, Hkv, BS] fp32 (one-byte caches only)
+  const float* v_scale;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const float* lam;            // [Hq / 2]
+  const void* norm_w;          // [2 D] bf16, or NULL
+  float* part_o;               // [2 G, 2, gs, 2 D] fp32 partial outputs (unnormalised)
+  float* part_ml;              // [2 G, 2, gs, 2] fp32 (running max in log2 units, sum)
+  int32_t* prefix;             // [B + 1] items-per-sequence exclusive prefix (CTA 0 writes)
+  int32_t* status;
+  int B, P, MBS, NB, BS;       // P: KV head pairs
+  int g;                       // query pairs per KV pair
+  int gs;                      // query pairs per work unit (at most 8)
+  int nsg;                     // work units per KV pair
+  int G;                       // CTAs of the decode kernel
+  int D, item;                 // head_dim, tokens per work item
+  float scale_log2;            // softmax scale * log2(e)
+  float eps, out_scale;
+  unsigned long long timeout_ns;
+};
+struct DiffKernelInfo {
+  const void* fn;
+  int threads, smem;           // smem: dynamic bytes without the batch's prefix
+  int box;                     // tokens per TMA box
+  int item;                    // tokens per work item
+};
+bool select_diff_bf16(int D, int BS, DiffKernelInfo* info);
+bool select_diff_int8(int D, int BS, DiffKernelInfo* info);
+bool select_diff_e4m3(int D, int BS, DiffKernelInfo* info);
+bool select_diff_e5m2(int D, int BS, DiffKernelInfo* info);
+void launch_diff_merge(const DiffParams& p, cudaStream_t stream);
+
 cudaError_t launch_append_bf16(const void* k, const void* v, void* k_cache, void* v_cache,
                                const int64_t* slots, int T, int Hkv, int D, int BS, int NB,
                                cudaStream_t stream);

@@ -38,6 +38,7 @@ DEV_BAD_CONTEXT_LEN = 0x1
 DEV_BAD_BLOCK_ID = 0x2
 DEV_TIMEOUT = 0x4
 DEV_BAD_PREFIX = 0x8
+DEV_BAD_POSITION = 0x10
 
 KV_BF16 = 0
 KV_INT8 = 1
@@ -63,6 +64,15 @@ class Dims(ctypes.Structure):
                 ("max_blocks_per_seq", ctypes.c_int32)]
 
 
+class Rotary(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("q_norm", ctypes.c_void_p),
+                ("k_norm", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("num_positions", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
 EXPORTS = {
     "pkv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "pkv_version": (ctypes.c_int, []),
@@ -85,6 +95,21 @@ EXPORTS = {
                                                                ctypes.c_void_p, ctypes.c_void_p,
                                                                ctypes.c_size_t, ctypes.c_void_p,
                                                                ctypes.c_void_p]),
+    "pkv_rotate_append_bf16": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int32] +
+                               [ctypes.c_void_p] * 3),
+    "pkv_rotate_append_q8": (ctypes.c_int, [ctypes.c_void_p] * 11 + [ctypes.c_int32,
+                                                                     ctypes.c_int] +
+                             [ctypes.c_void_p] * 3),
+    "pkv_gather_tokens": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int32, ctypes.c_int] +
+                          [ctypes.c_void_p] * 3),
+    "pkv_decode_diff_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int,
+                                                       ctypes.POINTER(ctypes.c_size_t)]),
+    "pkv_decode_diff_bf16": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_float] * 3 +
+                             [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                              ctypes.c_void_p, ctypes.c_void_p]),
+    "pkv_decode_diff_q8": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_float] * 3 +
+                           [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                            ctypes.c_void_p, ctypes.c_void_p]),
     "pkv_copy_blocks": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int32, ctypes.c_int,
                                                                 ctypes.c_void_p, ctypes.c_void_p,
                                                                 ctypes.c_void_p]),
@@ -304,6 +329,168 @@ def paged_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, 
     _check(st, "pkv_append_fp8")
 
 
+def _token_rows(t, name, device):
+    """Checks a [T, H, D] bf16 tensor of contiguous rows of heads; returns its token stride
+    (any, as of a slice of a fused projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device (no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    tokens, heads, d = t.shape
+    st = t.stride()
+    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous rows")
+    return st[0] if tokens > 1 else heads * d
+
+
+def _rotate_append(kv, q, k, v, positions, cos_sin, k_cache, v_cache, k_scale, v_scale,
+                   slot_mapping, q_norm, k_norm, eps, interleaved, out, status):
+    _require_any(k_cache, "k_cache", _code_dtypes(kv), 4, None)
+    dev = k_cache.device
+    _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, dev)
+    if kv != KV_BF16:
+        _require(k_scale, "k_scale", torch.float32, 3, dev)
+        _require(v_scale, "v_scale", torch.float32, 3, dev)
+    strides = [_token_rows(t, n, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    _require(positions, "positions", torch.int64, 1, dev)
+    _require(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    _require(cos_sin, "cos_sin", torch.float32, 2, dev)
+    status = _status_word(status, dev)
+    tokens, hq, d = q.shape
+    nb, hkv, bs, dc = k_cache.shape
+    if d != dc:
+        raise ValueError("cache shapes disagree with q")
+    _cache_shapes(k_cache, v_cache, k_scale, v_scale)
+    _same_shape(k, "k", (tokens, hkv, d))
+    _same_shape(v, "v", (tokens, hkv, d))
+    _same_shape(positions, "positions", (tokens,))
+    _same_shape(slot_mapping, "slot_mapping", (tokens,))
+    for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _require(t, n, torch.bfloat16, 1, dev)
+            _same_shape(t, n, (d,))
+    if out is None:
+        out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=dev)
+        out_stride = hq * d
+    else:
+        out_stride = _token_rows(out, "out", dev)
+        _same_shape(out, "out", (tokens, hq, d))
+    rotary = Rotary(cos_sin.data_ptr(), q_norm.data_ptr() if q_norm is not None else None,
+                    k_norm.data_ptr() if k_norm is not None else None, out_stride, *strides,
+                    cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, float(eps))
+    dims = Dims(0, hq, hkv, d, bs, nb, 1)
+    with _OnDevice(dev):
+        if kv == KV_BF16:
+            name = "pkv_rotate_append_bf16"
+            st = _lib().pkv_rotate_append_bf16(
+                _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(positions), ctypes.byref(rotary),
+                _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), tokens, ctypes.byref(dims),
+                _ptr(status), _stream(dev))
+        else:
+            name = "pkv_rotate_append_q8"
+            st = _lib().pkv_rotate_append_q8(
+                _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(positions), ctypes.byref(rotary),
+                _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
+                tokens, kv, ctypes.byref(dims), _ptr(status), _stream(dev))
+    _check(st, name)
+    return out
+
+
+def paged_kv_rotate_append(q, k, v, positions, cos_sin, k_cache, v_cache, slot_mapping,
+                           q_norm=None, k_norm=None, eps=1e-6, interleaved=False, out=None,
+                           status=None):
+    """Norm and rotate new tokens' queries and keys and write K and V into the bf16 paged
+    caches, in one pass.
+
+    q [T, Hq, D], k and v [T, Hkv, D] bf16 (any token stride that is a multiple of 8, as
+    slices of a fused projection have); positions [T] int64; cos_sin [positions, R] fp32,
+    R / 2 cosines then R / 2 sines per position, R the rotated part of a row (a multiple of
+    16, at most D): element i turns with i + R / 2, or 2i with 2i + 1 (``interleaved``).
+    ``q_norm`` / ``k_norm`` ([D] bf16): root-mean-square norm weights of each head's row
+    (None: no norm). ``slot_mapping`` as for :func:`paged_kv_append`. Returns the rotated q
+    [T, Hq, D] bf16 (``out``, which may be q). A position outside the table gives a zero q
+    row, writes no K or V and is flagged DEV_BAD_POSITION in ``status`` (int32 [1])."""
+    return _rotate_append(KV_BF16, q, k, v, positions, cos_sin, k_cache, v_cache, None, None,
+                          slot_mapping, q_norm, k_norm, eps, interleaved, out, status)
+
+
+def paged_kv_rotate_append_q8(q, k, v, positions, cos_sin, k_cache, v_cache, k_scale, v_scale,
+                              slot_mapping, fmt="e5m2", q_norm=None, k_norm=None, eps=1e-6,
+                              interleaved=False, out=None, status=None):
+    """:func:`paged_kv_rotate_append` into a one-byte cache: int8 codes (INT8), or FP8 codes
+    (uint8 with ``fmt`` "e4m3" / "e5m2", or the matching torch float8 dtype), with
+    per-(token, KV head) fp32 scales ``k_scale``/``v_scale`` [NB, Hkv, bs], quantised as
+    :func:`paged_kv_append_int8` / :func:`paged_kv_append_fp8` do."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    return _rotate_append(_q8_kind(k_cache, fmt), q, k, v, positions, cos_sin, k_cache, v_cache,
+                          k_scale, v_scale, slot_mapping, q_norm, k_norm, eps, interleaved, out,
+                          status)
+
+
+def paged_kv_gather(k_cache, v_cache, block_tables, out_offsets, num_tokens=None,
+                    token_starts=None, k_scale=None, v_scale=None, fmt="e5m2", out_k=None,
+                    out_v=None, status=None):
+    """Cached rows read back as dense bf16 rows: row ``out_offsets[s] + i`` of the result is
+    token ``token_starts[s] + i`` (0 without ``token_starts``) of sequence s.
+
+    Caches [NB, Hkv, bs, D] bf16, or one-byte codes with ``k_scale``/``v_scale`` as for
+    :func:`paged_decode_attention_multi_q8` (a value is code times scale, rounded once);
+    block_tables [B, MBS] int32; out_offsets [B + 1] int32, never falling; token_starts [B]
+    int32. Returns (out_k, out_v), [num_tokens, Hkv, D] bf16: the tensors given, whose rows
+    past ``out_offsets[B]`` stay as they were, or new ones of ``num_tokens`` rows. A token
+    outside its table row or a block id outside the pool gives a zero row, flagged in
+    ``status`` (int32 [1])."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    kv = KV_BF16 if k_cache.dtype == torch.bfloat16 else _q8_kind(k_cache, fmt)
+    _require_any(k_cache, "k_cache", _code_dtypes(kv), 4, None)
+    dev = k_cache.device
+    _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, dev)
+    if kv == KV_BF16:
+        k_scale = v_scale = None
+    else:
+        _require(k_scale, "k_scale", torch.float32, 3, dev)
+        _require(v_scale, "v_scale", torch.float32, 3, dev)
+    _cache_shapes(k_cache, v_cache, k_scale, v_scale)
+    _require(block_tables, "block_tables", torch.int32, 2, dev)
+    _require(out_offsets, "out_offsets", torch.int32, 1, dev)
+    nb, hkv, bs, d = k_cache.shape
+    B = block_tables.shape[0]
+    _same_shape(out_offsets, "out_offsets", (B + 1,))
+    if token_starts is not None:
+        _require(token_starts, "token_starts", torch.int32, 1, dev)
+        _same_shape(token_starts, "token_starts", (B,))
+    status = _status_word(status, dev)
+    if num_tokens is None:
+        given = out_k if out_k is not None else out_v
+        if not isinstance(given, torch.Tensor):
+            raise ValueError("num_tokens is needed without out_k or out_v")
+        num_tokens = given.shape[0]
+    outs = []
+    for t, n in ((out_k, "out_k"), (out_v, "out_v")):
+        if t is None:
+            t = torch.empty((num_tokens, hkv, d), dtype=torch.bfloat16, device=dev)
+        else:
+            _require(t, n, torch.bfloat16, 3, dev)
+            _same_shape(t, n, (num_tokens, hkv, d))
+        outs.append(t)
+    dims = Dims(B, hkv, hkv, d, bs, nb, block_tables.shape[1])
+    with _OnDevice(dev):
+        st = _lib().pkv_gather_tokens(_ptr(outs[0]), _ptr(outs[1]), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+                                      _ptr(token_starts), _ptr(out_offsets), int(num_tokens), kv,
+                                      ctypes.byref(dims), _ptr(status), _stream(dev))
+    _check(st, "pkv_gather_tokens")
+    return outs[0], outs[1]
+
+
 def decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                            num_blocks, max_blocks_per_seq, kv_dtype=KV_BF16, device=None):
     dims = Dims(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
@@ -447,6 +634,101 @@ def paged_decode_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     scales ``k_scale``/``v_scale`` [NB, Hkv, bs]."""
     return _decode(_fp8_format(fmt), q, k_cache, v_cache, k_scale, v_scale, block_tables,
                    context_lens, scale, out, workspace, status)
+
+
+def diff_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                         max_blocks_per_seq, kv_dtype=KV_BF16, device=None):
+    """Workspace of :func:`paged_decode_attention_diff` / ``..._diff_q8``."""
+    dims = Dims(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                max_blocks_per_seq)
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        st = _lib().pkv_decode_diff_workspace_bytes(ctypes.byref(dims), int(kv_dtype),
+                                                    ctypes.byref(out))
+    _check(st, "pkv_decode_diff_workspace_bytes")
+    return int(out.value)
+
+
+def _decode_diff(kv, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, lam,
+                 scale, norm_weight, eps, out_scale, out, workspace, status):
+    _require(q, "q", torch.bfloat16, 3)
+    dev = q.device
+    status = _status_word(status, dev)
+    _require_any(k_cache, "k_cache", _code_dtypes(kv), 4, dev)
+    _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, dev)
+    if kv != KV_BF16:
+        _require(k_scale, "k_scale", torch.float32, 3, dev)
+        _require(v_scale, "v_scale", torch.float32, 3, dev)
+    _require(block_tables, "block_tables", torch.int32, 2, dev)
+    _require(context_lens, "context_lens", torch.int32, 1, dev)
+    _require(lam, "lam", torch.float32, 1, dev)
+    B, Hq, D = q.shape
+    if k_cache.shape[3] != D:
+        raise ValueError("cache shapes disagree with q")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("block_tables / context_lens must have num_seqs rows")
+    _cache_shapes(k_cache, v_cache, k_scale, v_scale)
+    _same_shape(lam, "lam", (Hq // 2,))
+    if norm_weight is not None:
+        _require(norm_weight, "norm_weight", torch.bfloat16, 1, dev)
+        _same_shape(norm_weight, "norm_weight", (2 * D,))
+    dims = _dims(B, Hq, k_cache, block_tables.shape[1])
+    if out is None:
+        out = torch.empty((B, Hq // 2, 2 * D), dtype=torch.bfloat16, device=dev)
+    else:
+        _require(out, "out", torch.bfloat16, 3, dev)
+        _same_shape(out, "out", (B, Hq // 2, 2 * D))
+    with _OnDevice(dev):
+        need = ctypes.c_size_t(0)
+        _check(_lib().pkv_decode_diff_workspace_bytes(ctypes.byref(dims), kv,
+                                                      ctypes.byref(need)),
+               "pkv_decode_diff_workspace_bytes")
+        workspace, ws_bytes = _workspace(workspace, need.value, dev)
+        tail = (_ptr(block_tables), _ptr(context_lens), _ptr(lam), _ptr(norm_weight), float(eps),
+                float(out_scale), float(scale))
+        end = (ctypes.byref(dims), _ptr(workspace), ws_bytes, _ptr(status), _stream(dev))
+        if kv == KV_BF16:
+            name = "pkv_decode_diff_bf16"
+            st = _lib().pkv_decode_diff_bf16(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                             *tail, *end)
+        else:
+            name = "pkv_decode_diff_q8"
+            st = _lib().pkv_decode_diff_q8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                           _ptr(k_scale), _ptr(v_scale), *tail, kv, *end)
+    _check(st, name)
+    return out
+
+
+def paged_decode_attention_diff(q, k_cache, v_cache, block_tables, context_lens, lam, scale,
+                                norm_weight=None, eps=1e-5, out_scale=1.0, out=None,
+                                workspace=None, status=None):
+    """Single-token differential attention over a bf16 paged KV cache: heads go in pairs
+    (2j, 2j + 1); with g = Hq / Hkv, query pair j reads KV pair p = j // g and
+
+        o[s, j] = (softmax(scale K_2p q_2j) - lam[j] softmax(scale K_2p+1 q_2j+1)) V',
+
+    V' = [V_2p | V_2p+1], 2 D wide; with ``norm_weight`` ([2 D] bf16) o is divided by the
+    root of its mean square (plus ``eps``) and multiplied by the weight; then by
+    ``out_scale``. q [B, Hq, D] bf16 with Hq and Hkv even; lam [Hq / 2] fp32; caches, tables
+    and lengths as for :func:`paged_decode_attention`. Returns out [B, Hq / 2, 2 D] bf16.
+    ``workspace`` (uint8, at least :func:`diff_workspace_bytes`) and ``status`` (int32 [1])
+    are optional."""
+    return _decode_diff(KV_BF16, q, k_cache, v_cache, None, None, block_tables, context_lens, lam,
+                        scale, norm_weight, eps, out_scale, out, workspace, status)
+
+
+def paged_decode_attention_diff_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                   context_lens, lam, scale, fmt="e5m2", norm_weight=None,
+                                   eps=1e-5, out_scale=1.0, out=None, workspace=None,
+                                   status=None):
+    """:func:`paged_decode_attention_diff` over a one-byte cache: int8 codes (INT8), or FP8
+    codes (uint8 with ``fmt`` "e4m3" / "e5m2", or the matching torch float8 dtype), with
+    per-(token, KV head) fp32 scales ``k_scale``/``v_scale`` [NB, Hkv, bs]."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    return _decode_diff(_q8_kind(k_cache, fmt), q, k_cache, v_cache, k_scale, v_scale,
+                        block_tables, context_lens, lam, scale, norm_weight, eps, out_scale, out,
+                        workspace, status)
 
 
 def _move_kv(k_cache, kv_dtype):
