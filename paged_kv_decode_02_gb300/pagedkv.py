@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import enum
 import os
+import struct
 import threading
 
 import torch
@@ -240,6 +241,62 @@ def _require(t, name, dtype, ndim, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+# ---------------------------------------------------------------------------
+# Lean marshalling: a small decode step is a few microseconds on the GPU, so the calls
+# below check and pass their arguments with as little Python as that takes. Pointers go as
+# integers, the C structs as packed bytes; _need() looks at a tensor through four cheap
+# accessors and leaves the wording of a refusal to _require().
+# ---------------------------------------------------------------------------
+_pack_dims = struct.Struct("7i").pack                  # pkv_dims
+_pack_rotary = struct.Struct("3P4q3if").pack           # pkv_rotary
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _need(t, name, dtype, ndim, index):
+    """:func:`_require` of a tensor on CUDA device ``index``."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.dim() == ndim and t.is_contiguous()):
+        _require(t, name, dtype, ndim, torch.device("cuda", max(index, 0)))
+
+
+def _need_caches(kv, k_cache, v_cache, k_scale, v_scale):
+    """Checks the caches of a KV dtype; returns (device index, K cache's shape)."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    index = k_cache.get_device()
+    if index < 0:
+        _require(k_cache, "k_cache", k_cache.dtype, 4)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        dts = _code_dtypes(kv)
+        dt = t.dtype if isinstance(t, torch.Tensor) and t.dtype in dts else dts[0]
+        _need(t, name, dt, 4, index)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
+        _same_shape(v_cache, "v_cache", shape)
+    if kv != KV_BF16:
+        _need(k_scale, "k_scale", _F32, 3, index)
+        _need(v_scale, "v_scale", _F32, 3, index)
+        if k_scale.shape != shape[:3] or v_scale.shape != shape[:3]:
+            _cache_shapes(k_cache, v_cache, k_scale, v_scale)
+    return index, shape
+
+
+def _run(name, index, *args):
+    """Calls the library on CUDA device ``index``, on its current stream; returns the
+    status."""
+    lib = _LIB if _LIB is not None else load_library()
+    if torch.cuda.current_device() == index:
+        return getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+
+
+def _status_ptr(status, index):
+    if status is None:
+        return None
+    return _status_word(status, torch.device("cuda", index)).data_ptr()
+
+
 def _dims(num_seqs, num_q_heads, k_cache, max_blocks_per_seq):
     nb, hkv, bs, d = k_cache.shape
     return Dims(num_seqs, num_q_heads, hkv, d, bs, nb, max_blocks_per_seq)
@@ -329,76 +386,65 @@ def paged_kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, 
     _check(st, "pkv_append_fp8")
 
 
-def _token_rows(t, name, device):
-    """Checks a [T, H, D] bf16 tensor of contiguous rows of heads; returns its token stride
-    (any, as of a slice of a fused projection's output)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (no CPU path)")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    tokens, heads, d = t.shape
+def _token_rows(t, name, index):
+    """Checks a [T, H, D] bf16 tensor of contiguous rows of heads; returns its shape and its
+    token stride (any, as of a slice of a fused projection's output)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == index
+            and t.dim() == 3):
+        _require(t, name, _BF16, 3, torch.device("cuda", max(index, 0)))
+    shape = t.shape
+    tokens, heads, d = shape
     st = t.stride()
     if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous rows")
-    return st[0] if tokens > 1 else heads * d
+    return shape, st[0] if tokens > 1 else heads * d
 
 
 def _rotate_append(kv, q, k, v, positions, cos_sin, k_cache, v_cache, k_scale, v_scale,
                    slot_mapping, q_norm, k_norm, eps, interleaved, out, status):
-    _require_any(k_cache, "k_cache", _code_dtypes(kv), 4, None)
-    dev = k_cache.device
-    _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, dev)
-    if kv != KV_BF16:
-        _require(k_scale, "k_scale", torch.float32, 3, dev)
-        _require(v_scale, "v_scale", torch.float32, 3, dev)
-    strides = [_token_rows(t, n, dev) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    _require(positions, "positions", torch.int64, 1, dev)
-    _require(slot_mapping, "slot_mapping", torch.int64, 1, dev)
-    _require(cos_sin, "cos_sin", torch.float32, 2, dev)
-    status = _status_word(status, dev)
-    tokens, hq, d = q.shape
-    nb, hkv, bs, dc = k_cache.shape
-    if d != dc:
+    index, (nb, hkv, bs, d) = _need_caches(kv, k_cache, v_cache, k_scale, v_scale)
+    q_shape, q_stride = _token_rows(q, "q", index)
+    k_shape, k_stride = _token_rows(k, "k", index)
+    v_shape, v_stride = _token_rows(v, "v", index)
+    tokens, hq, dq = q_shape
+    if dq != d:
         raise ValueError("cache shapes disagree with q")
-    _cache_shapes(k_cache, v_cache, k_scale, v_scale)
-    _same_shape(k, "k", (tokens, hkv, d))
-    _same_shape(v, "v", (tokens, hkv, d))
-    _same_shape(positions, "positions", (tokens,))
-    _same_shape(slot_mapping, "slot_mapping", (tokens,))
+    if k_shape != (tokens, hkv, d) or v_shape != k_shape:
+        _same_shape(k, "k", (tokens, hkv, d))
+        _same_shape(v, "v", (tokens, hkv, d))
+    _need(positions, "positions", _I64, 1, index)
+    _need(slot_mapping, "slot_mapping", _I64, 1, index)
+    _need(cos_sin, "cos_sin", _F32, 2, index)
+    if positions.shape[0] != tokens or slot_mapping.shape[0] != tokens:
+        _same_shape(positions, "positions", (tokens,))
+        _same_shape(slot_mapping, "slot_mapping", (tokens,))
+    norms = []
     for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
         if t is not None:
-            _require(t, n, torch.bfloat16, 1, dev)
+            _need(t, n, _BF16, 1, index)
             _same_shape(t, n, (d,))
+        norms.append(t.data_ptr() if t is not None else 0)
     if out is None:
-        out = torch.empty((tokens, hq, d), dtype=torch.bfloat16, device=dev)
-        out_stride = hq * d
+        out, out_stride = torch.empty((tokens, hq, d), dtype=_BF16, device=q.device), hq * d
     else:
-        out_stride = _token_rows(out, "out", dev)
-        _same_shape(out, "out", (tokens, hq, d))
-    rotary = Rotary(cos_sin.data_ptr(), q_norm.data_ptr() if q_norm is not None else None,
-                    k_norm.data_ptr() if k_norm is not None else None, out_stride, *strides,
-                    cos_sin.shape[0], cos_sin.shape[1], 1 if interleaved else 0, float(eps))
-    dims = Dims(0, hq, hkv, d, bs, nb, 1)
-    with _OnDevice(dev):
-        if kv == KV_BF16:
-            name = "pkv_rotate_append_bf16"
-            st = _lib().pkv_rotate_append_bf16(
-                _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(positions), ctypes.byref(rotary),
-                _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), tokens, ctypes.byref(dims),
-                _ptr(status), _stream(dev))
-        else:
-            name = "pkv_rotate_append_q8"
-            st = _lib().pkv_rotate_append_q8(
-                _ptr(out), _ptr(q), _ptr(k), _ptr(v), _ptr(positions), ctypes.byref(rotary),
-                _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
-                tokens, kv, ctypes.byref(dims), _ptr(status), _stream(dev))
-    _check(st, name)
+        out_shape, out_stride = _token_rows(out, "out", index)
+        if out_shape != q_shape:
+            _same_shape(out, "out", q_shape)
+    rotary = _pack_rotary(cos_sin.data_ptr(), *norms, out_stride, q_stride, k_stride, v_stride,
+                          *cos_sin.shape, 1 if interleaved else 0, float(eps))
+    dims = _pack_dims(0, hq, hkv, d, bs, nb, 1)
+    rows = (out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
+            rotary, k_cache.data_ptr(), v_cache.data_ptr())
+    status = _status_ptr(status, index)
+    if kv == KV_BF16:
+        name = "pkv_rotate_append_bf16"
+        st = _run(name, index, *rows, slot_mapping.data_ptr(), tokens, dims, status)
+    else:
+        name = "pkv_rotate_append_q8"
+        st = _run(name, index, *rows, k_scale.data_ptr(), v_scale.data_ptr(),
+                  slot_mapping.data_ptr(), tokens, kv, dims, status)
+    if st:
+        _check(st, name)
     return out
 
 
@@ -449,45 +495,39 @@ def paged_kv_gather(k_cache, v_cache, block_tables, out_offsets, num_tokens=None
     ``status`` (int32 [1])."""
     if not isinstance(k_cache, torch.Tensor):
         raise TypeError("k_cache must be a torch.Tensor")
-    kv = KV_BF16 if k_cache.dtype == torch.bfloat16 else _q8_kind(k_cache, fmt)
-    _require_any(k_cache, "k_cache", _code_dtypes(kv), 4, None)
-    dev = k_cache.device
-    _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, dev)
-    if kv == KV_BF16:
-        k_scale = v_scale = None
-    else:
-        _require(k_scale, "k_scale", torch.float32, 3, dev)
-        _require(v_scale, "v_scale", torch.float32, 3, dev)
-    _cache_shapes(k_cache, v_cache, k_scale, v_scale)
-    _require(block_tables, "block_tables", torch.int32, 2, dev)
-    _require(out_offsets, "out_offsets", torch.int32, 1, dev)
-    nb, hkv, bs, d = k_cache.shape
-    B = block_tables.shape[0]
+    kv = KV_BF16 if k_cache.dtype is _BF16 else _q8_kind(k_cache, fmt)
+    index, (nb, hkv, bs, d) = _need_caches(kv, k_cache, v_cache, k_scale, v_scale)
+    _need(block_tables, "block_tables", _I32, 2, index)
+    _need(out_offsets, "out_offsets", _I32, 1, index)
+    B, mbs = block_tables.shape
     _same_shape(out_offsets, "out_offsets", (B + 1,))
     if token_starts is not None:
-        _require(token_starts, "token_starts", torch.int32, 1, dev)
+        _need(token_starts, "token_starts", _I32, 1, index)
         _same_shape(token_starts, "token_starts", (B,))
-    status = _status_word(status, dev)
     if num_tokens is None:
         given = out_k if out_k is not None else out_v
         if not isinstance(given, torch.Tensor):
             raise ValueError("num_tokens is needed without out_k or out_v")
         num_tokens = given.shape[0]
+    rows = (num_tokens, hkv, d)
     outs = []
     for t, n in ((out_k, "out_k"), (out_v, "out_v")):
         if t is None:
-            t = torch.empty((num_tokens, hkv, d), dtype=torch.bfloat16, device=dev)
+            t = torch.empty(rows, dtype=_BF16, device=k_cache.device)
         else:
-            _require(t, n, torch.bfloat16, 3, dev)
-            _same_shape(t, n, (num_tokens, hkv, d))
+            _need(t, n, _BF16, 3, index)
+            if t.shape != rows:
+                _same_shape(t, n, rows)
         outs.append(t)
-    dims = Dims(B, hkv, hkv, d, bs, nb, block_tables.shape[1])
-    with _OnDevice(dev):
-        st = _lib().pkv_gather_tokens(_ptr(outs[0]), _ptr(outs[1]), _ptr(k_cache), _ptr(v_cache),
-                                      _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
-                                      _ptr(token_starts), _ptr(out_offsets), int(num_tokens), kv,
-                                      ctypes.byref(dims), _ptr(status), _stream(dev))
-    _check(st, "pkv_gather_tokens")
+    q8 = kv != KV_BF16
+    st = _run("pkv_gather_tokens", index, outs[0].data_ptr(), outs[1].data_ptr(),
+              k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if q8 else None,
+              v_scale.data_ptr() if q8 else None, block_tables.data_ptr(),
+              token_starts.data_ptr() if token_starts is not None else None,
+              out_offsets.data_ptr(), num_tokens, kv, _pack_dims(B, hkv, hkv, d, bs, nb, mbs),
+              _status_ptr(status, index))
+    if st:
+        _check(st, "pkv_gather_tokens")
     return outs[0], outs[1]
 
 
@@ -651,51 +691,51 @@ def diff_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_si
 
 def _decode_diff(kv, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, lam,
                  scale, norm_weight, eps, out_scale, out, workspace, status):
-    _require(q, "q", torch.bfloat16, 3)
-    dev = q.device
-    status = _status_word(status, dev)
-    _require_any(k_cache, "k_cache", _code_dtypes(kv), 4, dev)
-    _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, dev)
-    if kv != KV_BF16:
-        _require(k_scale, "k_scale", torch.float32, 3, dev)
-        _require(v_scale, "v_scale", torch.float32, 3, dev)
-    _require(block_tables, "block_tables", torch.int32, 2, dev)
-    _require(context_lens, "context_lens", torch.int32, 1, dev)
-    _require(lam, "lam", torch.float32, 1, dev)
-    B, Hq, D = q.shape
-    if k_cache.shape[3] != D:
+    index, (nb, hkv, bs, d) = _need_caches(kv, k_cache, v_cache, k_scale, v_scale)
+    _need(q, "q", _BF16, 3, index)
+    _need(block_tables, "block_tables", _I32, 2, index)
+    _need(context_lens, "context_lens", _I32, 1, index)
+    _need(lam, "lam", _F32, 1, index)
+    B, hq, dq = q.shape
+    rows, mbs = block_tables.shape
+    if dq != d:
         raise ValueError("cache shapes disagree with q")
-    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+    if rows != B or context_lens.shape[0] != B:
         raise ValueError("block_tables / context_lens must have num_seqs rows")
-    _cache_shapes(k_cache, v_cache, k_scale, v_scale)
-    _same_shape(lam, "lam", (Hq // 2,))
+    if lam.shape[0] != hq // 2:
+        _same_shape(lam, "lam", (hq // 2,))
     if norm_weight is not None:
-        _require(norm_weight, "norm_weight", torch.bfloat16, 1, dev)
-        _same_shape(norm_weight, "norm_weight", (2 * D,))
-    dims = _dims(B, Hq, k_cache, block_tables.shape[1])
+        _need(norm_weight, "norm_weight", _BF16, 1, index)
+        _same_shape(norm_weight, "norm_weight", (2 * d,))
     if out is None:
-        out = torch.empty((B, Hq // 2, 2 * D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((B, hq // 2, 2 * d), dtype=_BF16, device=q.device)
     else:
-        _require(out, "out", torch.bfloat16, 3, dev)
-        _same_shape(out, "out", (B, Hq // 2, 2 * D))
-    with _OnDevice(dev):
+        _need(out, "out", _BF16, 3, index)
+        if out.shape != (B, hq // 2, 2 * d):
+            _same_shape(out, "out", (B, hq // 2, 2 * d))
+    dims = _pack_dims(B, hq, hkv, d, bs, nb, mbs)
+    name = "pkv_decode_diff_bf16" if kv == KV_BF16 else "pkv_decode_diff_q8"
+    head = (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
+    tail = (block_tables.data_ptr(), context_lens.data_ptr(), lam.data_ptr(),
+            norm_weight.data_ptr() if norm_weight is not None else None, float(eps),
+            float(out_scale), float(scale))
+    if kv != KV_BF16:
+        head, tail = head + (k_scale.data_ptr(), v_scale.data_ptr()), tail + (kv,)
+    status = _status_ptr(status, index)
+
+    def go(ws, nbytes):
+        return _run(name, index, *head, *tail, dims, ws.data_ptr(), nbytes, status)
+    st = Status.ERR_WORKSPACE
+    if workspace is not None:
+        st = go(*_workspace(workspace, 0, q.device))
+    if st == Status.ERR_WORKSPACE:  # none given, or one that is too small
         need = ctypes.c_size_t(0)
-        _check(_lib().pkv_decode_diff_workspace_bytes(ctypes.byref(dims), kv,
-                                                      ctypes.byref(need)),
-               "pkv_decode_diff_workspace_bytes")
-        workspace, ws_bytes = _workspace(workspace, need.value, dev)
-        tail = (_ptr(block_tables), _ptr(context_lens), _ptr(lam), _ptr(norm_weight), float(eps),
-                float(out_scale), float(scale))
-        end = (ctypes.byref(dims), _ptr(workspace), ws_bytes, _ptr(status), _stream(dev))
-        if kv == KV_BF16:
-            name = "pkv_decode_diff_bf16"
-            st = _lib().pkv_decode_diff_bf16(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                             *tail, *end)
-        else:
-            name = "pkv_decode_diff_q8"
-            st = _lib().pkv_decode_diff_q8(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                           _ptr(k_scale), _ptr(v_scale), *tail, kv, *end)
-    _check(st, name)
+        with torch.cuda.device(index):
+            _check(_lib().pkv_decode_diff_workspace_bytes(dims, kv, ctypes.byref(need)),
+                   "pkv_decode_diff_workspace_bytes")
+        st = go(*_workspace(workspace, need.value, q.device))
+    if st:
+        _check(st, name)
     return out
 
 
