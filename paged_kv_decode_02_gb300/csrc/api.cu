@@ -735,16 +735,16 @@ pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
       return PKV_OK;
     }
   DiffPlan P{};
-  const bool found = kvt == PKV_KV_BF16   ? select_diff_bf16(d->head_dim, d->block_size, &P.k)
-                     : kvt == PKV_KV_INT8 ? select_diff_int8(d->head_dim, d->block_size, &P.k)
-                     : kvt == PKV_KV_FP8_E4M3
-                         ? select_diff_e4m3(d->head_dim, d->block_size, &P.k)
-                         : select_diff_e5m2(d->head_dim, d->block_size, &P.k);
-  if (!found) return PKV_ERR_UNSUPPORTED;
-  // up to 8 query pairs (16 rows of the MMA) per work unit, as evenly as they go
+  // up to 8 query pairs per work unit, as evenly as they go
   const int g = d->num_q_heads / d->num_kv_heads;
   P.nsg = (g + 7) / 8;
   P.gs = (g + P.nsg - 1) / P.nsg;
+  const bool found = kvt == PKV_KV_BF16   ? select_diff_bf16(d->head_dim, d->block_size, P.gs, &P.k)
+                     : kvt == PKV_KV_INT8 ? select_diff_int8(d->head_dim, d->block_size, P.gs, &P.k)
+                     : kvt == PKV_KV_FP8_E4M3
+                         ? select_diff_e4m3(d->head_dim, d->block_size, P.gs, &P.k)
+                         : select_diff_e5m2(d->head_dim, d->block_size, P.gs, &P.k);
+  if (!found) return PKV_ERR_UNSUPPORTED;
   int sms = 0, per_sm = 0, optin = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)

@@ -10,24 +10,27 @@
 // cached byte is read once per step and HBM bandwidth is the bound, at the same bytes as
 // the plain decode.
 //
-// * One contraction for both maps: the M = 16 rows of an m16n8k16 MMA are up to 8 query
-//   pairs' first maps (rows 0-7) and second maps (rows 8-15). Scores are
-//   [Q_0; 0] K_2p^T + [0; Q_1] K_2p+1^T, the two heads accumulating apart; P [16 x tokens]
-//   then multiplies V' once for both maps, so a V tile is read from shared memory once.
-//   Rows r and r + 8 of an MMA's accumulator are in the same lane: the difference, and the
-//   norm up to one 4-lane reduction, are local.
+// * Transposed contractions: tokens (scores) or value columns (P.V) on the M = 16 side of
+//   an m16n8k16 MMA, query rows on N = 8: row 2i is the first map of the warp's query pair
+//   i, row 2i + 1 the second. Four pairs fill the 8 columns, where rows on M would leave
+//   half of 16 empty and double the accumulators (128 registers a lane for 2 D = 256
+//   columns; here 64). S^T = K q^T runs per K head over all 8 columns; the columns of the
+//   other map are not read. The weights turn from S^T's accumulators into P^T's operand
+//   by a movmatrix per 8 tokens. A pair's two maps are neighbouring columns of one lane:
+//   the difference is local, the norm one reduction over 8 lanes.
 // * Work split: (sequence, unit, item) triples in one flat order, an item `kItem` tokens of
-//   one KV pair, cut into G equal ranges, one per CTA (two CTAs per SM). Warp w of a CTA
-//   takes items w, w + N, ... of its range with its own online-softmax state and its own
-//   one-item ring; at the end of a unit the N states fold pairwise through shared memory
-//   (fold.cuh's rescaling). A CTA rather than a warp owns a range because a cut unit's
-//   record is 16 rows of 2 D floats: N times fewer records than with a range per warp.
-//   A unit inside one CTA's range is finished there; a cut one leaves a record per CTA,
-//   which the merge kernel (diff_merge.cu) folds.
+//   one KV pair, cut into G equal ranges, one per CTA. A unit is up to 8 query pairs of a
+//   KV pair. The CTA's warps form streams of kRows warps (one per 4 pairs, reading the
+//   same tiles); stream i takes items i, i + N, ... of the range with its own
+//   online-softmax state and ring; at the end of a unit the streams' states fold through
+//   shared memory (a unit of one item: no fold). A CTA rather than a warp owns a range
+//   because a cut unit's record is 2 rows of 2 D floats per query pair: fewer, larger
+//   ranges leave fewer records. A unit inside one range is finished there; a cut one
+//   leaves a record per CTA, which the merge kernel (diff_merge.cu) folds.
 // * Data movement: a TMA tensor copy brings 16 (or 32) tokens of both heads of a pair at
 //   once (4-D map: swizzle span, token in block, block and head, half of the row). K and V
-//   of an item have a barrier each: the next item's K is requested as soon as the scores
-//   are done with this one's, its V when P.V is.
+//   of an item have a barrier each: the ring's next K is requested as soon as the scores
+//   are done with this one's, its V when P.V is (by the last of the stream's warps).
 // * One-byte caches as in decode.cuh: codes widened exactly to fp16, the K scale on the
 //   fp32 score, the V scale folded into the fp16 weight.
 #pragma once
@@ -39,8 +42,6 @@
 
 namespace pkv {
 
-constexpr int kDiffWarps = 4;
-
 // 4-D tiled tensor copy global -> shared; completes its bytes on the mbarrier.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int32_t x, int32_t y, int32_t z, int32_t w) {
@@ -49,6 +50,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
+}
+
+// Transposes an 8x8 matrix of 16-bit values held by the warp (lane: row lane / 4, columns
+// 2 (lane % 4) and the next).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 // A box: kBox tokens of both heads of a pair, as the TMA lands it: [half][head][token] rows
@@ -67,13 +76,8 @@ struct DiffGeom {
   static constexpr int kTile = kBoxBytes * SUB;          // K (or V) of an item
   static constexpr int kScaleBox = kQ8 ? 2 * BOX * 4 : 0;
   static constexpr int kScales = kScaleBox * SUB;
-  // a warp's ring: K, V, K scales, V scales, two barriers
-  static constexpr int kOffV = kTile, kOffKs = 2 * kTile, kOffVs = kOffKs + kScales;
-  static constexpr int kOffBar = kOffVs + kScales;
-  static constexpr int kRing = (kOffBar + 16 + 1023) / 1024 * 1024;
-  // one warp's state in the pairwise fold: o as 16-byte words per lane, (m, l) x 2 rows
-  static constexpr int kStateWords = 2 * D / 8;
-  static constexpr int kState = kStateWords * 512 + 512;
+  // half a warp's state in the fold: half of o as 16-byte words per lane, and m and l
+  static constexpr int kState = (D / 16 + 1) * 512;
   static_assert(kBoxBytes % 1024 == 0, "boxes must keep 1024-byte alignment");
 
   // Swizzled byte offset of 16-byte chunk cc of token t (of the item) of pair head hd.
@@ -89,196 +93,203 @@ struct DiffGeom {
   }
 };
 
-// State of one warp: rows gid (first map of the unit's query pair gid) and gid + 8 (second
-// map) of the 16-row MMA; o[nd][0..1] belong to the first, o[nd][2..3] to the second.
+// State of one warp. Lane (gid, cq) = (lane / 4, lane % 4) holds both maps (columns 2 cq
+// and 2 cq + 1) of query pair cq: o[mt][0..1] of one value column of m-tile mt,
+// o[mt][2..3] of another; m and l of the pair's maps (l summed over this lane's tokens
+// only, until close()).
 template <int D>
 struct DiffState {
-  static constexpr int kND = 2 * D / 8;
-  float o[kND][4];
+  static constexpr int kMT = 2 * D / 16;
+  float o[kMT][4];
   float m0, m1, l0, l1;
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int nd = 0; nd < kND; ++nd) o[nd][0] = o[nd][1] = o[nd][2] = o[nd][3] = 0.f;
+    for (int i = 0; i < kMT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.f;
   }
-  // New row maxima over an item: rescales the state, returns what the item's scores
-  // subtract. Every token of an item that a warp takes is of the context, so the maxima
-  // are of at least one score; -inf (a score of -inf) subtracts 0.
+  __device__ __forceinline__ void scale(float a0, float a1) {
+    l0 *= a0;
+    l1 *= a1;
+#pragma unroll
+    for (int i = 0; i < kMT; ++i) {
+      o[i][0] *= a0;
+      o[i][1] *= a1;
+      o[i][2] *= a0;
+      o[i][3] *= a1;
+    }
+  }
+  // New maxima over an item (mx: this lane's tokens): rescales the state, returns what the
+  // item's scores subtract. A map without a score above -inf yet subtracts 0.
   __device__ __forceinline__ void raise(float mx0, float mx1, float& mn0, float& mn1) {
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+#pragma unroll
+    for (int k = 4; k < 32; k <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, k));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, k));
+    }
     const float p0 = m0, p1 = m1;
     m0 = fmaxf(m0, mx0);
     m1 = fmaxf(m1, mx1);
     mn0 = m0 == -INFINITY ? 0.f : m0;
     mn1 = m1 == -INFINITY ? 0.f : m1;
-    const float a0 = fast_exp2(p0 - mn0), a1 = fast_exp2(p1 - mn1);
-    l0 *= a0;
-    l1 *= a1;
+    // most items raise no maximum: then every factor is 1 (or the state is still 0)
+    if (__any_sync(0xffffffffu, m0 != p0 || m1 != p1))
+      scale(fast_exp2(p0 - mn0), fast_exp2(p1 - mn1));
+  }
+  __device__ __forceinline__ void close() {
 #pragma unroll
-    for (int nd = 0; nd < kND; ++nd) {
-      o[nd][0] *= a0;
-      o[nd][1] *= a0;
-      o[nd][2] *= a1;
-      o[nd][3] *= a1;
+    for (int k = 4; k < 32; k <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, k);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, k);
     }
   }
-  __device__ __forceinline__ void put(uint8_t* buf, int lane) const {
-    float4* b = reinterpret_cast<float4*>(buf);
+  // Half h of the state into buf, for another warp to fold in.
+  __device__ __forceinline__ void put(uint8_t* buf, int h, int lane) const {
+    float4* b = reinterpret_cast<float4*>(buf) + lane;
 #pragma unroll
-    for (int nd = 0; nd < kND; ++nd)
-      b[nd * 32 + lane] = make_float4(o[nd][0], o[nd][1], o[nd][2], o[nd][3]);
-    b[kND * 32 + lane] = make_float4(m0, m1, l0, l1);
+    for (int i = 0; i < kMT / 2; ++i) {
+      const float* v = h ? o[kMT / 2 + i] : o[i];
+      b[i * 32] = make_float4(v[0], v[1], v[2], v[3]);
+    }
+    if (h == 0) b[kMT / 2 * 32] = make_float4(m0, m1, l0, l1);
   }
-  __device__ __forceinline__ void fold(const uint8_t* buf, int lane) {
-    const float4* b = reinterpret_cast<const float4*>(buf);
-    const float4 s = b[kND * 32 + lane];
-    const float n0 = fmaxf(m0, s.x), n1 = fmaxf(m1, s.y);
-    const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
-    const float a0 = fast_exp2(m0 - z0), a1 = fast_exp2(m1 - z1);
-    const float b0 = fast_exp2(s.x - z0), b1 = fast_exp2(s.y - z1);
-    m0 = n0;
-    m1 = n1;
-    l0 = l0 * a0 + s.z * b0;
-    l1 = l1 * a1 + s.w * b1;
+  // Folds another warp's half h in; f: the factors of its maps, set with half 0.
+  __device__ __forceinline__ void fold(const uint8_t* buf, int h, int lane, float2& f) {
+    const float4* b = reinterpret_cast<const float4*>(buf) + lane;
+    if (h == 0) {
+      const float4 s = b[kMT / 2 * 32];
+      const float n0 = fmaxf(m0, s.x), n1 = fmaxf(m1, s.y);
+      const float z0 = n0 == -INFINITY ? 0.f : n0, z1 = n1 == -INFINITY ? 0.f : n1;
+      f = make_float2(fast_exp2(s.x - z0), fast_exp2(s.y - z1));
+      scale(fast_exp2(m0 - z0), fast_exp2(m1 - z1));
+      m0 = n0;
+      m1 = n1;
+      l0 = fmaf(s.z, f.x, l0);
+      l1 = fmaf(s.w, f.y, l1);
+    }
 #pragma unroll
-    for (int nd = 0; nd < kND; ++nd) {
-      const float4 v = b[nd * 32 + lane];
-      o[nd][0] = o[nd][0] * a0 + v.x * b0;
-      o[nd][1] = o[nd][1] * a0 + v.y * b0;
-      o[nd][2] = o[nd][2] * a1 + v.z * b1;
-      o[nd][3] = o[nd][3] * a1 + v.w * b1;
+    for (int i = 0; i < kMT / 2; ++i) {
+      const float4 v = b[i * 32];
+      float* d = h ? o[kMT / 2 + i] : o[i];
+      d[0] = fmaf(v.x, f.x, d[0]);
+      d[1] = fmaf(v.y, f.y, d[1]);
+      d[2] = fmaf(v.z, f.x, d[2]);
+      d[3] = fmaf(v.w, f.y, d[3]);
     }
   }
 };
 
-// Tensor-core path over a bf16 cache. The softmax weights enter P.V as bf16 (half a step
-// of 2^-9 each, averaging out over tokens) and the row sums are of the rounded weights.
+// bf16 cache. The softmax weights enter P.V as bf16 (off by at most 2^-8 each, averaging
+// out over tokens), the row sums are of the rounded weights.
 template <int D, int BOX, int SUB>
 struct DiffPathBf16 {
   using Geo = DiffGeom<D, -1, BOX, SUB>;
-  static constexpr int kKS = D / 16, kNT = Geo::kItem / 8, kKK = Geo::kItem / 16;
+  static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr float kOutScale = 1.f;
-  uint32_t qa[kKS][4];
+  uint32_t qb[kKS][2];
   DiffState<D> st;
 
-  // A 2 D row from the lanes' columns: run k holds 2 neighbouring ones, from column(k, cq).
-  static constexpr int kRun = 2, kRuns = 2 * D / 8;
-  __device__ static __forceinline__ int column(int k, int cq) { return k * 8 + 2 * cq; }
-  __device__ static __forceinline__ float at(const float (&o)[kRuns][4], int k, int e, int row) {
-    return o[k][2 * row + e];
+  // A lane's columns of a 2 D row: kRun neighbouring ones from column(k, gid), in
+  // o[at(k, e)][half(k, e) * 2 + map].
+  static constexpr int kRun = 1, kRuns = 2 * D / 8;
+  __device__ static __forceinline__ int column(int k, int gid) { return 8 * k + gid; }
+  __device__ static __forceinline__ float at(const float (&o)[2 * D / 16][4], int k, int,
+                                             int map) {
+    return o[k / 2][2 * (k % 2) + map];
   }
 
-  // q0, q1: the two maps' query rows of query pair gid (D elements), when live.
-  __device__ __forceinline__ void begin(const __nv_bfloat16* q0, const __nv_bfloat16* q1,
-                                        bool live, int cq, float) {
-    const uint32_t* w0 = reinterpret_cast<const uint32_t*>(q0);
-    const uint32_t* w1 = reinterpret_cast<const uint32_t*>(q1);
+  // q: row gid (pair gid / 2's map gid % 2) of the warp's query rows, when live.
+  __device__ __forceinline__ void begin(const __nv_bfloat16* q, bool live, int lane, float) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(q) + (lane & 3);
 #pragma unroll
     for (int ks = 0; ks < kKS; ++ks) {
-      const int w = 8 * ks + cq;
-      qa[ks][0] = live ? __ldg(w0 + w) : 0u;
-      qa[ks][1] = live ? __ldg(w1 + w) : 0u;
-      qa[ks][2] = live ? __ldg(w0 + w + 4) : 0u;
-      qa[ks][3] = live ? __ldg(w1 + w + 4) : 0u;
+      qb[ks][0] = live ? __ldg(w + 8 * ks) : 0u;
+      qb[ks][1] = live ? __ldg(w + 8 * ks + 4) : 0u;
     }
     st.clear();
   }
 
-  // Scores of the item's tokens, in log2 units; tokens from nvalid on are -inf.
-  __device__ __forceinline__ void scores(float (&x)[kNT][4], uint32_t sK, uint32_t, int nvalid,
+  // Scores of tokens 16 t + gid (x[t][0..1], by map) and 16 t + 8 + gid (x[t][2..3]) in log2
+  // units; tokens from nvalid on are -inf.
+  __device__ __forceinline__ void scores(float (&x)[kT][4], uint32_t sK, uint32_t, int nvalid,
                                          int lane, float scale_log2) {
-    const int r8 = lane & 7, mi = lane >> 3, cq = lane & 3;
+    const int r8 = lane & 7, mi = lane >> 3, gid = lane >> 2;
 #pragma unroll
-    for (int np = 0; np < kNT / 2; ++np) {
-      float a[2][4] = {}, b[2][4] = {};  // first and second heads' scores apart
+    for (int t = 0; t < kT; ++t) {
+      float a[4] = {}, b[4] = {};
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t k0[4], k1[4];
-        const int t = np * 16 + ((mi >> 1) << 3) + r8, cc = 2 * ks + (mi & 1);
-        ldmatrix_x4(k0, sK + Geo::off(0, t, cc));
-        ldmatrix_x4(k1, sK + Geo::off(1, t, cc));
-        const uint32_t q0[4] = {qa[ks][0], 0u, qa[ks][2], 0u};
-        const uint32_t q1[4] = {0u, qa[ks][1], 0u, qa[ks][3]};
-        mma_bf16_16816(a[0], q0, k0[0], k0[1]);
-        mma_bf16_16816(a[1], q0, k0[2], k0[3]);
-        mma_bf16_16816(b[0], q1, k1[0], k1[1]);
-        mma_bf16_16816(b[1], q1, k1[2], k1[3]);
+        const int row = 16 * t + ((mi & 1) << 3) + r8, cc = 2 * ks + (mi >> 1);
+        ldmatrix_x4(k0, sK + Geo::off(0, row, cc));
+        ldmatrix_x4(k1, sK + Geo::off(1, row, cc));
+        mma_bf16_16816(a, k0, qb[ks][0], qb[ks][1]);
+        mma_bf16_16816(b, k1, qb[ks][0], qb[ks][1]);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const bool ok = np * 16 + h * 8 + 2 * cq + e < nvalid;
-          x[2 * np + h][e] = ok ? a[h][e] * scale_log2 : -INFINITY;
-          x[2 * np + h][e + 2] = ok ? b[h][e + 2] * scale_log2 : -INFINITY;
-        }
-      }
+      const bool lo = 16 * t + gid < nvalid, hi = 16 * t + 8 + gid < nvalid;
+      x[t][0] = lo ? a[0] * scale_log2 : -INFINITY;
+      x[t][1] = lo ? b[1] * scale_log2 : -INFINITY;
+      x[t][2] = hi ? a[2] * scale_log2 : -INFINITY;
+      x[t][3] = hi ? b[3] * scale_log2 : -INFINITY;
     }
   }
 
-  __device__ __forceinline__ void values(float (&x)[kNT][4], uint32_t sV, uint32_t, int,
+  __device__ __forceinline__ void values(float (&x)[kT][4], uint32_t sV, uint32_t, int,
                                          float mn0, float mn1, int lane) {
     const int r8 = lane & 7, mi = lane >> 3;
 #pragma unroll
-    for (int kk = 0; kk < kKK; ++kk) {
-      uint32_t pa[4];
+    for (int t = 0; t < kT; ++t) {
+      uint32_t pb[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float* s = x[2 * kk + h];
-        pa[2 * h] = pack_bf16x2(fast_exp2(s[0] - mn0), fast_exp2(s[1] - mn0));
-        pa[2 * h + 1] = pack_bf16x2(fast_exp2(s[2] - mn1), fast_exp2(s[3] - mn1));
-        const float2 f0 = unpack_bf16x2(pa[2 * h]), f1 = unpack_bf16x2(pa[2 * h + 1]);
-        st.l0 += f0.x + f0.y;
-        st.l1 += f1.x + f1.y;
+        const uint32_t w =
+            pack_bf16x2(fast_exp2(x[t][2 * h] - mn0), fast_exp2(x[t][2 * h + 1] - mn1));
+        const float2 f = unpack_bf16x2(w);
+        st.l0 += f.x;
+        st.l1 += f.y;
+        pb[h] = transpose_8x8(w);
       }
 #pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
-#pragma unroll
-        for (int n2 = 0; n2 < D / 16; ++n2) {
-          uint32_t b[4];
-          ldmatrix_x4_trans(
-              b, sV + Geo::off(hd, 16 * kk + ((mi & 1) << 3) + r8, 2 * n2 + (mi >> 1)));
-          mma_bf16_16816(st.o[hd * (D / 8) + 2 * n2], pa, b[0], b[1]);
-          mma_bf16_16816(st.o[hd * (D / 8) + 2 * n2 + 1], pa, b[2], b[3]);
-        }
+      for (int mt = 0; mt < 2 * D / 16; ++mt) {
+        uint32_t v[4];
+        ldmatrix_x4_trans(v, sV + Geo::off(mt / (D / 16), 16 * t + ((mi >> 1) << 3) + r8,
+                                           2 * (mt % (D / 16)) + (mi & 1)));
+        mma_bf16_16816(st.o[mt], v, pb[0], pb[1]);
       }
     }
   }
 };
 
-// Tensor-core path over one-byte codes (fp16 MMAs on exactly widened codes; kVUp as in
-// MmaPathInt8 keeps the weight times the V scale out of fp16's subnormal range).
+// One-byte codes (fp16 MMAs on exactly widened codes; kVUp as in MmaPathInt8 keeps the
+// weight times the V scale out of fp16's subnormal range).
 template <int D, int CODE, int BOX, int SUB>
 struct DiffPathQ8 {
   using Geo = DiffGeom<D, CODE, BOX, SUB>;
   using Codec = Code8<CODE>;
   static constexpr float kVUp = CODE == CODE_E5M2 ? 32768.f : CODE == CODE_E4M3 ? 256.f : 1.f;
   static constexpr float kOutScale = 1.f / kVUp;
-  static constexpr int kKS = D / 16, kNT = Geo::kItem / 8, kKK = Geo::kItem / 16;
+  static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr int kQB = D / 4, kQC = kQB / 16;  // bytes of a K row each lane reads
-  uint32_t qa[kKS][4];
-  float rs0, rs1, qb0, qb1;
+  uint32_t qb[kKS][2];
+  float rs0, rs1, off0, off1;
   DiffState<D> st;
 
-  // n-tile 4 k + i (k counts over both heads), column n holds element 32 k + 4 n + i of the
-  // 2 D row: a lane's run k is the 8 elements from 32 k + 8 cq.
-  static constexpr int kRun = 8, kRuns = 2 * D / 32;
-  __device__ static __forceinline__ int column(int k, int cq) { return 32 * k + 8 * cq; }
-  __device__ static __forceinline__ float at(const float (&o)[2 * D / 8][4], int k, int e,
-                                             int row) {
-    return o[4 * k + e % 4][2 * row + e / 4];
+  // m-tiles 2 k and 2 k + 1 (k counts over both heads): rows gid and gid + 8 hold elements
+  // 32 k + 4 gid + 0..1 and + 2..3 of the 2 D row: a lane's run k is 4 neighbours.
+  static constexpr int kRun = 4, kRuns = 2 * D / 32;
+  __device__ static __forceinline__ int column(int k, int gid) { return 32 * k + 4 * gid; }
+  __device__ static __forceinline__ float at(const float (&o)[2 * D / 16][4], int k, int e,
+                                             int map) {
+    return o[2 * k + e / 2][2 * (e % 2) + map];
   }
 
-  // One map's row: scaled by a power of two to near 2^14 (then exact in fp16 for entries
-  // above 2^-28 of the largest), rs the score scale that undoes it; INT8 codes enter the
-  // score MMA as code + 1152, whose 1152 * sum(q) comes off the score.
-  __device__ __forceinline__ void load_row(const __nv_bfloat16* q, bool live, int cq, int slot,
-                                           float scale_log2, float& rs, float& qb) {
+  // The row is scaled by a power of two to near 2^14 (then exact in fp16 for entries above
+  // 2^-28 of the largest), rs the score scale that undoes it; INT8 codes enter the score
+  // MMA as code + 1152, whose 1152 * sum(q) comes off the score.
+  __device__ __forceinline__ void begin(const __nv_bfloat16* q, bool live, int lane,
+                                        float scale_log2) {
+    const int cq = lane & 3;
     const uint2* qd = reinterpret_cast<const uint2*>(q);
     float f[kKS][4], mx = 0.f;
 #pragma unroll
@@ -293,114 +304,110 @@ struct DiffPathQ8 {
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     int ex = 0;
     if (mx > 0.f) { frexpf(mx, &ex); ex = 14 - ex; }
-    const float sc = ldexpf(1.f, ex);
-    rs = scale_log2 * ldexpf(1.f, -ex);
+    const float sc = ldexpf(1.f, ex), rs = scale_log2 * ldexpf(1.f, -ex);
     float t = 0.f;
 #pragma unroll
     for (int ks = 0; ks < kKS; ++ks) {
-      qa[ks][slot] = pack_f16x2(f[ks][0] * sc, f[ks][1] * sc);
-      qa[ks][slot + 2] = pack_f16x2(f[ks][2] * sc, f[ks][3] * sc);
-      const float2 a = unpack_f16x2(qa[ks][slot]), b = unpack_f16x2(qa[ks][slot + 2]);
+      qb[ks][0] = pack_f16x2(f[ks][0] * sc, f[ks][1] * sc);
+      qb[ks][1] = pack_f16x2(f[ks][2] * sc, f[ks][3] * sc);
+      const float2 a = unpack_f16x2(qb[ks][0]), b = unpack_f16x2(qb[ks][1]);
       t += (a.x + a.y) + (b.x + b.y);
     }
-    qb = 0.f;
+    float qs = 0.f;
     if constexpr (CODE == CODE_I8) {
       t += __shfl_xor_sync(0xffffffffu, t, 1);
       t += __shfl_xor_sync(0xffffffffu, t, 2);
-      qb = 1152.f * t;
+      qs = 1152.f * t;
     }
-  }
-
-  __device__ __forceinline__ void begin(const __nv_bfloat16* q0, const __nv_bfloat16* q1,
-                                        bool live, int cq, float scale_log2) {
-    load_row(q0, live, cq, 0, scale_log2, rs0, qb0);
-    load_row(q1, live, cq, 1, scale_log2, rs1, qb1);
+    // of this lane's columns: query rows 2 cq and 2 cq + 1
+    rs0 = __shfl_sync(0xffffffffu, rs, 8 * cq);
+    rs1 = __shfl_sync(0xffffffffu, rs, 8 * cq + 4);
+    off0 = __shfl_sync(0xffffffffu, qs, 8 * cq);
+    off1 = __shfl_sync(0xffffffffu, qs, 8 * cq + 4);
     st.clear();
   }
 
-  __device__ __forceinline__ void scores(float (&x)[kNT][4], uint32_t sK, uint32_t sKs,
+  __device__ __forceinline__ void scores(float (&x)[kT][4], uint32_t sK, uint32_t sKs,
                                          int nvalid, int lane, float) {
     const int gid = lane >> 2, cq = lane & 3;
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) {
-      float a[2][4] = {};
+    for (int t = 0; t < kT; ++t) {
+      float acc[2][4] = {};
 #pragma unroll
       for (int hd = 0; hd < 2; ++hd) {
 #pragma unroll
         for (int ch = 0; ch < kQC; ++ch) {
-          const uint4 raw = lds128(sK + Geo::off(hd, nt * 8 + gid, kQC * cq + ch));
-          const uint32_t w[4] = {Codec::pre(raw.x), Codec::pre(raw.y), Codec::pre(raw.z),
-                                 Codec::pre(raw.w)};
+          const uint4 r0 = lds128(sK + Geo::off(hd, 16 * t + gid, kQC * cq + ch));
+          const uint4 r1 = lds128(sK + Geo::off(hd, 16 * t + 8 + gid, kQC * cq + ch));
+          const uint32_t w0[4] = {Codec::pre(r0.x), Codec::pre(r0.y), Codec::pre(r0.z),
+                                  Codec::pre(r0.w)};
+          const uint32_t w1[4] = {Codec::pre(r1.x), Codec::pre(r1.y), Codec::pre(r1.z),
+                                  Codec::pre(r1.w)};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int ks = 4 * ch + k;
-            const uint32_t q[4] = {hd ? 0u : qa[ks][0], hd ? qa[ks][1] : 0u,
-                                   hd ? 0u : qa[ks][2], hd ? qa[ks][3] : 0u};
-            if constexpr (CODE == CODE_I8)
-              mma_f16_16816(a[hd], q, prmt(w[k], 0x64646464u, 0x4140u),
-                            prmt(w[k], 0x64646464u, 0x4342u));
-            else
-              mma_f16_16816(a[hd], q, Codec::lo(w[k]), Codec::hi(w[k]));
+            uint32_t a[4];
+            if constexpr (CODE == CODE_I8) {
+              a[0] = prmt(w0[k], 0x64646464u, 0x4140u);
+              a[1] = prmt(w1[k], 0x64646464u, 0x4140u);
+              a[2] = prmt(w0[k], 0x64646464u, 0x4342u);
+              a[3] = prmt(w1[k], 0x64646464u, 0x4342u);
+            } else {
+              a[0] = Codec::lo(w0[k]);
+              a[1] = Codec::lo(w1[k]);
+              a[2] = Codec::hi(w0[k]);
+              a[3] = Codec::hi(w1[k]);
+            }
+            mma_f16_16816(acc[hd], a, qb[ks][0], qb[ks][1]);
           }
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int tok = nt * 8 + 2 * cq + e;
+      for (int h = 0; h < 2; ++h) {
+        const int tok = 16 * t + 8 * h + gid;
         const bool ok = tok < nvalid;
-        x[nt][e] = ok ? (a[0][e] - qb0) * lds_f32(sKs + Geo::scale_off(0, tok)) * rs0 : -INFINITY;
-        x[nt][e + 2] =
-            ok ? (a[1][e + 2] - qb1) * lds_f32(sKs + Geo::scale_off(1, tok)) * rs1 : -INFINITY;
+        x[t][2 * h] = ok ? (acc[0][2 * h] - off0) * lds_f32(sKs + Geo::scale_off(0, tok)) * rs0
+                         : -INFINITY;
+        x[t][2 * h + 1] =
+            ok ? (acc[1][2 * h + 1] - off1) * lds_f32(sKs + Geo::scale_off(1, tok)) * rs1
+               : -INFINITY;
       }
     }
   }
 
-  __device__ __forceinline__ void values(float (&x)[kNT][4], uint32_t sV, uint32_t sVs,
+  __device__ __forceinline__ void values(float (&x)[kT][4], uint32_t sV, uint32_t sVs,
                                          int nvalid, float mn0, float mn1, int lane) {
     const int gid = lane >> 2, cq = lane & 3;
 #pragma unroll
-    for (int kk = 0; kk < kKK; ++kk) {
-      float w[2][4];  // weights of tokens 16 kk + 8 h + 2 cq (+ 1)
+    for (int t = 0; t < kT; ++t) {
+      uint32_t pb[2][2];  // each value head has its own scales
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float* s = x[2 * kk + h];
-        w[h][0] = fast_exp2(s[0] - mn0);
-        w[h][1] = fast_exp2(s[1] - mn0);
-        w[h][2] = fast_exp2(s[2] - mn1);
-        w[h][3] = fast_exp2(s[3] - mn1);
-        st.l0 += w[h][0] + w[h][1];
-        st.l1 += w[h][2] + w[h][3];
+        const float w0 = fast_exp2(x[t][2 * h] - mn0), w1 = fast_exp2(x[t][2 * h + 1] - mn1);
+        st.l0 += w0;
+        st.l1 += w1;
+        const int tok = 16 * t + 8 * h + gid;
+#pragma unroll
+        for (int hd = 0; hd < 2; ++hd) {
+          const float vs = tok < nvalid ? lds_f32(sVs + Geo::scale_off(hd, tok)) * kVUp : 0.f;
+          pb[hd][h] = transpose_8x8(pack_f16x2(w0 * vs, w1 * vs));
+        }
       }
-      const int ta = 16 * kk + 2 * cq;
+      const int ta = 16 * t + 2 * cq;
 #pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
-        uint32_t pa[4];  // each value head has its own scales
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float vs[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int tok = ta + 8 * h + e;
-            vs[e] = tok < nvalid ? lds_f32(sVs + Geo::scale_off(hd, tok)) * kVUp : 0.f;
-          }
-          pa[2 * h] = pack_f16x2(w[h][0] * vs[0], w[h][1] * vs[1]);
-          pa[2 * h + 1] = pack_f16x2(w[h][2] * vs[0], w[h][3] * vs[1]);
-        }
-#pragma unroll
-        for (int qg = 0; qg < D / 32; ++qg) {
-          const int bo = 32 * qg + 4 * gid, ch = bo >> 4, wi = bo & 15;
-          const uint32_t w0 = Codec::pre(lds32(sV + Geo::off(hd, ta, ch) + wi));
-          const uint32_t w1 = Codec::pre(lds32(sV + Geo::off(hd, ta + 1, ch) + wi));
-          const uint32_t w2 = Codec::pre(lds32(sV + Geo::off(hd, ta + 8, ch) + wi));
-          const uint32_t w3 = Codec::pre(lds32(sV + Geo::off(hd, ta + 9, ch) + wi));
-          const uint32_t x01 = prmt(w0, w1, 0x5140u), x23 = prmt(w0, w1, 0x7362u);
-          const uint32_t y01 = prmt(w2, w3, 0x5140u), y23 = prmt(w2, w3, 0x7362u);
-          float (*o)[4] = &st.o[hd * (D / 8) + 4 * qg];
-          mma_f16_16816(o[0], pa, Codec::lo(x01), Codec::lo(y01));
-          mma_f16_16816(o[1], pa, Codec::hi(x01), Codec::hi(y01));
-          mma_f16_16816(o[2], pa, Codec::lo(x23), Codec::lo(y23));
-          mma_f16_16816(o[3], pa, Codec::hi(x23), Codec::hi(y23));
-        }
+      for (int k = 0; k < 2 * D / 32; ++k) {
+        const int hd = k / (D / 32);
+        const int bo = 32 * (k % (D / 32)) + 4 * gid, ch = bo >> 4, wi = bo & 15;
+        const uint32_t w0 = Codec::pre(lds32(sV + Geo::off(hd, ta, ch) + wi));
+        const uint32_t w1 = Codec::pre(lds32(sV + Geo::off(hd, ta + 1, ch) + wi));
+        const uint32_t w2 = Codec::pre(lds32(sV + Geo::off(hd, ta + 8, ch) + wi));
+        const uint32_t w3 = Codec::pre(lds32(sV + Geo::off(hd, ta + 9, ch) + wi));
+        const uint32_t x01 = prmt(w0, w1, 0x5140u), x23 = prmt(w0, w1, 0x7362u);
+        const uint32_t y01 = prmt(w2, w3, 0x5140u), y23 = prmt(w2, w3, 0x7362u);
+        const uint32_t a[4] = {Codec::lo(x01), Codec::hi(x01), Codec::lo(y01), Codec::hi(y01)};
+        const uint32_t b[4] = {Codec::lo(x23), Codec::hi(x23), Codec::lo(y23), Codec::hi(y23)};
+        mma_f16_16816(st.o[2 * k], a, pb[hd][0], pb[hd][1]);
+        mma_f16_16816(st.o[2 * k + 1], b, pb[hd][0], pb[hd][1]);
       }
     }
   }
@@ -412,32 +419,55 @@ __device__ __forceinline__ int diff_items(const DiffParams& p, int i, int item) 
   return (max(0, min(L, p.MBS * p.BS)) + item - 1) / item;
 }
 
-template <int D, class Path>
-__global__ void __launch_bounds__(kDiffWarps * 32, 2)
+// Shared memory of a CTA: the streams' rings, the fold's states, barriers and counters,
+// the items' prefix.
+template <class Geo, int kStreams, int kRows, int kStages>
+struct DiffSmem {
+  static constexpr int kSlot = 2 * Geo::kTile;                    // K and V of an item
+  static constexpr int kRing = kStages * kSlot;
+  static constexpr int kOffScale = kStreams * kRing;
+  static constexpr int kOffState = kOffScale + kStreams * kStages * 2 * Geo::kScales;
+  static constexpr int kOffBar = kOffState + (kStreams > 1 ? kRows * Geo::kState : 0);
+  static constexpr int kOffCnt = kOffBar + kStreams * kStages * 16;
+  static constexpr int kOffPrefix = (kOffCnt + kStreams * kStages * 8 + 15) / 16 * 16;
+};
+
+template <int D, class Path, int kStreams, int kRows, int kStages, int kCtas>
+__global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     paged_diff_decode_kernel(const __grid_constant__ CUtensorMap tmk,
                              const __grid_constant__ CUtensorMap tmv, const DiffParams p) {
   using Geo = typename Path::Geo;
-  constexpr int N = kDiffWarps, kThreads = N * 32, kND = 2 * D / 8;
+  using S = DiffSmem<Geo, kStreams, kRows, kStages>;
+  constexpr int N = kStreams, kWarps = kStreams * kRows, kThreads = kWarps * 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (base - smem_u32(smem_raw));
-  uint8_t* states = gen + N * Geo::kRing;                       // [N / 2] folded states
-  int* prefix = reinterpret_cast<int*>(states + (N / 2) * Geo::kState);
-  __shared__ int warp_tot[N];
+  int* prefix = reinterpret_cast<int*>(gen + S::kOffPrefix);
+  __shared__ int warp_tot[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int stream = warp / kRows, tile = warp % kRows;  // tile: query pairs 4 tile .. + 3
   const int gid = lane >> 2, cq = lane & 3;
   const int B = p.B;
-  const uint32_t ring = base + warp * Geo::kRing;
-  const uint32_t sK = ring, sV = ring + Geo::kOffV;
-  const uint32_t sKs = ring + Geo::kOffKs, sVs = ring + Geo::kOffVs;
-  const uint32_t barK = ring + Geo::kOffBar, barV = barK + 8;
-  if (lane == 0) {
-    mbar_init(barK, 1);
-    mbar_init(barV, 1);
+  auto sK = [&](int st) { return base + stream * S::kRing + st * S::kSlot; };
+  auto sV = [&](int st) { return sK(st) + Geo::kTile; };
+  auto sKs = [&](int st) {
+    return base + S::kOffScale + (stream * kStages + st) * 2 * Geo::kScales;
+  };
+  auto sVs = [&](int st) { return sKs(st) + Geo::kScales; };
+  auto barK = [&](int st) { return base + S::kOffBar + (stream * kStages + st) * 16; };
+  auto barV = [&](int st) { return barK(st) + 8; };
+  if (lane == 0 && tile == 0) {
+    for (int st = 0; st < kStages; ++st) {
+      mbar_init(barK(st), 1);
+      mbar_init(barV(st), 1);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
+  }
+  if constexpr (kRows > 1) {
+    if (tid < kStreams * kStages * 2) reinterpret_cast<int*>(gen + S::kOffCnt)[tid] = 0;
   }
   pdl_wait_prior_grid();
 
@@ -475,9 +505,10 @@ __global__ void __launch_bounds__(kDiffWarps * 32, 2)
 
   Cursor cur;  // the segment: unit cur.u of sequence cur.s from its item cur.j on
   cursor_locate(cur, a, prefix, B, U);
-  // the producer's item: number pi of the CTA's range, every N-th one is this warp's
+  // the producer's item: number pi of the CTA's range, every N-th one is this stream's.
+  // Each of the stream's warps keeps it; the last one to leave a tile requests the next.
   Cursor pc = cur;
-  int pi = 0, pid[Geo::kSub], pL = 0;
+  int pi = 0, pid[Geo::kSub], pL = 0, pLs = -1;
   auto advance = [&](int k) {
     pi += k;
     if (pi >= n) return;
@@ -494,21 +525,19 @@ __global__ void __launch_bounds__(kDiffWarps * 32, 2)
   // lane 0: the physical blocks of the producer's item, read ahead of their copies
   auto fetch = [&]() {
     if (lane != 0 || pi >= n) return;
-    pL = min(__ldg(p.context_lens + pc.s), p.MBS * p.BS);
+    if (pc.s != pLs) {
+      pL = min(__ldg(p.context_lens + pc.s), p.MBS * p.BS);
+      pLs = pc.s;
+    }
 #pragma unroll
     for (int k = 0; k < Geo::kSub; ++k) {
       const int t = (pc.j * Geo::kSub + k) * Geo::kBox;
-      pid[k] = 0;
-      if (t < pL) {
-        const int id = __ldg(p.block_tables + size_t(pc.s) * p.MBS + t / p.BS);
-        pid[k] = id < 0 || id >= p.NB ? 0 : id;  // stay in the pool
-      }
+      pid[k] = t < pL ? __ldg(p.block_tables + size_t(pc.s) * p.MBS + t / p.BS) : 0;
     }
   };
   // lane 0: requests K (or V) of the producer's item; boxes past the context are left out
-  auto issue = [&](const CUtensorMap* map, uint32_t tile, uint32_t scales, const float* scale,
-                   uint32_t bar) {
-    if (lane != 0 || pi >= n) return;
+  auto request = [&](const CUtensorMap* map, uint32_t dst, uint32_t scales, const float* scale,
+                     uint32_t bar) {
     const int t0 = pc.j * Geo::kItem;
     const int boxes = min(Geo::kSub, (pL - t0 + Geo::kBox - 1) / Geo::kBox);
     mbar_arrive_expect_tx(bar, uint32_t(boxes) * (Geo::kBoxBytes + Geo::kScaleBox));
@@ -517,150 +546,179 @@ __global__ void __launch_bounds__(kDiffWarps * 32, 2)
     for (int k = 0; k < Geo::kSub; ++k) {
       if (k >= boxes) break;
       const int in = (t0 + k * Geo::kBox) % p.BS;
-      const int row = pid[k] * 2 * p.P + head;
-      tma_load_4d(tile + k * Geo::kBoxBytes, map, bar, 0, in, row, 0);
+      const int id = pid[k] < 0 || pid[k] >= p.NB ? 0 : pid[k];  // stay in the pool
+      const int row = id * 2 * p.P + head;
+      tma_load_4d(dst + k * Geo::kBoxBytes, map, bar, 0, in, row, 0);
       if constexpr (Geo::kQ8)  // a box is a whole block: both heads' scales are neighbours
         bulk_load(scales + k * Geo::kScaleBox, scale + size_t(row) * Geo::kBox, Geo::kScaleBox,
                   bar);
     }
   };
-  advance(warp);
+  // the warp has read its share of a tile (which: 0 K, 1 V): whether lane 0 is to refill it
+  auto released = [&](int st, int which) {
+    fence_proxy_async_smem();  // this lane's reads before the refill
+    __syncwarp();
+    if (lane != 0 || pi >= n) return false;
+    if constexpr (kRows > 1) {
+      int* c = reinterpret_cast<int*>(gen + S::kOffCnt) + (stream * kStages + st) * 2 + which;
+      __threadfence_block();
+      if ((atomicAdd(c, 1) + 1) % kRows != 0) return false;
+      __threadfence_block();
+    }
+    return true;
+  };
+
+  advance(stream);
+#pragma unroll
+  for (int st = 0; st < kStages; ++st) {
+    fetch();
+    if (tile == 0 && lane == 0 && pi < n) {
+      request(&tmk, sK(st), sKs(st), p.k_scale, barK(st));
+      request(&tmv, sV(st), sVs(st), p.v_scale, barV(st));
+    }
+    advance(N);
+  }
   fetch();
-  issue(&tmk, sK, sKs, p.k_scale, barK);
-  issue(&tmv, sV, sVs, p.v_scale, barV);
 
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+  const int Hq = 2 * p.P * p.g;
   Path path;
+  int st = 0;
   uint32_t par = 0;
   bool dead = false, first = true;
   for (int i = 0; i < n;) {
     const int len = min(n - i, cur.n - cur.j);
-    const int pair = cur.u / p.nsg, r0 = (cur.u % p.nsg) * p.gs;
-    const bool live = gid < p.gs && r0 + gid < p.g;
-    const int qp = pair * p.g + r0 + gid;  // this lane's query pair of the sequence
-    const int Hq = 2 * p.P * p.g;
-    const __nv_bfloat16* qr = q + (size_t(cur.s) * Hq + (live ? 2 * qp : 0)) * D;
-    path.begin(qr, qr + D, live, cq, p.scale_log2);
-    const int L = min(__ldg(p.context_lens + cur.s), p.MBS * p.BS);
-
-    int k = i + (warp - i % N + N) % N;
-    for (; k < i + len && !dead; k += N) {
-      const int nvalid = L - (cur.j + k - i) * Geo::kItem;
-      advance(N);  // pc: the item after this one
-      fetch();
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(barK, par, p.timeout_ns))) {
-        dead = true;  // let what is in flight land before the warp goes on
-        mbar_wait_bounded(barK, par, p.timeout_ns);
-        mbar_wait_bounded(barV, par, p.timeout_ns);
-        break;
-      }
-      float x[Path::kNT][4];
-      path.scores(x, sK, sKs, nvalid, lane, p.scale_log2);
-      fence_proxy_async_smem();  // this lane's reads of K before its refill
-      __syncwarp();
-      issue(&tmk, sK, sKs, p.k_scale, barK);
-      float mx0 = -INFINITY, mx1 = -INFINITY, mn0, mn1;
-#pragma unroll
-      for (int t = 0; t < Path::kNT; ++t) {
-        mx0 = fmax3(mx0, x[t][0], x[t][1]);
-        mx1 = fmax3(mx1, x[t][2], x[t][3]);
-      }
-      path.st.raise(mx0, mx1, mn0, mn1);
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(barV, par, p.timeout_ns))) {
-        dead = true;
-        mbar_wait_bounded(barV, par, p.timeout_ns);
-        if (pi < n) mbar_wait_bounded(barK, par ^ 1u, p.timeout_ns);  // the K just requested
-        break;
-      }
-      // rows past the context may hold anything (even NaN): zero them before P.V
-      if (nvalid < Geo::kItem) {
-        for (int c = lane; c < (Geo::kItem - nvalid) * 2 * Geo::kChunksPerRow; c += 32) {
-          const int t = nvalid + c / (2 * Geo::kChunksPerRow), cc = c % (2 * Geo::kChunksPerRow);
-          sts128_zero(sV + Geo::off(cc / Geo::kChunksPerRow, t, cc % Geo::kChunksPerRow));
+    const int pair0 = cur.u / p.nsg * p.g;                       // of the KV pair
+    const int r0 = (cur.u % p.nsg) * p.gs, rows = min(p.gs, p.g - r0);  // of the unit
+    // streams with items here fold into the one that takes the first item
+    const int rank = (stream - i % N + N) % N, active = min(len, N);
+    if (rank < active) {
+      const int row = 4 * tile + (gid >> 1);  // this lane's query row: pair and map
+      const bool live = row < rows;
+      path.begin(q + (size_t(cur.s) * Hq + (live ? 2 * (pair0 + r0 + row) + (gid & 1) : 0)) * D,
+                 live, lane, p.scale_log2);
+      const int L = min(__ldg(p.context_lens + cur.s), p.MBS * p.BS);
+      for (int k = i + rank; k < i + len && !dead; k += N) {
+        const int nvalid = L - (cur.j + k - i) * Geo::kItem;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(barK(st), par, p.timeout_ns))) {
+          dead = true;
+          break;
         }
-        __syncwarp();
+        float x[Path::kT][4];
+        path.scores(x, sK(st), sKs(st), nvalid, lane, p.scale_log2);
+        if (released(st, 0)) request(&tmk, sK(st), sKs(st), p.k_scale, barK(st));
+        float mx0 = -INFINITY, mx1 = -INFINITY, mn0, mn1;
+#pragma unroll
+        for (int t = 0; t < Path::kT; ++t) {
+          mx0 = fmax3(mx0, x[t][0], x[t][2]);
+          mx1 = fmax3(mx1, x[t][1], x[t][3]);
+        }
+        path.st.raise(mx0, mx1, mn0, mn1);
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(barV(st), par, p.timeout_ns))) {
+          dead = true;
+          break;
+        }
+        // rows past the context may hold anything (even NaN): zero them before P.V (every
+        // warp of the stream does, before its own reads: the same zeros)
+        if (nvalid < Geo::kItem) {
+          for (int c = lane; c < (Geo::kItem - nvalid) * 2 * Geo::kChunksPerRow; c += 32) {
+            const int t = nvalid + c / (2 * Geo::kChunksPerRow);
+            const int cc = c % (2 * Geo::kChunksPerRow);
+            sts128_zero(sV(st) + Geo::off(cc / Geo::kChunksPerRow, t, cc % Geo::kChunksPerRow));
+          }
+          __syncwarp();
+        }
+        path.values(x, sV(st), sVs(st), nvalid, mn0, mn1, lane);
+        if (released(st, 1)) request(&tmv, sV(st), sVs(st), p.v_scale, barV(st));
+        advance(N);
+        fetch();
+        if (++st == kStages) {
+          st = 0;
+          par ^= 1u;
+        }
       }
-      path.values(x, sV, sVs, nvalid, mn0, mn1, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      issue(&tmv, sV, sVs, p.v_scale, barV);
-      par ^= 1u;
+      path.st.close();
     }
-    if (dead && lane == 0 && p.status) atomicOr(p.status, PKV_DEV_TIMEOUT);
 
-    // ---- fold the warps' states into warp 0's ----
-    DiffState<D>& st = path.st;
-    st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, 1);
-    st.l0 += __shfl_xor_sync(0xffffffffu, st.l0, 2);
-    st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 1);
-    st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 2);
+    // ---- fold the streams' states into rank 0's ----
+    DiffState<D>& state = path.st;
+    if constexpr (kStreams > 1) {
+      uint8_t* buf = gen + S::kOffState + tile * Geo::kState;
+      for (int r = 1; r < active; ++r) {
+        float2 f = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int half = N / 2; half > 0; half >>= 1) {
-      if (warp >= half && warp < 2 * half) st.put(states + (warp - half) * Geo::kState, lane);
-      __syncthreads();
-      if (warp < half) st.fold(states + warp * Geo::kState, lane);
-      __syncthreads();  // before the next level, or the next unit, writes there again
+        for (int h = 0; h < 2; ++h) {
+          if (rank == r) state.put(buf, h, lane);
+          __syncthreads();
+          if (rank == 0) state.fold(buf, h, lane, f);
+          __syncthreads();  // before the next half, or unit, is put there
+        }
+      }
     }
-    if (warp == 0) {
-      const bool complete = cur.j == 0 && len == cur.n;
-      if (!complete) {
+    const int pr = 4 * tile + cq;  // this lane's query pair within the unit
+    if (rank == 0 && pr < rows) {
+      if (cur.j != 0 || len != cur.n) {
         const size_t slot = size_t(2) * blockIdx.x + (first ? 0 : 1);
-        const size_t r = slot * 2 * p.gs + gid;
-        if (gid < p.gs) {
-          float* o0 = p.part_o + r * (2 * D);
-          float* o1 = o0 + size_t(p.gs) * (2 * D);
+        const size_t r = slot * 2 * p.gs + pr;
+        float* o0 = p.part_o + r * (2 * D);
+        float* o1 = o0 + size_t(p.gs) * (2 * D);
 #pragma unroll
-          for (int k2 = 0; k2 < Path::kRuns; ++k2) {
-            const int c = Path::column(k2, cq);
+        for (int k = 0; k < Path::kRuns; ++k) {
+          const int c = Path::column(k, gid);
+          if constexpr (Path::kRun == 4) {
+            float v[2][4];
 #pragma unroll
-            for (int e = 0; e < Path::kRun; e += 2) {
-              *reinterpret_cast<float2*>(o0 + c + e) =
-                  make_float2(Path::at(st.o, k2, e, 0) * Path::kOutScale,
-                              Path::at(st.o, k2, e + 1, 0) * Path::kOutScale);
-              *reinterpret_cast<float2*>(o1 + c + e) =
-                  make_float2(Path::at(st.o, k2, e, 1) * Path::kOutScale,
-                              Path::at(st.o, k2, e + 1, 1) * Path::kOutScale);
+            for (int e = 0; e < 4; ++e) {
+              v[0][e] = Path::at(state.o, k, e, 0) * Path::kOutScale;
+              v[1][e] = Path::at(state.o, k, e, 1) * Path::kOutScale;
             }
+            *reinterpret_cast<float4*>(o0 + c) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+            *reinterpret_cast<float4*>(o1 + c) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
+          } else {
+            o0[c] = Path::at(state.o, k, 0, 0) * Path::kOutScale;
+            o1[c] = Path::at(state.o, k, 0, 1) * Path::kOutScale;
           }
-          if (cq == 0) {
-            float2* ml = reinterpret_cast<float2*>(p.part_ml);
-            ml[r] = make_float2(st.m0, st.l0);
-            ml[r + p.gs] = make_float2(st.m1, st.l1);
-          }
+        }
+        if (gid == 0) {
+          float2* ml = reinterpret_cast<float2*>(p.part_ml);
+          ml[r] = make_float2(state.m0, state.l0);
+          ml[r + p.gs] = make_float2(state.m1, state.l1);
         }
       } else {
-        const float i0 = Path::kOutScale / st.l0;
-        const float i1 = Path::kOutScale / st.l1 * (live ? __ldg(p.lam + qp) : 0.f);
-        float ss = 0.f;
+        const int qp = pair0 + r0 + pr;
+        const float i0 = Path::kOutScale / state.l0;
+        const float i1 = Path::kOutScale / state.l1 * __ldg(p.lam + qp);
+        float ss = 0.f, d[Path::kRuns][Path::kRun];
 #pragma unroll
-        for (int nd = 0; nd < kND; ++nd) {
+        for (int k = 0; k < Path::kRuns; ++k) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float d = st.o[nd][e] * i0 - st.o[nd][e + 2] * i1;
-            st.o[nd][e] = d;
-            ss = fmaf(d, d, ss);
+          for (int e = 0; e < Path::kRun; ++e) {
+            d[k][e] = Path::at(state.o, k, e, 0) * i0 - Path::at(state.o, k, e, 1) * i1;
+            ss = fmaf(d[k][e], d[k][e], ss);
           }
         }
-        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-        ss += __shfl_xor_sync(0xffffffffu, ss, 2);
+        // over the 8 lanes of the pair (they branch alike)
+        const uint32_t lanes = 0x11111111u << cq;
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) ss += __shfl_xor_sync(lanes, ss, k);
         const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.norm_w);
         const float f = w ? rsqrtf(ss * (1.f / (2 * D)) + p.eps) * p.out_scale : p.out_scale;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) +
-                             (size_t(cur.s) * (Hq / 2) + (live ? qp : 0)) * (2 * D);
-        if (live) {
+        __nv_bfloat16* out =
+            static_cast<__nv_bfloat16*>(p.out) + (size_t(cur.s) * (Hq / 2) + qp) * (2 * D);
 #pragma unroll
-          for (int k2 = 0; k2 < Path::kRuns; ++k2) {
-            const int c = Path::column(k2, cq);
-#pragma unroll
-            for (int e = 0; e < Path::kRun; e += 2) {
-              float2 g = make_float2(f, f);
-              if (w) {
-                g = unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t*>(w + c + e)));
-                g = make_float2(f * g.x, f * g.y);
-              }
-              *reinterpret_cast<uint32_t*>(out + c + e) =
-                  pack_bf16x2(Path::at(st.o, k2, e, 0) * g.x, Path::at(st.o, k2, e + 1, 0) * g.y);
+        for (int k = 0; k < Path::kRuns; ++k) {
+          const int c = Path::column(k, gid);
+          if constexpr (Path::kRun == 4) {
+            float4 g = make_float4(f, f, f, f);
+            if (w) {
+              const uint2 u = __ldg(reinterpret_cast<const uint2*>(w + c));
+              const float2 x0 = unpack_bf16x2(u.x), x1 = unpack_bf16x2(u.y);
+              g = make_float4(f * x0.x, f * x0.y, f * x1.x, f * x1.y);
             }
+            *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(d[k][0] * g.x, d[k][1] * g.y),
+                                                            pack_bf16x2(d[k][2] * g.z, d[k][3] * g.w));
+          } else {
+            out[c] = __float2bfloat16(d[k][0] * (w ? f * __bfloat162float(w[c]) : f));
           }
         }
       }
@@ -676,31 +734,46 @@ __global__ void __launch_bounds__(kDiffWarps * 32, 2)
       }
     }
   }
+  if (dead) {
+    if (lane == 0 && p.status) atomicOr(p.status, PKV_DEV_TIMEOUT);
+    // let copies in flight land before the CTA's shared memory goes: at most the current
+    // phase of each barrier is open (with nothing requested the wait runs out)
+    for (int k = 0; k < kStages; ++k) {
+      for (uint32_t p2 = 0; p2 < 2; ++p2) {
+        mbar_wait_bounded(barK(k), p2, p.timeout_ns);
+        mbar_wait_bounded(barV(k), p2, p.timeout_ns);
+      }
+    }
+  }
 }
 
-template <int D, int CODE, int BOX, int SUB>
+template <int D, class Path, int kStreams, int kRows, int kStages, int kCtas>
 DiffKernelInfo make_diff_info() {
-  using Geo = DiffGeom<D, CODE, BOX, SUB>;
+  using S = DiffSmem<typename Path::Geo, kStreams, kRows, kStages>;
   DiffKernelInfo info{};
-  if constexpr (CODE < 0)
-    info.fn = reinterpret_cast<const void*>(&paged_diff_decode_kernel<D, DiffPathBf16<D, BOX, SUB>>);
-  else
-    info.fn = reinterpret_cast<const void*>(
-        &paged_diff_decode_kernel<D, DiffPathQ8<D, CODE, BOX, SUB>>);
-  info.threads = kDiffWarps * 32;
-  info.smem = 1024 + kDiffWarps * Geo::kRing + kDiffWarps / 2 * Geo::kState;
-  info.box = BOX;
-  info.item = Geo::kItem;
+  info.fn = reinterpret_cast<const void*>(
+      &paged_diff_decode_kernel<D, Path, kStreams, kRows, kStages, kCtas>);
+  info.threads = kStreams * kRows * 32;
+  info.smem = 1024 + S::kOffPrefix;
+  info.box = Path::Geo::kBox;
+  info.item = Path::Geo::kItem;
   return info;
 }
 
+// The kernel for units of up to 4 query pairs (a warp per stream) or up to 8 (two).
+template <int D, class Path, int kStages1, int kStages2>
+DiffKernelInfo diff_shape(int pairs) {
+  if (pairs <= 4) return make_diff_info<D, Path, 4, 1, kStages1, 3>();
+  return make_diff_info<D, Path, 2, 2, kStages2, 3>();
+}
+
 template <int CODE>
-bool select_diff_q8(int D, int BS, DiffKernelInfo* info) {
+bool select_diff_q8(int D, int BS, int pairs, DiffKernelInfo* info) {
   // items of 32 tokens (K and V: 16 KiB at head_dim 128); a box is a block
-  if (D == 128 && BS == 16) *info = make_diff_info<128, CODE, 16, 2>();
-  else if (D == 128 && BS == 32) *info = make_diff_info<128, CODE, 32, 1>();
-  else if (D == 64 && BS == 16) *info = make_diff_info<64, CODE, 16, 2>();
-  else if (D == 64 && BS == 32) *info = make_diff_info<64, CODE, 32, 1>();
+  if (D == 128 && BS == 16) *info = diff_shape<128, DiffPathQ8<128, CODE, 16, 2>, 1, 2>(pairs);
+  else if (D == 128 && BS == 32) *info = diff_shape<128, DiffPathQ8<128, CODE, 32, 1>, 1, 2>(pairs);
+  else if (D == 64 && BS == 16) *info = diff_shape<64, DiffPathQ8<64, CODE, 16, 2>, 2, 4>(pairs);
+  else if (D == 64 && BS == 32) *info = diff_shape<64, DiffPathQ8<64, CODE, 32, 1>, 2, 4>(pairs);
   else return false;
   return true;
 }

@@ -1,109 +1,130 @@
 // diff_merge.cu -- folds the records of units cut between CTAs of the differential decode.
 //
-// One warp per (sequence, unit, query pair): both maps' parts fold with the online-softmax
-// rescaling (fold.cuh), a lane holding D / 64 output quads of each map; then the
-// difference, the optional norm (a warp reduction) and the bf16 row, as in
-// decode_diff.cuh. It also writes zeros for empty sequences and, when a status word is
-// given, checks the sequence's context length and block ids (a sequence that fails gets
-// zeros). Units that one CTA covered leave at once.
+// One CTA part per (sequence, unit, query pair): both maps' records fold with the
+// online-softmax rescaling (fold.cuh), one output quad of one map per lane, so D / 32 warps
+// hold both rows of 2 D columns and every record of a chunk is requested at once; kGroups
+// such sets share the records of a pair when few pairs leave the GPU idle otherwise. Then
+// the difference, the optional norm and the bf16 row, as in decode_diff.cuh. It also
+// writes zeros for empty sequences and, when a status word is given, checks the sequence's
+// context length and block ids (a sequence that fails gets zeros). Units that one CTA
+// covered leave at once.
 #include "common.cuh"
 #include "fold.cuh"
 #include "internal.h"
 
 namespace pkv {
 
-constexpr int kDiffMergeWarps = 8;
+namespace {
+constexpr int kDiffMergeThreads = 256;
+}
 
-template <int D>
-__global__ void __launch_bounds__(kDiffMergeWarps * 32) paged_diff_merge_kernel(const DiffParams p) {
-  constexpr int Q = D / 2, PER = Q / 32;  // quads of a 2 D row, per lane
+// kGroups == 1: a CTA takes several pairs; else one pair and kGroups sets of warps.
+template <int D, int kGroups>
+__global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D)
+    paged_diff_merge_kernel(const DiffParams p) {
+  constexpr int Q = D / 2;          // quads of a 2 D row
+  constexpr int kSet = 2 * Q;       // threads of a set: quads of both maps
+  constexpr int kSets = kGroups == 1 ? kDiffMergeThreads / kSet : kGroups;
+  __shared__ float4 s_o[kSets][kSet];
+  __shared__ float2 s_ml[kSets][kSet];
+  __shared__ float s_sum[kSets][Q / 32 + 1];
   pdl_wait_prior_grid();
-  const int lane = threadIdx.x & 31;
+  const int set = threadIdx.x / kSet, t = threadIdx.x % kSet;
+  const int map = t / Q, quad = t % Q, lane = threadIdx.x & 31;
+  const int group = kGroups == 1 ? 0 : set;
   const int U = p.P * p.nsg;
-  const long long item = (long long)blockIdx.x * kDiffMergeWarps + (threadIdx.x >> 5);
-  if (item >= (long long)p.B * U * p.gs) return;
-  const int r = int(item % p.gs);
-  const int u = int(item / p.gs % U), s = int(item / p.gs / U);
+  const long long item = kGroups == 1 ? (long long)blockIdx.x * kSets + set : blockIdx.x;
+  const bool valid = item < (long long)p.B * U * p.gs;
+  const int r = valid ? int(item % p.gs) : 0;
+  const int u = valid ? int(item / p.gs % U) : 0, s = valid ? int(item / p.gs / U) : 0;
   const int row = (u % p.nsg) * p.gs + r;  // query pair within the KV pair
-  const bool active = row < p.g;
   const int qp = u / p.nsg * p.g + row;
   const int n = p.prefix[s + 1] - p.prefix[s];
+  const long long total = p.prefix[p.B], before = p.prefix[s];
   uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
                                         (size_t(s) * p.P * p.g + qp) * (2 * D));
+  bool active = valid && row < p.g;
   bool zero = n == 0;
   if (p.status != nullptr) {
     int flags = 0;
     const int L = p.context_lens[s];
-    if (lane == 0 && (L < 0 || L > p.MBS * p.BS)) flags = PKV_DEV_BAD_CONTEXT_LEN;
+    if (L < 0 || L > p.MBS * p.BS) flags = PKV_DEV_BAD_CONTEXT_LEN;
     const int nblk = L <= 0 ? 0 : min((L + p.BS - 1) / p.BS, p.MBS);
-    for (int j = lane; j < nblk; j += 32) {
+    for (int j = lane; j < nblk; j += 32) {  // every warp for itself
       const int id = p.block_tables[size_t(s) * p.MBS + j];
       if (id < 0 || id >= p.NB) flags |= PKV_DEV_BAD_BLOCK_ID;
     }
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (flags) {
-      if (lane == 0 && u == 0 && r == 0) atomicOr(p.status, flags);
+      if (valid && t == 0 && group == 0 && u == 0 && r == 0) atomicOr(p.status, flags);
       zero = true;
     }
   }
-  if (!active) return;
-  if (zero) {
-#pragma unroll
-    for (int k = 0; k < PER; ++k) out[k * 32 + lane] = make_uint2(0u, 0u);
-    return;
-  }
-  const long long T = (long long)U * p.prefix[p.B];
-  const long long A = (long long)U * p.prefix[s] + (long long)u * n;
+  if (active && zero && map == 0 && group == 0) out[quad] = make_uint2(0u, 0u);
+  active = active && !zero;
+
+  const long long T = (long long)U * total;
+  const long long A = (long long)U * before + (long long)u * n;
   const int G = p.G;
   auto owner = [&](long long x) { return int(((x + 1) * G + T - 1) / T) - 1; };
-  const int w0 = owner(A), w1 = owner(A + n - 1);
-  if (w0 == w1) return;
-  const bool dense = T >= G;  // else ranges hold one item at most: part i is item A + i's
-  const int nparts = dense ? w1 - w0 + 1 : n;
-  const bool first_cut = T * w0 / G < A;  // CTA w0 had another unit before this one
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-  float4 v[2][PER];
-#pragma unroll
-  for (int m = 0; m < 2; ++m) {
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      Fold f = fold_empty();
-      fold_parts<8>(f, 0, 1, nparts, [&](int i, const float2*& pm, const float4*& po) {
-        const size_t slot = dense ? size_t(2 * (w0 + i) + (i == 0 && first_cut ? 1 : 0))
-                                  : size_t(2) * owner(A + i);
-        const size_t rr = (slot * 2 + m) * p.gs + r;
-        pm = ml + rr;
-        po = reinterpret_cast<const float4*>(p.part_o + rr * (2 * D)) + k * 32 + lane;
-      });
-      const float inv = (f.l > 0.f ? 1.f / f.l : 0.f) * (m == 0 ? 1.f : -p.lam[qp]);
-      v[m][k] = make_float4(f.o.x * inv, f.o.y * inv, f.o.z * inv, f.o.w * inv);
+  int w0 = 0, w1 = 0;
+  if (active) {
+    w0 = owner(A);
+    w1 = owner(A + n - 1);
+    active = w0 != w1;
+  }
+  Fold f = fold_empty();
+  if (active) {
+    const bool dense = T >= G;  // else ranges hold one item at most: part i is item A + i's
+    const int nparts = dense ? w1 - w0 + 1 : n;
+    const bool first_cut = T * w0 / G < A;  // CTA w0 had another unit before this one
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    fold_parts<8>(f, group, kGroups, nparts, [&](int i, const float2*& pm, const float4*& po) {
+      const size_t slot = dense ? size_t(2 * (w0 + i) + (i == 0 && first_cut ? 1 : 0))
+                                : size_t(2) * owner(A + i);
+      const size_t rr = (slot * 2 + map) * p.gs + r;
+      pm = ml + rr;
+      po = reinterpret_cast<const float4*>(p.part_o + rr * (2 * D)) + quad;
+    });
+  }
+  if constexpr (kGroups > 1) {
+    s_o[set][t] = f.o;
+    s_ml[set][t] = make_float2(f.m, f.l);
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll 1
+      for (int k = 1; k < kGroups; ++k)
+        fold_merge(f, Fold{s_ml[k][t].x, s_ml[k][t].y, s_o[k][t]});
     }
+    __syncthreads();
   }
-  float ss = 0.f;
+  const float inv = f.l > 0.f ? 1.f / f.l : 0.f;
+  float4 v = make_float4(f.o.x * inv, f.o.y * inv, f.o.z * inv, f.o.w * inv);
+  if (map == 1 && group == 0) s_o[set][quad] = v;
+  __syncthreads();
+  if (map == 0 && group == 0) {
+    const float lam = active ? p.lam[qp] : 0.f;
+    const float4 y = s_o[set][quad];
+    v = make_float4(v.x - lam * y.x, v.y - lam * y.y, v.z - lam * y.z, v.w - lam * y.w);
+    float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    v[0][k].x += v[1][k].x;
-    v[0][k].y += v[1][k].y;
-    v[0][k].z += v[1][k].z;
-    v[0][k].w += v[1][k].w;
-    const float4 a = v[0][k];
-    ss += a.x * a.x + a.y * a.y + a.z * a.z + a.w * a.w;
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (lane == 0) s_sum[set][quad / 32] = ss;
   }
+  __syncthreads();
+  if (map == 0 && group == 0 && active) {
+    float ss = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const uint2* w = static_cast<const uint2*>(p.norm_w);
-  const float f = w ? rsqrtf(ss * (1.f / (2 * D)) + p.eps) * p.out_scale : p.out_scale;
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    float4 g = make_float4(f, f, f, f);
+    for (int k = 0; k < Q / 32; ++k) ss += s_sum[set][k];
+    const uint2* w = static_cast<const uint2*>(p.norm_w);
+    const float g = w ? rsqrtf(ss * (1.f / (2 * D)) + p.eps) * p.out_scale : p.out_scale;
+    float4 m = make_float4(g, g, g, g);
     if (w) {
-      const uint2 u2 = w[k * 32 + lane];
+      const uint2 u2 = w[quad];
       const float2 a = unpack_bf16x2(u2.x), b = unpack_bf16x2(u2.y);
-      g = make_float4(f * a.x, f * a.y, f * b.x, f * b.y);
+      m = make_float4(g * a.x, g * a.y, g * b.x, g * b.y);
     }
-    const float4 a = v[0][k];
-    out[k * 32 + lane] =
-        make_uint2(pack_bf16x2(a.x * g.x, a.y * g.y), pack_bf16x2(a.z * g.z, a.w * g.w));
+    out[quad] = make_uint2(pack_bf16x2(v.x * m.x, v.y * m.y), pack_bf16x2(v.z * m.z, v.w * m.w));
   }
 }
 
@@ -112,10 +133,17 @@ void launch_diff_merge(const DiffParams& p, cudaStream_t stream) {
   if (items <= 0) return;
   DiffParams copy = p;
   void* args[] = {&copy};
-  const void* fn = p.D == 128 ? reinterpret_cast<const void*>(&paged_diff_merge_kernel<128>)
-                              : reinterpret_cast<const void*>(&paged_diff_merge_kernel<64>);
-  launch_pdl(fn, dim3(unsigned((items + kDiffMergeWarps - 1) / kDiffMergeWarps)),
-             dim3(kDiffMergeWarps * 32), args, 0, stream);
+  // few pairs may be cut into many records each: 8 sets of warps per pair
+  constexpr int kG = 8;
+  const bool few = items * kG * p.D <= 152 * 2048;
+  const int per = few ? 1 : kDiffMergeThreads / p.D;
+  const dim3 grid(unsigned((items + per - 1) / per)), block(few ? kG * p.D : kDiffMergeThreads);
+  const void* fn =
+      p.D == 128 ? (few ? reinterpret_cast<const void*>(&paged_diff_merge_kernel<128, kG>)
+                        : reinterpret_cast<const void*>(&paged_diff_merge_kernel<128, 1>))
+                 : (few ? reinterpret_cast<const void*>(&paged_diff_merge_kernel<64, kG>)
+                        : reinterpret_cast<const void*>(&paged_diff_merge_kernel<64, 1>));
+  launch_pdl(fn, grid, block, args, 0, stream);
 }
 
 }  // namespace pkv

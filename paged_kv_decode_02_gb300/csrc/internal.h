@@ -277,10 +277,11 @@ struct DiffKernelInfo {
   int box;                     // tokens per TMA box
   int item;                    // tokens per work item
 };
-bool select_diff_bf16(int D, int BS, DiffKernelInfo* info);
-bool select_diff_int8(int D, int BS, DiffKernelInfo* info);
-bool select_diff_e4m3(int D, int BS, DiffKernelInfo* info);
-bool select_diff_e5m2(int D, int BS, DiffKernelInfo* info);
+// pairs: query pairs per work unit (at most 8)
+bool select_diff_bf16(int D, int BS, int pairs, DiffKernelInfo* info);
+bool select_diff_int8(int D, int BS, int pairs, DiffKernelInfo* info);
+bool select_diff_e4m3(int D, int BS, int pairs, DiffKernelInfo* info);
+bool select_diff_e5m2(int D, int BS, int pairs, DiffKernelInfo* info);
 void launch_diff_merge(const DiffParams& p, cudaStream_t stream);
 
 cudaError_t launch_append_bf16(const void* k, const void* v, void* k_cache, void* v_cache,
