@@ -712,6 +712,7 @@ pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
   pkv_status st = check_dims(d);
   if (st != PKV_OK) return st;
   if (d->num_q_heads % 2 != 0 || d->num_kv_heads % 2 != 0) return PKV_ERR_SHAPE;
+  if ((long long)d->num_seqs * d->num_q_heads >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
   if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
   struct Key {
     pkv_dims d;
@@ -762,9 +763,9 @@ pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
       per_sm <= 0)
     return PKV_ERR_CUDA;
   P.G = sms * per_sm;
-  // workspace: [prefix (B + 1) int32][records' (m, l), 2 per CTA][records' o]
+  // workspace: [parts (B, units, 2) int32][records' (m, l), 2 per CTA][records' o]
   const size_t rows = size_t(2) * P.G * 2 * P.gs;
-  P.off_ml = align_up(size_t(d->num_seqs + 1) * 4, 256);
+  P.off_ml = align_up(size_t(d->num_seqs) * (d->num_kv_heads / 2) * P.nsg * 8, 256);
   P.off_o = align_up(P.off_ml + rows * 8, 256);
   P.ws_bytes = align_up(P.off_o + rows * 2 * d->head_dim * 4, 256);
   keys[next] = key;
@@ -815,7 +816,7 @@ pkv_status run_diff(int kvt, void* out, const void* q, const void* k_cache, cons
   p.norm_w = norm_weight;
   p.part_o = reinterpret_cast<float*>(ws + P.off_o);
   p.part_ml = reinterpret_cast<float*>(ws + P.off_ml);
-  p.prefix = reinterpret_cast<int32_t*>(ws);
+  p.parts = reinterpret_cast<int32_t*>(ws);
   p.status = status;
   p.B = d->num_seqs;
   p.P = d->num_kv_heads / 2;
@@ -825,9 +826,7 @@ pkv_status run_diff(int kvt, void* out, const void* q, const void* k_cache, cons
   p.g = d->num_q_heads / d->num_kv_heads;
   p.gs = P.gs;
   p.nsg = P.nsg;
-  p.G = P.G;
   p.D = d->head_dim;
-  p.item = P.k.item;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.eps = eps;
   p.out_scale = out_scale;

@@ -493,15 +493,14 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
       prefix[i + 1] = run;
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-      for (int i = tid; i <= B; i += kThreads) p.prefix[i] = prefix[i];
   }
 
   const int U = p.P * p.nsg;  // units per sequence
   const long long T = (long long)U * prefix[B];
-  const long long a = T * blockIdx.x / gridDim.x, b = T * (blockIdx.x + 1) / gridDim.x;
+  const int G = int(min((long long)gridDim.x, T));  // no range is empty
+  if (int(blockIdx.x) >= G) return;
+  const long long a = T * blockIdx.x / G, b = T * (blockIdx.x + 1) / G;
   const int n = int(b - a);
-  if (n == 0) return;
 
   Cursor cur;  // the segment: unit cur.u of sequence cur.s from its item cur.j on
   cursor_locate(cur, a, prefix, B, U);
@@ -553,6 +552,17 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         bulk_load(scales + k * Geo::kScaleBox, scale + size_t(row) * Geo::kBox, Geo::kScaleBox,
                   bar);
     }
+  };
+  // Brings the producer's query rows near when its unit is a new one (the unit's first
+  // items wait for them otherwise).
+  auto prefetch_q = [&](int s0, int u0) {
+    if (pi >= n || (pc.s == s0 && pc.u == u0)) return;
+    const int r0 = (pc.u % p.nsg) * p.gs;
+    const int lines = min(p.gs, p.g - r0) * (D / 32);  // of 128 bytes: 2 rows of D a pair
+    const char* rows = static_cast<const char*>(p.q) +
+                       (size_t(pc.s) * 2 * p.P * p.g + 2 * (pc.u / p.nsg * p.g + r0)) * (D * 2);
+    for (int k = lane; k < lines; k += 32)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(rows + k * 128));
   };
   // the warp has read its share of a tile (which: 0 K, 1 V): whether lane 0 is to refill it
   auto released = [&](int st, int which) {
@@ -630,8 +640,10 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         }
         path.values(x, sV(st), sVs(st), nvalid, mn0, mn1, lane);
         if (released(st, 1)) request(&tmv, sV(st), sVs(st), p.v_scale, barV(st));
+        const int s0 = pc.s, u0 = pc.u;
         advance(N);
         fetch();
+        prefetch_q(s0, u0);
         if (++st == kStages) {
           st = 0;
           par ^= 1u;
@@ -655,9 +667,17 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         }
       }
     }
+    const bool whole = cur.j == 0 && len == cur.n;
+    // where the merge finds the unit's records: the first's slot (-1: none, it is done
+    // here) and the last's CTA; the others are the first segments of the CTAs between
+    if (rank == 0 && tile == 0 && lane == 0) {
+      int* part = p.parts + 2 * (size_t(cur.s) * U + cur.u);
+      if (cur.j == 0) part[0] = whole ? -1 : 2 * int(blockIdx.x) + (first ? 0 : 1);
+      if (cur.j + len == cur.n) part[1] = int(blockIdx.x);
+    }
     const int pr = 4 * tile + cq;  // this lane's query pair within the unit
     if (rank == 0 && pr < rows) {
-      if (cur.j != 0 || len != cur.n) {
+      if (!whole) {
         const size_t slot = size_t(2) * blockIdx.x + (first ? 0 : 1);
         const size_t r = slot * 2 * p.gs + pr;
         float* o0 = p.part_o + r * (2 * D);

@@ -33,21 +33,21 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D
   const int map = t / Q, quad = t % Q, lane = threadIdx.x & 31;
   const int group = kGroups == 1 ? 0 : set;
   const int U = p.P * p.nsg;
-  const long long item = kGroups == 1 ? (long long)blockIdx.x * kSets + set : blockIdx.x;
-  const bool valid = item < (long long)p.B * U * p.gs;
-  const int r = valid ? int(item % p.gs) : 0;
-  const int u = valid ? int(item / p.gs % U) : 0, s = valid ? int(item / p.gs / U) : 0;
+  const unsigned item = kGroups == 1 ? blockIdx.x * kSets + set : blockIdx.x;
+  const unsigned unit = item / unsigned(p.gs);
+  const bool valid = unit < unsigned(p.B * U);
+  const int r = int(item % unsigned(p.gs));
+  const int s = valid ? int(unit / unsigned(U)) : 0, u = int(unit % unsigned(U));
   const int row = (u % p.nsg) * p.gs + r;  // query pair within the KV pair
   const int qp = u / p.nsg * p.g + row;
-  const int n = p.prefix[s + 1] - p.prefix[s];
-  const long long total = p.prefix[p.B], before = p.prefix[s];
+  const int L = p.context_lens[s];
+  const int2 part = valid ? reinterpret_cast<const int2*>(p.parts)[unit] : make_int2(-1, 0);
   uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
                                         (size_t(s) * p.P * p.g + qp) * (2 * D));
   bool active = valid && row < p.g;
-  bool zero = n == 0;
+  bool zero = L <= 0;
   if (p.status != nullptr) {
     int flags = 0;
-    const int L = p.context_lens[s];
     if (L < 0 || L > p.MBS * p.BS) flags = PKV_DEV_BAD_CONTEXT_LEN;
     const int nblk = L <= 0 ? 0 : min((L + p.BS - 1) / p.BS, p.MBS);
     for (int j = lane; j < nblk; j += 32) {  // every warp for itself
@@ -61,27 +61,14 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D
     }
   }
   if (active && zero && map == 0 && group == 0) out[quad] = make_uint2(0u, 0u);
-  active = active && !zero;
+  active = active && !zero && part.x >= 0;  // (an empty sequence has no entry)
 
-  const long long T = (long long)U * total;
-  const long long A = (long long)U * before + (long long)u * n;
-  const int G = p.G;
-  auto owner = [&](long long x) { return int(((x + 1) * G + T - 1) / T) - 1; };
-  int w0 = 0, w1 = 0;
-  if (active) {
-    w0 = owner(A);
-    w1 = owner(A + n - 1);
-    active = w0 != w1;
-  }
   Fold f = fold_empty();
   if (active) {
-    const bool dense = T >= G;  // else ranges hold one item at most: part i is item A + i's
-    const int nparts = dense ? w1 - w0 + 1 : n;
-    const bool first_cut = T * w0 / G < A;  // CTA w0 had another unit before this one
+    const int w0 = part.x >> 1, nparts = part.y - w0 + 1;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
     fold_parts<8>(f, group, kGroups, nparts, [&](int i, const float2*& pm, const float4*& po) {
-      const size_t slot = dense ? size_t(2 * (w0 + i) + (i == 0 && first_cut ? 1 : 0))
-                                : size_t(2) * owner(A + i);
+      const size_t slot = i == 0 ? part.x : 2 * (w0 + i);
       const size_t rr = (slot * 2 + map) * p.gs + r;
       pm = ml + rr;
       po = reinterpret_cast<const float4*>(p.part_o + rr * (2 * D)) + quad;
@@ -129,7 +116,7 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D
 }
 
 void launch_diff_merge(const DiffParams& p, cudaStream_t stream) {
-  const long long items = (long long)p.B * p.P * p.nsg * p.gs;
+  const long long items = (long long)p.B * p.P * p.nsg * p.gs;  // below 2^31: api.cu
   if (items <= 0) return;
   DiffParams copy = p;
   void* args[] = {&copy};

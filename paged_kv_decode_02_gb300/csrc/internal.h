@@ -257,16 +257,15 @@ struct DiffParams {
   const int32_t* context_lens;
   const float* lam;            // [Hq / 2]
   const void* norm_w;          // [2 D] bf16, or NULL
-  float* part_o;               // [2 G, 2, gs, 2 D] fp32 partial outputs (unnormalised)
+  float* part_o;               // [2 G, 2, gs, 2 D] fp32 records' outputs (unnormalised)
   float* part_ml;              // [2 G, 2, gs, 2] fp32 (running max in log2 units, sum)
-  int32_t* prefix;             // [B + 1] items-per-sequence exclusive prefix (CTA 0 writes)
+  int32_t* parts;              // [B, units, 2] a unit's first record (-1: none) and last CTA
   int32_t* status;
   int B, P, MBS, NB, BS;       // P: KV head pairs
   int g;                       // query pairs per KV pair
   int gs;                      // query pairs per work unit (at most 8)
   int nsg;                     // work units per KV pair
-  int G;                       // CTAs of the decode kernel
-  int D, item;                 // head_dim, tokens per work item
+  int D;                       // head_dim
   float scale_log2;            // softmax scale * log2(e)
   float eps, out_scale;
   unsigned long long timeout_ns;
