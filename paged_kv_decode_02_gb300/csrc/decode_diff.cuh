@@ -198,6 +198,10 @@ struct DiffPathBf16 {
                                              int map) {
     return o[k / 2][2 * (k % 2) + map];
   }
+  __device__ static __forceinline__ void times(float (&d)[1], const __nv_bfloat16* w) {
+    const unsigned short u = __ldg(reinterpret_cast<const unsigned short*>(w));
+    d[0] *= __uint_as_float(uint32_t(u) << 16);
+  }
 
   // q: row gid (pair gid / 2's map gid % 2) of the warp's query rows, when live.
   __device__ __forceinline__ void begin(const __nv_bfloat16* q, bool live, int lane, float) {
@@ -282,6 +286,14 @@ struct DiffPathQ8 {
   __device__ static __forceinline__ float at(const float (&o)[2 * D / 16][4], int k, int e,
                                              int map) {
     return o[2 * k + e / 2][2 * (e % 2) + map];
+  }
+  __device__ static __forceinline__ void times(float (&d)[4], const __nv_bfloat16* w) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(w));
+    const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
+    d[0] *= a.x;
+    d[1] *= a.y;
+    d[2] *= b.x;
+    d[3] *= b.y;
   }
 
   // The row is scaled by a power of two to near 2^14 (then exact in fp16 for entries above
@@ -531,7 +543,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
 #pragma unroll
     for (int k = 0; k < Geo::kSub; ++k) {
       const int t = (pc.j * Geo::kSub + k) * Geo::kBox;
-      pid[k] = t < pL ? __ldg(p.block_tables + size_t(pc.s) * p.MBS + t / p.BS) : 0;
+      pid[k] = __ldg(p.block_tables + size_t(pc.s) * p.MBS + min(t / p.BS, p.MBS - 1));
     }
   };
   // lane 0: requests K (or V) of the producer's item; boxes past the context are left out
@@ -708,6 +720,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         const int qp = pair0 + r0 + pr;
         const float i0 = Path::kOutScale / state.l0;
         const float i1 = Path::kOutScale / state.l1 * __ldg(p.lam + qp);
+        const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.norm_w);
         float ss = 0.f, d[Path::kRuns][Path::kRun];
 #pragma unroll
         for (int k = 0; k < Path::kRuns; ++k) {
@@ -721,25 +734,22 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         const uint32_t lanes = 0x11111111u << cq;
 #pragma unroll
         for (int k = 4; k < 32; k <<= 1) ss += __shfl_xor_sync(lanes, ss, k);
-        const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.norm_w);
-        const float f = w ? rsqrtf(ss * (1.f / (2 * D)) + p.eps) * p.out_scale : p.out_scale;
+        float f = p.out_scale;
+        if (w) {  // every weight is asked for before the first store
+          f *= rsqrtf(ss * (1.f / (2 * D)) + p.eps);
+#pragma unroll
+          for (int k = 0; k < Path::kRuns; ++k) Path::times(d[k], w + Path::column(k, gid));
+        }
         __nv_bfloat16* out =
             static_cast<__nv_bfloat16*>(p.out) + (size_t(cur.s) * (Hq / 2) + qp) * (2 * D);
 #pragma unroll
         for (int k = 0; k < Path::kRuns; ++k) {
           const int c = Path::column(k, gid);
-          if constexpr (Path::kRun == 4) {
-            float4 g = make_float4(f, f, f, f);
-            if (w) {
-              const uint2 u = __ldg(reinterpret_cast<const uint2*>(w + c));
-              const float2 x0 = unpack_bf16x2(u.x), x1 = unpack_bf16x2(u.y);
-              g = make_float4(f * x0.x, f * x0.y, f * x1.x, f * x1.y);
-            }
-            *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(d[k][0] * g.x, d[k][1] * g.y),
-                                                            pack_bf16x2(d[k][2] * g.z, d[k][3] * g.w));
-          } else {
-            out[c] = __float2bfloat16(d[k][0] * (w ? f * __bfloat162float(w[c]) : f));
-          }
+          if constexpr (Path::kRun == 4)
+            *reinterpret_cast<uint2*>(out + c) = make_uint2(pack_bf16x2(d[k][0] * f, d[k][1] * f),
+                                                            pack_bf16x2(d[k][2] * f, d[k][3] * f));
+          else
+            out[c] = __float2bfloat16(d[k][0] * f);
         }
       }
     }
