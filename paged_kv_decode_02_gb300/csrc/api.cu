@@ -29,6 +29,11 @@ constexpr int kTcSplitRows = 64;
 // head, with the softmax row sums on the tensor cores) put the best at 2 (1: 8-15 %
 // slower, 3: 1-3 %, 4 and 5: 3-5 %)
 constexpr int kTcHeadCost = 2;
+// differential decode: the same for a unit, in items (a CTA that ends many short units
+// spends 2 to 4 us on each, an item about 1 us). Whole calls on GB300, ragged batch of 64
+// (64 / 8 heads, head_dim 128, bf16): cost 0 92.3 us, 1 92.1, 2 89.8, 3 88.1, 4 87.3, 6
+// 86.8; INT8, 128 x 8192: 353 us at 0 to 4, 354 at 6
+constexpr int kDiffUnitCost = 4;
 // cascade decode: the prefix kernel runs on about 1/kCascadePrefixShare of the SMs
 constexpr int kCascadePrefixShare = 3;
 
@@ -827,6 +832,7 @@ pkv_status run_diff(int kvt, void* out, const void* q, const void* k_cache, cons
   p.gs = P.gs;
   p.nsg = P.nsg;
   p.D = d->head_dim;
+  p.unit_cost = kDiffUnitCost;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.eps = eps;
   p.out_scale = out_scale;

@@ -431,6 +431,12 @@ __device__ __forceinline__ int diff_items(const DiffParams& p, int i, int item) 
   return (max(0, min(L, p.MBS * p.BS)) + item - 1) / item;
 }
 
+// Start of range w of G equal ranges of T positions (G <= T): floor(T w / G), with T / G
+// given as q and the rest r.
+__device__ __forceinline__ long long diff_start(long long q, unsigned r, unsigned w, unsigned G) {
+  return q * w + r * w / G;  // r, w <= G: within 32 bits
+}
+
 // Shared memory of a CTA: the streams' rings, the fold's states, barriers and counters,
 // the items' prefix.
 template <class Geo, int kStreams, int kRows, int kStages>
@@ -451,16 +457,17 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
   using Geo = typename Path::Geo;
   using S = DiffSmem<Geo, kStreams, kRows, kStages>;
   constexpr int N = kStreams, kWarps = kStreams * kRows, kThreads = kWarps * 32;
+  const int B = p.B;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gen = smem_raw + (base - smem_u32(smem_raw));
-  int* prefix = reinterpret_cast<int*>(gen + S::kOffPrefix);
-  __shared__ int warp_tot[kWarps];
+  int* prefix = reinterpret_cast<int*>(gen + S::kOffPrefix);  // items before sequence s
+  __shared__ int2 warp_tot[kWarps];
+  __shared__ int4 bound[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int stream = warp / kRows, tile = warp % kRows;  // tile: query pairs 4 tile .. + 3
   const int gid = lane >> 2, cq = lane & 3;
-  const int B = p.B;
   auto sK = [&](int st) { return base + stream * S::kRing + st * S::kSlot; };
   auto sV = [&](int st) { return sK(st) + Geo::kTile; };
   auto sKs = [&](int st) {
@@ -482,40 +489,95 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     if (tid < kStreams * kStages * 2) reinterpret_cast<int*>(gen + S::kOffCnt)[tid] = 0;
   }
   pdl_wait_prior_grid();
+  if (p.norm_w && tid < D / 32)  // read at the end of a unit
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p.norm_w) + tid * 128));
+  if (tid < (p.P * p.g + 31) / 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.lam + tid * 32));
 
-  // ---- items per sequence and their exclusive prefix (every CTA computes it) ----
+  // ---- this CTA's range and the items per sequence (every CTA computes them) ----
+  // The ranges are G equal cuts of a weighted order, in which a unit takes its items and
+  // then unit_cost positions that hold none: what ending it costs the CTA.
+  const int U = p.P * p.nsg;  // units per sequence
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  auto weight_of = [&](int m) { return m > 0 ? m + p.unit_cost : 0; };
+  int2 run = make_int2(0, 0);  // items and weight before sequence b0
+  for (int i = b0; i < b1; ++i) {
+    const int m = diff_items(p, i, Geo::kItem);
+    run.x += m;
+    run.y += weight_of(m);
+  }
   {
-    const int per = (B + kThreads - 1) / kThreads;
-    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int sum = 0;
-    for (int i = b0; i < b1; ++i) sum += diff_items(p, i, Geo::kItem);
-    int incl = sum;
+    int2 incl = run;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += y;
+      const int x = __shfl_up_sync(0xffffffffu, incl.x, off);
+      const int y = __shfl_up_sync(0xffffffffu, incl.y, off);
+      if (lane >= off) {
+        incl.x += x;
+        incl.y += y;
+      }
     }
     if (lane == 31) warp_tot[warp] = incl;
-    __syncthreads();
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += warp_tot[w];
-    if (tid == 0) prefix[0] = 0;
-    for (int i = b0; i < b1; ++i) {
-      run += diff_items(p, i, Geo::kItem);
-      prefix[i + 1] = run;
-    }
-    __syncthreads();
+    run = make_int2(incl.x - run.x, incl.y - run.y);
   }
-
-  const int U = p.P * p.nsg;  // units per sequence
-  const long long T = (long long)U * prefix[B];
-  const int G = int(min((long long)gridDim.x, T));  // no range is empty
+  __syncthreads();
+  int2 total = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) {
+      run.x += total.x;
+      run.y += total.y;
+    }
+    total.x += warp_tot[w].x;
+    total.y += warp_tot[w].y;
+  }
+  const long long T = (long long)U * total.y;
+  const int G = int(min((long long)gridDim.x, T));
   if (int(blockIdx.x) >= G) return;
-  const long long a = T * blockIdx.x / G, b = T * (blockIdx.x + 1) / G;
-  const int n = int(b - a);
-
+  const long long q0 = T < (1ll << 32) ? (long long)(unsigned(T) / unsigned(G)) : T / G;
+  const unsigned rest = unsigned(T - q0 * G);
+  const long long at[2] = {diff_start(q0, rest, blockIdx.x, G),
+                           diff_start(q0, rest, blockIdx.x + 1, G)};
+  if (tid == 0) prefix[0] = 0;
+  for (int i = b0; i < b1; ++i) {
+    const int m = diff_items(p, i, Geo::kItem), w = weight_of(m);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {  // the thread whose sequence holds an end of the range
+      const long long rem = at[e] - (long long)U * run.y;
+      if (rem >= 0 && rem < (long long)U * w) bound[e] = make_int4(i, run.x, run.y, m);
+    }
+    run.x += m;
+    run.y += w;
+    prefix[i + 1] = run.x;
+  }
+  __syncthreads();
+  // the first unit and item at or after an end, and the items before it
+  auto locate = [&](int e, Cursor& c) {
+    const int4 f = bound[e];
+    const int w = weight_of(f.w);
+    const long long rem = at[e] - (long long)U * f.z;
+    c.s = f.x;
+    c.n = f.w;
+    c.u = rem < (1ll << 32) ? int(unsigned(rem) / unsigned(w)) : int(rem / w);
+    c.j = min(c.n, int(rem - (long long)c.u * w));
+    const long long before = (long long)U * f.y + (long long)c.u * c.n + c.j;
+    if (c.j == c.n) {  // among a unit's empty positions: the next unit
+      c.j = 0;
+      if (++c.u == U) {
+        c.u = 0;
+        do { ++c.s; } while (c.s < B && prefix[c.s + 1] == prefix[c.s]);
+        c.n = c.s < B ? prefix[c.s + 1] - prefix[c.s] : 0;
+      }
+    }
+    return before;
+  };
   Cursor cur;  // the segment: unit cur.u of sequence cur.s from its item cur.j on
-  cursor_locate(cur, a, prefix, B, U);
+  const long long end =
+      int(blockIdx.x) + 1 == G ? (long long)U * total.x : locate(1, cur);
+  const int n = int(end - locate(0, cur));
+  if (n == 0) return;
+
   // the producer's item: number pi of the CTA's range, every N-th one is this stream's.
   // Each of the stream's warps keeps it; the last one to leave a tile requests the next.
   Cursor pc = cur;

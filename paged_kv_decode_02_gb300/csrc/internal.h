@@ -266,6 +266,7 @@ struct DiffParams {
   int gs;                      // query pairs per work unit (at most 8)
   int nsg;                     // work units per KV pair
   int D;                       // head_dim
+  int unit_cost;               // what ending a unit costs a CTA, in items
   float scale_log2;            // softmax scale * log2(e)
   float eps, out_scale;
   unsigned long long timeout_ns;
