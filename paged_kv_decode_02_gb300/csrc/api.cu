@@ -663,6 +663,8 @@ pkv_status run_rotate(int kvt, void* out, const void* q, const void* k, const vo
     if (T > 1 && strides[i] < (int64_t)heads * d->head_dim) return PKV_ERR_SHAPE;
     if (strides[i] % 8 != 0) return PKV_ERR_ALIGNMENT;
   }
+  if ((long long)T * (d->num_q_heads + 2ll * d->num_kv_heads) >= (1ll << 31))
+    return PKV_ERR_UNSUPPORTED;
   if (T == 0) return PKV_OK;
   if (!out || !q || !k || !v || !positions || !ro->cos_sin || !k_cache || !v_cache || !slots)
     return PKV_ERR_NULL;

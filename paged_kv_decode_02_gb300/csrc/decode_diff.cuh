@@ -180,8 +180,9 @@ struct DiffState {
   }
 };
 
-// bf16 cache. The softmax weights enter P.V as bf16 (off by at most 2^-8 each, averaging
-// out over tokens), the row sums are of the rounded weights.
+// bf16 cache. The difference of the two maps loses what they have in common, and with it
+// whatever was rounded in that part; so a softmax weight enters P.V as two bf16 terms, the
+// weight rounded and the rest rounded (2^-17 of it in all), on the same V operand.
 template <int D, int BOX, int SUB>
 struct DiffPathBf16 {
   using Geo = DiffGeom<D, -1, BOX, SUB>;
@@ -244,15 +245,16 @@ struct DiffPathBf16 {
     const int r8 = lane & 7, mi = lane >> 3;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
-      uint32_t pb[2];
+      uint32_t pb[2], pl[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t w =
-            pack_bf16x2(fast_exp2(x[t][2 * h] - mn0), fast_exp2(x[t][2 * h + 1] - mn1));
+        const float w0 = fast_exp2(x[t][2 * h] - mn0), w1 = fast_exp2(x[t][2 * h + 1] - mn1);
+        st.l0 += w0;
+        st.l1 += w1;
+        const uint32_t w = pack_bf16x2(w0, w1);
         const float2 f = unpack_bf16x2(w);
-        st.l0 += f.x;
-        st.l1 += f.y;
         pb[h] = transpose_8x8(w);
+        pl[h] = transpose_8x8(pack_bf16x2(w0 - f.x, w1 - f.y));
       }
 #pragma unroll
       for (int mt = 0; mt < 2 * D / 16; ++mt) {
@@ -260,6 +262,7 @@ struct DiffPathBf16 {
         ldmatrix_x4_trans(v, sV + Geo::off(mt / (D / 16), 16 * t + ((mi >> 1) << 3) + r8,
                                            2 * (mt % (D / 16)) + (mi & 1)));
         mma_bf16_16816(st.o[mt], v, pb[0], pb[1]);
+        mma_bf16_16816(st.o[mt], v, pl[0], pl[1]);
       }
     }
   }

@@ -15,7 +15,9 @@
 // Bound by memory: a row is read and written once. D / 16 lanes share a row; a lane holds
 // the two 16-byte chunks that its rotation pairs (chunks j and j + R/16, or 2j and 2j + 1
 // interleaved; R is a multiple of 16), so both elements of every pair are in one lane and
-// only the norm's and the quantiser's row reductions cross lanes.
+// only the norm's and the quantiser's row reductions cross lanes. With many rows a lane
+// group takes kU rows of one token: their loads are in flight together and share the
+// token's position, slot and table row.
 #include "common.cuh"
 #include "encode.cuh"
 #include "internal.h"
@@ -47,137 +49,165 @@ __device__ __forceinline__ void load8(const float* p, float* f) {
 }  // namespace
 
 // CODE: CODE_I8 / CODE_E4M3 / CODE_E5M2, or -1 for a bf16 cache.
-template <int D, int CODE>
+template <int D, int CODE, int kU>
 __global__ void __launch_bounds__(kRotThreads)
     paged_kv_rotate_append_kernel(const RotateParams p) {
   constexpr int LPR = D / 16;  // lanes per row
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int rows = p.Hq + 2 * p.Hkv;  // rows per token: q, then k, then v heads
-  const long long row = ((long long)blockIdx.x * kRotThreads + threadIdx.x) / LPR;
+  const unsigned sets = unsigned(rows + kU - 1) / kU;  // of a token; set i: rows i + k sets
+  const unsigned item = blockIdx.x * (kRotThreads / LPR) + threadIdx.x / LPR;
   const int j = threadIdx.x % LPR;
   // the row's lanes: they branch alike
   const uint32_t group = ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
-  const bool live = row < (long long)p.T * rows;
-  const int t = live ? int(row / rows) : 0;
-  const int r = live ? int(row % rows) : 0;
-  const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
-  const int h = isq ? r : isv ? r - p.Hq - p.Hkv : r - p.Hq;
+  const unsigned t = item / sets;
+  if (t >= unsigned(p.T)) return;
+  const int first = int(item % sets);
 
-  // the lane's two chunks of the row: a rotation pair's, or two of the rest
+  // the lane's two chunks of a row: a rotation pair's, or two of the rest
   const int nrot = p.R / 16;
-  const bool turns = j < nrot && !isv;
+  const bool turns = j < nrot;
   int ca = 2 * j, cb = 2 * j + 1;
-  if (!p.interleaved && j < nrot) {
+  if (!p.interleaved && turns) {
     ca = j;
     cb = j + nrot;
   }
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(isq ? p.q : isv ? p.v : p.k) +
-                             (long long)t * (isq ? p.q_stride : isv ? p.v_stride : p.k_stride) +
-                             h * D;
-  float x[16];
   // (a row read here may be the one written below: out may be q)
-  unpack8(reinterpret_cast<const uint4*>(src)[ca], x);
-  unpack8(reinterpret_cast<const uint4*>(src)[cb], x + 8);
-  const long long pos = p.positions[t];
-  const long long slot = isq ? 0 : p.slots[t];
-  const bool bad = pos < 0 || pos >= p.P;
-  if (bad && live && r == 0 && j == 0 && p.status) atomicOr(p.status, PKV_DEV_BAD_POSITION);
-
-  const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(isq ? p.q_norm : p.k_norm);
-  if (!isv && w != nullptr) {
-    float ss = 0.f;
+  uint4 raw[kU][2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-    const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
-    float f[16];
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ca), f);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(w) + cb), f + 8);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = x[e] * rstd * f[e];
+  for (int k = 0; k < kU; ++k) {
+    const int r = first + k * int(sets);
+    if (r >= rows) break;
+    const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(isq ? p.q : isv ? p.v : p.k) +
+        (long long)t * (isq ? p.q_stride : isv ? p.v_stride : p.k_stride) +
+        (isq ? r : isv ? r - p.Hq - p.Hkv : r - p.Hq) * D);
+    raw[k][0] = src[ca];
+    raw[k][1] = src[cb];
   }
+  const long long pos = p.positions[t];
+  const long long slot = p.slots[t];
+  const bool bad = pos < 0 || pos >= p.P;
+  if (bad && first == 0 && j == 0 && p.status) atomicOr(p.status, PKV_DEV_BAD_POSITION);
+  float c[8], s[8];
   if (turns && !bad) {
     const float* cs = p.cos_sin + pos * p.R + 8 * j;
-    float c[8], s[8];
     load8(cs, c);
     load8(cs + p.R / 2, s);
-    if (p.interleaved) {
+  }
+  const bool skip = bad || slot < 0 || slot >= (long long)p.NB * p.BS;
+  const long long blk = slot / p.BS, off = slot % p.BS;
+
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * c[i] - b * s[i];
-        x[2 * i + 1] = b * c[i] + a * s[i];
+  for (int k = 0; k < kU; ++k) {
+    const int r = first + k * int(sets);
+    if (r >= rows) break;
+    const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
+    const int h = isq ? r : isv ? r - p.Hq - p.Hkv : r - p.Hq;
+    float x[16];
+    unpack8(raw[k][0], x);
+    unpack8(raw[k][1], x + 8);
+    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(isq ? p.q_norm : p.k_norm);
+    if (!isv && w != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+      const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
+      float f[16];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ca), f);
+      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + cb), f + 8);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = x[e] * rstd * f[e];
+    }
+    if (turns && !bad && !isv) {
+      if (p.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = x[2 * i], b = x[2 * i + 1];
+          x[2 * i] = a * c[i] - b * s[i];
+          x[2 * i + 1] = b * c[i] + a * s[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float a = x[i], b = x[8 + i];
+          x[i] = a * c[i] - b * s[i];
+          x[8 + i] = b * c[i] + a * s[i];
+        }
       }
+    }
+    if (isq) {
+      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                            (long long)t * p.out_stride + h * D);
+      dst[ca] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x);
+      dst[cb] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x + 8);
+      continue;
+    }
+    const long long drow = (blk * p.Hkv + h) * p.BS + off;
+    if constexpr (CODE < 0) {
+      if (skip) continue;
+      uint4* dst = reinterpret_cast<uint4*>(isv ? p.vc : p.kc) + drow * (D / 8);
+      dst[ca] = pack8(x);
+      dst[cb] = pack8(x + 8);
     } else {
+      using Enc = Encode8<CODE>;
+      float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = x[i], b = x[8 + i];
-        x[i] = a * c[i] - b * s[i];
-        x[8 + i] = b * c[i] + a * s[i];
+      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
+      if (skip) continue;
+      const float sc = __fdiv_rn(amax, Enc::kMax);
+      uint32_t u[4] = {0u, 0u, 0u, 0u};
+      if (sc > 0.f) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) u[e / 4] |= uint32_t(Enc::code(x[e], sc)) << (8 * (e % 4));
       }
+      uint2* dst = reinterpret_cast<uint2*>(isv ? p.vc : p.kc) + drow * (D / 8);
+      dst[ca] = make_uint2(u[0], u[1]);
+      dst[cb] = make_uint2(u[2], u[3]);
+      if (j == 0) (isv ? p.vs : p.ks)[drow] = sc;
     }
   }
-  if (isq) {
-    if (!live) return;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                          (long long)t * p.out_stride + h * D);
-    dst[ca] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x);
-    dst[cb] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x + 8);
-    return;
-  }
-  const bool skip = !live || bad || slot < 0 || slot >= (long long)p.NB * p.BS;
-  const long long drow = (slot / p.BS * p.Hkv + h) * p.BS + slot % p.BS;
-  if constexpr (CODE < 0) {
-    if (skip) return;
-    uint4* dst = reinterpret_cast<uint4*>(isv ? p.vc : p.kc) + drow * (D / 8);
-    dst[ca] = pack8(x);
-    dst[cb] = pack8(x + 8);
-  } else {
-    using Enc = Encode8<CODE>;
-    float amax = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1)
-      amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
-    if (skip) return;
-    const float s = __fdiv_rn(amax, Enc::kMax);
-    uint32_t u[4] = {0u, 0u, 0u, 0u};
-    if (s > 0.f) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) u[e / 4] |= uint32_t(Enc::code(x[e], s)) << (8 * (e % 4));
-    }
-    uint2* dst = reinterpret_cast<uint2*>(isv ? p.vc : p.kc) + drow * (D / 8);
-    dst[ca] = make_uint2(u[0], u[1]);
-    dst[cb] = make_uint2(u[2], u[3]);
-    if (j == 0) (isv ? p.vs : p.ks)[drow] = s;
-  }
+}
+
+template <int D, int CODE>
+cudaError_t launch_rotate(const RotateParams& p, cudaStream_t stream) {
+  // few rows: a row per lane group, as many of them as there are; rows enough for every
+  // SM's threads twice over: kMany rows each
+  constexpr int kMany = 4;
+  const long long rows = p.Hq + 2 * p.Hkv;
+  if (p.T * rows >= (1ll << 31)) return cudaErrorInvalidValue;
+  const bool many = p.T * rows * (D / 16) >= 2ll * 152 * 2048;
+  const long long items = p.T * (many ? (rows + kMany - 1) / kMany : rows);
+  constexpr int per = kRotThreads / (D / 16);
+  RotateParams copy = p;
+  void* args[] = {&copy};
+  const void* fn =
+      many ? reinterpret_cast<const void*>(&paged_kv_rotate_append_kernel<D, CODE, kMany>)
+           : reinterpret_cast<const void*>(&paged_kv_rotate_append_kernel<D, CODE, 1>);
+  return launch_pdl(fn, dim3(unsigned((items + per - 1) / per)), dim3(kRotThreads), args, 0,
+                    stream);
 }
 
 cudaError_t launch_rotate_append(int code, int D, const RotateParams& p, cudaStream_t stream) {
   if (p.T <= 0) return cudaSuccess;
-  const long long threads = (long long)p.T * (p.Hq + 2 * p.Hkv) * (D / 16);
-  const long long grid = (threads + kRotThreads - 1) / kRotThreads;
-  if (grid >= (1ll << 31)) return cudaErrorInvalidValue;
-  const void* fn = nullptr;
-#define PKV_ROTATE(DD, CC) \
-  if (D == DD && code == CC) \
-    fn = reinterpret_cast<const void*>(&paged_kv_rotate_append_kernel<DD, CC>);
-  PKV_ROTATE(128, -1)
-  PKV_ROTATE(64, -1)
-  PKV_ROTATE(128, CODE_I8)
-  PKV_ROTATE(64, CODE_I8)
-  PKV_ROTATE(128, CODE_E4M3)
-  PKV_ROTATE(64, CODE_E4M3)
-  PKV_ROTATE(128, CODE_E5M2)
-  PKV_ROTATE(64, CODE_E5M2)
-#undef PKV_ROTATE
-  if (!fn) return cudaErrorInvalidValue;
-  RotateParams copy = p;
-  void* args[] = {&copy};
-  return launch_pdl(fn, dim3(unsigned(grid)), dim3(kRotThreads), args, 0, stream);
+  switch (code) {
+    case -1: return D == 128 ? launch_rotate<128, -1>(p, stream) : launch_rotate<64, -1>(p, stream);
+    case CODE_I8:
+      return D == 128 ? launch_rotate<128, CODE_I8>(p, stream) : launch_rotate<64, CODE_I8>(p, stream);
+    case CODE_E4M3:
+      return D == 128 ? launch_rotate<128, CODE_E4M3>(p, stream)
+                      : launch_rotate<64, CODE_E4M3>(p, stream);
+    case CODE_E5M2:
+      return D == 128 ? launch_rotate<128, CODE_E5M2>(p, stream)
+                      : launch_rotate<64, CODE_E5M2>(p, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace pkv

@@ -42,10 +42,9 @@ def diff_reference(w, lam, norm_weight=None, eps=0.0, out_scale=1.0):
     """(out, bound) [B, Hq / 2, 2 D] in float64.
 
     Per map, the weighted mean O_m = sum a v of rounded weights a (1 + d): off by at most
-    u * sum a |v - O_m| where the row sum is of the same rounded weights (bf16, u = 2^-8), or
-    u * sum a |v| where it is not (one-byte caches: weight times V scale in fp16, u = 2^-11,
-    plus half a subnormal step of fp16, 2^-25, times the code, over the row sum, which is at
-    least 1, of the scaled weight). Then |lambda| times that for the second map, through the
+    u * sum a |v|. bf16 caches: a weight is two bf16 terms, u = 2^-8 * 2^-8 = 2^-16; one-byte
+    caches: weight times V scale in fp16, u = 2^-11, plus half a subnormal step of fp16,
+    2^-25, times the code, over the row sum, which is at least 1, of the scaled weight. Then |lambda| times that for the second map, through the
     norm to first order, and half a step of the bf16 output."""
     B, Hq, D = w.q.shape
     q = to_f64(w.q)
@@ -71,7 +70,7 @@ def diff_reference(w, lam, norm_weight=None, eps=0.0, out_scale=1.0):
                 o = np.sum(a * v, 0)
                 off = FP32_SLACK * np.sum(a * np.abs(v - o), 0) + 2.0 ** -20 * np.abs(o)
                 if w.kv_dtype == "bf16":
-                    off += 2.0 ** -8 * np.sum(a * np.abs(v - o), 0)
+                    off += 2.0 ** -16 * np.sum(a * np.abs(v), 0)
                 else:
                     off += 2.0 ** -11 * np.sum(a * np.abs(v), 0)
                     off += 2.0 ** -25 / up * np.sum(c, 0) * maps[j, m].max()
