@@ -696,7 +696,7 @@ pkv_status run_rotate(int kvt, void* out, const void* q, const void* k, const vo
   p.T = T;
   p.Hq = d->num_q_heads;
   p.Hkv = d->num_kv_heads;
-  p.BS = d->block_size;
+  p.bs_log2 = d->block_size == 32 ? 5 : 4;
   p.NB = d->num_blocks;
   p.P = ro->num_positions;
   p.R = ro->rotary_dim;

@@ -35,4 +35,42 @@ struct Encode8<CODE_E5M2> {
   }
 };
 
+// Codes of a row's elements over one scale, as Encode8 gives them, with one reciprocal per
+// row in place of a division per element. By Markstein's theorem (IBM J. Res. Dev. 34(1),
+// 1990) the correctly rounded quotient is q + (x - q s) r, fused, for r the correctly
+// rounded reciprocal of s and q = x r, as long as x - q s is exact: with s from 2^-80 to
+// 2^100 it is for |x| >= 2^-102, and below that x / s is under half of every format's
+// smallest code. Other scales divide.
+template <int CODE>
+struct RowEncoder {
+  float s, r;
+  bool fast;
+  __device__ __forceinline__ explicit RowEncoder(float s_)
+      : s(s_), r(1.f / s_), fast(s_ >= 0x1p-80f && s_ <= 0x1p100f) {}
+  // codes of x[0..3], the first in the low byte
+  __device__ __forceinline__ uint32_t four(const float* x) const {
+    if (!fast) {
+      uint32_t u = 0u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u |= uint32_t(Encode8<CODE>::code(x[e], s)) << (8 * e);
+      return u;
+    }
+    float q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float t = x[e] * r;
+      q[e] = fmaf(fmaf(-t, s, x[e]), r, t);
+    }
+    if constexpr (CODE == CODE_I8) {  // |q| rounds to 127 at most: |x| <= 127 s (1 + 2^-24)
+      const int i0 = __float2int_rn(q[0]), i1 = __float2int_rn(q[1]);
+      const int i2 = __float2int_rn(q[2]), i3 = __float2int_rn(q[3]);
+      return prmt(prmt(i0, i1, 0x0040u), prmt(i2, i3, 0x0040u), 0x5410u);
+    } else {
+      constexpr auto kind = CODE == CODE_E4M3 ? __NV_E4M3 : __NV_E5M2;
+      return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, kind)) |
+             uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, kind)) << 16;
+    }
+  }
+};
+
 }  // namespace pkv

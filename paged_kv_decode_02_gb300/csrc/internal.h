@@ -223,7 +223,8 @@ struct RotateParams {
   float* vs;
   int32_t* status;
   long long out_stride, q_stride, k_stride, v_stride;
-  int T, Hq, Hkv, BS, NB, P, R, interleaved;
+  int T, Hq, Hkv, NB, P, R, interleaved;
+  int bs_log2;                 // of the block size
   float eps;
 };
 // code: CODE_I8, CODE_E4M3 or CODE_E5M2; -1: bf16 cache

@@ -50,7 +50,7 @@ __device__ __forceinline__ void load8(const float* p, float* f) {
 
 // CODE: CODE_I8 / CODE_E4M3 / CODE_E5M2, or -1 for a bf16 cache.
 template <int D, int CODE, int kU>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, 3)
     paged_kv_rotate_append_kernel(const RotateParams p) {
   constexpr int LPR = D / 16;  // lanes per row
   pdl_wait_prior_grid();
@@ -61,9 +61,9 @@ __global__ void __launch_bounds__(kRotThreads)
   const int j = threadIdx.x % LPR;
   // the row's lanes: they branch alike
   const uint32_t group = ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
-  const unsigned t = item / sets;
-  if (t >= unsigned(p.T)) return;
-  const int first = int(item % sets);
+  const long long t = item / sets;
+  if (t >= p.T) return;
+  const int first = int(item - unsigned(t) * sets);
 
   // the lane's two chunks of a row: a rotation pair's, or two of the rest
   const int nrot = p.R / 16;
@@ -73,19 +73,22 @@ __global__ void __launch_bounds__(kRotThreads)
     ca = j;
     cb = j + nrot;
   }
+  // the token's q, k and v rows
+  const __nv_bfloat16* rows_of[3] = {
+      static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride,
+      static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride - p.Hq * D,
+      static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride - (p.Hq + p.Hkv) * D};
   // (a row read here may be the one written below: out may be q)
   uint4 raw[kU][2];
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
     const int r = first + k * int(sets);
-    if (r >= rows) break;
-    const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        static_cast<const __nv_bfloat16*>(isq ? p.q : isv ? p.v : p.k) +
-        (long long)t * (isq ? p.q_stride : isv ? p.v_stride : p.k_stride) +
-        (isq ? r : isv ? r - p.Hq - p.Hkv : r - p.Hq) * D);
-    raw[k][0] = src[ca];
-    raw[k][1] = src[cb];
+    if (r < rows) {
+      const uint4* src = reinterpret_cast<const uint4*>(
+          rows_of[r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2] + r * D);
+      raw[k][0] = src[ca];
+      raw[k][1] = src[cb];
+    }
   }
   const long long pos = p.positions[t];
   const long long slot = p.slots[t];
@@ -97,19 +100,20 @@ __global__ void __launch_bounds__(kRotThreads)
     load8(cs, c);
     load8(cs + p.R / 2, s);
   }
-  const bool skip = bad || slot < 0 || slot >= (long long)p.NB * p.BS;
-  const long long blk = slot / p.BS, off = slot % p.BS;
+  const bool skip = bad || slot < 0 || slot >= (long long)p.NB << p.bs_log2;
+  // cache row of KV head 0: (block * Hkv + head) * BS + offset
+  const long long drow0 = (((slot >> p.bs_log2) * p.Hkv) << p.bs_log2) +
+                          (slot & ((1 << p.bs_log2) - 1));
 
 #pragma unroll
   for (int k = 0; k < kU; ++k) {
     const int r = first + k * int(sets);
     if (r >= rows) break;
     const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
-    const int h = isq ? r : isv ? r - p.Hq - p.Hkv : r - p.Hq;
     float x[16];
     unpack8(raw[k][0], x);
     unpack8(raw[k][1], x + 8);
-    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(isq ? p.q_norm : p.k_norm);
+    const uint4* w = static_cast<const uint4*>(isq ? p.q_norm : p.k_norm);
     if (!isv && w != nullptr) {
       float ss = 0.f;
 #pragma unroll
@@ -118,8 +122,8 @@ __global__ void __launch_bounds__(kRotThreads)
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
       const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
       float f[16];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + ca), f);
-      unpack8(__ldg(reinterpret_cast<const uint4*>(w) + cb), f + 8);
+      unpack8(__ldg(w + ca), f);
+      unpack8(__ldg(w + cb), f + 8);
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = x[e] * rstd * f[e];
     }
@@ -142,30 +146,31 @@ __global__ void __launch_bounds__(kRotThreads)
     }
     if (isq) {
       uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                            (long long)t * p.out_stride + h * D);
+                                            t * p.out_stride + r * D);
       dst[ca] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x);
       dst[cb] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x + 8);
       continue;
     }
-    const long long drow = (blk * p.Hkv + h) * p.BS + off;
+    const int h = isv ? r - p.Hq - p.Hkv : r - p.Hq;
+    const long long drow = drow0 + (h << p.bs_log2);
     if constexpr (CODE < 0) {
       if (skip) continue;
       uint4* dst = reinterpret_cast<uint4*>(isv ? p.vc : p.kc) + drow * (D / 8);
       dst[ca] = pack8(x);
       dst[cb] = pack8(x + 8);
     } else {
-      using Enc = Encode8<CODE>;
       float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+      for (int e = 0; e < 16; e += 2) amax = fmax3(amax, fabsf(x[e]), fabsf(x[e + 1]));
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
       if (skip) continue;
-      const float sc = __fdiv_rn(amax, Enc::kMax);
+      const float sc = __fdiv_rn(amax, Encode8<CODE>::kMax);
       uint32_t u[4] = {0u, 0u, 0u, 0u};
       if (sc > 0.f) {
+        const RowEncoder<CODE> enc(sc);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) u[e / 4] |= uint32_t(Enc::code(x[e], sc)) << (8 * (e % 4));
+        for (int e = 0; e < 4; ++e) u[e] = enc.four(x + 4 * e);
       }
       uint2* dst = reinterpret_cast<uint2*>(isv ? p.vc : p.kc) + drow * (D / 8);
       dst[ca] = make_uint2(u[0], u[1]);
