@@ -1192,7 +1192,7 @@ pkv_status pkv_gather_tokens(void* out_k, void* out_v, const void* k_cache, cons
   p.status = status;
   p.B = dims->num_seqs;
   p.Hkv = dims->num_kv_heads;
-  p.BS = dims->block_size;
+  p.bs_log2 = dims->block_size == 32 ? 5 : 4;
   p.NB = dims->num_blocks;
   p.MBS = dims->max_blocks_per_seq;
   p.N = num_out_tokens;

@@ -20,7 +20,8 @@ constexpr int kDiffMergeThreads = 256;
 
 // kGroups == 1: a CTA takes several pairs; else one pair and kGroups sets of warps.
 template <int D, int kGroups>
-__global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D, kGroups == 1 ? 5 : 1)
+__global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D,
+                                  kGroups == 1 ? 5 : 1)
     paged_diff_merge_kernel(const DiffParams p) {
   constexpr int Q = D / 2;          // quads of a 2 D row
   constexpr int kSet = 2 * Q;       // threads of a set: quads of both maps
@@ -67,12 +68,13 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D
   if (active) {
     const int w0 = part.x >> 1, nparts = part.y - w0 + 1;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    fold_parts<kGroups == 1 ? 4 : 8>(f, group, kGroups, nparts, [&](int i, const float2*& pm, const float4*& po) {
+    auto part_of = [&](int i, const float2*& pm, const float4*& po) {
       const size_t slot = i == 0 ? part.x : 2 * (w0 + i);
       const size_t rr = (slot * 2 + map) * p.gs + r;
       pm = ml + rr;
       po = reinterpret_cast<const float4*>(p.part_o + rr * (2 * D)) + quad;
-    });
+    };
+    fold_parts<kGroups == 1 ? 4 : 8>(f, group, kGroups, nparts, part_of);
   }
   if constexpr (kGroups > 1) {
     s_o[set][t] = f.o;

@@ -67,8 +67,9 @@ struct RowEncoder {
       return prmt(prmt(i0, i1, 0x0040u), prmt(i2, i3, 0x0040u), 0x5410u);
     } else {
       constexpr auto kind = CODE == CODE_E4M3 ? __NV_E4M3 : __NV_E5M2;
-      return uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, kind)) |
-             uint32_t(__nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, kind)) << 16;
+      const float2 lo = make_float2(q[0], q[1]), hi = make_float2(q[2], q[3]);
+      return uint32_t(__nv_cvt_float2_to_fp8x2(lo, __NV_SATFINITE, kind)) |
+             uint32_t(__nv_cvt_float2_to_fp8x2(hi, __NV_SATFINITE, kind)) << 16;
     }
   }
 };

@@ -242,8 +242,9 @@ struct GatherParams {
   const int32_t* starts;       // [B] first token of each sequence, or NULL: 0
   const int32_t* offsets;      // [B + 1]
   int32_t* status;
-  int B, Hkv, BS, NB, MBS, N;
-  int tile_log2;               // tokens per CTA, log2
+  int B, Hkv, NB, MBS, N;
+  int bs_log2;                 // of the block size
+  int tile_log2;               // of the tokens per CTA
 };
 // code as for launch_rotate_append
 cudaError_t launch_gather(int code, int D, const GatherParams& p, cudaStream_t stream);
