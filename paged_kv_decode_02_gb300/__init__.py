@@ -26,5 +26,6 @@ __all__ = list(_API)
 def __getattr__(name):
     if name in _API:
         from . import pagedkv
-        return getattr(pagedkv, name)
+        value = globals()[name] = getattr(pagedkv, name)
+        return value
     raise AttributeError(name)

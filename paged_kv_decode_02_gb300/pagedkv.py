@@ -266,12 +266,15 @@ def _need_caches(kv, k_cache, v_cache, k_scale, v_scale):
     index = k_cache.get_device()
     if index < 0:
         _require(k_cache, "k_cache", k_cache.dtype, 4)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        dts = _code_dtypes(kv)
-        dt = t.dtype if isinstance(t, torch.Tensor) and t.dtype in dts else dts[0]
-        _need(t, name, dt, 4, index)
+    dt = k_cache.dtype
+    if dt not in _code_dtypes(kv):
+        dt = _code_dtypes(kv)[0]
+    _need(k_cache, "k_cache", dt, 4, index)
     shape = k_cache.shape
-    if v_cache.shape != shape:
+    if not (isinstance(v_cache, torch.Tensor) and v_cache.dtype is dt
+            and v_cache.get_device() == index and v_cache.shape == shape
+            and v_cache.is_contiguous()):
+        _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, k_cache.device)
         _same_shape(v_cache, "v_cache", shape)
     if kv != KV_BF16:
         _need(k_scale, "k_scale", _F32, 3, index)
@@ -284,11 +287,11 @@ def _need_caches(kv, k_cache, v_cache, k_scale, v_scale):
 def _run(name, index, *args):
     """Calls the library on CUDA device ``index``, on its current stream; returns the
     status."""
-    lib = _LIB if _LIB is not None else load_library()
-    if torch.cuda.current_device() == index:
-        return getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+    fn = getattr(_LIB if _LIB is not None else load_library(), name)
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(index):
-        return getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index))
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _status_ptr(status, index):
@@ -394,10 +397,10 @@ def _token_rows(t, name, index):
         _require(t, name, _BF16, 3, torch.device("cuda", max(index, 0)))
     shape = t.shape
     tokens, heads, d = shape
-    st = t.stride()
-    if (d > 1 and st[2] != 1) or (heads > 1 and st[1] != d):
+    st0, st1, st2 = t.stride()
+    if (d > 1 and st2 != 1) or (heads > 1 and st1 != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous rows")
-    return shape, st[0] if tokens > 1 else heads * d
+    return shape, st0 if tokens > 1 else heads * d
 
 
 def _rotate_append(kv, q, k, v, positions, cos_sin, k_cache, v_cache, k_scale, v_scale,
@@ -418,19 +421,22 @@ def _rotate_append(kv, q, k, v, positions, cos_sin, k_cache, v_cache, k_scale, v
     if positions.shape[0] != tokens or slot_mapping.shape[0] != tokens:
         _same_shape(positions, "positions", (tokens,))
         _same_shape(slot_mapping, "slot_mapping", (tokens,))
-    norms = []
-    for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None:
-            _need(t, n, _BF16, 1, index)
-            _same_shape(t, n, (d,))
-        norms.append(t.data_ptr() if t is not None else 0)
+    qw = kw = 0
+    if q_norm is not None:
+        _need(q_norm, "q_norm", _BF16, 1, index)
+        qw = q_norm.data_ptr()
+    if k_norm is not None:
+        _need(k_norm, "k_norm", _BF16, 1, index)
+        kw = k_norm.data_ptr()
+    if (qw and q_norm.shape[0] != d) or (kw and k_norm.shape[0] != d):
+        raise ValueError(f"q_norm and k_norm must have {d} elements")
     if out is None:
         out, out_stride = torch.empty((tokens, hq, d), dtype=_BF16, device=q.device), hq * d
     else:
         out_shape, out_stride = _token_rows(out, "out", index)
         if out_shape != q_shape:
             _same_shape(out, "out", q_shape)
-    rotary = _pack_rotary(cos_sin.data_ptr(), *norms, out_stride, q_stride, k_stride, v_stride,
+    rotary = _pack_rotary(cos_sin.data_ptr(), qw, kw, out_stride, q_stride, k_stride, v_stride,
                           *cos_sin.shape, 1 if interleaved else 0, float(eps))
     dims = _pack_dims(0, hq, hkv, d, bs, nb, 1)
     rows = (out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
