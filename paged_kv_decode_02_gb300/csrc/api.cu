@@ -743,9 +743,9 @@ pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
       return PKV_OK;
     }
   DiffPlan P{};
-  // up to 8 query pairs per work unit, as evenly as they go
+  // up to 16 query pairs per work unit, as evenly as they go
   const int g = d->num_q_heads / d->num_kv_heads;
-  P.nsg = (g + 7) / 8;
+  P.nsg = (g + 15) / 16;
   P.gs = (g + P.nsg - 1) / P.nsg;
   const bool found = kvt == PKV_KV_BF16   ? select_diff_bf16(d->head_dim, d->block_size, P.gs, &P.k)
                      : kvt == PKV_KV_INT8 ? select_diff_int8(d->head_dim, d->block_size, P.gs, &P.k)

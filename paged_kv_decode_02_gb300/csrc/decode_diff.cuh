@@ -14,14 +14,15 @@
 //   an m16n8k16 MMA, query rows on N = 8: row 2i is the first map of the warp's query pair
 //   i, row 2i + 1 the second. Four pairs fill the 8 columns, where rows on M would leave
 //   half of 16 empty and double the accumulators (128 registers a lane for 2 D = 256
-//   columns; here 64). S^T = K q^T runs per K head over all 8 columns; the columns of the
+//   columns; here 64). More pairs are more groups of 8 columns on the same K and V operands,
+//   two to a warp at most. S^T = K q^T runs per K head over all 8 columns; the columns of the
 //   other map are not read. The weights turn from S^T's accumulators into P^T's operand
 //   by a movmatrix per 8 tokens. A pair's two maps are neighbouring columns of one lane:
 //   the difference is local, the norm one reduction over 8 lanes.
 // * Work split: (sequence, unit, item) triples in one flat order, an item `kItem` tokens of
-//   one KV pair, cut into G equal ranges, one per CTA. A unit is up to 8 query pairs of a
-//   KV pair. The CTA's warps form streams of kRows warps (one per 4 pairs, reading the
-//   same tiles); stream i takes items i, i + N, ... of the range with its own
+//   one KV pair, cut into G equal ranges, one per CTA. A unit is up to 16 query pairs of a
+//   KV pair. The CTA's warps form streams of kRows warps (of up to 8 pairs each, reading
+//   the same tiles); stream i takes items i, i + N, ... of the range with its own
 //   online-softmax state and ring; at the end of a unit the streams' states fold through
 //   shared memory (a unit of one item: no fold). A CTA rather than a warp owns a range
 //   because a cut unit's record is 2 rows of 2 D floats per query pair: fewer, larger
@@ -183,13 +184,14 @@ struct DiffState {
 // bf16 cache. The difference of the two maps loses what they have in common, and with it
 // whatever was rounded in that part; so a softmax weight enters P.V as two bf16 terms, the
 // weight rounded and the rest rounded (2^-17 of it in all), on the same V operand.
-template <int D, int BOX, int SUB>
+template <int D, int BOX, int SUB, int NT>
 struct DiffPathBf16 {
   using Geo = DiffGeom<D, -1, BOX, SUB>;
+  static constexpr int kNT = NT;  // groups of 4 query pairs of the warp
   static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr float kOutScale = 1.f;
-  uint32_t qb[kKS][2];
-  DiffState<D> st;
+  uint32_t qb[NT][kKS][2];
+  DiffState<D> st[NT];
 
   // A lane's columns of a 2 D row: kRun neighbouring ones from column(k, gid), in
   // o[at(k, e)][half(k, e) * 2 + map].
@@ -204,65 +206,80 @@ struct DiffPathBf16 {
     d[0] *= __uint_as_float(uint32_t(u) << 16);
   }
 
-  // q: row gid (pair gid / 2's map gid % 2) of the warp's query rows, when live.
-  __device__ __forceinline__ void begin(const __nv_bfloat16* q, bool live, int lane, float) {
+  // q: row gid (pair gid / 2's map gid % 2) of the query rows of group g, when live.
+  __device__ __forceinline__ void begin(int g, const __nv_bfloat16* q, bool live, int lane,
+                                        float) {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(q) + (lane & 3);
 #pragma unroll
     for (int ks = 0; ks < kKS; ++ks) {
-      qb[ks][0] = live ? __ldg(w + 8 * ks) : 0u;
-      qb[ks][1] = live ? __ldg(w + 8 * ks + 4) : 0u;
+      qb[g][ks][0] = live ? __ldg(w + 8 * ks) : 0u;
+      qb[g][ks][1] = live ? __ldg(w + 8 * ks + 4) : 0u;
     }
-    st.clear();
+    st[g].clear();
   }
 
-  // Scores of tokens 16 t + gid (x[t][0..1], by map) and 16 t + 8 + gid (x[t][2..3]) in log2
-  // units; tokens from nvalid on are -inf.
-  __device__ __forceinline__ void scores(float (&x)[kT][4], uint32_t sK, uint32_t, int nvalid,
-                                         int lane, float scale_log2) {
+  // Scores of tokens 16 t + gid (x[g][t][0..1], by map) and 16 t + 8 + gid (x[g][t][2..3]) in
+  // log2 units; tokens from nvalid on are -inf.
+  __device__ __forceinline__ void scores(float (&x)[NT][kT][4], uint32_t sK, uint32_t,
+                                         int nvalid, int lane, float scale_log2) {
     const int r8 = lane & 7, mi = lane >> 3, gid = lane >> 2;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
-      float a[4] = {}, b[4] = {};
+      float a[NT][4] = {}, b[NT][4] = {};
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t k0[4], k1[4];
         const int row = 16 * t + ((mi & 1) << 3) + r8, cc = 2 * ks + (mi >> 1);
         ldmatrix_x4(k0, sK + Geo::off(0, row, cc));
         ldmatrix_x4(k1, sK + Geo::off(1, row, cc));
-        mma_bf16_16816(a, k0, qb[ks][0], qb[ks][1]);
-        mma_bf16_16816(b, k1, qb[ks][0], qb[ks][1]);
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
+          mma_bf16_16816(a[g], k0, qb[g][ks][0], qb[g][ks][1]);
+          mma_bf16_16816(b[g], k1, qb[g][ks][0], qb[g][ks][1]);
+        }
       }
       const bool lo = 16 * t + gid < nvalid, hi = 16 * t + 8 + gid < nvalid;
-      x[t][0] = lo ? a[0] * scale_log2 : -INFINITY;
-      x[t][1] = lo ? b[1] * scale_log2 : -INFINITY;
-      x[t][2] = hi ? a[2] * scale_log2 : -INFINITY;
-      x[t][3] = hi ? b[3] * scale_log2 : -INFINITY;
+#pragma unroll
+      for (int g = 0; g < NT; ++g) {
+        x[g][t][0] = lo ? a[g][0] * scale_log2 : -INFINITY;
+        x[g][t][1] = lo ? b[g][1] * scale_log2 : -INFINITY;
+        x[g][t][2] = hi ? a[g][2] * scale_log2 : -INFINITY;
+        x[g][t][3] = hi ? b[g][3] * scale_log2 : -INFINITY;
+      }
     }
   }
 
-  __device__ __forceinline__ void values(float (&x)[kT][4], uint32_t sV, uint32_t, int,
-                                         float mn0, float mn1, int lane) {
+  // mn: what the scores of each map of each group subtract.
+  __device__ __forceinline__ void values(float (&x)[NT][kT][4], uint32_t sV, uint32_t, int,
+                                         const float2 (&mn)[NT], int lane) {
     const int r8 = lane & 7, mi = lane >> 3;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
-      uint32_t pb[2], pl[2];
+      uint32_t pb[NT][2], pl[NT][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float w0 = fast_exp2(x[t][2 * h] - mn0), w1 = fast_exp2(x[t][2 * h + 1] - mn1);
-        st.l0 += w0;
-        st.l1 += w1;
-        const uint32_t w = pack_bf16x2(w0, w1);
-        const float2 f = unpack_bf16x2(w);
-        pb[h] = transpose_8x8(w);
-        pl[h] = transpose_8x8(pack_bf16x2(w0 - f.x, w1 - f.y));
+      for (int g = 0; g < NT; ++g) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float w0 = fast_exp2(x[g][t][2 * h] - mn[g].x);
+          const float w1 = fast_exp2(x[g][t][2 * h + 1] - mn[g].y);
+          st[g].l0 += w0;
+          st[g].l1 += w1;
+          const uint32_t w = pack_bf16x2(w0, w1);
+          const float2 f = unpack_bf16x2(w);
+          pb[g][h] = transpose_8x8(w);
+          pl[g][h] = transpose_8x8(pack_bf16x2(w0 - f.x, w1 - f.y));
+        }
       }
 #pragma unroll
       for (int mt = 0; mt < 2 * D / 16; ++mt) {
         uint32_t v[4];
         ldmatrix_x4_trans(v, sV + Geo::off(mt / (D / 16), 16 * t + ((mi >> 1) << 3) + r8,
                                            2 * (mt % (D / 16)) + (mi & 1)));
-        mma_bf16_16816(st.o[mt], v, pb[0], pb[1]);
-        mma_bf16_16816(st.o[mt], v, pl[0], pl[1]);
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
+          mma_bf16_16816(st[g].o[mt], v, pb[g][0], pb[g][1]);
+          mma_bf16_16816(st[g].o[mt], v, pl[g][0], pl[g][1]);
+        }
       }
     }
   }
@@ -270,17 +287,18 @@ struct DiffPathBf16 {
 
 // One-byte codes (fp16 MMAs on exactly widened codes; kVUp as in MmaPathInt8 keeps the
 // weight times the V scale out of fp16's subnormal range).
-template <int D, int CODE, int BOX, int SUB>
+template <int D, int CODE, int BOX, int SUB, int NT>
 struct DiffPathQ8 {
   using Geo = DiffGeom<D, CODE, BOX, SUB>;
+  static constexpr int kNT = NT;  // groups of 4 query pairs: they share each widened code
   using Codec = Code8<CODE>;
   static constexpr float kVUp = CODE == CODE_E5M2 ? 32768.f : CODE == CODE_E4M3 ? 256.f : 1.f;
   static constexpr float kOutScale = 1.f / kVUp;
   static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr int kQB = D / 4, kQC = kQB / 16;  // bytes of a K row each lane reads
-  uint32_t qb[kKS][2];
-  float rs0, rs1, off0, off1;
-  DiffState<D> st;
+  uint32_t qb[NT][kKS][2];
+  float rs0[NT], rs1[NT], off0[NT], off1[NT];
+  DiffState<D> st[NT];
 
   // m-tiles 2 k and 2 k + 1 (k counts over both heads): rows gid and gid + 8 hold elements
   // 32 k + 4 gid + 0..1 and + 2..3 of the 2 D row: a lane's run k is 4 neighbours.
@@ -302,7 +320,7 @@ struct DiffPathQ8 {
   // The row is scaled by a power of two to near 2^14 (then exact in fp16 for entries above
   // 2^-28 of the largest), rs the score scale that undoes it; INT8 codes enter the score
   // MMA as code + 1152, whose 1152 * sum(q) comes off the score.
-  __device__ __forceinline__ void begin(const __nv_bfloat16* q, bool live, int lane,
+  __device__ __forceinline__ void begin(int g, const __nv_bfloat16* q, bool live, int lane,
                                         float scale_log2) {
     const int cq = lane & 3;
     const uint2* qd = reinterpret_cast<const uint2*>(q);
@@ -317,15 +335,17 @@ struct DiffPathQ8 {
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    int ex = 0;
-    if (mx > 0.f) { frexpf(mx, &ex); ex = 14 - ex; }
-    const float sc = ldexpf(1.f, ex), rs = scale_log2 * ldexpf(1.f, -ex);
+    // 2^(14 - e) for mx in [2^(e-1), 2^e), by its exponent field (at most 2^126, whose
+    // inverse is a normal number too)
+    const uint32_t field = min(267u - (__float_as_uint(mx) >> 23), 253u);
+    const float sc = __uint_as_float(field << 23);
+    const float rs = scale_log2 * __uint_as_float((254u - field) << 23);
     float t = 0.f;
 #pragma unroll
     for (int ks = 0; ks < kKS; ++ks) {
-      qb[ks][0] = pack_f16x2(f[ks][0] * sc, f[ks][1] * sc);
-      qb[ks][1] = pack_f16x2(f[ks][2] * sc, f[ks][3] * sc);
-      const float2 a = unpack_f16x2(qb[ks][0]), b = unpack_f16x2(qb[ks][1]);
+      qb[g][ks][0] = pack_f16x2(f[ks][0] * sc, f[ks][1] * sc);
+      qb[g][ks][1] = pack_f16x2(f[ks][2] * sc, f[ks][3] * sc);
+      const float2 a = unpack_f16x2(qb[g][ks][0]), b = unpack_f16x2(qb[g][ks][1]);
       t += (a.x + a.y) + (b.x + b.y);
     }
     float qs = 0.f;
@@ -335,19 +355,19 @@ struct DiffPathQ8 {
       qs = 1152.f * t;
     }
     // of this lane's columns: query rows 2 cq and 2 cq + 1
-    rs0 = __shfl_sync(0xffffffffu, rs, 8 * cq);
-    rs1 = __shfl_sync(0xffffffffu, rs, 8 * cq + 4);
-    off0 = __shfl_sync(0xffffffffu, qs, 8 * cq);
-    off1 = __shfl_sync(0xffffffffu, qs, 8 * cq + 4);
-    st.clear();
+    rs0[g] = __shfl_sync(0xffffffffu, rs, 8 * cq);
+    rs1[g] = __shfl_sync(0xffffffffu, rs, 8 * cq + 4);
+    off0[g] = __shfl_sync(0xffffffffu, qs, 8 * cq);
+    off1[g] = __shfl_sync(0xffffffffu, qs, 8 * cq + 4);
+    st[g].clear();
   }
 
-  __device__ __forceinline__ void scores(float (&x)[kT][4], uint32_t sK, uint32_t sKs,
+  __device__ __forceinline__ void scores(float (&x)[NT][kT][4], uint32_t sK, uint32_t sKs,
                                          int nvalid, int lane, float) {
     const int gid = lane >> 2, cq = lane & 3;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
-      float acc[2][4] = {};
+      float acc[NT][2][4] = {};
 #pragma unroll
       for (int hd = 0; hd < 2; ++hd) {
 #pragma unroll
@@ -373,7 +393,9 @@ struct DiffPathQ8 {
               a[2] = Codec::hi(w0[k]);
               a[3] = Codec::hi(w1[k]);
             }
-            mma_f16_16816(acc[hd], a, qb[ks][0], qb[ks][1]);
+#pragma unroll
+            for (int g = 0; g < NT; ++g)
+              mma_f16_16816(acc[g][hd], a, qb[g][ks][0], qb[g][ks][1]);
           }
         }
       }
@@ -381,31 +403,39 @@ struct DiffPathQ8 {
       for (int h = 0; h < 2; ++h) {
         const int tok = 16 * t + 8 * h + gid;
         const bool ok = tok < nvalid;
-        x[t][2 * h] = ok ? (acc[0][2 * h] - off0) * lds_f32(sKs + Geo::scale_off(0, tok)) * rs0
-                         : -INFINITY;
-        x[t][2 * h + 1] =
-            ok ? (acc[1][2 * h + 1] - off1) * lds_f32(sKs + Geo::scale_off(1, tok)) * rs1
-               : -INFINITY;
+        const float k0 = lds_f32(sKs + Geo::scale_off(0, tok));
+        const float k1 = lds_f32(sKs + Geo::scale_off(1, tok));
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
+          x[g][t][2 * h] = ok ? (acc[g][0][2 * h] - off0[g]) * k0 * rs0[g] : -INFINITY;
+          x[g][t][2 * h + 1] = ok ? (acc[g][1][2 * h + 1] - off1[g]) * k1 * rs1[g] : -INFINITY;
+        }
       }
     }
   }
 
-  __device__ __forceinline__ void values(float (&x)[kT][4], uint32_t sV, uint32_t sVs,
-                                         int nvalid, float mn0, float mn1, int lane) {
+  __device__ __forceinline__ void values(float (&x)[NT][kT][4], uint32_t sV, uint32_t sVs,
+                                         int nvalid, const float2 (&mn)[NT], int lane) {
     const int gid = lane >> 2, cq = lane & 3;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
-      uint32_t pb[2][2];  // each value head has its own scales
+      uint32_t pb[NT][2][2];  // each value head has its own scales
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float w0 = fast_exp2(x[t][2 * h] - mn0), w1 = fast_exp2(x[t][2 * h + 1] - mn1);
-        st.l0 += w0;
-        st.l1 += w1;
         const int tok = 16 * t + 8 * h + gid;
+        float vs[2];
 #pragma unroll
-        for (int hd = 0; hd < 2; ++hd) {
-          const float vs = tok < nvalid ? lds_f32(sVs + Geo::scale_off(hd, tok)) * kVUp : 0.f;
-          pb[hd][h] = transpose_8x8(pack_f16x2(w0 * vs, w1 * vs));
+        for (int hd = 0; hd < 2; ++hd)
+          vs[hd] = tok < nvalid ? lds_f32(sVs + Geo::scale_off(hd, tok)) * kVUp : 0.f;
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
+          const float w0 = fast_exp2(x[g][t][2 * h] - mn[g].x);
+          const float w1 = fast_exp2(x[g][t][2 * h + 1] - mn[g].y);
+          st[g].l0 += w0;
+          st[g].l1 += w1;
+#pragma unroll
+          for (int hd = 0; hd < 2; ++hd)
+            pb[g][hd][h] = transpose_8x8(pack_f16x2(w0 * vs[hd], w1 * vs[hd]));
         }
       }
       const int ta = 16 * t + 2 * cq;
@@ -421,8 +451,11 @@ struct DiffPathQ8 {
         const uint32_t y01 = prmt(w2, w3, 0x5140u), y23 = prmt(w2, w3, 0x7362u);
         const uint32_t a[4] = {Codec::lo(x01), Codec::hi(x01), Codec::lo(y01), Codec::hi(y01)};
         const uint32_t b[4] = {Codec::lo(x23), Codec::hi(x23), Codec::lo(y23), Codec::hi(y23)};
-        mma_f16_16816(st.o[2 * k], a, pb[hd][0], pb[hd][1]);
-        mma_f16_16816(st.o[2 * k + 1], b, pb[hd][0], pb[hd][1]);
+#pragma unroll
+        for (int g = 0; g < NT; ++g) {
+          mma_f16_16816(st[g].o[2 * k], a, pb[g][hd][0], pb[g][hd][1]);
+          mma_f16_16816(st[g].o[2 * k + 1], b, pb[g][hd][0], pb[g][hd][1]);
+        }
       }
     }
   }
@@ -460,6 +493,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
   using Geo = typename Path::Geo;
   using S = DiffSmem<Geo, kStreams, kRows, kStages>;
   constexpr int N = kStreams, kWarps = kStreams * kRows, kThreads = kWarps * 32;
+  constexpr int NT = Path::kNT;
   const int B = p.B;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -469,7 +503,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
   __shared__ int4 bound[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int stream = warp / kRows, tile = warp % kRows;  // tile: query pairs 4 tile .. + 3
+  const int stream = warp / kRows, tile = warp % kRows;
   const int gid = lane >> 2, cq = lane & 3;
   auto sK = [&](int st) { return base + stream * S::kRing + st * S::kSlot; };
   auto sV = [&](int st) { return sK(st) + Geo::kTile; };
@@ -630,14 +664,13 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
                   bar);
     }
   };
-  // Brings the producer's query rows near when its unit is a new one (the unit's first
-  // items wait for them otherwise).
+  // Brings a unit's query rows near ahead of its first item: loads queue behind the copies
+  // (3.5 us for the first unit's, asked for after the first copies).
   auto prefetch_q = [&](int s0, int u0) {
-    if (pi >= n || (pc.s == s0 && pc.u == u0)) return;
-    const int r0 = (pc.u % p.nsg) * p.gs;
+    const int r0 = (u0 % p.nsg) * p.gs;
     const int lines = min(p.gs, p.g - r0) * (D / 32);  // of 128 bytes: 2 rows of D a pair
     const char* rows = static_cast<const char*>(p.q) +
-                       (size_t(pc.s) * 2 * p.P * p.g + 2 * (pc.u / p.nsg * p.g + r0)) * (D * 2);
+                       (size_t(s0) * 2 * p.P * p.g + 2 * (u0 / p.nsg * p.g + r0)) * (D * 2);
     for (int k = lane; k < lines; k += 32)
       asm volatile("prefetch.global.L1 [%0];" ::"l"(rows + k * 128));
   };
@@ -655,6 +688,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     return true;
   };
 
+  if (warp == 0) prefetch_q(cur.s, cur.u);
   advance(stream);
 #pragma unroll
   for (int st = 0; st < kStages; ++st) {
@@ -680,10 +714,14 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     // streams with items here fold into the one that takes the first item
     const int rank = (stream - i % N + N) % N, active = min(len, N);
     if (rank < active) {
-      const int row = 4 * tile + (gid >> 1);  // this lane's query row: pair and map
-      const bool live = row < rows;
-      path.begin(q + (size_t(cur.s) * Hq + (live ? 2 * (pair0 + r0 + row) + (gid & 1) : 0)) * D,
-                 live, lane, p.scale_log2);
+#pragma unroll
+      for (int g = 0; g < NT; ++g) {
+        const int row = 4 * (tile * NT + g) + (gid >> 1);  // of this lane's query row
+        const bool live = row < rows;
+        path.begin(g, q + (size_t(cur.s) * Hq +
+                           (live ? 2 * (pair0 + r0 + row) + (gid & 1) : 0)) * D,
+                   live, lane, p.scale_log2);
+      }
       const int L = min(__ldg(p.context_lens + cur.s), p.MBS * p.BS);
       for (int k = i + rank; k < i + len && !dead; k += N) {
         const int nvalid = L - (cur.j + k - i) * Geo::kItem;
@@ -691,16 +729,20 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
           dead = true;
           break;
         }
-        float x[Path::kT][4];
+        float x[NT][Path::kT][4];
         path.scores(x, sK(st), sKs(st), nvalid, lane, p.scale_log2);
         if (released(st, 0)) request(&tmk, sK(st), sKs(st), p.k_scale, barK(st));
-        float mx0 = -INFINITY, mx1 = -INFINITY, mn0, mn1;
+        float2 mn[NT];
 #pragma unroll
-        for (int t = 0; t < Path::kT; ++t) {
-          mx0 = fmax3(mx0, x[t][0], x[t][2]);
-          mx1 = fmax3(mx1, x[t][1], x[t][3]);
+        for (int g = 0; g < NT; ++g) {
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < Path::kT; ++t) {
+            mx0 = fmax3(mx0, x[g][t][0], x[g][t][2]);
+            mx1 = fmax3(mx1, x[g][t][1], x[g][t][3]);
+          }
+          path.st[g].raise(mx0, mx1, mn[g].x, mn[g].y);
         }
-        path.st.raise(mx0, mx1, mn0, mn1);
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(barV(st), par, p.timeout_ns))) {
           dead = true;
           break;
@@ -715,32 +757,35 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
           }
           __syncwarp();
         }
-        path.values(x, sV(st), sVs(st), nvalid, mn0, mn1, lane);
+        path.values(x, sV(st), sVs(st), nvalid, mn, lane);
         if (released(st, 1)) request(&tmv, sV(st), sVs(st), p.v_scale, barV(st));
         const int s0 = pc.s, u0 = pc.u;
         advance(N);
         fetch();
-        prefetch_q(s0, u0);
+        if (pi < n && (pc.s != s0 || pc.u != u0)) prefetch_q(pc.s, pc.u);
         if (++st == kStages) {
           st = 0;
           par ^= 1u;
         }
       }
-      path.st.close();
+#pragma unroll
+      for (int g = 0; g < NT; ++g) path.st[g].close();
     }
 
     // ---- fold the streams' states into rank 0's ----
-    DiffState<D>& state = path.st;
     if constexpr (kStreams > 1) {
       uint8_t* buf = gen + S::kOffState + tile * Geo::kState;
       for (int r = 1; r < active; ++r) {
-        float2 f = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (rank == r) state.put(buf, h, lane);
-          __syncthreads();
-          if (rank == 0) state.fold(buf, h, lane, f);
-          __syncthreads();  // before the next half, or unit, is put there
+        for (int g = 0; g < NT; ++g) {
+          float2 f = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (rank == r) path.st[g].put(buf, h, lane);
+            __syncthreads();
+            if (rank == 0) path.st[g].fold(buf, h, lane, f);
+            __syncthreads();  // before the next half, or unit, is put there
+          }
         }
       }
     }
@@ -752,8 +797,11 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
       if (cur.j == 0) part[0] = whole ? -1 : 2 * int(blockIdx.x) + (first ? 0 : 1);
       if (cur.j + len == cur.n) part[1] = int(blockIdx.x);
     }
-    const int pr = 4 * tile + cq;  // this lane's query pair within the unit
-    if (rank == 0 && pr < rows) {
+#pragma unroll
+    for (int g = 0; g < NT; ++g) {
+      const int pr = 4 * (tile * NT + g) + cq;  // this lane's query pair within the unit
+      if (rank != 0 || pr >= rows) continue;
+      DiffState<D>& state = path.st[g];
       if (!whole) {
         const size_t slot = size_t(2) * blockIdx.x + (first ? 0 : 1);
         const size_t r = slot * 2 * p.gs + pr;
@@ -855,20 +903,23 @@ DiffKernelInfo make_diff_info() {
   return info;
 }
 
-// The kernel for units of up to 4 query pairs (a warp per stream) or up to 8 (two).
-template <int D, class Path, int kStages1, int kStages2>
-DiffKernelInfo diff_shape(int pairs) {
-  if (pairs <= 4) return make_diff_info<D, Path, 4, 1, kStages1, 3>();
-  return make_diff_info<D, Path, 2, 2, kStages2, 3>();
+// One-byte caches, units of up to 4 query pairs: a warp per stream; up to 8: the warp takes
+// both groups of 4, so that a code is widened once for both; up to 16: two such warps.
+template <int D, int CODE, int BOX, int SUB>
+DiffKernelInfo diff_shape_q8(int pairs) {
+  constexpr int kS = D == 128 ? 1 : 2;  // items of 16 or 8 KiB
+  if (pairs <= 4) return make_diff_info<D, DiffPathQ8<D, CODE, BOX, SUB, 1>, 4, 1, kS, 3>();
+  if (pairs <= 8) return make_diff_info<D, DiffPathQ8<D, CODE, BOX, SUB, 2>, 4, 1, kS, 2>();
+  return make_diff_info<D, DiffPathQ8<D, CODE, BOX, SUB, 2>, 2, 2, 2 * kS, 2>();
 }
 
 template <int CODE>
 bool select_diff_q8(int D, int BS, int pairs, DiffKernelInfo* info) {
   // items of 32 tokens (K and V: 16 KiB at head_dim 128); a box is a block
-  if (D == 128 && BS == 16) *info = diff_shape<128, DiffPathQ8<128, CODE, 16, 2>, 1, 2>(pairs);
-  else if (D == 128 && BS == 32) *info = diff_shape<128, DiffPathQ8<128, CODE, 32, 1>, 1, 2>(pairs);
-  else if (D == 64 && BS == 16) *info = diff_shape<64, DiffPathQ8<64, CODE, 16, 2>, 2, 4>(pairs);
-  else if (D == 64 && BS == 32) *info = diff_shape<64, DiffPathQ8<64, CODE, 32, 1>, 2, 4>(pairs);
+  if (D == 128 && BS == 16) *info = diff_shape_q8<128, CODE, 16, 2>(pairs);
+  else if (D == 128 && BS == 32) *info = diff_shape_q8<128, CODE, 32, 1>(pairs);
+  else if (D == 64 && BS == 16) *info = diff_shape_q8<64, CODE, 16, 2>(pairs);
+  else if (D == 64 && BS == 32) *info = diff_shape_q8<64, CODE, 32, 1>(pairs);
   else return false;
   return true;
 }

@@ -265,7 +265,7 @@ struct DiffParams {
   int32_t* status;
   int B, P, MBS, NB, BS;       // P: KV head pairs
   int g;                       // query pairs per KV pair
-  int gs;                      // query pairs per work unit (at most 8)
+  int gs;                      // query pairs per work unit (at most 16)
   int nsg;                     // work units per KV pair
   int D;                       // head_dim
   int unit_cost;               // what ending a unit costs a CTA, in items
@@ -279,7 +279,7 @@ struct DiffKernelInfo {
   int box;                     // tokens per TMA box
   int item;                    // tokens per work item
 };
-// pairs: query pairs per work unit (at most 8)
+// pairs: query pairs per work unit (at most 16)
 bool select_diff_bf16(int D, int BS, int pairs, DiffKernelInfo* info);
 bool select_diff_int8(int D, int BS, int pairs, DiffKernelInfo* info);
 bool select_diff_e4m3(int D, int BS, int pairs, DiffKernelInfo* info);

@@ -58,15 +58,29 @@ def test_diff_small(pk, kv, d, bs, hq, hkv, norm):
     assert torch.all(out[1] == 0)                            # the empty sequence
 
 
-@pytest.mark.parametrize("hq,hkv", [(6, 2), (10, 2), (14, 2), (16, 2), (18, 2), (26, 2), (40, 4)])
-def test_diff_group_sizes(pk, hq, hkv):
-    """Groups of 3, 5, 7, 8 query pairs in one unit; 9, 13 and 10 in two, the last one
-    partly filled."""
-    w = build("bf16", [40, 7, 129], hq, hkv, 64, 16)
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8_e5m2"])
+@pytest.mark.parametrize("hq,hkv", [(6, 2), (10, 2), (14, 2), (16, 2), (18, 2), (26, 2), (32, 2),
+                                    (34, 2), (40, 2)])
+def test_diff_group_sizes(pk, kv, hq, hkv):
+    """Groups of 3, 5, 7, 8, 9, 13 and 16 query pairs in one unit; 17 and 20 in two, the
+    second one partly filled (17: 9 and 8)."""
+    w = build(kv, [40, 7, 129], hq, hkv, 64, 16)
     lam = random_lambda(hq, DEV)
     nw = random_norm(64, DEV)
     out = call(pk, w, lam, norm_weight=nw)
     ref, bound = diff_reference(w, lam, nw, 1e-5)
+    assert_diff(out, ref, bound)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("hq", [16, 20, 32])
+def test_diff_large_groups_split(pk, kv, hq):
+    """Groups of 8, 10 and 16 query pairs over contexts cut between many CTAs, head_dim 128."""
+    w = build(kv, [1200, 31, 650], hq, 2, 128, 32)
+    lam = random_lambda(hq, DEV)
+    nw = random_norm(128, DEV)
+    out = call(pk, w, lam, norm_weight=nw, out_scale=0.3)
+    ref, bound = diff_reference(w, lam, nw, 1e-5, 0.3)
     assert_diff(out, ref, bound)
 
 
