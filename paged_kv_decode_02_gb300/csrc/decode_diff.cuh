@@ -475,13 +475,18 @@ __device__ __forceinline__ long long diff_start(long long q, unsigned r, unsigne
 
 // Shared memory of a CTA: the streams' rings, the fold's states, barriers and counters,
 // the items' prefix.
-template <class Geo, int kStreams, int kRows, int kStages>
+template <class Geo, int NT, int kStreams, int kRows, int kStages>
 struct DiffSmem {
+  // Folds go pairwise, whole states at once, where two groups of 4 query pairs per warp leave
+  // two CTAs to the SM and so the room for N / 2 states; else one after the other, a half
+  // state at a time.
+  static constexpr bool kTree = NT > 1 && kStreams > 2;
+  static constexpr int kFold = kStreams == 1 ? 0 : kTree ? kStreams / 2 * 2 * NT : 1;  // halves
   static constexpr int kSlot = 2 * Geo::kTile;                    // K and V of an item
   static constexpr int kRing = kStages * kSlot;
   static constexpr int kOffScale = kStreams * kRing;
   static constexpr int kOffState = kOffScale + kStreams * kStages * 2 * Geo::kScales;
-  static constexpr int kOffBar = kOffState + (kStreams > 1 ? kRows * Geo::kState : 0);
+  static constexpr int kOffBar = kOffState + kRows * kFold * Geo::kState;
   static constexpr int kOffCnt = kOffBar + kStreams * kStages * 16;
   static constexpr int kOffPrefix = (kOffCnt + kStreams * kStages * 8 + 15) / 16 * 16;
 };
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     paged_diff_decode_kernel(const __grid_constant__ CUtensorMap tmk,
                              const __grid_constant__ CUtensorMap tmv, const DiffParams p) {
   using Geo = typename Path::Geo;
-  using S = DiffSmem<Geo, kStreams, kRows, kStages>;
+  using S = DiffSmem<Geo, Path::kNT, kStreams, kRows, kStages>;
   constexpr int N = kStreams, kWarps = kStreams * kRows, kThreads = kWarps * 32;
   constexpr int NT = Path::kNT;
   const int B = p.B;
@@ -773,8 +778,24 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     }
 
     // ---- fold the streams' states into rank 0's ----
-    if constexpr (kStreams > 1) {
-      uint8_t* buf = gen + S::kOffState + tile * Geo::kState;
+    uint8_t* buf = gen + S::kOffState + tile * S::kFold * Geo::kState;
+    if constexpr (S::kTree) {
+#pragma unroll
+      for (int far = N / 2; far > 0; far >>= 1) {
+        if (active <= far) continue;  // (the same for all threads, like every branch round a sync)
+#pragma unroll
+        for (int g = 0; g < 2 * NT; ++g)
+          if (rank >= far && rank < min(2 * far, active))
+            path.st[g / 2].put(buf + ((rank - far) * 2 * NT + g) * Geo::kState, g % 2, lane);
+        __syncthreads();
+        float2 f = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int g = 0; g < 2 * NT; ++g)
+          if (rank + far < min(2 * far, active))
+            path.st[g / 2].fold(buf + (rank * 2 * NT + g) * Geo::kState, g % 2, lane, f);
+        __syncthreads();  // before the next states are put there
+      }
+    } else if constexpr (kStreams > 1) {
       for (int r = 1; r < active; ++r) {
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
@@ -892,7 +913,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
 
 template <int D, class Path, int kStreams, int kRows, int kStages, int kCtas>
 DiffKernelInfo make_diff_info() {
-  using S = DiffSmem<typename Path::Geo, kStreams, kRows, kStages>;
+  using S = DiffSmem<typename Path::Geo, Path::kNT, kStreams, kRows, kStages>;
   DiffKernelInfo info{};
   info.fn = reinterpret_cast<const void*>(
       &paged_diff_decode_kernel<D, Path, kStreams, kRows, kStages, kCtas>);
