@@ -47,19 +47,21 @@ struct RowEncoder {
   bool fast;
   __device__ __forceinline__ explicit RowEncoder(float s_)
       : s(s_), r(1.f / s_), fast(s_ >= 0x1p-80f && s_ <= 0x1p100f) {}
-  // codes of x[0..3], the first in the low byte
-  __device__ __forceinline__ uint32_t four(const float* x) const {
+  // codes of x[0].x, x[0].y, x[1].x, x[1].y, the first in the low byte
+  __device__ __forceinline__ uint32_t four(const float2* x) const {
     if (!fast) {
-      uint32_t u = 0u;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u |= uint32_t(Encode8<CODE>::code(x[e], s)) << (8 * e);
-      return u;
+      return uint32_t(Encode8<CODE>::code(x[0].x, s)) |
+             uint32_t(Encode8<CODE>::code(x[0].y, s)) << 8 |
+             uint32_t(Encode8<CODE>::code(x[1].x, s)) << 16 |
+             uint32_t(Encode8<CODE>::code(x[1].y, s)) << 24;
     }
     float q[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float t = x[e] * r;
-      q[e] = fmaf(fmaf(-t, s, x[e]), r, t);
+    for (int e = 0; e < 2; ++e) {
+      const float2 r2 = make_float2(r, r), t = __fmul2_rn(x[e], r2);
+      const float2 y = __ffma2_rn(__ffma2_rn(t, make_float2(-s, -s), x[e]), r2, t);
+      q[2 * e] = y.x;
+      q[2 * e + 1] = y.y;
     }
     if constexpr (CODE == CODE_I8) {  // |q| rounds to 127 at most: |x| <= 127 s (1 + 2^-24)
       const int i0 = __float2int_rn(q[0]), i1 = __float2int_rn(q[1]);

@@ -28,30 +28,31 @@ namespace {
 // Small CTAs: a CTA loads, then computes, then stores, and many small ones overlap these.
 // With kMany rows per lane group on GB300, 8192 tokens of 32/32 heads of 128 (bf16 cache):
 // 512 threads 80.5 us, 256 63.3, 128 61.5, 64 61.0; 4096 tokens of 64/8 heads, normed, INT8:
-// 38 us at 256, 34 at 64. Rows per lane group (256 threads): 1 84.9 us, 2 67.7, 4 63.3.
+// 38 us at 256, 34 at 64. Rows per lane group (256 threads): 1 84.9 us, 2 67.7, 4 63.3. The
+// arithmetic on pairs (packed fp32 products) and 10 CTAs: 59.9 and 32 us; 12 CTAs spill.
 constexpr int kRotThreads = 64;
-constexpr int kRotCtas = 12;       // per SM: 80 registers a thread
+constexpr int kRotCtas = 10;       // per SM
 constexpr int kMany = 4;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 p = unpack_bf16x2(w[e]);
-    f[2 * e] = p.x;
-    f[2 * e + 1] = p.y;
-  }
+__device__ __forceinline__ void unpack8(const uint4& u, float2* f) {
+  f[0] = unpack_bf16x2(u.x);
+  f[1] = unpack_bf16x2(u.y);
+  f[2] = unpack_bf16x2(u.z);
+  f[3] = unpack_bf16x2(u.w);
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2* f) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y),
+                    pack_bf16x2(f[2].x, f[2].y), pack_bf16x2(f[3].x, f[3].y));
 }
-__device__ __forceinline__ void load8(const float* p, float* f) {
+__device__ __forceinline__ void load8(const float* p, float2* f) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  f[0] = make_float2(a.x, a.y);
+  f[1] = make_float2(a.z, a.w);
+  f[2] = make_float2(b.x, b.y);
+  f[3] = make_float2(b.z, b.w);
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 }  // namespace
 
 // CODE: CODE_I8 / CODE_E4M3 / CODE_E5M2, or -1 for a bf16 cache.
@@ -79,11 +80,14 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
     ca = j;
     cb = j + nrot;
   }
+  const uint4* qw = static_cast<const uint4*>(p.q_norm);
+  const uint4* kw = static_cast<const uint4*>(p.k_norm);
   // the token's q, k and v rows
-  const __nv_bfloat16* rows_of[3] = {
-      static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride,
-      static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride - p.Hq * D,
-      static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride - (p.Hq + p.Hkv) * D};
+  const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride;
+  const __nv_bfloat16* krow =
+      static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride - p.Hq * D;
+  const __nv_bfloat16* vrow =
+      static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride - (p.Hq + p.Hkv) * D;
   // (a row read here may be the one written below: out may be q)
   uint4 raw[kU][2];
 #pragma unroll
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
     const int r = first + k * int(sets);
     if (r < rows) {
       const uint4* src = reinterpret_cast<const uint4*>(
-          rows_of[r < p.Hq ? 0 : r < p.Hq + p.Hkv ? 1 : 2] + r * D);
+          (r < p.Hq ? qrow : r < p.Hq + p.Hkv ? krow : vrow) + r * D);
       raw[k][0] = src[ca];
       raw[k][1] = src[cb];
     }
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
   const long long slot = p.slots[t];
   const bool bad = pos < 0 || pos >= p.P;
   if (bad && first == 0 && j == 0 && p.status) atomicOr(p.status, PKV_DEV_BAD_POSITION);
-  float c[8], s[8];
+  float2 c[4], s[4];
   if (turns && !bad) {
     const float* cs = p.cos_sin + pos * p.R + 8 * j;
     load8(cs, c);
@@ -116,37 +120,39 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
     const int r = first + k * int(sets);
     if (r >= rows) break;
     const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
-    float x[16];
+    float2 x[8];  // chunk ca, then chunk cb
     unpack8(raw[k][0], x);
-    unpack8(raw[k][1], x + 8);
-    const uint4* w = static_cast<const uint4*>(isq ? p.q_norm : p.k_norm);
+    unpack8(raw[k][1], x + 4);
+    const uint4* w = isq ? qw : kw;
     if (!isv && w != nullptr) {
-      float ss = 0.f;
+      float2 s2 = both(0.f);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int e = 0; e < 8; ++e) s2 = __ffma2_rn(x[e], x[e], s2);
+      float ss = s2.x + s2.y;
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-      const float rstd = rsqrtf(ss * (1.f / D) + p.eps);
-      float f[16];
+      const float2 rstd = both(rsqrtf(ss * (1.f / D) + p.eps));
+      float2 f[4];
       unpack8(__ldg(w + ca), f);
-      unpack8(__ldg(w + cb), f + 8);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) x[e] = x[e] * rstd * f[e];
+      for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(__fmul2_rn(x[e], rstd), f[e]);
+      unpack8(__ldg(w + cb), f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 + e] = __fmul2_rn(__fmul2_rn(x[4 + e], rstd), f[e]);
     }
     if (turns && !bad && !isv) {
       if (p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = a * c[i] - b * s[i];
-          x[2 * i + 1] = b * c[i] + a * s[i];
+          const float ci = i % 2 ? c[i / 2].y : c[i / 2].x, si = i % 2 ? s[i / 2].y : s[i / 2].x;
+          x[i] = make_float2(x[i].x * ci - x[i].y * si, x[i].y * ci + x[i].x * si);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float a = x[i], b = x[8 + i];
-          x[i] = a * c[i] - b * s[i];
-          x[8 + i] = b * c[i] + a * s[i];
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = x[i], b = x[4 + i];
+          x[i] = __ffma2_rn(a, c[i], __fmul2_rn(b, make_float2(-s[i].x, -s[i].y)));
+          x[4 + i] = __ffma2_rn(b, c[i], __fmul2_rn(a, s[i]));
         }
       }
     }
@@ -154,7 +160,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
       uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
                                             t * p.out_stride + r * D);
       dst[ca] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x);
-      dst[cb] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x + 8);
+      dst[cb] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x + 4);
       continue;
     }
     const int h = isv ? r - p.Hq - p.Hkv : r - p.Hq;
@@ -163,11 +169,11 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
       if (skip) continue;
       uint4* dst = reinterpret_cast<uint4*>(isv ? p.vc : p.kc) + drow * (D / 8);
       dst[ca] = pack8(x);
-      dst[cb] = pack8(x + 8);
+      dst[cb] = pack8(x + 4);
     } else {
       float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) amax = fmax3(amax, fabsf(x[e]), fabsf(x[e + 1]));
+      for (int e = 0; e < 8; ++e) amax = fmax3(amax, fabsf(x[e].x), fabsf(x[e].y));
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
       if (skip) continue;
@@ -176,7 +182,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
       if (sc > 0.f) {
         const RowEncoder<CODE> enc(sc);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = enc.four(x + 4 * e);
+        for (int e = 0; e < 4; ++e) u[e] = enc.four(x + 2 * e);
       }
       uint2* dst = reinterpret_cast<uint2*>(isv ? p.vc : p.kc) + drow * (D / 8);
       dst[ca] = make_uint2(u[0], u[1]);
