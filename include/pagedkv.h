@@ -304,8 +304,9 @@ pkv_status pkv_decode_diff_bf16(void* out, const void* q, const void* k_cache,
 
 /*
  * pkv_decode_diff_q8 -- pkv_decode_diff_bf16 over a one-byte cache (kv_dtype PKV_KV_INT8,
- * PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2, else PKV_ERR_DTYPE), with the arithmetic and the
- * limits on V scales of pkv_decode_int8 / pkv_decode_fp8.
+ * PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2, else PKV_ERR_DTYPE): codes widened exactly, the K
+ * scale on the fp32 score, the V scale (times 2^6, 2^8 or 2^15, undone on the output) in
+ * fp16 softmax weights, so V rows' absmax must stay below about 1e5 in every format.
  */
 pkv_status pkv_decode_diff_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale,

@@ -285,14 +285,17 @@ struct DiffPathBf16 {
   }
 };
 
-// One-byte codes (fp16 MMAs on exactly widened codes; kVUp as in MmaPathInt8 keeps the
-// weight times the V scale out of fp16's subnormal range).
+// One-byte codes (fp16 MMAs on exactly widened codes). A softmax weight times its token's V
+// scale is rounded to fp16 (2^-11 of it; the row sums are of the unrounded weights): a scale
+// is absmax over the largest code, so the product also carries kVUp, which makes it about
+// weight * absmax / 2 in every format and keeps it from fp16's subnormals for as long, and
+// from its overflow for rows with absmax below 1e5.
 template <int D, int CODE, int BOX, int SUB, int NT>
 struct DiffPathQ8 {
   using Geo = DiffGeom<D, CODE, BOX, SUB>;
   static constexpr int kNT = NT;  // groups of 4 query pairs: they share each widened code
   using Codec = Code8<CODE>;
-  static constexpr float kVUp = CODE == CODE_E5M2 ? 32768.f : CODE == CODE_E4M3 ? 256.f : 1.f;
+  static constexpr float kVUp = CODE == CODE_E5M2 ? 32768.f : CODE == CODE_E4M3 ? 256.f : 64.f;
   static constexpr float kOutScale = 1.f / kVUp;
   static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr int kQB = D / 4, kQC = kQB / 16;  // bytes of a K row each lane reads

@@ -50,7 +50,7 @@ def diff_reference(w, lam, norm_weight=None, eps=0.0, out_scale=1.0):
     q = to_f64(w.q)
     lam = to_f64(lam)
     nw = None if norm_weight is None else to_f64(norm_weight)
-    up = {"bf16": 1.0, "int8": 1.0, "fp8_e4m3": 256.0, "fp8_e5m2": 32768.0}[w.kv_dtype]
+    up = {"bf16": 1.0, "int8": 64.0, "fp8_e4m3": 256.0, "fp8_e5m2": 32768.0}[w.kv_dtype]
     out = np.zeros((B, Hq // 2, 2 * D))
     bound = np.zeros_like(out)
     g = w.group

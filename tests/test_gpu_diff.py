@@ -106,6 +106,61 @@ def test_diff_many_units_per_cta(pk):
     assert_diff(out, ref, bound)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_diff_large_batches_and_empty_ones(pk, kv):
+    """More sequences than threads of a CTA, many of them empty; a batch without any token; a
+    table of one block."""
+    lengths = [(5 * i) % 4 for i in range(1500)]
+    w = build(kv, lengths, 4, 2, 64, 16)
+    lam = random_lambda(4, DEV)
+    out = call(pk, w, lam, out_scale=2.0)
+    ref, bound = diff_reference(w, lam, out_scale=2.0)
+    assert_diff(out, ref, bound)
+    w.context_lens.zero_()
+    assert torch.all(call(pk, w, lam, out=torch.ones_like(out)) == 0)
+    one = build(kv, [16, 3], 4, 2, 128, 32)
+    assert one.block_tables.shape[1] == 1
+    out = call(pk, one, lam)
+    ref, bound = diff_reference(one, lam)
+    assert_diff(out, ref, bound)
+
+
+@pytest.mark.parametrize("kv", ["int8", "fp8_e4m3", "fp8_e5m2"])
+def test_diff_small_and_large_values(pk, kv):
+    """V rows of absmax 1e-3 and of 3e4 (fp16 weights times V scales neither vanish nor
+    overflow), q and K rows far from 1."""
+    for vmul, qmul in ((1e-3 / 3, 2.0 ** 20), (1e4, 2.0 ** -20)):
+        w = build(kv, [70, 33], 8, 4, 128, 16)
+        w.v_scale *= vmul
+        w.q = (w.q.float() * qmul).to(torch.bfloat16)
+        w.k_scale /= qmul
+        lam = random_lambda(8, DEV)
+        out = call(pk, w, lam)
+        ref, bound = diff_reference(w, lam)
+        assert_diff(out, ref, bound)
+
+
+def test_diff_float8_tensors_are_their_bytes(pk):
+    for kv, dt in (("fp8_e4m3", torch.float8_e4m3fn), ("fp8_e5m2", torch.float8_e5m2)):
+        w = build(kv, [70, 33], 8, 4, 64, 16)
+        lam = random_lambda(8, DEV)
+        want = call(pk, w, lam)
+        w.k_cache, w.v_cache = w.k_cache.view(dt), w.v_cache.view(dt)
+        assert torch.equal(call(pk, w, lam), want)
+
+
+def test_diff_first_call_of_a_shape_inside_a_capture(pk):
+    w = build("bf16", [300, 11], 12, 6, 64, 32)              # a shape no other test plans
+    lam = random_lambda(12, DEV)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call(pk, w, lam)
+    out.fill_(1.0)
+    g.replay()
+    assert torch.equal(out, call(pk, w, lam))
+
+
 def test_diff_growing_and_huge_scores(pk):
     """Scores that grow from tile to tile rescale every state; rows of one head far above the
     other's keep apart."""

@@ -120,6 +120,37 @@ def test_rotate_sizes_and_strides(pk, T, hq, hkv, d, bs):
     assert torch.equal(parts[1], k) and torch.equal(parts[2], v)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e5m2"])
+@pytest.mark.parametrize("T,hq,hkv,d", [(5300, 5, 5, 128), (13003, 9, 3, 64), (8200, 6, 2, 128)])
+def test_rotate_many_tokens(pk, fmt, T, hq, hkv, d):
+    """Thousands of tokens, whose lane groups take several rows each (15, 15 and 10 rows per
+    token, none a multiple of 4): the same bits as in calls of 500 tokens, and sampled rows
+    against the oracle."""
+    bs = 16
+    q, k, v, pos, slots, qw, kw, nb = inputs(T, hq, hkv, d, bs, seed=T)
+    slots[::97] = -1
+    cs = table(500, d // 2)
+    dt = {"bf16": torch.bfloat16, "int8": torch.int8}.get(fmt, torch.uint8)
+
+    def go(cuts):
+        c = [torch.zeros((nb, hkv, bs, d), dtype=dt, device=DEV) for _ in range(2)]
+        s = [torch.zeros((nb, hkv, bs), device=DEV) for _ in range(2)]
+        outs = []
+        for a, b in zip(cuts, cuts[1:]):
+            args = (q[a:b], k[a:b], v[a:b], pos[a:b], cs, *c)
+            if fmt == "bf16":
+                outs.append(pk.paged_kv_rotate_append(*args, slots[a:b], q_norm=qw, k_norm=kw))
+            else:
+                outs.append(pk.paged_kv_rotate_append_q8(*args, *s, slots[a:b], fmt=fmt,
+                                                         q_norm=qw, k_norm=kw))
+        return [torch.cat(outs), *c, *s]
+    whole = go([0, T])
+    for x, y in zip(whole, go([*range(0, T, 500), T])):
+        assert torch.equal(x, y)
+    some = torch.randperm(T, device=DEV)[:40]
+    assert_bf16(whole[0][some], *reference(q[some], qw, pos[some], cs, 1e-6, False))
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3", "e5m2"])
 @pytest.mark.parametrize("d,bs,interleaved", [(128, 16, False), (64, 32, True)])
 def test_rotate_q8(pk, fmt, d, bs, interleaved):
@@ -194,6 +225,33 @@ def test_position_zero_is_append(pk, fmt):
     assert torch.equal(out, q)
     assert torch.equal(a[0], a[2]) and torch.equal(a[1], a[3])
     assert torch.equal(s[0], s[2]) and torch.equal(s[1], s[3])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "e5m2"])
+def test_quantised_rows_of_every_magnitude(pk, fmt):
+    """V rows from 1e-38 (scales that are subnormal or 0) to 3e38, zeros, infinities and NaN
+    among the elements: the codes and scales that append writes, bit for bit."""
+    T, hkv, d, bs = 600, 2, 128, 16
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    mag = torch.logspace(-38, 38, T, device=DEV)
+    v = (torch.randn((T, hkv, d), generator=gen, device=DEV) * mag[:, None, None])
+    v *= 10.0 ** (-8 * torch.rand((T, hkv, d), generator=gen, device=DEV))
+    v = v.to(torch.bfloat16)
+    v[7, 0, 5], v[8, 1, 3], v[9, 0, 0] = float("nan"), float("inf"), -float("inf")
+    v[10] = 0
+    nb = T // bs + 1
+    slots = torch.randperm(nb * bs, generator=gen, device=DEV)[:T]
+    dt = torch.int8 if fmt == "int8" else torch.uint8
+    a = [torch.zeros((nb, hkv, bs, d), dtype=dt, device=DEV) for _ in range(4)]
+    s = [torch.zeros((nb, hkv, bs), device=DEV) for _ in range(4)]
+    pk.paged_kv_rotate_append_q8(v, v, v, torch.zeros_like(slots), table(1, d), a[0], a[1], s[0],
+                                 s[1], slots, fmt=fmt)
+    if fmt == "int8":
+        pk.paged_kv_append_int8(v, v, a[2], a[3], s[2], s[3], slots)
+    else:
+        pk.paged_kv_append_fp8(v, v, a[2], a[3], s[2], s[3], slots, fmt=fmt)
+    assert torch.equal(s[1].view(torch.int32), s[3].view(torch.int32))
+    assert torch.equal(a[1], a[3])
 
 
 def test_bad_positions_write_nothing(pk):
