@@ -81,6 +81,15 @@ struct DiffGeom {
   static constexpr int kState = (D / 16 + 1) * 512;
   static_assert(kBoxBytes % 1024 == 0, "boxes must keep 1024-byte alignment");
 
+  // The swizzle repeats every 8 rows, so the offset of a chunk is that of its row's place in
+  // 8 (a lane's own, in a register) plus a constant for the rest.
+  __device__ static __forceinline__ uint32_t lane_off(int row, int ci) {
+    return swz<kSeg>(uint32_t(row * kSeg + ci * 16));
+  }
+  // t: a multiple of 8
+  __device__ static constexpr uint32_t rest_off(int hd, int t, int half) {
+    return uint32_t((t / BOX) * kBoxBytes + ((half * 2 + hd) * BOX + t % BOX) * kSeg);
+  }
   // Swizzled byte offset of 16-byte chunk cc of token t (of the item) of pair head hd.
   __device__ static __forceinline__ uint32_t off(int hd, int t, int cc) {
     const int b = t / BOX, tb = t % BOX;
@@ -190,8 +199,19 @@ struct DiffPathBf16 {
   static constexpr int kNT = NT;  // groups of 4 query pairs of the warp
   static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr float kOutScale = 1.f;
+  static constexpr int kPer = Geo::kChunksPerSeg / 2;  // 32-byte steps of a row segment
   uint32_t qb[NT][kKS][2];
+  uint32_t ko[kPer], vo[kPer];  // the lane's places in K and V tiles
   DiffState<D> st[NT];
+
+  __device__ __forceinline__ void init(int lane) {
+    const int r8 = lane & 7, mi = lane >> 3;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      ko[i] = Geo::lane_off(r8, 2 * i + (mi >> 1)) + (mi & 1) * 8 * Geo::kSeg;
+      vo[i] = Geo::lane_off(r8, 2 * i + (mi & 1)) + (mi >> 1) * 8 * Geo::kSeg;
+    }
+  }
 
   // A lane's columns of a 2 D row: kRun neighbouring ones from column(k, gid), in
   // o[at(k, e)][half(k, e) * 2 + map].
@@ -222,16 +242,15 @@ struct DiffPathBf16 {
   // log2 units; tokens from nvalid on are -inf.
   __device__ __forceinline__ void scores(float (&x)[NT][kT][4], uint32_t sK, uint32_t,
                                          int nvalid, int lane, float scale_log2) {
-    const int r8 = lane & 7, mi = lane >> 3, gid = lane >> 2;
+    const int gid = lane >> 2;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       float a[NT][4] = {}, b[NT][4] = {};
 #pragma unroll
       for (int ks = 0; ks < kKS; ++ks) {
         uint32_t k0[4], k1[4];
-        const int row = 16 * t + ((mi & 1) << 3) + r8, cc = 2 * ks + (mi >> 1);
-        ldmatrix_x4(k0, sK + Geo::off(0, row, cc));
-        ldmatrix_x4(k1, sK + Geo::off(1, row, cc));
+        ldmatrix_x4(k0, sK + ko[ks % kPer] + Geo::rest_off(0, 16 * t, ks / kPer));
+        ldmatrix_x4(k1, sK + ko[ks % kPer] + Geo::rest_off(1, 16 * t, ks / kPer));
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
           mma_bf16_16816(a[g], k0, qb[g][ks][0], qb[g][ks][1]);
@@ -251,8 +270,7 @@ struct DiffPathBf16 {
 
   // mn: what the scores of each map of each group subtract.
   __device__ __forceinline__ void values(float (&x)[NT][kT][4], uint32_t sV, uint32_t, int,
-                                         const float2 (&mn)[NT], int lane) {
-    const int r8 = lane & 7, mi = lane >> 3;
+                                         const float2 (&mn)[NT], int) {
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       uint32_t pb[NT][2], pl[NT][2];
@@ -273,8 +291,9 @@ struct DiffPathBf16 {
 #pragma unroll
       for (int mt = 0; mt < 2 * D / 16; ++mt) {
         uint32_t v[4];
-        ldmatrix_x4_trans(v, sV + Geo::off(mt / (D / 16), 16 * t + ((mi >> 1) << 3) + r8,
-                                           2 * (mt % (D / 16)) + (mi & 1)));
+        constexpr int kMt = D / 16;  // m-tiles of a head
+        ldmatrix_x4_trans(v, sV + vo[mt % kPer] +
+                                 Geo::rest_off(mt / kMt, 16 * t, mt % kMt / kPer));
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
           mma_bf16_16816(st[g].o[mt], v, pb[g][0], pb[g][1]);
@@ -299,9 +318,24 @@ struct DiffPathQ8 {
   static constexpr float kOutScale = 1.f / kVUp;
   static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr int kQB = D / 4, kQC = kQB / 16;  // bytes of a K row each lane reads
+  static constexpr int kVK = D / 32;  // 32-column steps of a head's V row
   uint32_t qb[NT][kKS][2];
+  uint32_t ko[kQC], vo[kVK];  // the lane's places in K and V tiles
   float rs0[NT], rs1[NT], off0[NT], off1[NT];
   DiffState<D> st[NT];
+
+  __device__ __forceinline__ void init(int lane) {
+    const int gid = lane >> 2, cq = lane & 3;
+#pragma unroll
+    for (int i = 0; i < kQC; ++i) ko[i] = Geo::lane_off(gid, kQC * cq + i);
+#pragma unroll
+    for (int i = 0; i < kVK; ++i)
+      vo[i] = Geo::lane_off(2 * cq, 2 * i + (gid >> 2)) + 4 * (gid & 3);
+  }
+  // the same place one row on (from an even row)
+  __device__ static __forceinline__ uint32_t next_row(uint32_t at) {
+    return Geo::kSeg == 128 ? (at ^ 16u) + 128u : at + 64u;
+  }
 
   // m-tiles 2 k and 2 k + 1 (k counts over both heads): rows gid and gid + 8 hold elements
   // 32 k + 4 gid + 0..1 and + 2..3 of the 2 D row: a lane's run k is 4 neighbours.
@@ -367,7 +401,7 @@ struct DiffPathQ8 {
 
   __device__ __forceinline__ void scores(float (&x)[NT][kT][4], uint32_t sK, uint32_t sKs,
                                          int nvalid, int lane, float) {
-    const int gid = lane >> 2, cq = lane & 3;
+    const int gid = lane >> 2;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       float acc[NT][2][4] = {};
@@ -375,8 +409,8 @@ struct DiffPathQ8 {
       for (int hd = 0; hd < 2; ++hd) {
 #pragma unroll
         for (int ch = 0; ch < kQC; ++ch) {
-          const uint4 r0 = lds128(sK + Geo::off(hd, 16 * t + gid, kQC * cq + ch));
-          const uint4 r1 = lds128(sK + Geo::off(hd, 16 * t + 8 + gid, kQC * cq + ch));
+          const uint4 r0 = lds128(sK + ko[ch] + Geo::rest_off(hd, 16 * t, 0));
+          const uint4 r1 = lds128(sK + ko[ch] + Geo::rest_off(hd, 16 * t + 8, 0));
           const uint32_t w0[4] = {Codec::pre(r0.x), Codec::pre(r0.y), Codec::pre(r0.z),
                                   Codec::pre(r0.w)};
           const uint32_t w1[4] = {Codec::pre(r1.x), Codec::pre(r1.y), Codec::pre(r1.z),
@@ -419,7 +453,7 @@ struct DiffPathQ8 {
 
   __device__ __forceinline__ void values(float (&x)[NT][kT][4], uint32_t sV, uint32_t sVs,
                                          int nvalid, const float2 (&mn)[NT], int lane) {
-    const int gid = lane >> 2, cq = lane & 3;
+    const int gid = lane >> 2;
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       uint32_t pb[NT][2][2];  // each value head has its own scales
@@ -441,15 +475,14 @@ struct DiffPathQ8 {
             pb[g][hd][h] = transpose_8x8(pack_f16x2(w0 * vs[hd], w1 * vs[hd]));
         }
       }
-      const int ta = 16 * t + 2 * cq;
 #pragma unroll
-      for (int k = 0; k < 2 * D / 32; ++k) {
-        const int hd = k / (D / 32);
-        const int bo = 32 * (k % (D / 32)) + 4 * gid, ch = bo >> 4, wi = bo & 15;
-        const uint32_t w0 = Codec::pre(lds32(sV + Geo::off(hd, ta, ch) + wi));
-        const uint32_t w1 = Codec::pre(lds32(sV + Geo::off(hd, ta + 1, ch) + wi));
-        const uint32_t w2 = Codec::pre(lds32(sV + Geo::off(hd, ta + 8, ch) + wi));
-        const uint32_t w3 = Codec::pre(lds32(sV + Geo::off(hd, ta + 9, ch) + wi));
+      for (int k = 0; k < 2 * kVK; ++k) {
+        const int hd = k / kVK;  // tokens 16 t + 2 cq, the next, and both 8 on
+        const uint32_t at = sV + vo[k % kVK], at1 = next_row(at);
+        const uint32_t w0 = Codec::pre(lds32(at + Geo::rest_off(hd, 16 * t, 0)));
+        const uint32_t w1 = Codec::pre(lds32(at1 + Geo::rest_off(hd, 16 * t, 0)));
+        const uint32_t w2 = Codec::pre(lds32(at + Geo::rest_off(hd, 16 * t + 8, 0)));
+        const uint32_t w3 = Codec::pre(lds32(at1 + Geo::rest_off(hd, 16 * t + 8, 0)));
         const uint32_t x01 = prmt(w0, w1, 0x5140u), x23 = prmt(w0, w1, 0x7362u);
         const uint32_t y01 = prmt(w2, w3, 0x5140u), y23 = prmt(w2, w3, 0x7362u);
         const uint32_t a[4] = {Codec::lo(x01), Codec::hi(x01), Codec::lo(y01), Codec::hi(y01)};
@@ -712,6 +745,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
   const int Hq = 2 * p.P * p.g;
   Path path;
+  path.init(lane);
   int st = 0;
   uint32_t par = 0;
   bool dead = false, first = true;
