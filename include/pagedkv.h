@@ -152,13 +152,14 @@ typedef struct pkv_rotary {
  *   (y_a, y_b) := (y_a cos_i - y_b sin_i, y_b cos_i + y_a sin_i), i < rotary_dim / 2,
  * with a, b the pair's elements and cos_i, sin_i row n of the table. q rows leave in q_out
  * (bf16); k rows go to their slot (bf16, one rounding); v rows are copied there unchanged.
- *   q, q_out      [num_tokens, Hq, D] bf16; q_out may be q (same stride), else must not
- *                 overlap an input.
+ *   q, q_out      [num_tokens, Hq, D] bf16; q_out may be q (same stride, else
+ *                 PKV_ERR_SHAPE); otherwise it must not overlap an input.
  *   k, v          [num_tokens, Hkv, D] bf16.
  *   positions     [num_tokens] int64. A position outside [0, num_positions) gives a zero
  *                 q row and writes no K or V; it is flagged PKV_DEV_BAD_POSITION in the
  *                 optional device int32 *status.
- *   slot_mapping  as for pkv_append_bf16 (a skipped token's q row is still written).
+ *   slot_mapping  as for pkv_append_bf16 (a skipped token's q row is still written). Two
+ *                 tokens of one call must not share a slot (its rows would mix).
  * num_tokens == 0 is a no-op returning PKV_OK.
  */
 pkv_status pkv_rotate_append_bf16(void* q_out, const void* q, const void* k, const void* v,
@@ -292,6 +293,8 @@ pkv_status pkv_decode_fp8(void* out, const void* q, const uint8_t* k_cache,
  *   norm_weight   [2 D] bf16, device; NULL: no norm (eps is then not used).
  *   workspace     at least pkv_decode_diff_workspace_bytes() bytes; otherwise as for
  *                 pkv_decode_bf16, like status, empty sequences and unused table entries.
+ * A map whose scores hold a NaN, or none above -inf, gives NaN. num_seqs times
+ * max_blocks_per_seq * block_size / 16 must stay below 2^31 (else PKV_ERR_UNSUPPORTED).
  */
 pkv_status pkv_decode_diff_workspace_bytes(const pkv_dims* dims, pkv_kv_dtype kv_dtype,
                                            size_t* bytes);

@@ -674,6 +674,7 @@ pkv_status run_rotate(int kvt, void* out, const void* q, const void* k, const vo
       !aligned16(ro->cos_sin) || !aligned16(k_cache) || !aligned16(v_cache) ||
       (ro->q_norm && !aligned16(ro->q_norm)) || (ro->k_norm && !aligned16(ro->k_norm)))
     return PKV_ERR_ALIGNMENT;
+  if (out == q && T > 1 && ro->out_stride != ro->q_stride) return PKV_ERR_SHAPE;
   RotateParams p{};
   p.out = out;
   p.q = q;
@@ -720,6 +721,11 @@ pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
   if (st != PKV_OK) return st;
   if (d->num_q_heads % 2 != 0 || d->num_kv_heads % 2 != 0) return PKV_ERR_SHAPE;
   if ((long long)d->num_seqs * d->num_q_heads >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
+  // the kernel counts items (of 16 or 32 tokens) and their weights in 32 bits
+  if ((long long)d->num_seqs *
+          ((long long)d->max_blocks_per_seq * (d->block_size / 16) + kDiffUnitCost) >=
+      (1ll << 31))
+    return PKV_ERR_UNSUPPORTED;
   if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
   struct Key {
     pkv_dims d;

@@ -896,8 +896,10 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         }
         if (gid == 0) {
           float2* ml = reinterpret_cast<float2*>(p.part_ml);
-          ml[r] = make_float2(state.m0, state.l0);
-          ml[r + p.gs] = make_float2(state.m1, state.l1);
+          // NaN scores alone leave m at -inf, which the merge takes for no token: m = 0
+          // keeps such a record in
+          ml[r] = make_float2(isnan(state.l0) ? 0.f : state.m0, state.l0);
+          ml[r + p.gs] = make_float2(isnan(state.l1) ? 0.f : state.m1, state.l1);
         }
       } else {
         const int qp = pair0 + r0 + pr;

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D
   if (p.status != nullptr) {
     int flags = 0;
     if (L < 0 || L > p.MBS * p.BS) flags = PKV_DEV_BAD_CONTEXT_LEN;
-    const int nblk = L <= 0 ? 0 : min((L + p.BS - 1) / p.BS, p.MBS);
+    const int nblk = L <= 0 ? 0 : (min(L, p.MBS * p.BS) - 1) / p.BS + 1;
     for (int j = lane; j < nblk; j += 32) {  // every warp for itself
       const int id = p.block_tables[size_t(s) * p.MBS + j];
       if (id < 0 || id >= p.NB) flags |= PKV_DEV_BAD_BLOCK_ID;
@@ -87,7 +87,8 @@ __global__ void __launch_bounds__(kGroups == 1 ? kDiffMergeThreads : kGroups * D
     }
     __syncthreads();
   }
-  const float inv = f.l > 0.f ? 1.f / f.l : 0.f;
+  // (a map without a score above -inf is 0 / 0, NaN, like a unit that is not cut)
+  const float inv = 1.f / f.l;
   float4 v = make_float4(f.o.x * inv, f.o.y * inv, f.o.z * inv, f.o.w * inv);
   if (map == 1 && group == 0) s_o[set][quad] = v;
   __syncthreads();

@@ -60,6 +60,8 @@ def test_rotate_refusals(lib):
     assert _rotate(lib, _rotary(), T=-1) == Status.ERR_SHAPE
     assert _rotate(lib, _rotary(), T=0) == Status.OK
     assert _rotate(lib, _rotary(), dims=Dims(4, 8, 4, 96, 16, 64, 4)) == Status.ERR_UNSUPPORTED
+    # in place, the rows of q and q_out have to be the same
+    assert _rotate(lib, _rotary(out_stride=512, q_stride=1024)) == Status.ERR_SHAPE
     good = _good()
     ro = _rotary()
     for kv in (0, 9):
@@ -110,6 +112,8 @@ def test_diff_refusals(lib):
         assert lib.pkv_decode_diff_workspace_bytes(ctypes.byref(dims), 0, ctypes.byref(n)) == \
             Status.ERR_SHAPE
     assert diff(Dims(0, 8, 4, 64, 16, 64, 4)) == Status.OK   # no sequences
+    huge = Dims(17, 8, 4, 64, 16, 64, (1 << 27) - 1)         # more items than 32 bits count
+    assert diff(huge) == Status.ERR_UNSUPPORTED
     good = _good()
     assert lib.pkv_decode_diff_workspace_bytes(ctypes.byref(good), 0, None) == Status.ERR_NULL
     assert lib.pkv_decode_diff_workspace_bytes(ctypes.byref(good), 4, ctypes.byref(n)) == \

@@ -178,6 +178,64 @@ def test_diff_growing_and_huge_scores(pk):
     assert_diff(out, ref, bound)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8_e4m3", "fp8_e5m2"])
+def test_diff_nan_stays_in_its_rows(pk, kv):
+    """A NaN in a query row, or in a cached K row, makes the pairs that read it NaN, in units
+    of one CTA and in cut ones, and no other pair."""
+    w = build(kv, [7, 40, 6000], 8, 4, 128, 16)
+    lam = torch.linspace(0.2, 0.8, 4, device=DEV)
+    clean = call(pk, w, lam)
+    assert torch.isfinite(clean).all()
+    q = w.q.clone()
+    w.q[:, 3, 5] = float("nan")              # second map of query pair 1
+    out = call(pk, w, lam)
+    assert torch.isnan(out[:, 1]).all()
+    assert torch.equal(out[:, [0, 2, 3]], clean[:, [0, 2, 3]])
+    w.q.copy_(q)
+    if kv != "bf16":
+        w.k_scale[w.block_tables[:, 0].long(), 3, 2] = float("nan")  # KV pair 1: pairs 2, 3
+    else:
+        w.k_cache[w.block_tables[:, 0].long(), 3, 2, 9] = float("nan")
+    out = call(pk, w, lam)
+    assert torch.isnan(out[:, 2:]).all()
+    assert torch.equal(out[:, :2], clean[:, :2])
+
+
+def test_diff_scores_of_minus_infinity(pk):
+    """Tokens whose score is -inf have no weight; a map that has no other gives NaN."""
+    lengths = [40, 300, 6000]
+    w = build("bf16", lengths, 8, 4, 128, 16)
+    w.q[:, :, 0] = 1.0
+    for s, L in enumerate(lengths):
+        gone = torch.cat([torch.arange(0, 37), torch.arange(38, L, 3)]).to(DEV)
+        w.k_cache[w.block_tables[s, gone // 16].long(), :, gone % 16, 0] = float("-inf")
+    lam = random_lambda(8, DEV)
+    ref, bound = diff_reference(w, lam)
+    assert_diff(call(pk, w, lam), ref, bound)
+    w.k_cache[..., 0] = float("-inf")
+    assert torch.isnan(call(pk, w, lam)).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_diff_far_blocks(pk, kv):
+    """Blocks more than 2^32 bytes into the cache give what the same rows give near its
+    start."""
+    w = build(kv, [100, 3000], 16, 8, 128, 16)
+    lam = random_lambda(16, DEV)
+    near = call(pk, w, lam)
+    n, block_bytes = w.k_cache.shape[0], w.k_cache[0].numel() * w.k_cache.element_size()
+    far = 2 ** 32 // block_bytes + 5
+    for name in ("k_cache", "v_cache", "k_scale", "v_scale"):
+        old = getattr(w, name)
+        if old is None:
+            continue
+        new = torch.zeros((far + n,) + tuple(old.shape[1:]), dtype=old.dtype, device=DEV)
+        new[far:] = old
+        setattr(w, name, new)
+    w.block_tables += far
+    assert torch.equal(call(pk, w, lam), near)
+
+
 def test_diff_lambda_zero_is_plain_decode(pk):
     """lambda 0: the first map alone, as the plain decode of the even heads over each value
     head gives it (both within their rounding: two halves of a bf16 step)."""

@@ -171,6 +171,35 @@ def test_gather_argument_checks(pk):
 # the operators together: a prompt, decode steps, and the cache read back
 # ---------------------------------------------------------------------------
 
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_rows_far_into_a_cache(pk, kv):
+    """Written to and read from blocks on both sides of 2^32 bytes into the cache: as near its
+    start."""
+    hkv, d, bs, T = 8, 128, 16, 50
+    block_bytes = hkv * bs * d * (2 if kv == "bf16" else 1)
+    far = 2 ** 32 // block_bytes - 2
+    nb = far + 4
+    dt = torch.bfloat16 if kv == "bf16" else torch.int8
+    caches = [torch.zeros((nb, hkv, bs, d), dtype=dt, device=DEV) for _ in range(2)]
+    scales = [torch.zeros((nb, hkv, bs), device=DEV) for _ in range(2 * (kv != "bf16"))]
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    q, k, v = (torch.randn((T, hkv, d), generator=gen, device=DEV).to(torch.bfloat16)
+               for _ in range(3))
+    cs = torch.cat([torch.cos(torch.arange(T * 64.0, device=DEV)).view(T, 64),
+                    torch.sin(torch.arange(T * 64.0, device=DEV)).view(T, 64)], 1)
+    pos = torch.arange(T, device=DEV)
+    write = pk.paged_kv_rotate_append if kv == "bf16" else pk.paged_kv_rotate_append_q8
+    got = []
+    for first in (0, far):
+        slots = first * bs + pos
+        write(q, k, v, pos, cs, *caches, *scales, slots)
+        tab = first + torch.arange(4, dtype=torch.int32, device=DEV)[None]
+        got += pk.paged_kv_gather(*caches, tab, offsets_of([T]), T,
+                                  **(dict(k_scale=scales[0], v_scale=scales[1]) if scales else {}))
+    assert torch.equal(got[0], got[2]) and torch.equal(got[1], got[3])
+    assert got[0].abs().amax() > 1 and (kv != "bf16" or torch.equal(got[1], v))
+
+
 @pytest.mark.parametrize("kv", ["bf16", "int8", "fp8_e4m3", "fp8_e5m2"])
 def test_prompt_steps_and_read_back(pk, kv):
     """Prompts written in one call, three decode steps (rotate, append, differential
