@@ -34,6 +34,10 @@ constexpr int kTcHeadCost = 2;
 // (64 / 8 heads, head_dim 128, bf16): cost 0 92.3 us, 1 92.1, 2 89.8, 3 88.1, 4 87.3, 6
 // 86.8; INT8, 128 x 8192: 353 us at 0 to 4, 354 at 6
 constexpr int kDiffUnitCost = 4;
+// and the least length of a CTA's range, in items: shorter ones leave more records to merge
+// than they save. One sequence (2 / 2 heads, bf16), at 1, 2, 3, 4: 300 tokens 7.9, 8.0, 8.3,
+// 8.6 us, 8192 tokens 11.7, 10.0, 10.0, 9.7; 3 of ~700 (32 / 8, E4M3): 11.8, 10.8, 10.6, 11.2
+constexpr int kDiffMinRange = 2;
 // cascade decode: the prefix kernel runs on about 1/kCascadePrefixShare of the SMs
 constexpr int kCascadePrefixShare = 3;
 
@@ -841,6 +845,7 @@ pkv_status run_diff(int kvt, void* out, const void* q, const void* k_cache, cons
   p.nsg = P.nsg;
   p.D = d->head_dim;
   p.unit_cost = kDiffUnitCost;
+  p.min_range = kDiffMinRange;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.eps = eps;
   p.out_scale = out_scale;

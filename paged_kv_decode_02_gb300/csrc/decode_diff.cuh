@@ -591,8 +591,10 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   auto weight_of = [&](int m) { return m > 0 ? m + p.unit_cost : 0; };
   int2 run = make_int2(0, 0);  // items and weight before sequence b0
+  bool all_short = true;       // no unit has more items than the CTA has streams
   for (int i = b0; i < b1; ++i) {
     const int m = diff_items(p, i, Geo::kItem);
+    all_short &= m <= N;
     run.x += m;
     run.y += weight_of(m);
   }
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     if (lane == 31) warp_tot[warp] = incl;
     run = make_int2(incl.x - run.x, incl.y - run.y);
   }
-  __syncthreads();
+  all_short = __syncthreads_and(all_short);
   int2 total = make_int2(0, 0);
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     total.y += warp_tot[w].y;
   }
   const long long T = (long long)U * total.y;
-  const int G = int(min((long long)gridDim.x, T));
+  const int G = int(min((long long)gridDim.x, (T + p.min_range - 1) / p.min_range));
   if (int(blockIdx.x) >= G) return;
   const long long q0 = T < (1ll << 32) ? (long long)(unsigned(T) / unsigned(G)) : T / G;
   const unsigned rest = unsigned(T - q0 * G);
@@ -650,6 +652,9 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     c.n = f.w;
     c.u = rem < (1ll << 32) ? int(unsigned(rem) / unsigned(w)) : int(rem / w);
     c.j = min(c.n, int(rem - (long long)c.u * w));
+    // where the streams take every unit at once, none is cut: its first item decides (4
+    // sequences of ~30 tokens, head_dim 64: 8.2 -> 6.7 us; 200 of ~20: 8.8 -> 7.6)
+    if (c.j > 0 && all_short) c.j = c.n;
     const long long before = (long long)U * f.y + (long long)c.u * c.n + c.j;
     if (c.j == c.n) {  // among a unit's empty positions: the next unit
       c.j = 0;

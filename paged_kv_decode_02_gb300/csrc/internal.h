@@ -269,6 +269,7 @@ struct DiffParams {
   int nsg;                     // work units per KV pair
   int D;                       // head_dim
   int unit_cost;               // what ending a unit costs a CTA, in items
+  int min_range;               // positions of a CTA's range at least
   float scale_log2;            // softmax scale * log2(e)
   float eps, out_scale;
   unsigned long long timeout_ns;

@@ -96,6 +96,38 @@ def test_diff_long_and_split(pk, kv):
         assert_diff(out, ref, bound)
 
 
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("int8", 128), ("fp8_e5m2", 64)])
+@pytest.mark.parametrize("lengths,hq,hkv", [([9000], 2, 2), ([5000], 34, 2), ([7000, 0, 40], 64, 2),
+                                            ([2500, 1, 0, 1700, 33], 28, 4),
+                                            ([900, 1100, 0, 1000] * 6, 28, 4)])
+def test_diff_few_pairs_many_records(pk, kv, d, lengths, hq, hkv):
+    """One unit cut over most of the GPU; 32 and up to 384 query pairs, empty sequences among
+    them: with and without a norm, with a status word, on a workspace of NaN, twice the same."""
+    w = build(kv, lengths, hq, hkv, d, 16)
+    lam, nw = random_lambda(hq, DEV), random_norm(d, DEV)
+    ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for more in (dict(), dict(norm_weight=nw, eps=1e-5, out_scale=0.7)):
+        out = call(pk, w, lam, workspace=ws, status=status, **more)
+        ref, bound = diff_reference(w, lam, more.get("norm_weight"), more.get("eps", 0.0),
+                                    more.get("out_scale", 1.0))
+        assert_diff(out, ref, bound)
+        assert status.item() == 0
+        assert torch.equal(out, call(pk, w, lam, **more))
+    w.block_tables[0, 3] = -1
+    out = call(pk, w, lam, workspace=ws, status=status)
+    assert status.item() == pk.pagedkv.DEV_BAD_BLOCK_ID and not out[0].any()
+
+
+def test_diff_batches_of_short_sequences(pk):
+    """No unit longer than the streams of a CTA take at once: no unit is cut."""
+    for n in (3, 90, 300):
+        w = build("bf16", [(7 * i) % 65 for i in range(n)], 8, 4, 64, 16)
+        lam = random_lambda(8, DEV)
+        ref, bound = diff_reference(w, lam)
+        assert_diff(call(pk, w, lam), ref, bound)
+
+
 def test_diff_many_units_per_cta(pk):
     """More units than CTAs, most of them one item long: a CTA folds and writes many."""
     lengths = [1 + (7 * i) % 50 for i in range(200)]
