@@ -2,13 +2,15 @@
 // rows (one-byte codes times their row's scale, rounded once).
 //
 // Row out_offsets[s] + i of the output is token starts[s] + i of sequence s, reached
-// through the block table ("分页注意力", chenk.top page). A copy, bound by memory. A CTA
-// takes 2^tile_log2 consecutive output tokens: its warps find each token's sequence (a
-// 32-way search of the offsets by the warp's lanes, two dependent loads for a thousand
-// sequences where a bisection has ten) and its cache row through the table, then all
-// threads move rows, 8 elements each (a 16-byte store), with several loads in flight. Rows
-// of one head and consecutive tokens are neighbours in the cache, rows of one token
-// neighbours in the output, so both sides move whole rows of D elements.
+// through the block table ("分页注意力", chenk.top page). A copy, bound by memory: K and V of
+// 65536 tokens, 32 heads of 128, bf16: 2148 MB in 309 us (6950 GB/s); 110943 tokens of 8
+// heads, E5M2: 689 MB in 104 us (6600 GB/s). A CTA takes 2^tile_log2 consecutive output
+// tokens: a warp finds the sequence of the first of up to 32 of them (a 32-way search of the
+// offsets by its lanes, two dependent loads for a thousand sequences where a bisection has
+// ten), each lane its own token's and the cache row through the table, then all threads move
+// rows, 8 elements each (a 16-byte store), with several loads in flight. Rows of one head and
+// consecutive tokens are neighbours in the cache, rows of one token neighbours in the output,
+// so both sides move whole rows of D elements.
 #include "common.cuh"
 #include "decode.cuh"
 #include "internal.h"
@@ -16,9 +18,9 @@
 namespace pkv {
 
 namespace {
-constexpr int kGatherThreads = 256;
+constexpr int kGatherThreads = 128;
 constexpr int kUnroll = 4;         // loads in flight per thread
-constexpr int kGatherMaxLog2 = 5;  // at most 32 tokens per CTA
+constexpr int kGatherMaxLog2 = 7;  // at most 128 tokens per CTA
 }  // namespace
 
 // The last of the sequences 0 .. B - 1 whose offset is at most n (0 if none is), by the
@@ -40,18 +42,31 @@ template <int D, int CODE>
 __global__ void __launch_bounds__(kGatherThreads) paged_kv_gather_kernel(const GatherParams p) {
   constexpr int CPR = D / 8;                   // 8-element chunks per row
   constexpr int RPS = kGatherThreads / CPR;    // rows per step of the CTA
-  __shared__ long long s_row[1 << kGatherMaxLog2];  // cache row of head 0; -1: zeros, -2: none
+  __shared__ int s_row[1 << kGatherMaxLog2];  // cache row of head 0; -1: zeros, -2: none
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   const int tid = threadIdx.x, lane = tid & 31;
   const int tokens = 1 << p.tile_log2;
   const long long n0 = (long long)blockIdx.x << p.tile_log2;
-  for (int i = tid >> 5; i < tokens; i += kGatherThreads / 32) {
+  // A warp finds the sequence of the first of up to 32 tokens; a lane's own is the same one,
+  // or some way on (bisected for).
+  for (int i0 = tid & ~31; i0 < tokens; i0 += kGatherThreads) {
+    const int i = i0 + lane;
     const long long n = n0 + i;
-    long long row = -2;
-    if (n < p.N) {
-      const int s = gather_sequence_of(p.offsets, p.B, n, lane);
-      const int o0 = __ldg(p.offsets + s), o1 = __ldg(p.offsets + s + 1);
+    int s = gather_sequence_of(p.offsets, p.B, n0 + i0, lane);
+    int row = -2;
+    if (i < tokens && n < p.N) {
+      int o0 = __ldg(p.offsets + s), o1 = __ldg(p.offsets + s + 1);
+      if (o1 <= n) {
+        int end = p.B;  // the answer is in [s, end)
+        while (end - s > 1) {
+          const int mid = s + (end - s) / 2;
+          if (__ldg(p.offsets + mid) <= n) s = mid;
+          else end = mid;
+        }
+        o0 = __ldg(p.offsets + s);
+        o1 = __ldg(p.offsets + s + 1);
+      }
       if (o0 <= n && n < o1) {
         const long long tok = (p.starts ? (long long)__ldg(p.starts + s) : 0ll) + (n - o0);
         int flag = 0;
@@ -62,12 +77,12 @@ __global__ void __launch_bounds__(kGatherThreads) paged_kv_gather_kernel(const G
           const int id = __ldg(p.block_tables + size_t(s) * p.MBS + (tok >> p.bs_log2));
           if (id < 0 || id >= p.NB) flag = PKV_DEV_BAD_BLOCK_ID;
           else
-            row = (((long long)id * p.Hkv) << p.bs_log2) + (tok & ((1 << p.bs_log2) - 1));
+            row = ((id * p.Hkv) << p.bs_log2) + int(tok & ((1 << p.bs_log2) - 1));
         }
-        if (flag && p.status && lane == 0) atomicOr(p.status, flag);
+        if (flag && p.status) atomicOr(p.status, flag);
       }
     }
-    if (lane == 0) s_row[i] = row;
+    if (i < tokens) s_row[i] = row;
   }
   // the offsets themselves: 0 <= offsets[0], never falling, at most N
   if (p.status && blockIdx.x == 0 && blockIdx.y == 0) {
@@ -87,19 +102,19 @@ __global__ void __launch_bounds__(kGatherThreads) paged_kv_gather_kernel(const G
     for (int i0 = tid / CPR; i0 < rows; i0 += RPS * kUnroll) {
       uint4 raw[kUnroll];
       float sc[kUnroll];
-      long long src[kUnroll];
+      int src[kUnroll];  // (fewer than 2^31 rows: api.cu)
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         const int i = i0 + k * RPS;
-        const long long r = i < rows ? s_row[i & (tokens - 1)] : -2;
-        src[k] = r < 0 ? r : r + ((long long)(i >> p.tile_log2) << p.bs_log2);
+        const int r = i < rows ? s_row[i & (tokens - 1)] : -2;
+        src[k] = r < 0 ? r : r + ((i >> p.tile_log2) << p.bs_log2);
         raw[k] = make_uint4(0u, 0u, 0u, 0u);
         sc[k] = 0.f;
         if (src[k] >= 0) {
           if constexpr (CODE < 0) {
-            raw[k] = __ldg(reinterpret_cast<const uint4*>(cache) + src[k] * CPR + c);
+            raw[k] = __ldg(reinterpret_cast<const uint4*>(cache) + size_t(src[k]) * CPR + c);
           } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(cache) + src[k] * CPR + c);
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(cache) + size_t(src[k]) * CPR + c);
             raw[k].x = v.x;
             raw[k].y = v.y;
             sc[k] = __ldg(scale + src[k]);
@@ -146,9 +161,12 @@ cudaError_t launch_gather(int code, int D, const GatherParams& p, cudaStream_t s
 #undef PKV_GATHER
   if (!fn) return cudaErrorInvalidValue;
   GatherParams copy = p;
-  // A CTA moves K and V of as many tokens as give a thread 8 chunks: on GB300, INT8, 24511
-  // tokens of 8 heads of 128, 8 tokens took 28.4 us, 16 29.5, 4 36.0; bf16, 65536 tokens of
-  // 32 heads, 4 tokens 311 us, 16 320. Where that leaves SMs idle, K and V apart and fewer
+  // A CTA moves K and V of as many tokens as give a thread 8 chunks. On GB300 with 4, 8, 12
+  // and 16 chunks (CTAs of 256 threads): INT8, ~30000 tokens of 8 heads of 128, 49.0, 38.4,
+  // 38.6, 38.6 us; bf16, 65536 tokens of 32 heads, 332, 308, 310, 310. With 8, CTAs of 256,
+  // 128 and 64 threads: 38.4, 37.7, 37.9 us; 16 sequences of ~100 tokens 4.4, 3.9, 3.9. A
+  // warp per token's search, where lanes now have a token each: 40.9, and one head of 64
+  // (640000 tokens) 173 us for 49. Where the tiles leave SMs idle, K and V apart and fewer
   // tokens, down to one chunk per thread (47 tokens of 8 heads of 64: 3.6 -> 2.1 us).
   const int per_token = p.Hkv * (D / 8);  // chunks of K
   auto tiles = [&] { return ((long long)p.N + (1 << copy.tile_log2) - 1) >> copy.tile_log2; };

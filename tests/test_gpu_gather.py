@@ -98,6 +98,21 @@ def test_gather_many_and_long(pk, B, n):
     assert torch.equal(v.view(B, n, 2, 64), w.v_cache[blk, :, off])
 
 
+@pytest.mark.parametrize("hkv,d", [(1, 64), (1, 128), (2, 64)])
+@pytest.mark.parametrize("lengths", [[0, 5, 0, 0, 1, 1, 700, 0, 0, 2, 0], [1] * 500 + [0] * 40 + [3] * 90,
+                                     [0] * 70 + [200, 129, 128, 127] + [0] * 33, [9000, 0, 1]])
+def test_gather_tiles_over_many_sequences(pk, hkv, d, lengths):
+    """Tiles of up to 128 tokens (one narrow head) that span many sequences, empty ones among
+    them, first and last."""
+    w = build("bf16", lengths, hkv, d, 16)
+    n = sum(lengths)
+    k, v = gather(pk, w, offsets_of(lengths), num_tokens=n)
+    for x, which in ((k, "k"), (v, "v")):
+        want = np.concatenate([np.stack(rows_of(w, s, which)[0], 1) if L else
+                               np.zeros((0, hkv, d)) for s, L in enumerate(lengths)])
+        assert_rows(x, want, True)
+
+
 def test_gather_bad_pages_and_ranges(pk):
     """Bad ids and tokens outside the table give zero rows and a flag, with and without a
     status word; offsets past the buffer or falling are flagged and stay inside it."""
