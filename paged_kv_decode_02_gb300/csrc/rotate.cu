@@ -25,14 +25,16 @@
 namespace pkv {
 
 namespace {
-// Small CTAs: a CTA loads, then computes, then stores, and many small ones overlap these.
-// With kMany rows per lane group on GB300, 8192 tokens of 32/32 heads of 128 (bf16 cache):
-// 512 threads 80.5 us, 256 63.3, 128 61.5, 64 61.0; 4096 tokens of 64/8 heads, normed, INT8:
-// 38 us at 256, 34 at 64. Rows per lane group (256 threads): 1 84.9 us, 2 67.7, 4 63.3. The
-// arithmetic on pairs (packed fp32 products) and 10 CTAs: 59.9 and 32 us; 12 CTAs spill.
+// Small CTAs: a CTA loads, then computes, then stores, and many small ones overlap these. On
+// GB300, 8192 tokens of 32/32 heads of 128 (bf16 cache, 4 rows per lane group): 512 threads
+// 80.5 us, 256 63.3, 128 61.5, 64 61.0. Rows per lane group and CTAs per SM (8192 tokens of
+// 32/8 heads, normed, bf16 and INT8 caches; 65536 tokens of 2/2 heads, INT8): 1 and 16 51.4,
+// 51.8, 53.9 us; 2 and 16 32.7, 38.2, 47.9; 3 and 12 32.1, 37.3, 40.4; 4 and 10 33.2, 38.8,
+// 45.1. CTAs that stay and load ahead of their computing have fewer registers for rows and
+// lose (2 and 10: 34.8, 37.7, 50.2).
 constexpr int kRotThreads = 64;
-constexpr int kRotCtas = 10;       // per SM
-constexpr int kMany = 4;
+constexpr int kRotCtas = 12;       // per SM
+constexpr int kMany = 3;           // rows per lane group
 
 __device__ __forceinline__ void unpack8(const uint4& u, float2* f) {
   f[0] = unpack_bf16x2(u.x);
@@ -68,10 +70,6 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
   const int j = threadIdx.x % LPR;
   // the row's lanes: they branch alike
   const uint32_t group = ((1u << LPR) - 1u) << (threadIdx.x & 31 & ~(LPR - 1));
-  const long long t = item / sets;
-  if (t >= p.T) return;
-  const int first = int(item - unsigned(t) * sets);
-
   // the lane's two chunks of a row: a rotation pair's, or two of the rest
   const int nrot = p.R / 16;
   const bool turns = j < nrot;
@@ -82,6 +80,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
   }
   const uint4* qw = static_cast<const uint4*>(p.q_norm);
   const uint4* kw = static_cast<const uint4*>(p.k_norm);
+  if (item >= unsigned(p.T) * sets) return;
+  const long long t = item / sets;
+  const int first = int(item - unsigned(t) * sets);
   // the token's q, k and v rows
   const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(p.q) + t * p.q_stride;
   const __nv_bfloat16* krow =
@@ -102,94 +103,99 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas)
   }
   const long long pos = p.positions[t];
   const long long slot = p.slots[t];
-  const bool bad = pos < 0 || pos >= p.P;
-  if (bad && first == 0 && j == 0 && p.status) atomicOr(p.status, PKV_DEV_BAD_POSITION);
-  float2 c[4], s[4];
-  if (turns && !bad) {
-    const float* cs = p.cos_sin + pos * p.R + 8 * j;
-    load8(cs, c);
-    load8(cs + p.R / 2, s);
-  }
-  const bool skip = bad || slot < 0 || slot >= (long long)p.NB << p.bs_log2;
-  // cache row of KV head 0: (block * Hkv + head) * BS + offset
-  const long long drow0 = (((slot >> p.bs_log2) * p.Hkv) << p.bs_log2) +
-                          (slot & ((1 << p.bs_log2) - 1));
+  // (a lambda: as the rest of the kernel it compiles to more address arithmetic; 8192 tokens
+  // of 32/8 heads, bf16: 33.0 us, so 32.0)
+  const auto finish = [&](const uint4 (&raw)[kU][2]) {
+    const bool bad = pos < 0 || pos >= p.P;
+    if (bad && first == 0 && j == 0 && p.status) atomicOr(p.status, PKV_DEV_BAD_POSITION);
+    float2 c[4], s[4];
+    if (turns && !bad) {
+      const float* cs = p.cos_sin + pos * p.R + 8 * j;
+      load8(cs, c);
+      load8(cs + p.R / 2, s);
+    }
+    const bool skip = bad || slot < 0 || slot >= (long long)p.NB << p.bs_log2;
+    // cache row of KV head 0: (block * Hkv + head) * BS + offset
+    const long long drow0 = (((slot >> p.bs_log2) * p.Hkv) << p.bs_log2) +
+                            (slot & ((1 << p.bs_log2) - 1));
 
 #pragma unroll
-  for (int k = 0; k < kU; ++k) {
-    const int r = first + k * int(sets);
-    if (r >= rows) break;
-    const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
-    float2 x[8];  // chunk ca, then chunk cb
-    unpack8(raw[k][0], x);
-    unpack8(raw[k][1], x + 4);
-    const uint4* w = isq ? qw : kw;
-    if (!isv && w != nullptr) {
-      float2 s2 = both(0.f);
+    for (int k = 0; k < kU; ++k) {
+      const int r = first + k * int(sets);
+      if (r >= rows) break;
+      const bool isq = r < p.Hq, isv = r >= p.Hq + p.Hkv;
+      float2 x[8];  // chunk ca, then chunk cb
+      unpack8(raw[k][0], x);
+      unpack8(raw[k][1], x + 4);
+      const uint4* w = isq ? qw : kw;
+      if (!isv && w != nullptr) {
+        float2 s2 = both(0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s2 = __ffma2_rn(x[e], x[e], s2);
-      float ss = s2.x + s2.y;
+        for (int e = 0; e < 8; ++e) s2 = __ffma2_rn(x[e], x[e], s2);
+        float ss = s2.x + s2.y;
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-      const float2 rstd = both(rsqrtf(ss * (1.f / D) + p.eps));
-      float2 f[4];
-      unpack8(__ldg(w + ca), f);
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+        const float2 rstd = both(rsqrtf(ss * (1.f / D) + p.eps));
+        float2 f[4];
+        unpack8(__ldg(w + ca), f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(__fmul2_rn(x[e], rstd), f[e]);
-      unpack8(__ldg(w + cb), f);
+        for (int e = 0; e < 4; ++e) x[e] = __fmul2_rn(__fmul2_rn(x[e], rstd), f[e]);
+        unpack8(__ldg(w + cb), f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[4 + e] = __fmul2_rn(__fmul2_rn(x[4 + e], rstd), f[e]);
-    }
-    if (turns && !bad && !isv) {
-      if (p.interleaved) {
+        for (int e = 0; e < 4; ++e) x[4 + e] = __fmul2_rn(__fmul2_rn(x[4 + e], rstd), f[e]);
+      }
+      if (turns && !bad && !isv) {
+        if (p.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float ci = i % 2 ? c[i / 2].y : c[i / 2].x, si = i % 2 ? s[i / 2].y : s[i / 2].x;
-          x[i] = make_float2(x[i].x * ci - x[i].y * si, x[i].y * ci + x[i].x * si);
+          for (int i = 0; i < 8; ++i) {
+            const float ci = i % 2 ? c[i / 2].y : c[i / 2].x, si = i % 2 ? s[i / 2].y : s[i / 2].x;
+            x[i] = make_float2(x[i].x * ci - x[i].y * si, x[i].y * ci + x[i].x * si);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = x[i], b = x[4 + i];
+            x[i] = __ffma2_rn(a, c[i], __fmul2_rn(b, make_float2(-s[i].x, -s[i].y)));
+            x[4 + i] = __ffma2_rn(b, c[i], __fmul2_rn(a, s[i]));
+          }
         }
+      }
+      if (isq) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                              t * p.out_stride + r * D);
+        dst[ca] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x);
+        dst[cb] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x + 4);
+        continue;
+      }
+      const int h = isv ? r - p.Hq - p.Hkv : r - p.Hq;
+      const long long drow = drow0 + (h << p.bs_log2);
+      if constexpr (CODE < 0) {
+        if (skip) continue;
+        uint4* dst = reinterpret_cast<uint4*>(isv ? p.vc : p.kc) + drow * (D / 8);
+        dst[ca] = pack8(x);
+        dst[cb] = pack8(x + 4);
       } else {
+        float amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 a = x[i], b = x[4 + i];
-          x[i] = __ffma2_rn(a, c[i], __fmul2_rn(b, make_float2(-s[i].x, -s[i].y)));
-          x[4 + i] = __ffma2_rn(b, c[i], __fmul2_rn(a, s[i]));
+        for (int e = 0; e < 8; ++e) amax = fmax3(amax, fabsf(x[e].x), fabsf(x[e].y));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
+        if (skip) continue;
+        const float sc = __fdiv_rn(amax, Encode8<CODE>::kMax);
+        uint32_t u[4] = {0u, 0u, 0u, 0u};
+        if (sc > 0.f) {
+          const RowEncoder<CODE> enc(sc);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[e] = enc.four(x + 2 * e);
         }
+        uint2* dst = reinterpret_cast<uint2*>(isv ? p.vc : p.kc) + drow * (D / 8);
+        dst[ca] = make_uint2(u[0], u[1]);
+        dst[cb] = make_uint2(u[2], u[3]);
+        if (j == 0) (isv ? p.vs : p.ks)[drow] = sc;
       }
     }
-    if (isq) {
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                            t * p.out_stride + r * D);
-      dst[ca] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x);
-      dst[cb] = bad ? make_uint4(0u, 0u, 0u, 0u) : pack8(x + 4);
-      continue;
-    }
-    const int h = isv ? r - p.Hq - p.Hkv : r - p.Hq;
-    const long long drow = drow0 + (h << p.bs_log2);
-    if constexpr (CODE < 0) {
-      if (skip) continue;
-      uint4* dst = reinterpret_cast<uint4*>(isv ? p.vc : p.kc) + drow * (D / 8);
-      dst[ca] = pack8(x);
-      dst[cb] = pack8(x + 4);
-    } else {
-      float amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmax3(amax, fabsf(x[e].x), fabsf(x[e].y));
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(group, amax, o));
-      if (skip) continue;
-      const float sc = __fdiv_rn(amax, Encode8<CODE>::kMax);
-      uint32_t u[4] = {0u, 0u, 0u, 0u};
-      if (sc > 0.f) {
-        const RowEncoder<CODE> enc(sc);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = enc.four(x + 2 * e);
-      }
-      uint2* dst = reinterpret_cast<uint2*>(isv ? p.vc : p.kc) + drow * (D / 8);
-      dst[ca] = make_uint2(u[0], u[1]);
-      dst[cb] = make_uint2(u[2], u[3]);
-      if (j == 0) (isv ? p.vs : p.ks)[drow] = sc;
-    }
-  }
+  };
+  finish(raw);
 }
 
 template <int D, int CODE>
