@@ -18,7 +18,8 @@
 //   two to a warp at most. S^T = K q^T runs per K head over all 8 columns; the columns of the
 //   other map are not read. The weights turn from S^T's accumulators into P^T's operand
 //   by a movmatrix per 8 tokens. A pair's two maps are neighbouring columns of one lane:
-//   the difference is local, the norm one reduction over 8 lanes.
+//   the difference is local, the norm one reduction over 8 lanes. (Rows on M measured 499 us
+//   for 355 on 128 x 8192 tokens, INT8, 32/8 heads.)
 // * Work split: (sequence, unit, item) triples in one flat order, an item `kItem` tokens of
 //   one KV pair, cut into G equal ranges, one per CTA. A unit is up to 16 query pairs of a
 //   KV pair. The CTA's warps form streams of kRows warps (of up to 8 pairs each, reading
@@ -34,6 +35,13 @@
 //   are done with this one's, its V when P.V is (by the last of the stream's warps).
 // * One-byte caches as in decode.cuh: codes widened exactly to fp16, the K scale on the
 //   fp32 score, the V scale folded into the fp16 weight.
+// * Measured on GB300, head_dim 128, whole calls: INT8, 128 x 8192 tokens, 32/8 heads 347 us
+//   (2217 MB, 6390 GB/s); bf16, 64 ragged contexts (110943 tokens), 64/8 heads 79 us (457 MB,
+//   5800 GB/s: some 3 us before the first tile, 7 us of merge, and the ends of units); E4M3,
+//   one context of 131071, 32/8 heads 51 us (277 MB, 5460 GB/s). With more than 4 query pairs
+//   per KV pair a one-byte cache is bound by the warps' own instructions (8 warps of 255
+//   registers per SM, 41 % of the issue slots): 64 x 2048, 64/8 heads, INT8 70 us (279 MB,
+//   3960 GB/s), E4M3 61 us.
 #pragma once
 
 #include "common.cuh"
