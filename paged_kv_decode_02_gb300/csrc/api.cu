@@ -717,7 +717,7 @@ pkv_status run_rotate(int kvt, void* out, const void* q, const void* k, const vo
 struct DiffPlan {
   DiffKernelInfo k;
   int gs, nsg, G;
-  size_t smem, off_ml, off_o, ws_bytes;
+  size_t smem, off_cuts, off_ml, off_o, ws_bytes;
 };
 
 pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
@@ -780,9 +780,11 @@ pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
       per_sm <= 0)
     return PKV_ERR_CUDA;
   P.G = sms * per_sm;
-  // workspace: [parts (B, units, 2) int32][records' (m, l), 2 per CTA][records' o]
+  // workspace: [parts (B, units, 2) int32][cuts (G) int32][records' (m, l), 2 per CTA]
+  // [records' o]
   const size_t rows = size_t(2) * P.G * 2 * P.gs;
-  P.off_ml = align_up(size_t(d->num_seqs) * (d->num_kv_heads / 2) * P.nsg * 8, 256);
+  P.off_cuts = align_up(size_t(d->num_seqs) * (d->num_kv_heads / 2) * P.nsg * 8, 256);
+  P.off_ml = align_up(P.off_cuts + size_t(P.G) * 4, 256);
   P.off_o = align_up(P.off_ml + rows * 8, 256);
   P.ws_bytes = align_up(P.off_o + rows * 2 * d->head_dim * 4, 256);
   keys[next] = key;
@@ -834,7 +836,9 @@ pkv_status run_diff(int kvt, void* out, const void* q, const void* k_cache, cons
   p.part_o = reinterpret_cast<float*>(ws + P.off_o);
   p.part_ml = reinterpret_cast<float*>(ws + P.off_ml);
   p.parts = reinterpret_cast<int32_t*>(ws);
+  p.cuts = reinterpret_cast<int32_t*>(ws + P.off_cuts);
   p.status = status;
+  p.G = P.G;
   p.B = d->num_seqs;
   p.P = d->num_kv_heads / 2;
   p.MBS = d->max_blocks_per_seq;

@@ -586,6 +586,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     if (tid < kStreams * kStages * 2) reinterpret_cast<int*>(gen + S::kOffCnt)[tid] = 0;
   }
   pdl_wait_prior_grid();
+  if (tid == 0) p.cuts[blockIdx.x] = -1;  // no unit is left to others, so far
   if (p.norm_w && tid < D / 32)  // read at the end of a unit
     asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p.norm_w) + tid * 128));
   if (tid < (p.P * p.g + 31) / 32)
@@ -878,6 +879,8 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
     if (rank == 0 && tile == 0 && lane == 0) {
       int* part = p.parts + 2 * (size_t(cur.s) * U + cur.u);
       if (cur.j == 0) part[0] = whole ? -1 : 2 * int(blockIdx.x) + (first ? 0 : 1);
+      if (cur.j == 0 && !whole)  // at most one: the range's last segment
+        p.cuts[blockIdx.x] = 2 * (cur.s * U + cur.u) + (first ? 0 : 1);
       if (cur.j + len == cur.n) part[1] = int(blockIdx.x);
     }
 #pragma unroll

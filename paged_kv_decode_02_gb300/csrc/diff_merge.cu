@@ -4,7 +4,8 @@
 // rescaling (fold.cuh), one output quad of one map per lane; then the difference, the
 // optional norm and the bf16 row, as in decode_diff.cuh. It also writes zeros for empty
 // sequences and, when a status word is given, checks the sequence's context length and
-// block ids (a sequence that fails gets zeros). Units that one CTA covered leave at once.
+// block ids (a sequence that fails gets zeros). Units that one CTA covered leave at once, and
+// are not visited at all where units are many.
 //
 // Bound by latency (records are 2 KiB per CTA of the decode and query pair, mostly in L2), so
 // the work of a pair spreads as far as the GPU has room: with many pairs D lanes fold a pair's
@@ -34,7 +35,22 @@ __device__ __forceinline__ void store_row(const DiffParams& p, uint2* out, int q
 }
 }
 
-template <int D>
+// Whether sequence s fails the status word's checks, by a warp: the flags (0: it passes).
+__device__ __forceinline__ int seq_flags(const DiffParams& p, int s, int L, int lane) {
+  int flags = 0;
+  if (L < 0 || L > p.MBS * p.BS) flags = PKV_DEV_BAD_CONTEXT_LEN;
+  const int nblk = L <= 0 ? 0 : (min(L, p.MBS * p.BS) - 1) / p.BS + 1;
+  for (int j = lane; j < nblk; j += 32) {
+    const int id = p.block_tables[size_t(s) * p.MBS + j];
+    if (id < 0 || id >= p.NB) flags |= PKV_DEV_BAD_BLOCK_ID;
+  }
+  return __reduce_or_sync(0xffffffffu, flags);
+}
+
+// kByCta: the cut units go by the CTAs that began them (more units than CTAs: most are whole);
+// behind them a warp per sequence checks it and writes the zeros. Else a set per (sequence,
+// unit, query pair) does it all.
+template <int D, bool kByCta>
 __global__ void __launch_bounds__(kDiffMergeThreads, 5) paged_diff_merge_kernel(const DiffParams p) {
   constexpr int Q = D / 2;          // quads of a 2 D row
   constexpr int kSet = 2 * Q;       // threads of a set: quads of both maps
@@ -46,33 +62,49 @@ __global__ void __launch_bounds__(kDiffMergeThreads, 5) paged_diff_merge_kernel(
   const int map = t / Q, quad = t % Q, lane = threadIdx.x & 31;
   const int U = p.P * p.nsg;
   const unsigned item = blockIdx.x * kSets + set;
-  const unsigned unit = item / unsigned(p.gs);
-  const bool valid = unit < unsigned(p.B * U);
+  const unsigned owner = item / unsigned(p.gs);  // unit, or CTA
   const int r = int(item % unsigned(p.gs));
+  unsigned unit = owner;
+  int cut = 0;
+  bool valid;
+  if constexpr (kByCta) {
+    const unsigned merging = (unsigned(p.G * p.gs) + kSets - 1) / kSets;  // CTAs
+    if (blockIdx.x >= merging) {
+      const int s = int(blockIdx.x - merging) * (kDiffMergeThreads / 32) + threadIdx.x / 32;
+      if (s >= p.B) return;
+      const int L = p.context_lens[s];
+      const int flags = p.status != nullptr ? seq_flags(p, s, L, lane) : 0;
+      if (flags && lane == 0) atomicOr(p.status, flags);
+      if (L > 0 && !flags) return;
+      const size_t n = size_t(p.P) * p.g * (2 * D / 8);  // 16-byte words of the sequence
+      uint4* o = static_cast<uint4*>(p.out) + s * n;
+      for (size_t i = lane; i < n; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
+    cut = owner < unsigned(p.G) ? p.cuts[owner] : -1;
+    valid = cut >= 0;
+    unit = valid ? unsigned(cut) >> 1 : 0u;
+  } else {
+    valid = unit < unsigned(p.B * U);
+  }
   const int s = valid ? int(unit / unsigned(U)) : 0, u = int(unit % unsigned(U));
   const int row = (u % p.nsg) * p.gs + r;  // query pair within the KV pair
   const int qp = u / p.nsg * p.g + row;
   const int L = p.context_lens[s];
-  const int2 part = valid ? reinterpret_cast<const int2*>(p.parts)[unit] : make_int2(-1, 0);
+  int2 part = valid ? reinterpret_cast<const int2*>(p.parts)[unit] : make_int2(-1, 0);
+  if constexpr (kByCta) part.x = valid ? int(2 * owner) + (cut & 1) : -1;
   uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
                                         (size_t(s) * p.P * p.g + qp) * (2 * D));
   bool active = valid && row < p.g;
   bool zero = L <= 0;
   if (p.status != nullptr) {
-    int flags = 0;
-    if (L < 0 || L > p.MBS * p.BS) flags = PKV_DEV_BAD_CONTEXT_LEN;
-    const int nblk = L <= 0 ? 0 : (min(L, p.MBS * p.BS) - 1) / p.BS + 1;
-    for (int j = lane; j < nblk; j += 32) {  // every warp for itself
-      const int id = p.block_tables[size_t(s) * p.MBS + j];
-      if (id < 0 || id >= p.NB) flags |= PKV_DEV_BAD_BLOCK_ID;
-    }
-    flags = __reduce_or_sync(0xffffffffu, flags);
+    const int flags = seq_flags(p, s, L, lane);
     if (flags) {
-      if (valid && t == 0 && u == 0 && r == 0) atomicOr(p.status, flags);
+      if (!kByCta && valid && t == 0 && u == 0 && r == 0) atomicOr(p.status, flags);
       zero = true;
     }
   }
-  if (active && zero && map == 0) out[quad] = make_uint2(0u, 0u);
+  if (!kByCta && active && zero && map == 0) out[quad] = make_uint2(0u, 0u);
   active = active && !zero && part.x >= 0;  // (an empty sequence has no entry)
 
   Fold f = fold_empty();
@@ -250,13 +282,23 @@ void launch_diff_merge(const DiffParams& p, cudaStream_t stream) {
   const void* fns[2][3] = {
       {reinterpret_cast<const void*>(&paged_diff_merge_wide_kernel<64, 8, 256>),
        reinterpret_cast<const void*>(&paged_diff_merge_wide_kernel<64, 4, 64>),
-       reinterpret_cast<const void*>(&paged_diff_merge_kernel<64>)},
+       reinterpret_cast<const void*>(&paged_diff_merge_kernel<64, false>)},
       {reinterpret_cast<const void*>(&paged_diff_merge_wide_kernel<128, 8, 256>),
        reinterpret_cast<const void*>(&paged_diff_merge_wide_kernel<128, 4, 64>),
-       reinterpret_cast<const void*>(&paged_diff_merge_kernel<128>)}};
+       reinterpret_cast<const void*>(&paged_diff_merge_kernel<128, false>)}};
   const int per = kDiffMergeThreads / p.D;  // pairs per CTA of the last
-  const dim3 grid(unsigned(pick < 2 ? items * kCtas[pick] : (items + per - 1) / per));
-  launch_pdl(fns[p.D == 128][pick], grid, dim3(kThr[pick]), args, 0, stream);
+  unsigned grid = unsigned(pick < 2 ? items * kCtas[pick] : (items + per - 1) / per);
+  const void* fn = fns[p.D == 128][pick];
+  // at most one cut unit per CTA of the decode begins there: where units are more than CTAs
+  // (256 sequences of ~46 tokens, 64/8 heads, bf16: 1024 units, 37.1 us -> 32.8; of ~300
+  // tokens, 32/8 heads: 61.2 -> 59.7; of one token: 12.5 -> 10.8)
+  if (pick == 2 && (long long)p.B * p.P * p.nsg > p.G) {
+    constexpr int kWarps = kDiffMergeThreads / 32;
+    grid = unsigned((p.G * p.gs + per - 1) / per) + unsigned((p.B + kWarps - 1) / kWarps);
+    fn = p.D == 128 ? reinterpret_cast<const void*>(&paged_diff_merge_kernel<128, true>)
+                    : reinterpret_cast<const void*>(&paged_diff_merge_kernel<64, true>);
+  }
+  launch_pdl(fn, dim3(grid), dim3(kThr[pick]), args, 0, stream);
 }
 
 }  // namespace pkv

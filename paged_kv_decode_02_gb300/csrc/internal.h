@@ -262,6 +262,8 @@ struct DiffParams {
   float* part_o;               // [2 G, 2, gs, 2 D] fp32 records' outputs (unnormalised)
   float* part_ml;              // [2 G, 2, gs, 2] fp32 (running max in log2 units, sum)
   int32_t* parts;              // [B, units, 2] a unit's first record (-1: none) and last CTA
+  int32_t* cuts;               // [G] 2 unit + the record's place, of the cut unit that a CTA
+                               // begins; -1: none
   int32_t* status;
   int B, P, MBS, NB, BS;       // P: KV head pairs
   int g;                       // query pairs per KV pair
@@ -269,6 +271,7 @@ struct DiffParams {
   int nsg;                     // work units per KV pair
   int D;                       // head_dim
   int unit_cost;               // what ending a unit costs a CTA, in items
+  int G;                       // CTAs
   int min_range;               // positions of a CTA's range at least
   float scale_log2;            // softmax scale * log2(e)
   float eps, out_scale;

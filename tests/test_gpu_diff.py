@@ -119,6 +119,34 @@ def test_diff_few_pairs_many_records(pk, kv, d, lengths, hq, hkv):
     assert status.item() == pk.pagedkv.DEV_BAD_BLOCK_ID and not out[0].any()
 
 
+@pytest.mark.parametrize("kv,hq,hkv,d", [("bf16", 8, 8, 64), ("int8", 16, 8, 128),
+                                         ("bf16", 48, 4, 64), ("fp8_e4m3", 8, 8, 128)])
+def test_diff_more_units_than_ctas(pk, kv, hq, hkv, d):
+    """Most units whole, some cut: with empty sequences, a bad page, a bad length, a status word
+    and without."""
+    lengths = [(37 * i) % 201 if i % 9 else 0 for i in range(300)]
+    w = build(kv, lengths, hq, hkv, d, 16)
+    lam, nw = random_lambda(hq, DEV), random_norm(d, DEV)
+    ref, bound = diff_reference(w, lam, nw, 1e-5, 0.5)
+    more = dict(norm_weight=nw, eps=1e-5, out_scale=0.5)
+    out = torch.full((300, hq // 2, 2 * d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    assert_diff(call(pk, w, lam, out=out, **more), ref, bound)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    good = call(pk, w, lam, status=status, **more)
+    assert status.item() == 0 and torch.equal(good, out)
+    w.block_tables[[10, 100, 215], 0] = 1 << 30
+    w.context_lens[150] = -3
+    w.context_lens[151] = w.block_tables.shape[1] * 16 + 1
+    got = call(pk, w, lam, status=status, **more)
+    assert status.item() == pk.pagedkv.DEV_BAD_BLOCK_ID | pk.pagedkv.DEV_BAD_CONTEXT_LEN
+    bad = torch.zeros(300, dtype=torch.bool, device=DEV)
+    bad[[10, 100, 215, 150, 151]] = True
+    assert not got[bad].any()
+    # the rest as before (where cuts fall moves with the lengths: within the bound, not the bits)
+    ref[bad.cpu().numpy()] = 0.0
+    assert_diff(got, ref, bound)
+
+
 def test_diff_batches_of_short_sequences(pk):
     """No unit longer than the streams of a CTA take at once: no unit is cut."""
     for n in (3, 90, 300):
