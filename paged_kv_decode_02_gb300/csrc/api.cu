@@ -30,10 +30,12 @@ constexpr int kTcSplitRows = 64;
 // slower, 3: 1-3 %, 4 and 5: 3-5 %)
 constexpr int kTcHeadCost = 2;
 // differential decode: the same for a unit, in items (a CTA that ends many short units
-// spends 2 to 4 us on each, an item about 1 us). Whole calls on GB300, ragged batch of 64
-// (64 / 8 heads, head_dim 128, bf16): cost 0 92.3 us, 1 92.1, 2 89.8, 3 88.1, 4 87.3, 6
-// 86.8; INT8, 128 x 8192: 353 us at 0 to 4, 354 at 6
-constexpr int kDiffUnitCost = 4;
+// spends 2 to 4 us on each, an item about 1 us). Whole calls on GB300 at cost 1, 2, 3, 4, 5, 6,
+// 8: ragged batch of 64 (64 / 8 heads, bf16) 87.5, 84.0, 81.7, 83.2, 79.6, 80.4, 78.5 us; 256
+// of ~264 tokens (32 / 8, INT8) 49.9, 49.9, 46.5, 48.8, 45.7, 47.0, 47.1; 64 of ~500 (32 / 4,
+// INT8) 28.8, 26.5, 26.1, 24.1, 23.9, 23.3, 23.4; 256 of ~100 (32 / 8, E4M3) 28.2, 27.3, 28.2,
+// 28.2, 28.5, 29.2, 29.9; INT8, 128 x 8192: 350 to 352 at all
+constexpr int kDiffUnitCost = 5;
 // and the least length of a CTA's range, in items: shorter ones leave more records to merge
 // than they save. One sequence (2 / 2 heads, bf16), at 1, 2, 3, 4: 300 tokens 7.9, 8.0, 8.3,
 // 8.6 us, 8192 tokens 11.7, 10.0, 10.0, 9.7; 3 of ~700 (32 / 8, E4M3): 11.8, 10.8, 10.6, 11.2
