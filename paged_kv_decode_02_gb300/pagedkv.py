@@ -250,28 +250,34 @@ def _require(t, name, dtype, ndim, device=None):
 _pack_dims = struct.Struct("7i").pack                  # pkv_dims
 _pack_rotary = struct.Struct("3P4q3if").pack           # pkv_rotary
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_Tensor = torch.Tensor
+_current_device = getattr(torch._C, "_cuda_getDevice", None)      # (None: torch without CUDA)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_CACHE_DTYPES = {KV_BF16: (torch.bfloat16,), KV_INT8: (torch.int8,),
+                 KV_FP8_E4M3: (torch.uint8, torch.float8_e4m3fn),
+                 KV_FP8_E5M2: (torch.uint8, torch.float8_e5m2)}
 
 
 def _need(t, name, dtype, ndim, index):
     """:func:`_require` of a tensor on CUDA device ``index``."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index
             and t.dim() == ndim and t.is_contiguous()):
         _require(t, name, dtype, ndim, torch.device("cuda", max(index, 0)))
 
 
 def _need_caches(kv, k_cache, v_cache, k_scale, v_scale):
     """Checks the caches of a KV dtype; returns (device index, K cache's shape)."""
-    if not isinstance(k_cache, torch.Tensor):
+    if not isinstance(k_cache, _Tensor):
         raise TypeError("k_cache must be a torch.Tensor")
     index = k_cache.get_device()
     if index < 0:
         _require(k_cache, "k_cache", k_cache.dtype, 4)
     dt = k_cache.dtype
-    if dt not in _code_dtypes(kv):
-        dt = _code_dtypes(kv)[0]
+    if dt not in _CACHE_DTYPES[kv]:
+        dt = _CACHE_DTYPES[kv][0]
     _need(k_cache, "k_cache", dt, 4, index)
     shape = k_cache.shape
-    if not (isinstance(v_cache, torch.Tensor) and v_cache.dtype is dt
+    if not (isinstance(v_cache, _Tensor) and v_cache.dtype is dt
             and v_cache.get_device() == index and v_cache.shape == shape
             and v_cache.is_contiguous()):
         _require_any(v_cache, "v_cache", _code_dtypes(kv), 4, k_cache.device)
@@ -288,10 +294,10 @@ def _run(name, index, *args):
     """Calls the library on CUDA device ``index``, on its current stream; returns the
     status."""
     fn = getattr(_LIB if _LIB is not None else load_library(), name)
-    if torch._C._cuda_getDevice() == index:
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _current_device() == index:
+        return fn(*args, _raw_stream(index))
     with torch.cuda.device(index):
-        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        return fn(*args, _raw_stream(index))
 
 
 def _status_ptr(status, index):
