@@ -308,8 +308,11 @@ pkv_status pkv_decode_diff_bf16(void* out, const void* q, const void* k_cache,
 /*
  * pkv_decode_diff_q8 -- pkv_decode_diff_bf16 over a one-byte cache (kv_dtype PKV_KV_INT8,
  * PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2, else PKV_ERR_DTYPE): codes widened exactly, the K
- * scale on the fp32 score, the V scale (times 2^6, 2^8 or 2^15, undone on the output) in
- * fp16 softmax weights, so V rows' absmax must stay below about 1e5 in every format.
+ * scale on the fp32 score, the V scale in fp16 softmax weights (each rounded by at most
+ * 2^-11 of it), in units that follow the largest V scale of the head's context: V rows may
+ * be of any size, and a weight below 2^-28 of the largest, on a row of that scale, is off by
+ * at most 2^-39 of it (rows of much smaller scales than the head's largest: correspondingly
+ * sooner).
  */
 pkv_status pkv_decode_diff_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale,

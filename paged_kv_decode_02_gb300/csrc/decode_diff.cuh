@@ -34,7 +34,8 @@
 //   of an item have a barrier each: the ring's next K is requested as soon as the scores
 //   are done with this one's, its V when P.V is (by the last of the stream's warps).
 // * One-byte caches as in decode.cuh: codes widened exactly to fp16, the K scale on the
-//   fp32 score, the V scale folded into the fp16 weight.
+//   fp32 score, the V scale folded into the fp16 weight, there under a power of two that
+//   follows the V scales (DiffPathQ8).
 // * Measured on GB300, head_dim 128, whole calls: INT8, 128 x 8192 tokens, 32/8 heads 347 us
 //   (2217 MB, 6390 GB/s); bf16, 64 ragged contexts (110943 tokens), 64/8 heads 79 us (457 MB,
 //   5800 GB/s: some 3 us before the first tile, 7 us of merge, and the ends of units); E4M3,
@@ -141,12 +142,18 @@ struct DiffState {
   __device__ __forceinline__ void scale(float a0, float a1) {
     l0 *= a0;
     l1 *= a1;
+    times(0, kMT, make_float2(a0, a1));
+  }
+  // Tiles [t0, t1) of o times f, by map.
+  __device__ __forceinline__ void times(int t0, int t1, float2 f) {
 #pragma unroll
-    for (int i = 0; i < kMT; ++i) {
-      o[i][0] *= a0;
-      o[i][1] *= a1;
-      o[i][2] *= a0;
-      o[i][3] *= a1;
+    for (int i = t0; i < t1; ++i) {
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        const float2 v = __fmul2_rn(make_float2(o[i][c], o[i][c + 1]), f);
+        o[i][c] = v.x;
+        o[i][c + 1] = v.y;
+      }
     }
   }
   // New maxima over an item (mx: this lane's tokens): rescales the state, returns what the
@@ -201,10 +208,12 @@ struct DiffState {
     for (int i = 0; i < kMT / 2; ++i) {
       const float4 v = b[i * 32];
       float* d = h ? o[kMT / 2 + i] : o[i];
-      d[0] = fmaf(v.x, f.x, d[0]);
-      d[1] = fmaf(v.y, f.y, d[1]);
-      d[2] = fmaf(v.z, f.x, d[2]);
-      d[3] = fmaf(v.w, f.y, d[3]);
+      const float2 a = __ffma2_rn(make_float2(v.x, v.y), f, make_float2(d[0], d[1]));
+      const float2 b = __ffma2_rn(make_float2(v.z, v.w), f, make_float2(d[2], d[3]));
+      d[0] = a.x;
+      d[1] = a.y;
+      d[2] = b.x;
+      d[3] = b.y;
     }
   }
 };
@@ -217,7 +226,6 @@ struct DiffPathBf16 {
   using Geo = DiffGeom<D, -1, BOX, SUB>;
   static constexpr int kNT = NT;  // groups of 4 query pairs of the warp
   static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
-  static constexpr float kOutScale = 1.f;
   static constexpr int kPer = Geo::kChunksPerSeg / 2;  // 32-byte steps of a row segment
   uint32_t qb[NT][kKS][2];
   uint32_t ko[kPer], vo[kPer];  // the lane's places in K and V tiles
@@ -256,6 +264,7 @@ struct DiffPathBf16 {
     }
     st[g].clear();
   }
+  __device__ __forceinline__ void close(int g) { st[g].close(); }
 
   // Scores of tokens 16 t + gid (x[g][t][0..1], by map) and 16 t + 8 + gid (x[g][t][2..3]) in
   // log2 units; tokens from nvalid on are -inf.
@@ -324,23 +333,28 @@ struct DiffPathBf16 {
 };
 
 // One-byte codes (fp16 MMAs on exactly widened codes). A softmax weight times its token's V
-// scale is rounded to fp16 (2^-11 of it; the row sums are of the unrounded weights): a scale
-// is absmax over the largest code, so the product also carries kVUp, which makes it about
-// weight * absmax / 2 in every format and keeps it from fp16's subnormals for as long, and
-// from its overflow for rows with absmax below 1e5.
+// scale is rounded to fp16 (2^-11 of it; the row sums are of the unrounded weights). The
+// product also carries a power of two per value head, which takes the largest V scale of the
+// stream's tokens so far to 2^14 to 2^15; a larger one rescales the state, as a larger score
+// does, and the unit's end undoes it. So rows of any size stay in fp16's normal numbers for
+// weights down to 2^-28 of the largest, and a smaller weight is off by 2^-39 of that scale at
+// most (131072 of them: by 2^-22 of the largest row). With a constant in its place (2^6, 2^8,
+// 2^15) 32766 tokens 8 to 10 nats below four others lost 23 to 88 % of the output on V rows of
+// absmax 1e-3 and 1e-4, and rows above 1e5 overflowed. The price, on GB300 (64 x 2048 tokens of
+// head_dim 128): 64/8 heads INT8 70.7 -> 72.1 us, E4M3 66.0 -> 66.7, E5M2 61.5 -> 64.1; 128/8
+// INT8 118.5 -> 122.2; 0.3 % with up to 4 query pairs, where memory is the bound.
 template <int D, int CODE, int BOX, int SUB, int NT>
 struct DiffPathQ8 {
   using Geo = DiffGeom<D, CODE, BOX, SUB>;
   static constexpr int kNT = NT;  // groups of 4 query pairs: they share each widened code
   using Codec = Code8<CODE>;
-  static constexpr float kVUp = CODE == CODE_E5M2 ? 32768.f : CODE == CODE_E4M3 ? 256.f : 64.f;
-  static constexpr float kOutScale = 1.f / kVUp;
   static constexpr int kKS = D / 16, kT = Geo::kItem / 16;
   static constexpr int kQB = D / 4, kQC = kQB / 16;  // bytes of a K row each lane reads
   static constexpr int kVK = D / 32;  // 32-column steps of a head's V row
   uint32_t qb[NT][kKS][2];
   uint32_t ko[kQC], vo[kVK];  // the lane's places in K and V tiles
   float rs0[NT], rs1[NT], off0[NT], off1[NT];
+  float up[2];  // each value head's power of two
   DiffState<D> st[NT];
 
   __device__ __forceinline__ void init(int lane) {
@@ -371,6 +385,31 @@ struct DiffPathQ8 {
     d[1] *= a.y;
     d[2] *= b.x;
     d[3] *= b.y;
+  }
+
+  // A larger V scale than the powers of two were made for: takes the item's largest (mx: this
+  // lane's token's, by head) to 2^14 to 2^15, and the states to the new units. (At first 2^126,
+  // whose inverse is a normal number too.)
+  __device__ __forceinline__ void raise_v(const float (&mx)[2]) {
+#pragma unroll
+    for (int hd = 0; hd < 2; ++hd) {
+      // (as integers: positive floats keep their order)
+      const uint32_t e = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(mx[hd]))) >> 23;
+      const uint32_t old = __float_as_uint(up[hd]) >> 23, now = min(268u - e, old);
+      const float f = old - now < 127u ? __uint_as_float((127u - (old - now)) << 23) : 0.f;
+      up[hd] = __uint_as_float(now << 23);
+#pragma unroll
+      for (int g = 0; g < NT; ++g)
+        st[g].times(hd * (D / 16), (hd + 1) * (D / 16), make_float2(f, f));
+    }
+  }
+  __device__ __forceinline__ void close(int g) {
+    st[g].close();
+#pragma unroll
+    for (int hd = 0; hd < 2; ++hd) {
+      const float f = __uint_as_float((254u << 23) - __float_as_uint(up[hd]));  // 1 / up
+      st[g].times(hd * (D / 16), (hd + 1) * (D / 16), make_float2(f, f));
+    }
   }
 
   // The row is scaled by a power of two to near 2^14 (then exact in fp16 for entries above
@@ -415,6 +454,7 @@ struct DiffPathQ8 {
     rs1[g] = __shfl_sync(0xffffffffu, rs, 8 * cq + 4);
     off0[g] = __shfl_sync(0xffffffffu, qs, 8 * cq);
     off1[g] = __shfl_sync(0xffffffffu, qs, 8 * cq + 4);
+    up[0] = up[1] = 0x1p126f;
     st[g].clear();
   }
 
@@ -473,25 +513,30 @@ struct DiffPathQ8 {
   __device__ __forceinline__ void values(float (&x)[NT][kT][4], uint32_t sV, uint32_t sVs,
                                          int nvalid, const float2 (&mn)[NT], int lane) {
     const int gid = lane >> 2;
+    // V scales (past the context: 0), a token per lane, of which most items raise none
+    static_assert(Geo::kItem == 32, "a token per lane");
+    float mx[2];
+#pragma unroll
+    for (int hd = 0; hd < 2; ++hd)
+      mx[hd] = lane < nvalid ? lds_f32(sVs + Geo::scale_off(hd, lane)) : 0.f;
+    const bool above = fmaxf(fabsf(mx[0]) * up[0], fabsf(mx[1]) * up[1]) >= 0x1p15f;
+    if (__builtin_expect(__any_sync(0xffffffffu, above), 0)) raise_v(mx);
 #pragma unroll
     for (int t = 0; t < kT; ++t) {
       uint32_t pb[NT][2][2];  // each value head has its own scales
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int tok = 16 * t + 8 * h + gid;
-        float vs[2];
-#pragma unroll
-        for (int hd = 0; hd < 2; ++hd)
-          vs[hd] = tok < nvalid ? lds_f32(sVs + Geo::scale_off(hd, tok)) * kVUp : 0.f;
+        const float v0 = tok < nvalid ? lds_f32(sVs + Geo::scale_off(0, tok)) * up[0] : 0.f;
+        const float v1 = tok < nvalid ? lds_f32(sVs + Geo::scale_off(1, tok)) * up[1] : 0.f;
 #pragma unroll
         for (int g = 0; g < NT; ++g) {
           const float w0 = fast_exp2(x[g][t][2 * h] - mn[g].x);
           const float w1 = fast_exp2(x[g][t][2 * h + 1] - mn[g].y);
           st[g].l0 += w0;
           st[g].l1 += w1;
-#pragma unroll
-          for (int hd = 0; hd < 2; ++hd)
-            pb[g][hd][h] = transpose_8x8(pack_f16x2(w0 * vs[hd], w1 * vs[hd]));
+          pb[g][0][h] = transpose_8x8(pack_f16x2(w0 * v0, w1 * v0));
+          pb[g][1][h] = transpose_8x8(pack_f16x2(w0 * v1, w1 * v1));
         }
       }
 #pragma unroll
@@ -837,7 +882,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         }
       }
 #pragma unroll
-      for (int g = 0; g < NT; ++g) path.st[g].close();
+      for (int g = 0; g < NT; ++g) path.close(g);
     }
 
     // ---- fold the streams' states into rank 0's ----
@@ -900,14 +945,14 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
             float v[2][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              v[0][e] = Path::at(state.o, k, e, 0) * Path::kOutScale;
-              v[1][e] = Path::at(state.o, k, e, 1) * Path::kOutScale;
+              v[0][e] = Path::at(state.o, k, e, 0);
+              v[1][e] = Path::at(state.o, k, e, 1);
             }
             *reinterpret_cast<float4*>(o0 + c) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
             *reinterpret_cast<float4*>(o1 + c) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
           } else {
-            o0[c] = Path::at(state.o, k, 0, 0) * Path::kOutScale;
-            o1[c] = Path::at(state.o, k, 0, 1) * Path::kOutScale;
+            o0[c] = Path::at(state.o, k, 0, 0);
+            o1[c] = Path::at(state.o, k, 0, 1);
           }
         }
         if (gid == 0) {
@@ -919,8 +964,8 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
         }
       } else {
         const int qp = pair0 + r0 + pr;
-        const float i0 = Path::kOutScale / state.l0;
-        const float i1 = Path::kOutScale / state.l1 * __ldg(p.lam + qp);
+        const float i0 = 1.f / state.l0;
+        const float i1 = 1.f / state.l1 * __ldg(p.lam + qp);
         const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.norm_w);
         float ss = 0.f, d[Path::kRuns][Path::kRun];
 #pragma unroll
