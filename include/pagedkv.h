@@ -293,8 +293,10 @@ pkv_status pkv_decode_fp8(void* out, const void* q, const uint8_t* k_cache,
  *   norm_weight   [2 D] bf16, device; NULL: no norm (eps is then not used).
  *   workspace     at least pkv_decode_diff_workspace_bytes() bytes; otherwise as for
  *                 pkv_decode_bf16, like status, empty sequences and unused table entries.
- * A map whose scores hold a NaN, or none above -inf, gives NaN. num_seqs times
- * max_blocks_per_seq * block_size / 16 must stay below 2^31 (else PKV_ERR_UNSUPPORTED).
+ * A map whose scores hold a NaN, or none above -inf, gives NaN. PKV_ERR_UNSUPPORTED, from the
+ * query too: num_seqs times (max_blocks_per_seq * block_size / 16 + 5) of 2^31 or more; a
+ * batch whose 4 bytes per sequence do not fit beside the tiles in a CTA's shared memory (30000
+ * sequences always do; from some 1300 on the table costs CTAs per SM, and so speed).
  */
 pkv_status pkv_decode_diff_workspace_bytes(const pkv_dims* dims, pkv_kv_dtype kv_dtype,
                                            size_t* bytes);

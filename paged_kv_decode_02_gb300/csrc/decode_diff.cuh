@@ -1031,6 +1031,9 @@ DiffKernelInfo make_diff_info() {
       &paged_diff_decode_kernel<D, Path, kStreams, kRows, kStages, kCtas>);
   info.threads = kStreams * kRows * 32;
   info.smem = 1024 + S::kOffPrefix;
+  // the sequences that every instance takes (pagedkv.h), 1 KiB left to static variables and
+  // the system
+  static_assert(1024 + S::kOffPrefix + 4 * (30000 + 4) + 2048 <= 227 * 1024, "batch table");
   info.box = Path::Geo::kBox;
   info.item = Path::Geo::kItem;
   return info;
