@@ -727,9 +727,9 @@ pkv_status make_diff_plan(const pkv_dims* d, int kvt, DiffPlan* out) {
   if (st != PKV_OK) return st;
   if (d->num_q_heads % 2 != 0 || d->num_kv_heads % 2 != 0) return PKV_ERR_SHAPE;
   if ((long long)d->num_seqs * d->num_q_heads >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
-  // the kernel counts items (of 16 or 32 tokens) and their weights in 32 bits
+  // the kernel counts items and their weights in 32 bits
   if ((long long)d->num_seqs *
-          ((long long)d->max_blocks_per_seq * (d->block_size / 16) + kDiffUnitCost) >=
+          ((long long)d->max_blocks_per_seq * (d->block_size / kDiffLeastItem) + kDiffUnitCost) >=
       (1ll << 31))
     return PKV_ERR_UNSUPPORTED;
   if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;

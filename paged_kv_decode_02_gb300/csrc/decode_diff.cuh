@@ -1026,6 +1026,7 @@ __global__ void __launch_bounds__(kStreams * kRows * 32, kCtas)
 template <int D, class Path, int kStreams, int kRows, int kStages, int kCtas>
 DiffKernelInfo make_diff_info() {
   using S = DiffSmem<typename Path::Geo, Path::kNT, kStreams, kRows, kStages>;
+  static_assert(Path::Geo::kItem >= kDiffLeastItem, "more items than the host counts with");
   DiffKernelInfo info{};
   info.fn = reinterpret_cast<const void*>(
       &paged_diff_decode_kernel<D, Path, kStreams, kRows, kStages, kCtas>);
@@ -1035,7 +1036,6 @@ DiffKernelInfo make_diff_info() {
   // the system
   static_assert(1024 + S::kOffPrefix + 4 * (30000 + 4) + 2048 <= 227 * 1024, "batch table");
   info.box = Path::Geo::kBox;
-  info.item = Path::Geo::kItem;
   return info;
 }
 

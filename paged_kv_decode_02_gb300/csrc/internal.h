@@ -277,11 +277,12 @@ struct DiffParams {
   float eps, out_scale;
   unsigned long long timeout_ns;
 };
+// tokens of an instance's work items at least: the host bounds their number by it
+constexpr int kDiffLeastItem = 16;
 struct DiffKernelInfo {
   const void* fn;
   int threads, smem;           // smem: dynamic bytes without the batch's prefix
   int box;                     // tokens per TMA box
-  int item;                    // tokens per work item
 };
 // pairs: query pairs per work unit (at most 16)
 bool select_diff_bf16(int D, int BS, int pairs, DiffKernelInfo* info);
