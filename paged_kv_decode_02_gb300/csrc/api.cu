@@ -30,11 +30,12 @@ constexpr int kTcSplitRows = 64;
 // slower, 3: 1-3 %, 4 and 5: 3-5 %)
 constexpr int kTcHeadCost = 2;
 // differential decode: the same for a unit, in items (a CTA that ends many short units
-// spends 2 to 4 us on each, an item about 1 us). Whole calls on GB300 at cost 1, 2, 3, 4, 5, 6,
-// 8: ragged batch of 64 (64 / 8 heads, bf16) 87.5, 84.0, 81.7, 83.2, 79.6, 80.4, 78.5 us; 256
-// of ~264 tokens (32 / 8, INT8) 49.9, 49.9, 46.5, 48.8, 45.7, 47.0, 47.1; 64 of ~500 (32 / 4,
-// INT8) 28.8, 26.5, 26.1, 24.1, 23.9, 23.3, 23.4; 256 of ~100 (32 / 8, E4M3) 28.2, 27.3, 28.2,
-// 28.2, 28.5, 29.2, 29.9; INT8, 128 x 8192: 350 to 352 at all
+// spends 2 to 4 us on each, an item about 1 us). Whole calls on GB300 at cost 2, 3, 4, 5, 6, 8
+// (the median of three runs, which differ by up to 1 %): ragged batch of 64 (64 / 8 heads, bf16)
+// 81.6, 78.7, 77.5, 75.9, 76.3, 76.2 us; 256 of ~268 tokens (32 / 8, INT8) 44.8, 43.2, 43.3,
+// 43.1, 43.6, 43.0; 64 of ~517 (32 / 4, INT8) 23.1, 22.9, 21.8, 22.2, 22.4, 22.2; 256 of ~103
+// (32 / 8, E4M3) 27.4, 27.3, 27.1, 27.5, 27.3, 28.9; INT8, 128 x 8192: 352.0, 353.1, 353.0,
+// 354.5, 354.6, 352.7. Within 2 % of each's best from 4 to 6: one value for all
 constexpr int kDiffUnitCost = 5;
 // and the least length of a CTA's range, in items: shorter ones leave more records to merge
 // than they save. One sequence (2 / 2 heads, bf16), at 1, 2, 3, 4: 300 tokens 7.9, 8.0, 8.3,

@@ -36,13 +36,13 @@
 // * One-byte caches as in decode.cuh: codes widened exactly to fp16, the K scale on the
 //   fp32 score, the V scale folded into the fp16 weight, there under a power of two that
 //   follows the V scales (DiffPathQ8).
-// * Measured on GB300, head_dim 128, whole calls: INT8, 128 x 8192 tokens, 32/8 heads 347 us
-//   (2217 MB, 6390 GB/s); bf16, 64 ragged contexts (110943 tokens), 64/8 heads 79 us (457 MB,
-//   5800 GB/s: some 3 us before the first tile, 7 us of merge, and the ends of units); E4M3,
-//   one context of 131071, 32/8 heads 51 us (277 MB, 5460 GB/s). With more than 4 query pairs
-//   per KV pair a one-byte cache is bound by the warps' own instructions (8 warps of 255
-//   registers per SM, 41 % of the issue slots): 64 x 2048, 64/8 heads, INT8 70 us (279 MB,
-//   3960 GB/s), E4M3 61 us.
+// * Measured on GB300, head_dim 128, whole calls: INT8, 128 x 8192 tokens, 32/8 heads 346 us
+//   (2217 MB, 6400 GB/s); bf16, 64 ragged contexts (110943 tokens), 64/8 heads 77.5 us (457 MB,
+//   5890 GB/s: some 3 us before the first tile, 7 us of merge, and the ends of units); E4M3,
+//   one context of 131071, 32/8 heads 47.7 to 50 us (277 MB, 5800 to 5540 GB/s). With more than
+//   4 query pairs per KV pair a one-byte cache is bound by the warps' own instructions (8 warps
+//   of 255 registers per SM): 64 x 2048, 64/8 heads, blocks of 16 and 32 tokens, INT8 72.0 and
+//   68.4 us (279 MB, 3870 and 4080 GB/s), E4M3 66.5 and 63.6.
 #pragma once
 
 #include "common.cuh"

@@ -14,13 +14,13 @@
 //
 // Bound by memory: a row is read and written once. Measured on GB300: 8192 tokens of 32/32
 // heads of 128, half rotated, interleaved, bf16 cache 60 us (405 MB, 6740 GB/s); of 32/8
-// heads, normed, 32 us (206 MB, 6420 GB/s); into INT8 37.5 us (189 MB, 5050 GB/s: there the
-// quantiser's instructions count, half the issue slots). D / 16 lanes share a row; a lane holds
-// the two 16-byte chunks that its rotation pairs (chunks j and j + R/16, or 2j and 2j + 1
-// interleaved; R is a multiple of 16), so both elements of every pair are in one lane and
-// only the norm's and the quantiser's row reductions cross lanes. With many rows a lane
-// group takes kU rows of one token: their loads are in flight together and share the
-// token's position, slot and table row.
+// heads, normed, 32 us (206 MB, 6420 GB/s); into INT8 37.1 us (189 MB, 5110 GB/s: there the
+// quantiser's instructions count, half the issue slots), E4M3 and E5M2 36.2. D / 16 lanes
+// share a row; a lane holds the two 16-byte chunks that its rotation pairs (chunks j and
+// j + R/16, or 2j and 2j + 1 interleaved; R is a multiple of 16), so both elements of every
+// pair are in one lane and only the norm's and the quantiser's row reductions cross lanes.
+// With many rows a lane group takes kU rows of one token: their loads are in flight together
+// and share the token's position, slot and table row.
 #include "common.cuh"
 #include "encode.cuh"
 #include "internal.h"
