@@ -296,7 +296,7 @@ pkv_status pkv_decode_fp8(void* out, const void* q, const uint8_t* k_cache,
  * A map whose scores hold a NaN, or none above -inf, gives NaN. PKV_ERR_UNSUPPORTED, from the
  * query too: num_seqs times (max_blocks_per_seq * block_size / 16 + 5) of 2^31 or more; a
  * batch whose 4 bytes per sequence do not fit beside the tiles in a CTA's shared memory (30000
- * sequences always do; from some 1300 on the table costs CTAs per SM, and so speed).
+ * sequences always do; from some 800 on the table costs CTAs per SM, and so speed).
  */
 pkv_status pkv_decode_diff_workspace_bytes(const pkv_dims* dims, pkv_kv_dtype kv_dtype,
                                            size_t* bytes);
