@@ -343,6 +343,12 @@ struct DiffPathBf16 {
 // absmax 1e-3 and 1e-4, and rows above 1e5 overflowed. The price, on GB300 (64 x 2048 tokens of
 // head_dim 128): 64/8 heads INT8 70.7 -> 72.1 us, E4M3 66.0 -> 66.7, E5M2 61.5 -> 64.1; 128/8
 // INT8 118.5 -> 122.2; 0.3 % with up to 4 query pairs, where memory is the bound.
+// One fp16 term per weight, where a bf16 cache has two bf16 ones: a second term takes 64/8
+// heads INT8 from 72.5 to 80.4 us and 128/8 from 123 to 138 (nothing with up to 4 query pairs
+// over long contexts). What it mends, maps that cancel to 3 % of themselves, whose normed
+// difference is off by 0.9 to 1.2 % (0.17 % with two terms, the output's own rounding), is
+// less than what the codes have cost such a difference: 1.2 % (INT8), 4 % (E4M3), 8 % (E5M2)
+// where both maps read the same K rows, 27 % and more where they do not.
 template <int D, int CODE, int BOX, int SUB, int NT>
 struct DiffPathQ8 {
   using Geo = DiffGeom<D, CODE, BOX, SUB>;
