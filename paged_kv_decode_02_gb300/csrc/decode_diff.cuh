@@ -208,12 +208,12 @@ struct DiffState {
     for (int i = 0; i < kMT / 2; ++i) {
       const float4 v = b[i * 32];
       float* d = h ? o[kMT / 2 + i] : o[i];
-      const float2 a = __ffma2_rn(make_float2(v.x, v.y), f, make_float2(d[0], d[1]));
-      const float2 b = __ffma2_rn(make_float2(v.z, v.w), f, make_float2(d[2], d[3]));
-      d[0] = a.x;
-      d[1] = a.y;
-      d[2] = b.x;
-      d[3] = b.y;
+      const float2 lo = __ffma2_rn(make_float2(v.x, v.y), f, make_float2(d[0], d[1]));
+      const float2 hi = __ffma2_rn(make_float2(v.z, v.w), f, make_float2(d[2], d[3]));
+      d[0] = lo.x;
+      d[1] = lo.y;
+      d[2] = hi.x;
+      d[3] = hi.y;
     }
   }
 };
@@ -1038,8 +1038,7 @@ DiffKernelInfo make_diff_info() {
       &paged_diff_decode_kernel<D, Path, kStreams, kRows, kStages, kCtas>);
   info.threads = kStreams * kRows * 32;
   info.smem = 1024 + S::kOffPrefix;
-  // the sequences that every instance takes (pagedkv.h), 1 KiB left to static variables and
-  // the system
+  // the sequences that every instance takes (pagedkv.h), 2 KiB left to static variables
   static_assert(1024 + S::kOffPrefix + 4 * (30000 + 4) + 2048 <= 227 * 1024, "batch table");
   info.box = Path::Geo::kBox;
   return info;
