@@ -84,6 +84,7 @@ typedef struct pkv_dims {
 #define PKV_DEV_TIMEOUT         0x4  /* a shared-memory copy did not complete in time */
 #define PKV_DEV_BAD_PREFIX      0x8  /* cascade: a table does not start with the shared prefix */
 #define PKV_DEV_BAD_POSITION    0x10 /* rotate-and-append: a position outside the cos/sin table */
+#define PKV_DEV_NO_BLOCKS       0x20 /* resize: blocks or token rows ran out, or the free list does not fit */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* pkv_status_string(pkv_status status);
@@ -127,6 +128,70 @@ pkv_status pkv_append_bf16(const void* k, const void* v, void* k_cache, void* v_
 pkv_status pkv_append_int8(const void* k, const void* v, int8_t* k_cache, int8_t* v_cache,
                            float* k_scale, float* v_scale, const int64_t* slot_mapping,
                            int32_t num_tokens, const pkv_dims* dims, pkv_stream_t stream);
+
+/*
+ * pkv_resize_sequences -- block tables, slots and positions from lengths, on the GPU: every
+ * sequence goes from context_lens[s] cached tokens to target_lens[s]. A sequence of L tokens
+ * holds the first ceil(L / block_size) entries of its table row ("块管理器：分页如何运作",
+ * chenk.top page: the block manager appends blocks as a request grows and takes them back).
+ *   growing    new blocks from the list into the next entries of the row; each new token n =
+ *              context_lens[s] .. target_lens[s] - 1 gets positions[r] = n and slot_mapping[r]
+ *              = table[s, n / block_size] * block_size + n % block_size, at row r =
+ *              token_offsets[s] + n - context_lens[s]: what pkv_append_* and
+ *              pkv_rotate_append_* take.
+ *   shrinking  the entries past the new length give their blocks back (a finished request:
+ *              target 0; a verified draft: what was accepted). Entries keep their old ids, and
+ *              cached rows are not touched. A block that several sequences share must not be
+ *              given back while one of them lives: shrink to the shared prefix at most.
+ *   free_blocks  [free_capacity] int32, a stack: the first *free_count ids are free. All blocks
+ *              given back in a call go on it, the last of the last sequence first, before the
+ *              growing sequences take theirs in order off its end; so shrinking what a call has
+ *              grown restores the list. Ids are moved and not looked at.
+ *   block_tables, context_lens, free_blocks, free_count  device, updated in place.
+ *   target_lens    [num_seqs] int32; must not overlap context_lens.
+ *   slot_mapping, positions  [num_tokens] int64, written whole: rows past the last new token,
+ *              and those of a sequence that could not grow, get slot -1 (which the appends
+ *              skip) and position 0. May be NULL when num_tokens is 0.
+ *   token_offsets  [num_seqs + 1] int32, written: the rows of sequence s are
+ *              token_offsets[s] .. token_offsets[s + 1] - 1 (exclusive sums of the tokens asked
+ *              for).
+ *   status     optional device int32. PKV_DEV_BAD_CONTEXT_LEN: a length that is negative or
+ *              past the table row; the sequence stays as it was and counts no tokens.
+ *              PKV_DEV_NO_BLOCKS: a sequence whose blocks or token rows are not there stays as it was
+ *              (as do later ones that lack the same; earlier ones have grown); or *free_count
+ *              was outside [0, free_capacity] (taken as the nearer end), or the list could not
+ *              hold a block given back (the block is lost).
+ * num_seqs up to 16384, and num_seqs * max_blocks_per_seq and free_capacity below 2^30 (else
+ * PKV_ERR_UNSUPPORTED). num_seqs == 0 is a no-op returning PKV_OK. dims.num_q_heads,
+ * num_kv_heads, head_dim and num_blocks are not used beyond the common checks.
+ */
+pkv_status pkv_resize_sequences(int32_t* block_tables, int32_t* context_lens,
+                                const int32_t* target_lens, int32_t* free_blocks,
+                                int32_t* free_count, int32_t free_capacity,
+                                int64_t* slot_mapping, int64_t* positions,
+                                int32_t* token_offsets, int32_t num_tokens,
+                                const pkv_dims* dims, int32_t* status, pkv_stream_t stream);
+
+/*
+ * pkv_keep_tokens -- the kept tokens of a draft move up in the cache: cached row
+ * base_lens[s] + path[s, i] of sequence s becomes row base_lens[s] + i, for i <
+ * kept_lens[s], K and V (and scales) of every KV head ("推测解码", chenk.top page: of the drafted
+ * tokens the accepted ones stay; of a tree one path does). Bit-exact; rows past the kept ones
+ * stay as they were. pkv_resize_sequences then gives the rest of the draft's blocks back.
+ *   path       [num_seqs, path_width] int32, device; a sequence's used entries rise strictly
+ *              and are not negative.
+ *   kept_lens  [num_seqs] int32, device, 0 .. path_width; NULL: path_width for all.
+ *   k_scale, v_scale  one-byte caches only (ignored for bf16).
+ *   status     optional device int32: PKV_DEV_BAD_CONTEXT_LEN (a length, or a path that does
+ *              not rise or leaves the table row), PKV_DEV_BAD_BLOCK_ID; such a sequence stays as
+ *              it was. No row may be reached through two sequences' moves at once.
+ * num_seqs == 0 or path_width == 0 is a no-op returning PKV_OK.
+ */
+pkv_status pkv_keep_tokens(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                           const int32_t* block_tables, const int32_t* base_lens,
+                           const int32_t* path, const int32_t* kept_lens, int32_t path_width,
+                           pkv_kv_dtype kv_dtype, const pkv_dims* dims, int32_t* status,
+                           pkv_stream_t stream);
 
 /* Norms and position rotation of pkv_rotate_append_*. Strides are elements between the
  * rows of consecutive tokens (multiples of 8, at least heads * head_dim: q, k and v may be
@@ -429,6 +494,95 @@ pkv_status pkv_decode_multi_q8(void* out, const void* q, const void* k_cache,
                                int32_t q_len, float scale, pkv_kv_dtype kv_dtype,
                                const pkv_dims* dims, void* workspace, size_t workspace_bytes,
                                int32_t* status, pkv_stream_t stream);
+
+/*
+ * pkv_decode_tree_bf16 -- pkv_decode_multi_bf16 for a tree of drafted tokens in place of a
+ * chain: the verification pass of speculative decoding with several candidates per position
+ * ("推测解码", chenk.top page). The last t = tree_lens[s] cached tokens of sequence s are the
+ * tree's nodes, appended in node order (node i at position context_lens[s] - t + i of the
+ * cache, whatever position its rotation used); node i attends to every token before the nodes
+ * and to node j where bit j of its mask is set (its own bit included, if it is to see itself):
+ *   out[s, i, h, :] = softmax(scale * K q[s, i, h]) V over those tokens.
+ *   q, out     [num_seqs, q_len, num_q_heads, head_dim] bf16.
+ *   q_len      1 .. PKV_MAX_QUERY_LEN: the most nodes of a tree.
+ *   tree_mask  [num_seqs, q_len, ceil(q_len / 64)] 64-bit words, device: bit j % 64 of word
+ *              j / 64 of a node's row is node j's; bits of nodes at or past t are ignored.
+ *   tree_lens  [num_seqs] int32, device: nodes of each tree, 0 .. q_len; NULL: q_len for all.
+ *              Rows i >= tree_lens[s] of out get zeros, as does a node that sees no token.
+ *   workspace  at least pkv_decode_tree_workspace_bytes(dims, q_len, kv_dtype) bytes, as for
+ *              pkv_decode_bf16.
+ *   status     as for pkv_decode_multi_bf16, a tree_lens entry outside 0 .. q_len and a sequence
+ *              with 0 < context_len < tree_lens[s] included. Without it, such an entry is taken
+ *              as the nearest length that fits.
+ * Rows are (node, head) pairs in tiles of up to 128 on the tensor cores, for every row count.
+ * Cached V values a node does not see must be finite (their weight is 0).
+ */
+pkv_status pkv_decode_tree_workspace_bytes(const pkv_dims* dims, int32_t q_len,
+                                           pkv_kv_dtype kv_dtype, size_t* bytes);
+pkv_status pkv_decode_tree_bf16(void* out, const void* q, const void* k_cache,
+                                const void* v_cache, const int32_t* block_tables,
+                                const int32_t* context_lens, const uint64_t* tree_mask,
+                                const int32_t* tree_lens, int32_t q_len, float scale,
+                                const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                                int32_t* status, pkv_stream_t stream);
+
+/*
+ * pkv_decode_tree_q8 -- pkv_decode_tree_bf16 over a one-byte cache (kv_dtype PKV_KV_INT8,
+ * PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2, else PKV_ERR_DTYPE): codes widened exactly, the K scale
+ * on the fp32 score, V rounded once to fp16 (code x scale: V rows' absmax below 65504, and
+ * above 1e-3 or so for their small values to keep their precision), fp16 softmax weights.
+ */
+pkv_status pkv_decode_tree_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              const uint64_t* tree_mask, const int32_t* tree_lens, int32_t q_len,
+                              float scale, pkv_kv_dtype kv_dtype, const pkv_dims* dims,
+                              void* workspace, size_t workspace_bytes, int32_t* status,
+                              pkv_stream_t stream);
+
+/* Sizes of pkv_prompt_attention_bf16. Strides are elements between the rows of consecutive
+ * tokens (multiples of 8, at least heads * head_dim: q, k and v may be parts of one fused
+ * projection's output); the rows of a token's heads are contiguous. */
+typedef struct pkv_prompt_dims {
+  int32_t num_seqs;
+  int32_t num_q_heads;         /* Hq; a multiple of Hkv, at most 128 Hkv                */
+  int32_t num_kv_heads;        /* Hkv                                                   */
+  int32_t head_dim;            /* D: 64 or 128                                          */
+  int32_t num_q_tokens;        /* rows of q and out                                     */
+  int32_t num_kv_tokens;       /* rows of k and v                                       */
+  int64_t out_stride, q_stride, k_stride, v_stride;
+} pkv_prompt_dims;
+
+/*
+ * pkv_prompt_attention_bf16 -- causal attention of whole prompts, before or beside their write
+ * into the cache: the prefill phase ("两个特性截然不同的阶段", chenk.top page), sequences of
+ * different lengths packed one after the other. Sequence s has the nq = q_offsets[s + 1] -
+ * q_offsets[s] query rows and the nk = kv_offsets[s + 1] - kv_offsets[s] key and value rows
+ * from its offsets on; the queries are its last tokens: query i sees keys j <= nk - nq + i.
+ *   out[q_offsets[s] + i, h, :] = softmax(scale * K q[.., i, h]) V over those keys
+ * (zeros where there is none). nk == nq: whole prompts. nk > nq: a chunk of chunked prefill
+ * ("Orca 的迭代级调度", same page) over keys and values that pkv_gather_tokens read back.
+ *   q, out        [num_q_tokens, Hq, D] bf16; out must not overlap an input.
+ *   k, v          [num_kv_tokens, Hkv, D] bf16.
+ *   q_offsets, kv_offsets  [num_seqs + 1] int32, device, never falling (they may be the same
+ *                 array); what pkv_resize_sequences writes. Rows of out outside [q_offsets[0],
+ *                 q_offsets[num_seqs]) are left as they were.
+ *   workspace     at least pkv_prompt_workspace_bytes(dims) bytes, 256-byte aligned; its
+ *                 contents need no initialisation. Calls that share it must not overlap.
+ *   status        optional device int32: PKV_DEV_BAD_CONTEXT_LEN for a sequence whose offsets
+ *                 fall or leave the arrays (its rows are not written); PKV_DEV_TIMEOUT.
+ * fp32 scores, softmax statistics and sums; softmax weights rounded once to bf16 for P.V; bf16
+ * output. Values of keys a query does not see must be finite where they share a tile of 128
+ * keys with one it sees (their weight is 0); rows outside a sequence may hold anything.
+ * num_seqs == 0 or num_q_tokens == 0 is a no-op returning PKV_OK. Token counts of 2^30 and more
+ * and more than 128 query heads per KV head: PKV_ERR_UNSUPPORTED.
+ */
+pkv_status pkv_prompt_workspace_bytes(const pkv_prompt_dims* dims, size_t* bytes);
+pkv_status pkv_prompt_attention_bf16(void* out, const void* q, const void* k, const void* v,
+                                     const int32_t* q_offsets, const int32_t* kv_offsets,
+                                     float scale, const pkv_prompt_dims* dims, void* workspace,
+                                     size_t workspace_bytes, int32_t* status,
+                                     pkv_stream_t stream);
 
 /*
  * pkv_decode_cascade_bf16 -- pkv_decode_bf16 for a batch whose sequences all start

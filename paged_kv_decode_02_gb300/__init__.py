@@ -15,6 +15,9 @@ _API = (
     "cascade_workspace_bytes", "multi_workspace_bytes", "multi_q8_workspace_bytes",
     "paged_kv_rotate_append", "paged_kv_rotate_append_q8", "paged_kv_gather",
     "paged_decode_attention_diff", "paged_decode_attention_diff_q8", "diff_workspace_bytes",
+    "paged_kv_resize", "paged_kv_keep", "paged_decode_attention_tree",
+    "paged_decode_attention_tree_q8", "tree_workspace_bytes", "prompt_attention",
+    "prompt_workspace_bytes",
     "copy_blocks", "swap_out", "swap_in",
     "decode_workspace_bytes", "library_path", "load_library", "PagedKVError",
     "Status", "Dims",

@@ -41,6 +41,10 @@ constexpr int kDiffUnitCost = 5;
 // than they save. One sequence (2 / 2 heads, bf16), at 1, 2, 3, 4: 300 tokens 7.9, 8.0, 8.3,
 // 8.6 us, 8192 tokens 11.7, 10.0, 10.0, 9.7; 3 of ~700 (32 / 8, E4M3): 11.8, 10.8, 10.6, 11.2
 constexpr int kDiffMinRange = 2;
+// prompt attention: what ending an item costs a CTA, and the least length of its stretch, both
+// in keys of a 256-row item
+constexpr int kPromptItemCost = 256;
+constexpr int kPromptMinRange = 512;
 // cascade decode: the prefix kernel runs on about 1/kCascadePrefixShare of the SMs
 constexpr int kCascadePrefixShare = 3;
 
@@ -162,6 +166,45 @@ bool cache_map(CUtensorMap* map, const void* base, bool q8, int D, long long row
   return cached_map(map, MapKey{base, rows, D, BS, q8 ? 1 : 0, 0});
 }
 
+// 3-D map over dense rows [tokens, heads, D], tokens `stride` elements apart; a box is
+// box_tokens x box_heads rows by one 128-byte swizzle span. Kept like the cache maps.
+struct RowsKey {
+  const void* base;
+  long long stride;
+  int tokens, heads, D, box_heads, box_tokens;
+};
+bool rows_map(CUtensorMap* map, const RowsKey& key) {
+  static std::mutex mu;
+  static RowsKey keys[kMapCache];
+  static CUtensorMap maps[kMapCache];
+  static int count = 0, next = 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < count; ++i) {
+    const RowsKey& k = keys[i];
+    if (k.base == key.base && k.stride == key.stride && k.tokens == key.tokens &&
+        k.heads == key.heads && k.D == key.D && k.box_heads == key.box_heads &&
+        k.box_tokens == key.box_tokens) {
+      *map = maps[i];
+      return true;
+    }
+  }
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cuuint64_t(key.D), cuuint64_t(key.heads), cuuint64_t(key.tokens)};
+  cuuint64_t strides[2] = {cuuint64_t(key.D) * 2, cuuint64_t(key.stride) * 2};
+  cuuint32_t box[3] = {64u, cuuint32_t(key.box_heads), cuuint32_t(key.box_tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(key.base), dims, strides,
+          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  keys[next] = key;
+  maps[next] = *map;
+  next = (next + 1) % kMapCache;
+  if (count < kMapCache) ++count;
+  return true;
+}
+
 // rows: blocks x heads
 bool pair_map(CUtensorMap* map, const void* base, bool q8, int D, long long rows, int BS,
               int box_tokens) {
@@ -197,10 +240,10 @@ pkv_status check_dims(const pkv_dims* d) {
 // sets a kernel attribute, which costs tens of microseconds, so recent plans are kept.
 struct PlanKey {
   pkv_dims d;
-  int kvt, q_len, device, pair, sm_cap;
+  int kvt, q_len, device, pair, sm_cap, tree;
   bool operator==(const PlanKey& o) const {
     return std::memcmp(&d, &o.d, sizeof(d)) == 0 && kvt == o.kvt && q_len == o.q_len &&
-           device == o.device && pair == o.pair && sm_cap == o.sm_cap;
+           device == o.device && pair == o.pair && sm_cap == o.sm_cap && tree == o.tree;
   }
 };
 constexpr int kPlanCache = 16;
@@ -210,13 +253,14 @@ Plan g_plans[kPlanCache];
 int g_plan_count = 0, g_plan_next = 0;
 
 pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, int sm_cap,
-                              Plan* pl);
+                              bool tree, Plan* pl);
 
 // q_len > 1: the causal multi-query decode (bf16 caches). pair: 16-token blocks go in
 // pairs on the tensor-core paths (pairs start after a skipped prefix). sm_cap > 0: size
-// the grid for that many SMs (the rest run another kernel at the same time).
+// the grid for that many SMs (the rest run another kernel at the same time). tree: the new
+// tokens form a tree (q_len of any size).
 pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool pair = true,
-                     int sm_cap = 0) {
+                     int sm_cap = 0, bool tree = false) {
   pkv_status st = check_dims(d);
   if (st != PKV_OK) return st;
   int dev = 0;
@@ -229,13 +273,14 @@ pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool p
   key.device = dev;
   key.pair = pair ? 1 : 0;
   key.sm_cap = sm_cap;
+  key.tree = tree ? 1 : 0;
   std::lock_guard<std::mutex> lock(g_plan_mu);
   for (int i = 0; i < g_plan_count; ++i)
     if (g_plan_keys[i] == key) {
       *pl = g_plans[i];
       return PKV_OK;
     }
-  st = make_plan_uncached(d, kvt, q_len, pair, sm_cap, pl);
+  st = make_plan_uncached(d, kvt, q_len, pair, sm_cap, tree, pl);
   if (st != PKV_OK) return st;
   g_plan_keys[g_plan_next] = key;
   g_plans[g_plan_next] = *pl;
@@ -245,7 +290,7 @@ pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool p
 }
 
 pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, int sm_cap,
-                              Plan* pl) {
+                              bool tree, Plan* pl) {
   Plan P{};
   P.g = d->num_q_heads / d->num_kv_heads;
   // query rows per KV head: (new token, group member) pairs, split into work units of
@@ -264,7 +309,14 @@ pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, 
   P.HU = d->num_kv_heads * P.nsg;
   const int simt = mma ? 0 : P.g;
   bool found = false;
-  if (q_len > 1) {
+  if (tree) {
+    if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
+    P.nsg = (rows + kTcTileRows - 1) / kTcTileRows;
+    P.gs = (rows + P.nsg - 1) / P.nsg;
+    P.HU = d->num_kv_heads * P.nsg;
+    found = select_tree(d->head_dim, d->block_size, rows > kTcTileRows, rows <= kTcSplitRows, kvt,
+                        &P.k);
+  } else if (q_len > 1) {
     if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
     // KV heads with 48 or more query rows go through the tcgen05 kernel, fewer rows
     // through the mma.sync path: measured on GB300 with the spec-70b lengths, tcgen05 vs
@@ -354,7 +406,8 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
                       const int32_t* block_tables, const int32_t* context_lens, float scale,
                       const pkv_dims* d, void* workspace, size_t workspace_bytes,
                       int32_t* status, cudaStream_t stream, int q_len = 1,
-                      unsigned long long* counters = nullptr, size_t counter_words = 0) {
+                      unsigned long long* counters = nullptr, size_t counter_words = 0,
+                      const uint64_t* tree_mask = nullptr, const int32_t* tree_lens = nullptr) {
   pkv_status st = check_dims(d);
   if (st != PKV_OK) return st;
   if (q_len < 1 || q_len > kMaxQueryLen) return PKV_ERR_SHAPE;
@@ -367,7 +420,7 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
       (q8 && (!aligned16(k_scale) || !aligned16(v_scale))))
     return PKV_ERR_ALIGNMENT;
   Plan P;
-  st = make_plan(d, kvt, &P, q_len);
+  st = make_plan(d, kvt, &P, q_len, true, 0, tree_mask != nullptr);
   if (st != PKV_OK) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < P.ws_bytes)
@@ -417,6 +470,9 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
   p.unit_slot0 = -1;
   p.q_len = q_len;
   p.beta = P.k.tc ? kTcHeadCost : 0;
+  p.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  p.tree_lens = tree_lens;
+  p.tree_words = 2 * ((q_len + 63) / 64);
 
   // tcgen05 kernel: whole units leave through TMA tensor stores of g-row boxes when g is
   // 8, 16 or 32 and the row tiles start on tokens (each box then starts on a 1024-byte
@@ -457,6 +513,7 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
   m.W = P.k.tc ? P.W : P.W / P.nsg;  // CTAs, or workers of nsg warps
   m.beta = p.beta;
   m.wprefix = p.prefix_out + (d->num_seqs + 1);
+  m.tree_lens = tree_lens;
   if (!p.fixup) launch_merge(m, stream);  // else cut units were folded in the kernel
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   return PKV_OK;
@@ -712,6 +769,116 @@ pkv_status run_rotate(int kvt, void* out, const void* q, const void* k, const vo
   p.eps = ro->eps;
   return launch_rotate_append(code_of(kvt), d->head_dim, p, stream) == cudaSuccess ? PKV_OK
                                                                                   : PKV_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------
+// Prompt attention
+// ---------------------------------------------------------------------------
+// workspace: [cuts (G)][records' (m, l), 2 per CTA of 2 x 128 rows][records' o]
+struct PromptPlan {
+  PromptKernelInfo k;
+  int G;
+  size_t off_ml, off_o, ws_bytes;
+};
+
+pkv_status check_prompt(const pkv_prompt_dims* d, PromptKernelInfo* k) {
+  if (!d) return PKV_ERR_NULL;
+  if (d->num_seqs < 0 || d->num_q_heads <= 0 || d->num_kv_heads <= 0 || d->head_dim <= 0 ||
+      d->num_q_tokens < 0 || d->num_kv_tokens < 0 || d->num_q_heads % d->num_kv_heads != 0)
+    return PKV_ERR_SHAPE;
+  if (!select_prompt(d->head_dim, k)) return PKV_ERR_UNSUPPORTED;
+  if (d->num_q_heads / d->num_kv_heads > 128 || d->num_q_tokens >= (1 << 30) ||
+      d->num_kv_tokens >= (1 << 30))
+    return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+
+pkv_status make_prompt_plan(const pkv_prompt_dims* d, PromptPlan* P) {
+  pkv_status st = check_prompt(d, &P->k);
+  if (st != PKV_OK) return st;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  P->G = sms;  // all of a CTA's TMEM and shared memory: one per SM
+  const size_t rows = size_t(2) * P->G * 256;
+  P->off_ml = align_up(size_t(P->G) * sizeof(PromptCut), 256);
+  P->off_o = align_up(P->off_ml + rows * 8, 256);
+  P->ws_bytes = align_up(P->off_o + rows * d->head_dim * 4, 256);
+  return PKV_OK;
+}
+
+pkv_status run_prompt(void* out, const void* q, const void* k, const void* v,
+                      const int32_t* q_offsets, const int32_t* kv_offsets, float scale,
+                      const pkv_prompt_dims* d, void* workspace, size_t workspace_bytes,
+                      int32_t* status, cudaStream_t stream) {
+  PromptPlan P;
+  pkv_status st = check_prompt(d, &P.k);
+  if (st != PKV_OK) return st;
+  const int64_t strides[4] = {d->out_stride, d->q_stride, d->k_stride, d->v_stride};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t row = int64_t(i < 2 ? d->num_q_heads : d->num_kv_heads) * d->head_dim;
+    const int tokens = i < 2 ? d->num_q_tokens : d->num_kv_tokens;
+    if (strides[i] < row && tokens > 1) return PKV_ERR_SHAPE;
+    if (strides[i] % 8 != 0) return PKV_ERR_ALIGNMENT;
+    // the tensor maps' strides end at 2^40 bytes
+    if (strides[i] < 0 || strides[i] >= (int64_t(1) << 38)) return PKV_ERR_UNSUPPORTED;
+  }
+  if (d->num_seqs == 0 || d->num_q_tokens == 0) return PKV_OK;
+  const bool keys = d->num_kv_tokens > 0;
+  if (!out || !q || !q_offsets || !kv_offsets || (keys && (!k || !v))) return PKV_ERR_NULL;
+  if (!aligned16(out) || !aligned16(q) || (keys && (!aligned16(k) || !aligned16(v))))
+    return PKV_ERR_ALIGNMENT;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return PKV_ERR_WORKSPACE;
+  st = make_prompt_plan(d, &P);
+  if (st != PKV_OK) return st;
+  if (workspace_bytes < P.ws_bytes) return PKV_ERR_WORKSPACE;
+  const int g = d->num_q_heads / d->num_kv_heads;
+  const int tpt = 128 / g;
+  // a single row's stride is never used: any that the map takes
+  auto stride_of = [&](int64_t s, int tokens, int heads) {
+    return tokens > 1 ? s : int64_t(heads) * d->head_dim;
+  };
+  CUtensorMap tmq, tmk, tmv;
+  const long long qs = stride_of(d->q_stride, d->num_q_tokens, d->num_q_heads);
+  // without keys, any rows that can be read stand in for them: every one is masked
+  const int tk = keys ? d->num_kv_tokens : d->num_q_tokens;
+  const long long ks = keys ? stride_of(d->k_stride, tk, d->num_kv_heads) : qs;
+  const long long vs = keys ? stride_of(d->v_stride, tk, d->num_kv_heads) : qs;
+  if (!rows_map(&tmq, RowsKey{q, qs, d->num_q_tokens, d->num_q_heads, d->head_dim, g, tpt}) ||
+      !rows_map(&tmk, RowsKey{keys ? k : q, ks, tk, d->num_kv_heads, d->head_dim, 1, 128}) ||
+      !rows_map(&tmv, RowsKey{keys ? v : q, vs, tk, d->num_kv_heads, d->head_dim, 1, 128}))
+    return PKV_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  PromptParams p{};
+  p.out = out;
+  p.q_offsets = q_offsets;
+  p.kv_offsets = kv_offsets;
+  p.cuts = reinterpret_cast<PromptCut*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + P.off_ml);
+  p.part_o = reinterpret_cast<float*>(ws + P.off_o);
+  p.status = status;
+  p.out_stride = d->out_stride;
+  p.B = d->num_seqs;
+  p.Hkv = d->num_kv_heads;
+  p.g = g;
+  p.Tq = d->num_q_tokens;
+  p.Tk = d->num_kv_tokens;
+  p.D = d->head_dim;
+  p.tpt = tpt;
+  p.item_cost = kPromptItemCost;
+  p.min_range = kPromptMinRange;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = kTimeoutNs;
+  if (cudaFuncSetAttribute(P.k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, P.k.smem) !=
+      cudaSuccess)
+    return PKV_ERR_CUDA;
+  void* args[] = {&tmq, &tmk, &tmv, &p};
+  if (launch_pdl(P.k.fn, dim3(P.G), dim3(P.k.threads), args, P.k.smem, stream) != cudaSuccess ||
+      launch_prompt_merge(p, P.G, stream) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  return PKV_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -1218,6 +1385,137 @@ pkv_status pkv_gather_tokens(void* out_k, void* out_v, const void* k_cache, cons
                        reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PKV_OK
              : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_resize_sequences(int32_t* block_tables, int32_t* context_lens,
+                                const int32_t* target_lens, int32_t* free_blocks,
+                                int32_t* free_count, int32_t free_capacity,
+                                int64_t* slot_mapping, int64_t* positions,
+                                int32_t* token_offsets, int32_t num_tokens,
+                                const pkv_dims* dims, int32_t* status, pkv_stream_t stream) {
+  pkv_status st = check_dims(dims);
+  if (st != PKV_OK) return st;
+  if (free_capacity < 0 || num_tokens < 0) return PKV_ERR_SHAPE;
+  if (dims->num_seqs > kResizeMaxSeqs || free_capacity >= (1 << 30) ||
+      (long long)dims->num_seqs * dims->max_blocks_per_seq >= (1ll << 30) ||
+      (long long)dims->max_blocks_per_seq * dims->block_size >= (1ll << 31) - 32)
+    return PKV_ERR_UNSUPPORTED;
+  if (dims->num_seqs == 0) return PKV_OK;
+  if (!block_tables || !context_lens || !target_lens || !free_count || !token_offsets ||
+      (free_capacity > 0 && !free_blocks) || (num_tokens > 0 && (!slot_mapping || !positions)))
+    return PKV_ERR_NULL;
+  ResizeParams p{};
+  p.tables = block_tables;
+  p.lens = context_lens;
+  p.targets = target_lens;
+  p.free_list = free_blocks;
+  p.free_count = free_count;
+  p.slots = slot_mapping;
+  p.positions = positions;
+  p.offsets = token_offsets;
+  p.status = status;
+  p.B = dims->num_seqs;
+  p.MBS = dims->max_blocks_per_seq;
+  p.F = free_capacity;
+  p.T = num_tokens;
+  p.bs_log2 = dims->block_size == 32 ? 5 : 4;
+  return launch_resize(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PKV_OK
+                                                                                : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_keep_tokens(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                           const int32_t* block_tables, const int32_t* base_lens,
+                           const int32_t* path, const int32_t* kept_lens, int32_t path_width,
+                           pkv_kv_dtype kv_dtype, const pkv_dims* dims, int32_t* status,
+                           pkv_stream_t stream) {
+  pkv_status st = check_dims(dims);
+  if (st != PKV_OK) return st;
+  if (kv_dtype < PKV_KV_BF16 || kv_dtype > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
+  if (path_width < 0) return PKV_ERR_SHAPE;
+  if ((long long)dims->num_seqs * dims->num_kv_heads >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
+  if (dims->num_seqs == 0 || path_width == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !block_tables || !base_lens || !path) return PKV_ERR_NULL;
+  const bool q8 = kv_dtype != PKV_KV_BF16;
+  if (q8 && (!k_scale || !v_scale)) return PKV_ERR_NULL;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGNMENT;
+  KeepParams p{};
+  p.kc = static_cast<uint8_t*>(k_cache);
+  p.vc = static_cast<uint8_t*>(v_cache);
+  p.ks = q8 ? k_scale : nullptr;
+  p.vs = q8 ? v_scale : nullptr;
+  p.tables = block_tables;
+  p.base = base_lens;
+  p.path = path;
+  p.kept = kept_lens;
+  p.status = status;
+  p.B = dims->num_seqs;
+  p.Hkv = dims->num_kv_heads;
+  p.NB = dims->num_blocks;
+  p.MBS = dims->max_blocks_per_seq;
+  p.width = path_width;
+  p.bs_log2 = dims->block_size == 32 ? 5 : 4;
+  return launch_keep(dims->head_dim * (q8 ? 1 : 2), p,
+                     reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PKV_OK
+             : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_decode_tree_workspace_bytes(const pkv_dims* dims, int32_t q_len,
+                                           pkv_kv_dtype kv_dtype, size_t* bytes) {
+  if (!bytes) return PKV_ERR_NULL;
+  if (q_len < 1 || q_len > kMaxQueryLen) return PKV_ERR_SHAPE;
+  if (kv_dtype < PKV_KV_BF16 || kv_dtype > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
+  Plan P;
+  pkv_status st = make_plan(dims, kv_dtype, &P, q_len, true, 0, true);
+  if (st != PKV_OK) return st;
+  *bytes = P.ws_bytes;
+  return PKV_OK;
+}
+
+pkv_status pkv_decode_tree_bf16(void* out, const void* q, const void* k_cache,
+                                const void* v_cache, const int32_t* block_tables,
+                                const int32_t* context_lens, const uint64_t* tree_mask,
+                                const int32_t* tree_lens, int32_t q_len, float scale,
+                                const pkv_dims* dims, void* workspace, size_t workspace_bytes,
+                                int32_t* status, pkv_stream_t stream) {
+  if (!tree_mask) return PKV_ERR_NULL;
+  return run_decode(PKV_KV_BF16, out, q, k_cache, v_cache, nullptr, nullptr, block_tables,
+                    context_lens, scale, dims, workspace, workspace_bytes, status,
+                    reinterpret_cast<cudaStream_t>(stream), q_len, nullptr, 0, tree_mask,
+                    tree_lens);
+}
+
+pkv_status pkv_decode_tree_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              const uint64_t* tree_mask, const int32_t* tree_lens, int32_t q_len,
+                              float scale, pkv_kv_dtype kv_dtype, const pkv_dims* dims,
+                              void* workspace, size_t workspace_bytes, int32_t* status,
+                              pkv_stream_t stream) {
+  if (code_of(kv_dtype) < 0) return PKV_ERR_DTYPE;
+  if (!tree_mask) return PKV_ERR_NULL;
+  return run_decode(kv_dtype, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                    context_lens, scale, dims, workspace, workspace_bytes, status,
+                    reinterpret_cast<cudaStream_t>(stream), q_len, nullptr, 0, tree_mask,
+                    tree_lens);
+}
+
+pkv_status pkv_prompt_workspace_bytes(const pkv_prompt_dims* dims, size_t* bytes) {
+  if (!bytes) return PKV_ERR_NULL;
+  PromptPlan P;
+  pkv_status st = make_prompt_plan(dims, &P);
+  if (st != PKV_OK) return st;
+  *bytes = P.ws_bytes;
+  return PKV_OK;
+}
+
+pkv_status pkv_prompt_attention_bf16(void* out, const void* q, const void* k, const void* v,
+                                     const int32_t* q_offsets, const int32_t* kv_offsets,
+                                     float scale, const pkv_prompt_dims* dims, void* workspace,
+                                     size_t workspace_bytes, int32_t* status,
+                                     pkv_stream_t stream) {
+  return run_prompt(out, q, k, v, q_offsets, kv_offsets, scale, dims, workspace, workspace_bytes,
+                    status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 pkv_status pkv_decode_diff_workspace_bytes(const pkv_dims* dims, pkv_kv_dtype kv_dtype,

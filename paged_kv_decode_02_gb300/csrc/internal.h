@@ -41,6 +41,9 @@ struct DecodeParams {
   int HU;                      // work units per sequence (Hkv * nsg)
   float scale_log2;            // softmax scale * log2(e)
   unsigned long long timeout_ns;
+  const uint32_t* tree_mask;   // tree decode: [B, q_len, tree_words] node masks, 32 nodes a word
+  const int32_t* tree_lens;    // [B] nodes of each tree, or NULL: q_len
+  int tree_words;
 };
 
 // Parameters of the shared-prefix (cascade) kernel: for KV head h, the B*g query rows
@@ -104,6 +107,7 @@ struct MergeParams {
   int W;                       // decode workers (groups of nsg warps, or tcgen05 CTAs)
   const int32_t* wprefix;      // beta > 0: per-sequence prefix of tiles + beta * [tiles > 0]
   int beta;                    // as in DecodeParams (0: workers cut the plain order)
+  const int32_t* tree_lens;    // tree decode: [B] new tokens of each sequence, or NULL: q_len
 };
 
 void launch_merge(const MergeParams& p, cudaStream_t stream);
@@ -161,6 +165,13 @@ bool select_decode_tc(int D, int BS, bool row_tiles, bool split, int kvt,
 bool select_decode_tc_int8(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 bool select_decode_tc_e4m3(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 bool select_decode_tc_e5m2(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
+
+// The same kernels for a tree of new tokens (DecodeParams::tree_mask), one table per code in
+// tree_bf16.cu, tree_int8.cu, tree_e4m3.cu and tree_e5m2.cu.
+bool select_tree(int D, int BS, bool row_tiles, bool split, int kvt, DecodeKernelInfo* info);
+bool select_tree_int8(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
+bool select_tree_e4m3(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
+bool select_tree_e5m2(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 
 bool select_decode_int8(int D, int BS, int simt_heads, DecodeKernelInfo* info,
                         bool pair = false);
@@ -248,6 +259,71 @@ struct GatherParams {
 };
 // code as for launch_rotate_append
 cudaError_t launch_gather(int code, int D, const GatherParams& p, cudaStream_t stream);
+
+// Parameters of the resize of sequences (resize.cu).
+struct ResizeParams {
+  int32_t* tables;             // [B, MBS]
+  int32_t* lens;               // [B] tokens now, set to the targets
+  const int32_t* targets;      // [B]
+  int32_t* free_list;          // [F], the first *free_count entries free
+  int32_t* free_count;
+  int64_t* slots;              // [T]
+  int64_t* positions;          // [T]
+  int32_t* offsets;            // [B + 1]
+  int32_t* status;
+  int B, MBS, F, T;
+  int bs_log2;                 // of the block size
+};
+constexpr int kResizeMaxSeqs = 16384;  // three sums of 4 bytes each in a CTA's shared memory
+cudaError_t launch_resize(const ResizeParams& p, cudaStream_t stream);
+
+// Parameters of the move of kept tokens (keep.cu).
+struct KeepParams {
+  uint8_t* kc;
+  uint8_t* vc;
+  float* ks;                   // one-byte caches, else NULL
+  float* vs;
+  const int32_t* tables;       // [B, MBS]
+  const int32_t* base;         // [B] tokens before the draft
+  const int32_t* path;         // [B, width] kept tokens' places in the draft, rising
+  const int32_t* kept;         // [B] entries of path used, or NULL: width
+  int32_t* status;
+  int B, Hkv, NB, MBS, width;
+  int bs_log2;                 // of the block size
+};
+cudaError_t launch_keep(int row_bytes, const KeepParams& p, cudaStream_t stream);
+
+// Parameters of the prompt attention (prompt.cuh, prompt.cu).
+struct PromptCut;
+struct PromptParams {
+  void* out;                   // [Tq, Hq, D] bf16, rows out_stride elements apart
+  const int32_t* q_offsets;    // [B + 1]
+  const int32_t* kv_offsets;
+  float* part_o;               // [2 G, 2, 128, D] fp32 records' outputs (unnormalised)
+  float* part_ml;              // [2 G, 2, 128, 2] fp32 (running max in log2 units, sum)
+  PromptCut* cuts;             // [G]
+  int32_t* status;
+  long long out_stride;
+  int B, Hkv, g, Tq, Tk, D;
+  int tpt;                     // tokens per tile of 128 rows: 128 / g
+  int item_cost;               // what ending an item costs, in keys
+  int min_range;               // positions (keys) of a CTA's stretch at least
+  float scale_log2;            // softmax scale * log2(e)
+  unsigned long long timeout_ns;
+};
+// What a CTA's stretch of the line begins and ends with: whether its first item began before
+// it (and ends in it), and the item that it begins and does not end, with its record.
+enum : int { kPromptContinues = 1, kPromptEnds = 2, kPromptBegins = 4, kPromptEmpty = 8 };
+struct PromptCut {
+  int slot, s, h, i, state;
+};
+struct PromptKernelInfo {
+  const void* fn;
+  int threads, smem;
+};
+bool select_prompt(int D, PromptKernelInfo* info);
+// joins the records of `grid` CTAs
+cudaError_t launch_prompt_merge(const PromptParams& p, int grid, cudaStream_t stream);
 
 // Parameters of the differential decode (decode_diff.cuh, diff_merge.cu).
 struct DiffParams {

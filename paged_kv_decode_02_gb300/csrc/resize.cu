@@ -1,0 +1,208 @@
+// resize.cu -- sequences grow and shrink: block tables, slots and positions from lengths.
+//
+// Sequence s holds the first ceil(len / bs) entries of its table row. Growing from len to
+// target takes ceil(target / bs) - ceil(len / bs) blocks off a list of free ones and gives
+// each new token its position and slot; shrinking gives blocks back ("块管理器：分页如何运作",
+// chenk.top page: a request appends blocks as it grows and frees them when it ends).
+//
+// The list is a stack. All blocks given back are pushed, the last of the last sequence first,
+// so that the first one ends on top; then the growing sequences pop theirs in order. Nothing
+// is moved twice: with F blocks given back and N taken, taken block i is given-back block i
+// where i < F, else entry count - 1 - (i - F) of the list, and the given-back blocks i >= N
+// go to entries count + F - 1 - i. So every item's source follows from three exclusive sums
+// over the sequences (tokens, blocks taken, blocks given back), and a growth that is undone
+// by the next call leaves the list as it was.
+// Table rows are read where sequences shrink and written where they grow, the list is read
+// (N > F) or written (F > N): no item waits for another, but lengths and the list's count are
+// written only once every reader is done.
+//
+// One CTA: the sums are a scan over the batch by its threads, kept in shared memory; each
+// item finds its sequence by bisection there.
+#include "common.cuh"
+#include "internal.h"
+
+namespace pkv {
+
+namespace {
+constexpr int kResizeThreads = 1024;
+
+// The last of the sequences 0 .. n - 1 whose exclusive sum is at most x (0 if none is).
+__device__ __forceinline__ int owner_of(const int* sums, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sums[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int clamp_i32(long long x) {
+  return int(x < 0x7fffffffll ? x : 0x7fffffffll);
+}
+}  // namespace
+
+// What a sequence asks for (nothing if a length does not fit its table row).
+struct ResizeWant {
+  int len, target, tokens, take, give;
+  bool bad;
+};
+
+__device__ __forceinline__ ResizeWant resize_want(const ResizeParams& p, int s) {
+  ResizeWant w;
+  w.len = __ldcg(p.lens + s);
+  w.target = __ldcg(p.targets + s);
+  const long long room = (long long)p.MBS << p.bs_log2;
+  w.bad = w.len < 0 || w.target < 0 || w.len > room || w.target > room;
+  if (w.bad) w.target = w.len;
+  const int up = (1 << p.bs_log2) - 1;
+  // (lengths stay below 2^31 - 2^5: api.cu)
+  const int d = w.bad ? 0 : ((w.target + up) >> p.bs_log2) - ((w.len + up) >> p.bs_log2);
+  w.tokens = max(0, w.target - w.len);
+  w.take = max(0, d);
+  w.give = max(0, -d);
+  return w;
+}
+
+__global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const ResizeParams p) {
+  extern __shared__ int s_sums[];  // exclusive sums: tokens, blocks taken, blocks given back
+  const int B = p.B;
+  int* s_tok = s_sums;
+  int* s_take = s_tok + B + 1;
+  int* s_give = s_take + B + 1;
+  __shared__ long long s_warp[3][kResizeThreads / 32];
+  __shared__ int s_taken;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int up = (1 << p.bs_log2) - 1;
+  pdl_wait_prior_grid();
+  pdl_allow_next_grid();
+  if (tid == 0) s_taken = 0;
+  int flags = 0;
+  int count = __ldcg(p.free_count);
+  if (count < 0 || count > p.F) {
+    count = max(0, min(count, p.F));
+    flags |= PKV_DEV_NO_BLOCKS;
+  }
+  // ---- the three sums, 64 bits wide until they are stored (wishes may exceed any list) ----
+  const int per = (B + kResizeThreads - 1) / kResizeThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  long long sum[3] = {0, 0, 0};
+  for (int s = b0; s < b1; ++s) {
+    const ResizeWant w = resize_want(p, s);
+    if (w.bad) flags |= PKV_DEV_BAD_CONTEXT_LEN;
+    sum[0] += w.tokens;
+    sum[1] += w.take;
+    sum[2] += w.give;
+  }
+  long long incl[3] = {sum[0], sum[1], sum[2]};
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl[i], off);
+      if (lane >= off) incl[i] += y;
+    }
+  }
+  if (lane == 31)
+    for (int i = 0; i < 3; ++i) s_warp[i][warp] = incl[i];
+  __syncthreads();
+  long long run[3], total[3];
+  for (int i = 0; i < 3; ++i) {
+    run[i] = incl[i] - sum[i];
+    total[i] = 0;
+    for (int w = 0; w < kResizeThreads / 32; ++w) {
+      if (w < warp) run[i] += s_warp[i][w];
+      total[i] += s_warp[i][w];
+    }
+  }
+  // blocks given back cannot outnumber the list in a consistent state
+  const int given = clamp_i32(total[2]);
+  const long long avail = (long long)count + given;
+  // A sequence grows if its tokens have rows and its blocks are there. Once one in order
+  // lacks either, so does every later one that asks for the same: the blocks taken are the
+  // first ones.
+  auto fits = [&](long long tok0, const ResizeWant& w, long long take0) {
+    return tok0 + w.tokens <= p.T && (w.take == 0 || take0 + w.take <= avail);
+  };
+  for (int s = b0; s < b1; ++s) {
+    const ResizeWant w = resize_want(p, s);
+    s_tok[s] = clamp_i32(run[0]);
+    s_take[s] = clamp_i32(run[1]);
+    s_give[s] = clamp_i32(run[2]);
+    if (w.tokens > 0) {
+      if (!fits(run[0], w, run[1])) flags |= PKV_DEV_NO_BLOCKS;
+      else if (w.take > 0) atomicMax(&s_taken, int(run[1] + w.take));
+    }
+    run[0] += w.tokens;
+    run[1] += w.take;
+    run[2] += w.give;
+  }
+  if (tid == 0) {
+    s_tok[B] = clamp_i32(total[0]);
+    s_take[B] = clamp_i32(total[1]);
+    s_give[B] = given;
+  }
+  __syncthreads();
+  const int taken = s_taken;
+  // given-back block i: the entries that shrinking sequences no longer hold
+  auto given_block = [&](int i) {
+    const int s = owner_of(s_give, B, i);
+    const int col = ((__ldcg(p.targets + s) + up) >> p.bs_log2) + (i - s_give[s]);
+    return __ldcg(p.tables + size_t(s) * p.MBS + col);
+  };
+  auto taken_block = [&](int i) {
+    return i < given ? given_block(i) : __ldcg(p.free_list + (count - 1 - (i - given)));
+  };
+  for (int i = tid; i < taken; i += kResizeThreads) {
+    const int s = owner_of(s_take, B, i);
+    const int col = ((__ldcg(p.lens + s) + up) >> p.bs_log2) + (i - s_take[s]);
+    p.tables[size_t(s) * p.MBS + col] = taken_block(i);
+  }
+  for (int i = taken + tid; i < given; i += kResizeThreads) {
+    const long long at = (long long)count + given - 1 - i;
+    if (at < p.F) p.free_list[at] = given_block(i);
+    else flags |= PKV_DEV_NO_BLOCKS;  // more blocks than the list holds: lost
+  }
+  // ---- the new tokens ----
+  const int all = s_tok[B];
+  for (int t = tid; t < p.T; t += kResizeThreads) {
+    long long slot = -1, pos = 0;
+    if (t < all) {
+      const int s = owner_of(s_tok, B, t);
+      const ResizeWant w = resize_want(p, s);
+      if (fits(s_tok[s], w, s_take[s])) {
+        const int n = w.len + (t - s_tok[s]), col = n >> p.bs_log2;
+        const int held = (w.len + up) >> p.bs_log2;
+        const int id = col < held ? __ldcg(p.tables + size_t(s) * p.MBS + col)
+                                  : taken_block(s_take[s] + col - held);
+        slot = ((long long)id << p.bs_log2) + (n & up);
+        pos = n;
+      }
+    }
+    p.slots[t] = slot;
+    p.positions[t] = pos;
+  }
+  for (int s = tid; s <= B; s += kResizeThreads) p.offsets[s] = s_tok[s];
+  __syncthreads();  // every read of the lengths and the count is done
+  for (int s = tid; s < B; s += kResizeThreads) {
+    const ResizeWant w = resize_want(p, s);
+    if (!w.bad && (w.tokens == 0 || fits(s_tok[s], w, s_take[s]))) p.lens[s] = w.target;
+  }
+  if (tid == 0) *p.free_count = clamp_i32(min((long long)p.F, avail - taken));
+  if (flags && p.status) atomicOr(p.status, flags);
+}
+
+cudaError_t launch_resize(const ResizeParams& p, cudaStream_t stream) {
+  const void* fn = reinterpret_cast<const void*>(&paged_kv_resize_kernel);
+  const size_t smem = size_t(12) * (p.B + 1);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               12 * (kResizeMaxSeqs + 1));
+    if (e != cudaSuccess) return e;
+  }
+  ResizeParams copy = p;
+  void* args[] = {&copy};
+  return launch_pdl(fn, dim3(1), dim3(kResizeThreads), args, smem, stream);
+}
+
+}  // namespace pkv

@@ -40,6 +40,7 @@ DEV_BAD_BLOCK_ID = 0x2
 DEV_TIMEOUT = 0x4
 DEV_BAD_PREFIX = 0x8
 DEV_BAD_POSITION = 0x10
+DEV_NO_BLOCKS = 0x20
 
 KV_BF16 = 0
 KV_INT8 = 1
@@ -111,6 +112,35 @@ EXPORTS = {
     "pkv_decode_diff_q8": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_float] * 3 +
                            [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
                             ctypes.c_void_p, ctypes.c_void_p]),
+    "pkv_resize_sequences": (ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.c_int32] +
+                             [ctypes.c_void_p] * 3 + [ctypes.c_int32] + [ctypes.c_void_p] * 3),
+    "pkv_keep_tokens": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int32, ctypes.c_int] +
+                        [ctypes.c_void_p] * 3),
+    "pkv_decode_tree_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32,
+                                                       ctypes.c_int,
+                                                       ctypes.POINTER(ctypes.c_size_t)]),
+    "pkv_decode_tree_bf16": (ctypes.c_int, [ctypes.c_void_p] * 8 + [ctypes.c_int32,
+                                                                    ctypes.c_float,
+                                                                    ctypes.c_void_p,
+                                                                    ctypes.c_void_p,
+                                                                    ctypes.c_size_t,
+                                                                    ctypes.c_void_p,
+                                                                    ctypes.c_void_p]),
+    "pkv_decode_tree_q8": (ctypes.c_int, [ctypes.c_void_p] * 10 + [ctypes.c_int32,
+                                                                   ctypes.c_float, ctypes.c_int,
+                                                                   ctypes.c_void_p,
+                                                                   ctypes.c_void_p,
+                                                                   ctypes.c_size_t,
+                                                                   ctypes.c_void_p,
+                                                                   ctypes.c_void_p]),
+    "pkv_prompt_workspace_bytes": (ctypes.c_int, [ctypes.c_void_p,
+                                                  ctypes.POINTER(ctypes.c_size_t)]),
+    "pkv_prompt_attention_bf16": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_float,
+                                                                         ctypes.c_void_p,
+                                                                         ctypes.c_void_p,
+                                                                         ctypes.c_size_t,
+                                                                         ctypes.c_void_p,
+                                                                         ctypes.c_void_p]),
     "pkv_copy_blocks": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int32, ctypes.c_int,
                                                                 ctypes.c_void_p, ctypes.c_void_p,
                                                                 ctypes.c_void_p]),
@@ -249,6 +279,7 @@ def _require(t, name, dtype, ndim, device=None):
 # ---------------------------------------------------------------------------
 _pack_dims = struct.Struct("7i").pack                  # pkv_dims
 _pack_rotary = struct.Struct("3P4q3if").pack           # pkv_rotary
+_pack_prompt = struct.Struct("6i4q").pack              # pkv_prompt_dims
 _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _Tensor = torch.Tensor
 _current_device = getattr(torch._C, "_cuda_getDevice", None)      # (None: torch without CUDA)
@@ -541,6 +572,266 @@ def paged_kv_gather(k_cache, v_cache, block_tables, out_offsets, num_tokens=None
     if st:
         _check(st, "pkv_gather_tokens")
     return outs[0], outs[1]
+
+
+def paged_kv_resize(block_tables, context_lens, target_lens, free_blocks, free_count, block_size,
+                    num_tokens=None, slot_mapping=None, positions=None, token_offsets=None,
+                    status=None):
+    """Sequences grow and shrink from ``context_lens`` to ``target_lens`` cached tokens (both [B]
+    int32, two tensors): blocks come off and go back on the stack ``free_blocks`` ([F] int32,
+    the first ``free_count`` [1] int32 ids free) and in and out of ``block_tables`` [B, MBS]
+    int32, where a sequence of L tokens holds the first ceil(L / block_size) entries. In place;
+    ``context_lens`` becomes ``target_lens``.
+
+    Returns (slot_mapping, positions, token_offsets) of the new tokens, as the appends take
+    them: row ``token_offsets[s] + i`` is new token i of sequence s. Slots and positions are
+    [num_tokens] int64, the tensors given or new ones; rows past the last new token get slot
+    -1, which the appends skip. Without ``num_tokens`` and the tensors, no rows: a call that
+    only shrinks. A sequence whose blocks or rows are not there, or whose lengths do not fit its
+    table row, stays as it was, flagged in ``status`` (int32 [1]: DEV_NO_BLOCKS,
+    DEV_BAD_CONTEXT_LEN)."""
+    if not isinstance(block_tables, _Tensor):
+        raise TypeError("block_tables must be a torch.Tensor")
+    index = block_tables.get_device()
+    if index < 0:
+        _require(block_tables, "block_tables", _I32, 2)
+    _need(block_tables, "block_tables", _I32, 2, index)
+    _need(context_lens, "context_lens", _I32, 1, index)
+    _need(target_lens, "target_lens", _I32, 1, index)
+    _need(free_blocks, "free_blocks", _I32, 1, index)
+    _need(free_count, "free_count", _I32, 1, index)
+    B, mbs = block_tables.shape
+    if context_lens.shape[0] != B or target_lens.shape[0] != B:
+        raise ValueError("context_lens / target_lens must have num_seqs rows")
+    if free_count.shape[0] != 1:
+        raise ValueError("free_count must have one element")
+    if B and context_lens.data_ptr() == target_lens.data_ptr():
+        raise ValueError("context_lens and target_lens must be two tensors")
+    if num_tokens is None:
+        given = slot_mapping if slot_mapping is not None else positions
+        num_tokens = given.shape[0] if isinstance(given, _Tensor) else 0
+    rows = []
+    for t, n in ((slot_mapping, "slot_mapping"), (positions, "positions")):
+        if t is None:
+            t = torch.empty(num_tokens, dtype=_I64, device=block_tables.device)
+        else:
+            _need(t, n, _I64, 1, index)
+            if t.shape[0] != num_tokens:
+                _same_shape(t, n, (num_tokens,))
+        rows.append(t)
+    if token_offsets is None:
+        token_offsets = torch.empty(B + 1, dtype=_I32, device=block_tables.device)
+        if B == 0:
+            token_offsets.zero_()
+    else:
+        _need(token_offsets, "token_offsets", _I32, 1, index)
+        if token_offsets.shape[0] != B + 1:
+            _same_shape(token_offsets, "token_offsets", (B + 1,))
+    if B == 0:
+        rows[0].fill_(-1)
+        rows[1].zero_()
+        return rows[0], rows[1], token_offsets
+    # (heads, head_dim and num_blocks are not used: any the library takes)
+    st = _run("pkv_resize_sequences", index, block_tables.data_ptr(), context_lens.data_ptr(),
+              target_lens.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
+              free_blocks.shape[0], rows[0].data_ptr(), rows[1].data_ptr(),
+              token_offsets.data_ptr(), num_tokens,
+              _pack_dims(B, 1, 1, 64, block_size, 1, mbs), _status_ptr(status, index))
+    if st:
+        _check(st, "pkv_resize_sequences")
+    return rows[0], rows[1], token_offsets
+
+
+def paged_kv_keep(k_cache, v_cache, block_tables, base_lens, path, kept_lens=None, k_scale=None,
+                  v_scale=None, status=None):
+    """The kept tokens of a draft move up in the cache: cached row ``base_lens[s] + path[s, i]``
+    becomes row ``base_lens[s] + i`` for i < ``kept_lens[s]`` (``path``'s width without it), K
+    and V (and scales, over one-byte codes) of every head. ``path`` [B, N] int32, its used
+    entries strictly rising per sequence; ``base_lens``, ``kept_lens`` [B] int32. In place,
+    bit-exact. A sequence whose lengths, path or block ids do not fit stays as it was, flagged
+    in ``status`` (int32 [1])."""
+    kv = _move_kv(k_cache, None)
+    if kv == KV_BF16:
+        k_scale = v_scale = None
+    index, (nb, hkv, bs, d) = _need_caches(
+        KV_FP8_E4M3 if k_cache.dtype is torch.uint8 else kv, k_cache, v_cache, k_scale, v_scale)
+    _need(block_tables, "block_tables", _I32, 2, index)
+    _need(base_lens, "base_lens", _I32, 1, index)
+    _need(path, "path", _I32, 2, index)
+    B, mbs = block_tables.shape
+    if base_lens.shape[0] != B or path.shape[0] != B:
+        raise ValueError("base_lens / path must have num_seqs rows")
+    if kept_lens is not None:
+        _need(kept_lens, "kept_lens", _I32, 1, index)
+        if kept_lens.shape[0] != B:
+            _same_shape(kept_lens, "kept_lens", (B,))
+    q8 = kv != KV_BF16
+    st = _run("pkv_keep_tokens", index, k_cache.data_ptr(), v_cache.data_ptr(),
+              k_scale.data_ptr() if q8 else None, v_scale.data_ptr() if q8 else None,
+              block_tables.data_ptr(), base_lens.data_ptr(), path.data_ptr(),
+              kept_lens.data_ptr() if kept_lens is not None else None, path.shape[1], kv,
+              _pack_dims(B, hkv, hkv, d, bs, nb, mbs), _status_ptr(status, index))
+    if st:
+        _check(st, "pkv_keep_tokens")
+
+
+def tree_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                         max_blocks_per_seq, q_len, kv_dtype=KV_BF16, device=None):
+    dims = Dims(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                max_blocks_per_seq)
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        st = _lib().pkv_decode_tree_workspace_bytes(ctypes.byref(dims), int(q_len), int(kv_dtype),
+                                                    ctypes.byref(out))
+    _check(st, "pkv_decode_tree_workspace_bytes")
+    return int(out.value)
+
+
+def _decode_tree(kv, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, tree_mask,
+                 scale, tree_lens, out, workspace, status):
+    index, (nb, hkv, bs, d) = _need_caches(kv, k_cache, v_cache, k_scale, v_scale)
+    _need(q, "q", _BF16, 4, index)
+    _need(block_tables, "block_tables", _I32, 2, index)
+    _need(context_lens, "context_lens", _I32, 1, index)
+    _need(tree_mask, "tree_mask", _I64, 3, index)
+    shape = q.shape
+    B, n, Hq, dq = shape
+    if dq != d:
+        raise ValueError("cache shapes disagree with q")
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("block_tables / context_lens must have num_seqs rows")
+    if tree_mask.shape != (B, n, (n + 63) // 64):
+        _same_shape(tree_mask, "tree_mask", (B, n, (n + 63) // 64))
+    lens = None
+    if tree_lens is not None:
+        _need(tree_lens, "tree_lens", _I32, 1, index)
+        if tree_lens.shape[0] != B:
+            _same_shape(tree_lens, "tree_lens", (B,))
+        lens = tree_lens.data_ptr()
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", _BF16, 4, index)
+        if out.shape != shape:
+            _same_shape(out, "out", shape)
+    dims = _pack_dims(B, Hq, hkv, d, bs, nb, block_tables.shape[1])
+    status = _status_ptr(status, index)
+    rows = (block_tables.data_ptr(), context_lens.data_ptr(), tree_mask.data_ptr(), lens, n,
+            float(scale))
+
+    def go(ws, ws_bytes):
+        if kv == KV_BF16:
+            return _run("pkv_decode_tree_bf16", index, out.data_ptr(), q.data_ptr(),
+                        k_cache.data_ptr(), v_cache.data_ptr(), *rows, dims, ws.data_ptr(),
+                        ws_bytes, status)
+        return _run("pkv_decode_tree_q8", index, out.data_ptr(), q.data_ptr(),
+                    k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                    v_scale.data_ptr(), *rows, kv, dims, ws.data_ptr(), ws_bytes, status)
+
+    if workspace is not None:
+        st = go(*_workspace(workspace, 0, q.device))
+    else:
+        with torch.cuda.device(index):
+            need = ctypes.c_size_t(0)
+            _check(_lib().pkv_decode_tree_workspace_bytes(dims, n, kv, ctypes.byref(need)),
+                   "pkv_decode_tree_workspace_bytes")
+        st = go(*_workspace(None, need.value, q.device))
+    if st:
+        _check(st, "pkv_decode_tree_bf16" if kv == KV_BF16 else "pkv_decode_tree_q8")
+    return out
+
+
+def paged_decode_attention_tree(q, k_cache, v_cache, block_tables, context_lens, tree_mask, scale,
+                                tree_lens=None, out=None, workspace=None, status=None):
+    """Attention of a tree of drafted tokens over a paged bf16 cache.
+
+    q [B, N, Hq, D] bf16: the tree's nodes, whose K/V are the last ``tree_lens[s]`` (N without
+    it; [B] int32) of the ``context_lens[s]`` cached tokens, in node order. A node sees every
+    token before the nodes, and node j where bit j % 64 of ``tree_mask[s, i, j // 64]`` is set
+    ([B, N, ceil(N / 64)] int64; its own bit included). Returns out [B, N, Hq, D] bf16; rows past
+    ``tree_lens[s]``, and nodes that see nothing, are zeros. ``workspace`` (uint8, at least
+    :func:`tree_workspace_bytes`) and ``status`` (int32 [1]) as for
+    :func:`paged_decode_attention`."""
+    return _decode_tree(KV_BF16, q, k_cache, v_cache, None, None, block_tables, context_lens,
+                        tree_mask, scale, tree_lens, out, workspace, status)
+
+
+def paged_decode_attention_tree_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                                   context_lens, tree_mask, scale, fmt="e5m2", tree_lens=None,
+                                   out=None, workspace=None, status=None):
+    """:func:`paged_decode_attention_tree` over a one-byte cache (codes and scales as for
+    :func:`paged_decode_attention_multi_q8`)."""
+    return _decode_tree(_q8_kind(k_cache, fmt), q, k_cache, v_cache, k_scale, v_scale,
+                        block_tables, context_lens, tree_mask, scale, tree_lens, out, workspace,
+                        status)
+
+
+def prompt_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, num_q_tokens,
+                           num_kv_tokens, device=None):
+    dims = _pack_prompt(num_seqs, num_q_heads, num_kv_heads, head_dim, num_q_tokens,
+                        num_kv_tokens, 0, 0, 0, 0)
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        st = _lib().pkv_prompt_workspace_bytes(dims, ctypes.byref(out))
+    _check(st, "pkv_prompt_workspace_bytes")
+    return int(out.value)
+
+
+def prompt_attention(q, k, v, q_offsets, scale, kv_offsets=None, out=None, workspace=None,
+                     status=None):
+    """Causal attention of whole prompts packed one after the other.
+
+    q [Tq, Hq, D], k and v [Tk, Hkv, D] bf16 (tokens at any stride, as parts of a fused
+    projection's output); sequence s has rows ``q_offsets[s]`` .. ``q_offsets[s + 1] - 1`` of q
+    and those of ``kv_offsets`` (``q_offsets`` without it; both [B + 1] int32) of k and v. Its
+    queries are its last tokens: query i sees keys j <= nk - nq + i. Returns out [Tq, Hq, D]
+    bf16: the tensor given, whose rows outside every sequence stay as they were, or a new one.
+    A query without keys gets zeros. ``workspace`` (uint8, at least
+    :func:`prompt_workspace_bytes`); ``status`` (int32 [1]) flags offsets that fall or leave the
+    arrays, whose sequences are not computed."""
+    if not isinstance(q, _Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    index = q.get_device()
+    if index < 0:
+        _require(q, "q", _BF16, 3)
+    q_shape, q_stride = _token_rows(q, "q", index)
+    k_shape, k_stride = _token_rows(k, "k", index)
+    v_shape, v_stride = _token_rows(v, "v", index)
+    tq, hq, d = q_shape
+    tk, hkv, dk = k_shape
+    if v_shape != k_shape:
+        _same_shape(v, "v", k_shape)
+    if dk != d:
+        raise ValueError("k and v disagree with q in head_dim")
+    _need(q_offsets, "q_offsets", _I32, 1, index)
+    if kv_offsets is None:
+        kv_offsets = q_offsets
+    elif kv_offsets is not q_offsets:
+        _need(kv_offsets, "kv_offsets", _I32, 1, index)
+    B = q_offsets.shape[0] - 1
+    if B < 0 or kv_offsets.shape[0] != B + 1:
+        raise ValueError("q_offsets / kv_offsets must have num_seqs + 1 elements")
+    if out is None:
+        out, out_stride = torch.empty((tq, hq, d), dtype=_BF16, device=q.device), hq * d
+    else:
+        out_shape, out_stride = _token_rows(out, "out", index)
+        if out_shape != q_shape:
+            _same_shape(out, "out", q_shape)
+    dims = _pack_prompt(B, hq, hkv, d, tq, tk, out_stride, q_stride, k_stride, v_stride)
+    if workspace is None:
+        with torch.cuda.device(index):
+            need = ctypes.c_size_t(0)
+            _check(_lib().pkv_prompt_workspace_bytes(dims, ctypes.byref(need)),
+                   "pkv_prompt_workspace_bytes")
+        workspace, ws_bytes = _workspace(None, need.value, q.device)
+    else:
+        workspace, ws_bytes = _workspace(workspace, 0, q.device)
+    st = _run("pkv_prompt_attention_bf16", index, out.data_ptr(), q.data_ptr(), k.data_ptr(),
+              v.data_ptr(), q_offsets.data_ptr(), kv_offsets.data_ptr(), float(scale), dims,
+              workspace.data_ptr(), ws_bytes, _status_ptr(status, index))
+    if st:
+        _check(st, "pkv_prompt_attention_bf16")
+    return out
 
 
 def decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
