@@ -161,8 +161,8 @@ pkv_status pkv_append_int8(const void* k, const void* v, int8_t* k_cache, int8_t
  *              (as do later ones that lack the same; earlier ones have grown); or *free_count
  *              was outside [0, free_capacity] (taken as the nearer end), or the list could not
  *              hold a block given back (the block is lost).
- * num_seqs up to 16384, and num_seqs * max_blocks_per_seq and free_capacity below 2^30 (else
- * PKV_ERR_UNSUPPORTED). num_seqs == 0 is a no-op returning PKV_OK. dims.num_q_heads,
+ * num_seqs up to 16384, and num_seqs * max_blocks_per_seq, free_capacity and num_tokens below
+ * 2^30 (else PKV_ERR_UNSUPPORTED). num_seqs == 0 is a no-op returning PKV_OK. dims.num_q_heads,
  * num_kv_heads, head_dim and num_blocks are not used beyond the common checks.
  */
 pkv_status pkv_resize_sequences(int32_t* block_tables, int32_t* context_lens,

@@ -847,8 +847,8 @@ pkv_status run_prompt(void* out, const void* q, const void* k, const void* v,
   const long long ks = keys ? stride_of(d->k_stride, tk, d->num_kv_heads) : qs;
   const long long vs = keys ? stride_of(d->v_stride, tk, d->num_kv_heads) : qs;
   if (!rows_map(&tmq, RowsKey{q, qs, d->num_q_tokens, d->num_q_heads, d->head_dim, g, tpt}) ||
-      !rows_map(&tmk, RowsKey{keys ? k : q, ks, tk, d->num_kv_heads, d->head_dim, 1, 128}) ||
-      !rows_map(&tmv, RowsKey{keys ? v : q, vs, tk, d->num_kv_heads, d->head_dim, 1, 128}))
+      !rows_map(&tmk, RowsKey{keys ? k : q, ks, tk, d->num_kv_heads, d->head_dim, 1, P.k.keys}) ||
+      !rows_map(&tmv, RowsKey{keys ? v : q, vs, tk, d->num_kv_heads, d->head_dim, 1, P.k.keys}))
     return PKV_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PromptParams p{};
@@ -867,6 +867,7 @@ pkv_status run_prompt(void* out, const void* q, const void* k, const void* v,
   p.Tk = d->num_kv_tokens;
   p.D = d->head_dim;
   p.tpt = tpt;
+  p.keys = P.k.keys;
   p.item_cost = kPromptItemCost;
   p.min_range = kPromptMinRange;
   p.scale_log2 = scale * 1.4426950408889634f;
@@ -1396,7 +1397,7 @@ pkv_status pkv_resize_sequences(int32_t* block_tables, int32_t* context_lens,
   pkv_status st = check_dims(dims);
   if (st != PKV_OK) return st;
   if (free_capacity < 0 || num_tokens < 0) return PKV_ERR_SHAPE;
-  if (dims->num_seqs > kResizeMaxSeqs || free_capacity >= (1 << 30) ||
+  if (dims->num_seqs > kResizeMaxSeqs || free_capacity >= (1 << 30) || num_tokens >= (1 << 30) ||
       (long long)dims->num_seqs * dims->max_blocks_per_seq >= (1ll << 30) ||
       (long long)dims->max_blocks_per_seq * dims->block_size >= (1ll << 31) - 32)
     return PKV_ERR_UNSUPPORTED;

@@ -306,6 +306,7 @@ struct PromptParams {
   long long out_stride;
   int B, Hkv, g, Tq, Tk, D;
   int tpt;                     // tokens per tile of 128 rows: 128 / g
+  int keys;                    // keys per tile
   int item_cost;               // what ending an item costs, in keys
   int min_range;               // positions (keys) of a CTA's stretch at least
   float scale_log2;            // softmax scale * log2(e)
@@ -320,6 +321,7 @@ struct PromptCut {
 struct PromptKernelInfo {
   const void* fn;
   int threads, smem;
+  int keys;                    // keys per tile
 };
 bool select_prompt(int D, PromptKernelInfo* info);
 // joins the records of `grid` CTAs

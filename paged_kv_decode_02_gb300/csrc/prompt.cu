@@ -72,6 +72,7 @@ bool select_prompt(int D, PromptKernelInfo* info) {
   info->fn = D == 128 ? reinterpret_cast<const void*>(&prompt_attention_kernel<128>)
                       : reinterpret_cast<const void*>(&prompt_attention_kernel<64>);
   info->threads = PromptCfg<128>::kThreads;
+  info->keys = D == 128 ? PromptCfg<128>::kKeys : PromptCfg<64>::kKeys;
   info->smem = D == 128 ? PromptCfg<128>::kSmem : PromptCfg<64>::kSmem;
   return true;
 }

@@ -11,7 +11,7 @@
 // Work. The g query heads of a KV head share its keys, so a tile of 128 MMA rows is
 // tpt = 128 / g tokens times g heads (row = token * g + head; the last 128 % g rows are
 // unused), and K and V are read once for all of them. An item is two such tiles, X = 0 and 1,
-// of one KV head: 2 tpt consecutive tokens; its keys are walked in tiles of 128. The items of
+// of one KV head: 2 tpt consecutive tokens; its keys are walked in tiles of kKeys. The items of
 // all sequences and heads lie on one line on which an item takes as many positions as its
 // last token sees keys, plus a constant for its end, and each CTA takes an equal stretch of it:
 // stretches are cut between key tiles, an item that is cut leaves unnormalised records
@@ -19,16 +19,26 @@
 // short ones fill the SMs alike, without host knowledge of the lengths, and no order of
 // atomics touches a result.
 //
-// A CTA (384 threads) runs two score tiles against each other, so that the tensor cores work
-// on one while the exponentials of the other run:
+// A CTA (704 threads):
 //   warp 0      TMA: Q of both tiles, K and V tiles through one ring of stages;
-//   warp 1      TMEM, and one thread issues every MMA: S_X = Q_X K^T into the tile's score
-//               columns, then O_X += P_X V with P_X (bf16) read from TMEM, where it lies over
-//               the scores it came from;
-//   warp 2      zeroes V rows past the sequence's end (they may hold anything);
-//   warps 4..7  softmax of tile 0, warps 8..11 of tile 1: one query row per thread.
-// Per pair of 128 x 128 tiles and D = 128 the MMAs take 4 x 512 cycles and the exponentials
-// 128 per thread on four SM sub-partitions.
+//   warps 1, 2  one thread each issues S_X = Q_X K_j^T into the score columns of tile 0, tile 1;
+//   warps 3, 20 one thread each issues O_X += P_X V_j with P_X (bf16) read from TMEM, after the
+//               warp has zeroed V rows past the sequence's end (they may hold anything). Four
+//               issuers, since a thread spends 500 to 700 cycles on the waits and commits around
+//               its MMAs, with nearly none queued behind them, and 300 to 450 on the MMAs: one
+//               thread for all of them took 4900 cycles a step, two (one per tile) 2300;
+//   warp 21     walks the CTA's stretch and tells the others its segments, through a queue;
+//   warps 4..11 softmax of tile 0, warps 12..19 of tile 1: two threads per query row, each
+//               with half of the tile's columns (and of O's), so that four warps per SM
+//               sub-partition hide each other's latencies.
+// Scores, P and O of both tiles have TMEM columns of their own, so the scores of key tile j + 1
+// are computed while the exponentials of tile j run (as soon as its scores have been read), and
+// a softmax never waits for P.V: the tensor cores are what the loop should wait for. For D = 128
+// that fits 512 columns with key tiles of 80 (2 x (80 + 40 + 128)). Measured on GB300, cycles
+// of the MMAs of one 128-row tile per key tile, of the ideal rate's: N = 64 648 (79 %), 80 717
+// (89 %), 96 813 (94 %), 128 1025 (100 %; Q and K come from shared memory, whose bandwidth bounds
+// small N); with 128 keys, P over the scores it came from and so every step of a tile in
+// sequence, a step took 3500 cycles for two tiles, where the MMAs take 2050.
 // The softmax keeps a reference maximum per row that moves only when a tile's maximum exceeds
 // it by more than 8 (log2 units; weights then reach 2^8 and keep their relative precision), so
 // O is rescaled in TMEM a few times per item at most. Scores, maxima and sums are fp32; a
@@ -37,7 +47,7 @@
 // complete, frees its TMEM and leaves.
 #pragma once
 
-#include "internal.h"
+#include "decode.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -45,24 +55,32 @@ namespace pkv {
 template <int D>
 struct PromptCfg {
   static constexpr int kRows = 128;              // MMA rows of a tile
-  static constexpr int kKeys = 128;              // keys per tile
+  static constexpr int kKeys = 80;               // keys per tile
   static constexpr int kSlabs = D / 64;          // 128-byte column slabs of a row
-  static constexpr int kSlab = kKeys * 128;      // bytes of one slab of a tile
-  static constexpr int kTile = kSlabs * kSlab;   // a Q, K or V tile
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kSlabQ = kRows * 128;     // bytes of one slab of a Q tile
+  static constexpr int kTileQ = kSlabs * kSlabQ;
+  static constexpr int kSlab = kKeys * 128;      // bytes of one slab of a K or V tile
+  static constexpr int kTile = kSlabs * kSlab;
+  static constexpr int kStages = 6;
   static constexpr int kOffQ = 0;                // both tiles' queries
-  static constexpr int kOffKV = 2 * kTile;       // the ring: K, V, K, V, ...
-  static constexpr int kOffBar = kOffKV + kStages * kTile;
-  // full[stages] empty[stages] qfull[2] qempty[2] sfull[2] pfull[2] ofull[2] ofree[2] vfix vseen
-  // mdone
-  static constexpr int kNumBars = 2 * kStages + 15;
+  static constexpr int kOffKV = 2 * kTileQ;      // the ring: K, V, K, V, ...
+  static constexpr int kOffOut = kOffKV + kStages * kTile;  // 32 rows of 64 bytes per softmax warp
+  static constexpr int kQueue = 4;               // segments told ahead
+  static constexpr int kOffQueue = kOffOut + 16 * 2048;  // 64 bytes each
+  static constexpr int kOffBar = kOffQueue + kQueue * 64;
+  // full[stages] empty[stages] qfull[2] qempty[2] sfull[2] sread[2] pfull[2] pdone[2] ofree[2]
+  // mdone[4] told[queue] heard[queue]
+  static constexpr int kNumBars = 2 * kStages + 18 + 2 * kQueue;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
-  static constexpr int kOffSent = kOffAbort + 4;  // copies into the ring sent for so far
-  static constexpr int kOffScan = (kOffSent + 4 + 15) / 16 * 16;  // warps' sums, both ends
+  static constexpr int kOffScan = (kOffAbort + 4 + 15) / 16 * 16;  // warps' sums, both ends
   static constexpr int kSmem = kOffScan + 256 + 1024;              // + alignment of the base
-  static constexpr int kThreads = 384;
-  static constexpr int kColS = 0, kColO = 256;   // S_X (P_X over it) and O_X, 128 columns each
+  static constexpr int kThreads = 704;
+  // TMEM columns of tile 0 and tile 1: scores (fp32), P (bf16 pairs), O (fp32)
+  static constexpr int kColS = 0, kColP = 2 * kKeys, kColO = 3 * kKeys;
+  static_assert(kColO + 2 * D <= 512, "TMEM columns");
+  static_assert(kKeys % 16 == 0 && kSlab % 1024 == 0 && kOffOut % 1024 == 0, "swizzle atoms");
+  static_assert(kStages % 2 == 0, "K tiles on even stages");
   static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
 
@@ -98,8 +116,8 @@ struct PromptSeq {
     if (i == all) sum += nk;
     return sum;
   }
-  __device__ __forceinline__ int key_tiles(int end) const {
-    return max(1, (seen(end) + 127) / 128);
+  __device__ __forceinline__ int key_tiles(int end, int keys) const {
+    return max(1, (seen(end) + keys - 1) / keys);
   }
 };
 
@@ -109,15 +127,19 @@ struct PromptPlace {
 };
 
 // What a CTA does of one item: key tiles [ja, jb) of n; tile X takes those below nx[X].
-struct PromptSeg {
+struct alignas(16) PromptSeg {
   PromptSeq q;
   int s, h, i, ja, jb, n;
   int nx0, nx1;
+  int some;  // 0: there is none, the stretch is over
+  int pad[3];
   __device__ __forceinline__ int nx(int X) const { return X ? nx1 : nx0; }
   // tile X has key tiles [ja, end(X)) here
   __device__ __forceinline__ int end(int X) const { return min(jb, nx(X)); }
   __device__ __forceinline__ bool has(int X) const { return nx(X) > ja; }
 };
+
+static_assert(sizeof(PromptSeg) == 64, "a place in the queue");
 
 // Walks a CTA's stretch, one segment after the other.
 struct PromptWalk {
@@ -154,10 +176,10 @@ struct PromptWalk {
       g.s = at.s;
       g.h = at.h;
       g.i = at.i;
-      g.n = q.key_tiles(t1);
+      g.n = q.key_tiles(t1, p.keys);
       g.ja = at.j;
       g.jb = last ? min(stop.j, g.n) : g.n;
-      g.nx0 = q.key_tiles(min(q.nq, t0 + p.tpt));
+      g.nx0 = q.key_tiles(min(q.nq, t0 + p.tpt), p.keys);
       g.nx1 = t0 + p.tpt < q.nq ? g.n : 0;
       if (g.nx1 == 0) g.nx0 = g.n;
       at.j = 0;
@@ -185,9 +207,114 @@ __device__ __forceinline__ PromptPlace prompt_locate(const PromptParams& p, cons
   }
   c.i = lo;
   x -= q.before(lo, per, p.item_cost);
-  const int n = q.key_tiles(min(q.nq, (lo + 1) * per));
-  c.j = int(min((long long)n, (x + 127) / 128));
+  const int n = q.key_tiles(min(q.nq, (lo + 1) * per), p.keys);
+  c.j = int(min((long long)n, (x + p.keys - 1) / p.keys));
   return c;
+}
+
+// The two threads of a row (same lane of two warps, one per half of the tile's columns).
+struct PromptPair {
+  uint32_t mine, theirs;  // places in shared memory
+  int id;                 // barrier of the two warps
+  // Gives a value to the partner and returns the partner's. A place may be written again once
+  // its reader has met the writer at another barrier since.
+  __device__ __forceinline__ float swap(float x) const {
+    tc::sts32(mine, __float_as_uint(x));
+    meet();
+    return __uint_as_float(lds32(theirs));
+  }
+  __device__ __forceinline__ void meet() const {
+    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+  }
+};
+
+// A row's softmax state: the reference of its weights and of O (log2 units; the same in both
+// threads), and the sum of this thread's weights.
+struct PromptRow {
+  float m, l;
+};
+
+// A warp's place in its tile's pipeline: TMEM columns of scores, P and O; barriers; the step.
+struct PromptStep {
+  uint32_t ts, tp, to, sread, pdone, pfull, step;
+  int lane;
+  bool begun;  // O holds key tiles before this one
+};
+
+// Half a row (a thread) of a score tile: the scores become weights 2^(scale s - m), bf16 pairs in
+// P's columns. kWhole: the row sees all of the tile's columns, else the first `vis` of this half;
+// kNeg: the scale is negative. Returns false on a timeout.
+template <int D, bool kWhole, bool kNeg, typename Wait>
+__device__ __forceinline__ bool prompt_softmax(const PromptStep& at, float sl, int vis,
+                                               const PromptPair& pair, PromptRow& row,
+                                               const Wait& wait) {
+  constexpr int N = PromptCfg<D>::kKeys / 2;
+  uint32_t s[N];
+  tc::tmem_ld(at.ts, s);
+  tc::fence_before_sync();
+  __syncwarp();
+  if (at.lane == 0) mbar_arrive(at.sread);  // the next scores may come
+  if constexpr (!kWhole) {
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+      if (t >= vis) s[t] = kNeg ? 0x7f800000u : 0xff800000u;  // the scaled score: -inf
+  }
+  auto most = [](float x, float y, float z) {
+    return kNeg ? fminf(x, fminf(y, z)) : fmax3(x, y, z);
+  };
+  float mx[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) mx[t] = __uint_as_float(s[t]);
+#pragma unroll
+  for (int t = 0; t < (N - 8) / 2; ++t)
+    mx[t & 7] = most(mx[t & 7], __uint_as_float(s[8 + 2 * t]), __uint_as_float(s[9 + 2 * t]));
+  const float mine = sl * most(most(mx[0], mx[1], mx[2]), most(mx[3], mx[4], mx[5]),
+                               most(mx[6], mx[7], mx[7]));
+  const float top = fmaxf(mine, pair.swap(mine));
+  float alpha = 1.f;
+  const bool up = top > row.m + 8.f;
+  if (up) {
+    alpha = fast_exp2(row.m - top);  // 0 while the row has seen nothing
+    row.m = top;
+    row.l *= alpha;
+  }
+  // (scores of -inf alone: weights 0, not 2^(-inf + inf))
+  const float m = row.m > -INFINITY ? row.m : 0.f;
+  const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(-m, -m);
+  float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t pk[N / 2];
+#pragma unroll
+  for (int t = 0; t < N; t += 2) {
+    const float2 x =
+        __ffma2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])), sl2, nm2);
+    float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+    if constexpr (!kWhole) {
+      w.x = t < vis ? w.x : 0.f;
+      w.y = t + 1 < vis ? w.y : 0.f;
+    }
+    ls[(t >> 1) & 1] = __fadd2_rn(ls[(t >> 1) & 1], w);
+    pk[t / 2] = pack_bf16x2(w.x, w.y);
+  }
+  const float2 l2 = __fadd2_rn(ls[0], ls[1]);
+  row.l += l2.x + l2.y;
+  // P.V of the tile before has completed: P's columns are free, O holds what came before
+  if (at.step > 0 && !wait(at.pdone, at.step - 1)) return false;
+  tc::fence_after_sync();
+  if (at.begun && __any_sync(0xffffffffu, up)) {
+#pragma unroll 1
+    for (int c = 0; c < D / 2; c += 16) {
+      uint32_t o[16];
+      tc::tmem_ld16(at.to + c, o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+      tc::tmem_st16(at.to + c, o);
+    }
+  }
+  tc::tmem_st(at.tp, pk);
+  tc::fence_before_sync();
+  __syncwarp();
+  if (at.lane == 0) mbar_arrive(at.pfull);
+  return true;
 }
 
 template <int D>
@@ -201,9 +328,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + K::kOffAbort);
-  volatile int* sent = reinterpret_cast<volatile int*>(gbase + K::kOffSent);
-  long long* s_scan = reinterpret_cast<long long*>(gbase + K::kOffScan);  // [12] warps' sums
-  PromptPlace* s_place = reinterpret_cast<PromptPlace*>(s_scan + 12);     // [2]
+  long long* s_scan = reinterpret_cast<long long*>(gbase + K::kOffScan);  // [22] warps' sums
+  PromptPlace* s_place = reinterpret_cast<PromptPlace*>(s_scan + 22);     // [2]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return base + K::kOffBar + 8 * i; };
   auto full = [&](int st) { return bar(st); };
@@ -212,19 +338,24 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   auto qfull = [&](int X) { return bar(kB + X); };
   auto qempty = [&](int X) { return bar(kB + 2 + X); };
   auto sfull = [&](int X) { return bar(kB + 4 + X); };
-  auto pfull = [&](int X) { return bar(kB + 6 + X); };
-  auto ofull = [&](int X) { return bar(kB + 8 + X); };
-  auto ofree = [&](int X) { return bar(kB + 10 + X); };
-  const uint32_t vfix = bar(kB + 12), vseen = bar(kB + 13), mdone = bar(kB + 14);
+  auto sread = [&](int X) { return bar(kB + 6 + X); };
+  auto pfull = [&](int X) { return bar(kB + 8 + X); };
+  auto pdone = [&](int X) { return bar(kB + 10 + X); };
+  auto ofree = [&](int X) { return bar(kB + 12 + X); };
+  auto mdone = [&](int i) { return bar(kB + 14 + i); };
+  auto told = [&](int i) { return bar(kB + 18 + i); };
+  auto heard = [&](int i) { return bar(kB + 18 + K::kQueue + i); };
   const uint32_t tmem_slot = base + K::kOffTmemSlot;
 
   if (tid == 0) {
     for (int i = 0; i < K::kNumBars; ++i) {
-      const bool soft = i >= kB + 6 && i < kB + 8, epi = i >= kB + 10 && i < kB + 12;
-      mbar_init(bar(i), soft || epi ? 4 : 1);  // pfull, ofree: one arrival per softmax warp
+      const int k = (i - kB) >> 1;
+      // sread, pfull, ofree: one arrival per softmax warp; empty: one per tile
+      const bool soft = i >= kB && (k == 3 || k == 4 || k == 6);
+      // heard: one per warp that listens
+      mbar_init(bar(i), soft ? 8 : i >= K::kStages && i < kB ? 2 : i >= kB + 18 + K::kQueue ? 21 : 1);
     }
     *abort_flag = 0;
-    *sent = 0;
     fence_mbar_init();
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
@@ -291,6 +422,22 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   const PromptPlace first = s_place[0], stop = s_place[1];
   PromptWalk walk;
   walk.begin(first, stop);
+  // the next segment told, to one lane or to a whole warp; false: the stretch is over
+  uint32_t heard_of = 0;
+  auto take = [&](PromptSeg& g, bool whole_warp) {
+    const uint32_t slot = heard_of % K::kQueue;
+    bool ok = tc::poll_or_abort(told(slot), (heard_of / K::kQueue) & 1u, p.timeout_ns, abort_flag);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    ++heard_of;
+    const uint32_t from = base + K::kOffQueue + slot * 64;
+    uint4* to = reinterpret_cast<uint4*>(&g);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) to[k] = lds128(from + 16 * k);
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(heard(slot));
+    return g.some != 0;
+  };
   if (tid == 0) {  // for the kernel that joins the records
     PromptCut cut = {-1, 0, 0, 0, 0};
     if (active) {
@@ -308,7 +455,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         } else if (stop.j > 0 && stop.s < p.B && !(g.s == stop.s && g.h == stop.h && g.i == stop.i)) {
           PromptSeq q;
           q.load(p, stop.s);
-          if (stop.j < q.key_tiles(min(q.nq, (stop.i + 1) * per))) {
+          if (stop.j < q.key_tiles(min(q.nq, (stop.i + 1) * per), p.keys)) {
             cut.state |= kPromptBegins;
             cut.slot = 2 * c + 1;
             cut.s = stop.s, cut.h = stop.h, cut.i = stop.i;
@@ -319,148 +466,143 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     p.cuts[c] = cut;
   }
 
-  // the softmax warps take registers over from the first warpgroup: 128 x 72 + 256 x 216 =
-  // 384 x 168, what the block is launched with
-  if (warp >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  if (active && warp == 21) {
+    // ---------------- the walk ----------------
+    if (lane == 0) {
+      PromptSeg g;
+      bool ok = true;
+      for (uint32_t n = 0; ok; ++n) {
+        const uint32_t slot = n % K::kQueue;
+        g.some = walk.next(p, g) ? 1 : 0;
+        if (n >= K::kQueue)
+          ok = tc::wait_or_abort(heard(slot), (n / K::kQueue - 1) & 1u, p.timeout_ns, abort_flag);
+        if (!ok) break;
+        const uint4* from = reinterpret_cast<const uint4*>(&g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::sts128(base + K::kOffQueue + slot * 64 + 16 * k, from[k]);
+        mbar_arrive(told(slot));
+        if (!g.some) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 20) {
     if (active) {
       // ---------------- softmax: one query row per thread ----------------
-      const int X = warp >= 8 ? 1 : 0, quarter = warp & 3;
+      const int X = warp >= 12 ? 1 : 0, quarter = warp & 3, hp = (warp >> 2 & 1) ^ 1;
       const int r = quarter * 32 + lane;
       const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
-      const uint32_t ts = trow + K::kColS + X * 128, to = trow + K::kColO + X * 128;
-      const float sl = p.scale_log2, asl = fabsf(sl);
+      // this thread's half of the scores, of P and of O
+      const uint32_t ts = trow + K::kColS + X * K::kKeys + hp * (K::kKeys / 2);
+      const uint32_t tp = trow + K::kColP + X * (K::kKeys / 2) + hp * (K::kKeys / 4);
+      const uint32_t to = trow + K::kColO + X * D + hp * (D / 2);
+      const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 2048;
+      const PromptPair pair = {stage + lane * 4, stage + lane * 4 + (hp ? -4 : 4) * 2048,
+                               1 + X * 4 + quarter};
+      const float sl = p.scale_log2;
       const int rt = r / p.g, rh = r % p.g;  // token of the tile, head of the group
-      int step = 0;
+      uint32_t step = 0;
+      auto wait = [&](uint32_t b, uint32_t phase) {
+        return __all_sync(0xffffffffu,
+                          tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
+      };
       bool ok = true, first_seg = true;
       PromptSeg g;
-      while (ok && walk.next(p, g)) {
+      while (ok && take(g, true)) {
         const int tok = g.i * per + X * p.tpt + rt;
         const bool row_ok = rt < p.tpt && tok < g.q.nq;
-        const int sees = g.q.nk - g.q.nq + tok + 1;  // keys the row sees (if any)
-        float m = -INFINITY, l = 0.f;
+        // keys the row sees; rows that are not stored see what the warp's last one does, so that
+        // it runs one path
+        const int own = g.q.nk - g.q.nq + tok + 1;
+        const bool idle = !__any_sync(0xffffffffu, row_ok);
+        const int most = __reduce_max_sync(0xffffffffu, row_ok ? own : -0x7fffffff);
+        const int sees = row_ok ? own : most;
+        const int least = __reduce_min_sync(0xffffffffu, sees);
+        PromptRow row = {-INFINITY, 0.f};
         const int je = g.end(X);
         for (int j = g.ja; j < je; ++j, ++step) {
-          if (!__all_sync(0xffffffffu, tc::wait_or_abort(sfull(X), uint32_t(step) & 1u, p.timeout_ns,
-                                                         abort_flag))) {
-            ok = false;
-            break;
-          }
+          ok = wait(sfull(X), step);
+          if (!ok) break;
           tc::fence_after_sync();
-          // columns this row may see in the tile; rows that are not stored follow the warp's
-          // largest count, so that it runs one path
-          const int vis_row = row_ok ? min(K::kKeys, sees - j * K::kKeys) : -1;
-          const int vis_w = __reduce_max_sync(0xffffffffu, vis_row);
-          const int vis = row_ok ? vis_row : vis_w;
-          uint32_t s[K::kKeys];
-          tc::tmem_ld128(ts, s);
-          if (sl < 0.f) {  // a negative scale is carried by the scores' signs
-  #pragma unroll
-            for (int t = 0; t < K::kKeys; ++t) s[t] ^= 0x80000000u;
-          }
-          const bool whole = __all_sync(0xffffffffu, vis >= K::kKeys);
-          if (!whole) {
-  #pragma unroll
-            for (int t = 0; t < K::kKeys; ++t)
-              if (t >= vis) s[t] = 0xff800000u;  // -inf
-          }
-          float mx[8];
-  #pragma unroll
-          for (int t = 0; t < 8; ++t) mx[t] = __uint_as_float(s[t]);
-  #pragma unroll
-          for (int t = 0; t < (K::kKeys - 8) / 2; ++t)
-            mx[t & 7] = fmax3(mx[t & 7], __uint_as_float(s[8 + 2 * t]), __uint_as_float(s[9 + 2 * t]));
-          const float mt = asl * fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                       fmaxf(mx[6], mx[7]));
-          float alpha = 1.f;
-          bool rescale = false;
-          if (vis > 0 && mt > m + 8.f) {
-            alpha = fast_exp2(m - mt);  // 0 while the row has seen nothing
-            m = mt;
-            l *= alpha;
-            rescale = j > g.ja;
-          }
-          if (__any_sync(0xffffffffu, rescale)) {  // O holds the tiles before this one
-            if (!__all_sync(0xffffffffu, tc::wait_or_abort(ofull(X), uint32_t(step - 1) & 1u,
-                                                           p.timeout_ns, abort_flag))) {
-              ok = false;
-              break;
+          const int vis = sees - j * K::kKeys - hp * (K::kKeys / 2);  // columns of the half seen
+          const bool whole = least >= (j + 1) * K::kKeys;
+          const PromptStep at = {ts, tp, to, sread(X), pdone(X), pfull(X), step, lane, j > g.ja};
+          if (idle) {  // no row of this warp is stored
+            ok = step == 0 || wait(pdone(X), step - 1);
+            if (ok && lane == 0) {
+              mbar_arrive(sread(X));
+              mbar_arrive(pfull(X));
             }
-            tc::fence_after_sync();
-  #pragma unroll
-            for (int c1 = 0; c1 < D; c1 += 32) {
-              uint32_t o[32];
-              tc::tmem_ld32(to + c1, o);
-  #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc::tmem_st32(to + c1, o);
-            }
+          } else if (whole) {
+            ok = sl < 0.f ? prompt_softmax<D, true, true>(at, sl, vis, pair, row, wait)
+                          : prompt_softmax<D, true, false>(at, sl, vis, pair, row, wait);
+          } else {
+            ok = sl < 0.f ? prompt_softmax<D, false, true>(at, sl, vis, pair, row, wait)
+                          : prompt_softmax<D, false, false>(at, sl, vis, pair, row, wait);
           }
-          const float2 asl2 = make_float2(asl, asl), nm2 = make_float2(-m, -m);
-          float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                          make_float2(0.f, 0.f)};
-  #pragma unroll
-          for (int c1 = 0; c1 < K::kKeys; c1 += 64) {
-            uint32_t pk[32];
-  #pragma unroll
-            for (int t = 0; t < 64; t += 2) {
-              const int a = c1 + t;
-              const float2 x = __ffma2_rn(
-                  make_float2(__uint_as_float(s[a]), __uint_as_float(s[a + 1])), asl2, nm2);
-              float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-              if (!whole) {
-                w.x = a < vis ? w.x : 0.f;
-                w.y = a + 1 < vis ? w.y : 0.f;
-              }
-              ls[(t >> 1) & 3] = __fadd2_rn(ls[(t >> 1) & 3], w);
-              pk[t / 2] = pack_bf16x2(w.x, w.y);
-            }
-            tc::tmem_st32(ts + c1 / 2, pk);
-          }
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pfull(X));
-          const float2 l2 = __fadd2_rn(__fadd2_rn(ls[0], ls[1]), __fadd2_rn(ls[2], ls[3]));
-          l += l2.x + l2.y;
+          if (!ok) break;
         }
         if (!ok) break;
         const bool cut = g.ja > 0 || g.jb < g.n;
         const size_t rec = (size_t(2 * c + (first_seg ? 0 : 1)) * 2 + X) * K::kRows + r;
         first_seg = false;
-        if (cut) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(m, l);
+        const float l = row.l + pair.swap(row.l);
+        pair.meet();  // the place is about to hold output
+        if (cut && hp == 0) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(row.m, l);
         if (je <= g.ja) continue;  // nothing of this tile here
         // ---- the segment's end: the output, or a record ----
-        if (!__all_sync(0xffffffffu, tc::wait_or_abort(ofull(X), uint32_t(step - 1) & 1u, p.timeout_ns,
-                                                       abort_flag))) {
-          ok = false;
-          break;
-        }
+        ok = wait(pdone(X), step - 1);
+        if (!ok) break;
         tc::fence_after_sync();
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) +
-                              (long long)(g.q.q0 + tok) * p.out_stride +
-                              (long long)(g.h * p.g + rh) * D;
-  #pragma unroll
-        for (int c1 = 0; c1 < D; c1 += 32) {
-          uint32_t o[32];
+        // Through shared memory, 64 bytes of each of the warp's rows at a time (chunks swizzled
+        // by the row), so that four lanes store a row's 64 bytes.
+        uint8_t* row_out = cut ? reinterpret_cast<uint8_t*>(p.part_o + rec * D + hp * (D / 2))
+                               : reinterpret_cast<uint8_t*>(
+                                     reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                     (long long)(g.q.q0 + tok) * p.out_stride +
+                                     (long long)(g.h * p.g + rh) * D + hp * (D / 2));
+        if (!row_ok) row_out = nullptr;
+        auto put = [&](int ch, const uint4& v) {
+          tc::sts128(stage + lane * 64 + ((ch ^ (lane >> 1 & 3)) << 4), v);
+        };
+        auto flush = [&](int at) {  // the staged bytes are bytes `at` .. `at` + 63 of the rows
           __syncwarp();
-          tc::tmem_ld32(to + c1, o);
-          if (!row_ok) {
-          } else if (cut) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + rec * D + c1);
-  #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              dst[e / 4] = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                       __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(orow + c1);
-  #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              dst[e / 8] = make_uint4(
-                  pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
-                  pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv),
-                  pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv),
-                  pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int from = 8 * k + (lane >> 2), ch = lane & 3;
+            uint8_t* dst = reinterpret_cast<uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_out), from));
+            const uint4 v = lds128(stage + from * 64 + ((ch ^ (from >> 1 & 3)) << 4));
+            if (dst) *reinterpret_cast<uint4*>(dst + at + ch * 16) = v;
+          }
+          __syncwarp();
+        };
+        if (!idle) {
+#pragma unroll 1
+          for (int c1 = 0; c1 < D / 2; c1 += 32) {
+            uint32_t o[32];
+            tc::tmem_ld32(to + c1, o);
+            if (cut) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  put(e, make_uint4(o[16 * half + 4 * e], o[16 * half + 4 * e + 1],
+                                    o[16 * half + 4 * e + 2], o[16 * half + 4 * e + 3]));
+                flush((c1 + 16 * half) * 4);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                     __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                put(e, make_uint4(w[0], w[1], w[2], w[3]));
+              }
+              flush(c1 * 2);
+            }
           }
         }
         tc::fence_before_sync();
@@ -470,7 +612,6 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       tc::fence_before_sync();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (active && warp == 0) {
       // ---------------- TMA ----------------
       if (lane == 0) {
@@ -487,7 +628,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             tma_load_3d(base + K::kOffKV + st * K::kTile + sl * K::kSlab, map, full(st), sl * 64, h, row);
           ++u;
         };
-        while (ok && walk.next(p, g)) {
+        while (ok && take(g, false)) {
           load_tile(&tmk, g.h, g.q.k0 + g.ja * K::kKeys);
           for (int X = 0; ok && X < 2; ++X) {
             if (!g.has(X)) continue;
@@ -497,14 +638,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
             mbar_arrive_expect_tx(qfull(X), uint32_t(p.tpt * p.g) * D * 2);
   #pragma unroll
             for (int sl = 0; sl < K::kSlabs; ++sl)
-              tma_load_3d(base + K::kOffQ + X * K::kTile + sl * K::kSlab, &tmq, qfull(X), sl * 64,
+              tma_load_3d(base + K::kOffQ + X * K::kTileQ + sl * K::kSlabQ, &tmq, qfull(X), sl * 64,
                           g.h * p.g, g.q.q0 + g.i * per + X * p.tpt);
             ++qn[X];
           }
           for (int j = g.ja; ok && j < g.jb; ++j) {
             if (j > g.ja) load_tile(&tmk, g.h, g.q.k0 + j * K::kKeys);
             if (ok) load_tile(&tmv, g.h, g.q.k0 + j * K::kKeys);
-          *sent = u;
           }
         }
         // every copy issued must have landed before the CTA may exit
@@ -514,134 +654,111 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
           if (qn[X] > 0) mbar_wait_bounded(qfull(X), uint32_t(qn[X] - 1) & 1u, p.timeout_ns);
       }
       __syncwarp();
-    } else if (active && warp == 1) {
-      // ---------------- MMA issuer ----------------
+    } else if (active && warp <= 2) {
+      // ---------------- scores of tile X ----------------
       if (lane == 0) {
-        constexpr uint32_t kIdS = tc::idesc_bf16<128, K::kKeys, false>();
-        constexpr uint32_t kIdO = tc::idesc_bf16<128, D, true>();
-        constexpr uint32_t kTileDesc = K::kTile >> 4, kSlabDesc = K::kSlab >> 4;
-        const uint64_t desc_q = tc::sdesc_sw128(base + K::kOffQ, 16, 1024);
+        const int X = warp - 1;
+        constexpr uint32_t kId = tc::idesc_bf16<128, K::kKeys, false>();
+        const uint64_t desc_q = tc::sdesc_sw128(base + K::kOffQ + X * K::kTileQ, 16, 1024);
         const uint64_t desc_k = tc::sdesc_sw128(base + K::kOffKV, 16, 1024);
-        const uint64_t desc_v = tc::sdesc_sw128(base + K::kOffKV, K::kSlab, 1024);
-        int steps[2] = {0, 0};   // P.V issued per tile
-        int uses[2] = {0, 0};    // segments begun per tile (queries loaded)
-        int opened[2] = {0, 0};  // segments whose first P.V was issued
-        int fixes = 0;           // V tiles with zeroed rows so far
+        const uint32_t ts = tmem + K::kColS + X * K::kKeys;
         bool ok = true;
-        auto wait = [&](uint32_t b, int phase) {
-          ok = ok && tc::wait_or_abort(b, uint32_t(phase) & 1u, p.timeout_ns, abort_flag);
+        auto wait = [&](uint32_t b, uint32_t phase) {
+          ok = ok && tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
         };
-        // S_X of key tile j of segment g, whose K is ring load u
-        auto issue_s = [&](int X, const PromptSeg& g, int j, int u, bool last_user) {
-          const int st = u % K::kStages;
-          if (j == g.ja) wait(qfull(X), uses[X]++);
-          wait(full(st), u / K::kStages);
-          if (!ok) return;
-          tc::fence_after_sync();
-          const uint64_t qd = desc_q + X * kTileDesc, kd = desc_k + uint64_t(st) * kTileDesc;
-  #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t ko = (kk >> 2) * kSlabDesc + (kk & 3) * 2;
-            tc::mma_bf16(tmem + K::kColS + X * 128, qd + ko, kd + ko, kIdS, kk > 0 ? 1u : 0u);
-          }
-          tc::commit(sfull(X));
-          if (j == g.end(X) - 1) tc::commit(qempty(X));
-          if (last_user) tc::commit(empty(st));
-        };
-        auto issue_pv = [&](int X, const PromptSeg& g, int j, int u, bool last_user) {
-          const int st = u % K::kStages;
-          wait(full(st), u / K::kStages);
-          if ((j + 1) * K::kKeys > g.q.nk) {
-            wait(vfix, fixes);
-            if (ok && last_user) mbar_arrive(vseen);
-          }
-          wait(pfull(X), steps[X]);
-          if (j == g.ja && opened[X]++ > 0) wait(ofree(X), opened[X] - 2);
-          if (!ok) return;
-          tc::fence_after_sync();
-          const uint64_t vd = desc_v + uint64_t(st) * kTileDesc;
-  #pragma unroll
-          for (int kk = 0; kk < K::kKeys / 16; ++kk)
-            tc::mma_bf16_tmem_a(tmem + K::kColO + X * 128, tmem + K::kColS + X * 128 + kk * 8,
-                                vd + kk * 128, kIdO, (j > g.ja || kk > 0) ? 1u : 0u);
-          tc::commit(ofull(X));
-          if (last_user) tc::commit(empty(st));
-          ++steps[X];
-        };
-        PromptSeg g, nx;
-        int u = 0;  // ring load of the segment's first K
-        bool have = walk.next(p, g);
-        if (have)
-          for (int X = 0; ok && X < 2; ++X)
-            if (g.has(X)) issue_s(X, g, g.ja, 0, X == (g.nx1 > 0 ? 1 : 0));
-        while (ok && have) {
-          const bool more = walk.next(p, nx);
-          const int next_u = u + 2 * (g.jb - g.ja);
-          const int lastX = g.nx1 > 0 ? 1 : 0;
+        int st = 0;  // the ring's even stages hold K tiles
+        uint32_t turn = 0, n = 0, segs = 0;
+        PromptSeg g;
+        while (ok && take(g, false)) {
+          const int je = g.end(X);
+          if (g.ja < je) wait(qfull(X), segs++);
           for (int j = g.ja; ok && j < g.jb; ++j) {
-            for (int X = 0; ok && X < 2; ++X) {
-              if (j < g.nx(X)) issue_pv(X, g, j, u + 2 * (j - g.ja) + 1, X == lastX);
+            wait(full(st), turn);
+            if (j < je) {
+              if (n++ > 0) wait(sread(X), n - 2);  // the scores before have been read
               if (!ok) break;
-              if (j + 1 < g.end(X)) issue_s(X, g, j + 1, u + 2 * (j + 1 - g.ja), X == lastX);
-              else if (j == g.jb - 1 && more && nx.has(X))
-                issue_s(X, nx, nx.ja, next_u, X == (nx.nx1 > 0 ? 1 : 0));
+              tc::fence_after_sync();
+              const uint64_t kd = desc_k + uint64_t(st) * (K::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_bf16(ts, desc_q + (kk >> 2) * (K::kSlabQ >> 4) + (kk & 3) * 2,
+                             kd + (kk >> 2) * (K::kSlab >> 4) + (kk & 3) * 2, kId,
+                             kk > 0 ? 1u : 0u);
+              tc::commit(sfull(X));
+              tc::commit(empty(st));
+              if (j == je - 1) tc::commit(qempty(X));
+            } else if (ok) {  // not used (and not let go before it is there)
+              mbar_arrive(empty(st));
             }
-            if ((j + 1) * K::kKeys > g.q.nk) ++fixes;
+            if ((st += 2) == K::kStages) {
+              st = 0;
+              turn ^= 1u;
+            }
           }
-          g = nx;
-          u = next_u;
-          have = more;
         }
-        tc::commit(mdone);  // every MMA issued must have completed before TMEM is freed
-        mbar_wait_bounded(mdone, 0u, p.timeout_ns);
+        tc::commit(mdone(warp - 1));  // every MMA issued must have completed before TMEM is freed
+        mbar_wait_bounded(mdone(warp - 1), 0u, p.timeout_ns);
       }
       __syncwarp();
-    } else if (active && warp == 2) {
-      // ---------------- V rows past the sequence's end ----------------
-      PromptSeg g;
-      int u = 0, fixes = 0;
+    } else if (active) {
+      // ---------------- P.V of tile X ----------------
+      const int X = warp == 3 ? 0 : 1;
+      constexpr uint32_t kId = tc::idesc_bf16<128, D, true>();
+      const uint64_t desc_v = tc::sdesc_sw128(base + K::kOffKV, K::kSlab, 1024);
+      const uint32_t tp = tmem + K::kColP + X * (K::kKeys / 2);
+      const uint32_t to = tmem + K::kColO + X * D;
       bool ok = true;
-      while (ok && walk.next(p, g)) {
-        // only the last key tile of the sequence can reach past nk
-        const int j = max(0, (g.q.nk + K::kKeys - 1) / K::kKeys - 1);
-        if (j >= g.ja && j < g.jb && (j + 1) * K::kKeys > g.q.nk) {
-          const int v = u + 2 * (j - g.ja) + 1, st = v % K::kStages;
-          // Waits on a parity must not be two phases off. The stage's copy is under way (so
-          // `full` is in its phase, and stays there until the MMAs have had the tile), and the
-          // MMA thread has seen the last tile zeroed.
-          uint64_t since = global_timer_ns();
-          for (int n = *sent, last = n; n <= v && !*abort_flag; n = *sent) {
-            __nanosleep(100);
-            const uint64_t now = global_timer_ns();
-            if (n != last) {  // the walk goes on
-              last = n;
-              since = now;
-            } else if (now - since > p.timeout_ns) {
-              *abort_flag = 1;
-            }
-          }
-          __syncwarp();
-          if (__any_sync(0xffffffffu, *abort_flag)) break;
-          ok = fixes == 0 ||
-               __all_sync(0xffffffffu, tc::wait_or_abort(vseen, uint32_t(fixes - 1) & 1u,
-                                                         p.timeout_ns, abort_flag));
-          ok = ok && __all_sync(0xffffffffu,
-                                tc::wait_or_abort(full(st), uint32_t(v / K::kStages) & 1u,
-                                                  p.timeout_ns, abort_flag));
+      auto wait = [&](uint32_t b, uint32_t phase) {  // by the first lane, for the warp
+        ok = ok && (lane != 0 || tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag));
+        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      };
+      int st = 1;  // the ring's odd stages hold V tiles
+      uint32_t turn = 0, n = 0, segs = 0;
+      PromptSeg g;
+      while (ok && take(g, true)) {
+        const int je = g.end(X);
+        for (int j = g.ja; ok && j < g.jb; ++j) {
+          wait(full(st), turn);
           if (!ok) break;
-          ++fixes;
-          const uint32_t vb = base + K::kOffKV + st * K::kTile;
-          const int r0 = g.q.nk - j * K::kKeys;
-          for (int k = lane; k < (K::kKeys - r0) * 8; k += 32)  // whole rows: no need to unswizzle
-  #pragma unroll
-            for (int sl = 0; sl < K::kSlabs; ++sl)
-              tc::sts128(vb + sl * K::kSlab + r0 * 128 + k * 16, make_uint4(0u, 0u, 0u, 0u));
-          fence_proxy_async_smem();  // before the MMAs read them
-          __syncwarp();
-          if (lane == 0) mbar_arrive(vfix);
+          if (j < je) {
+            const int r0 = g.q.nk - j * K::kKeys;  // rows of the sequence
+            if (r0 < K::kKeys) {
+              const uint32_t vb = base + K::kOffKV + st * K::kTile + r0 * 128;
+              for (int k = lane; k < (K::kKeys - r0) * 8; k += 32)  // whole rows, swizzled or not
+#pragma unroll
+                for (int sl = 0; sl < K::kSlabs; ++sl)
+                  tc::sts128(vb + sl * K::kSlab + k * 16, make_uint4(0u, 0u, 0u, 0u));
+              fence_proxy_async_smem();  // before the MMAs read them
+              __syncwarp();
+            }
+            if (j == g.ja && segs++ > 0) wait(ofree(X), segs - 2);
+            wait(pfull(X), n++);
+            if (!ok) break;
+            if (lane == 0) {
+              tc::fence_after_sync();
+              const uint64_t vd = desc_v + uint64_t(st) * (K::kTile >> 4);
+#pragma unroll
+              for (int kk = 0; kk < K::kKeys / 16; ++kk)
+                tc::mma_bf16_tmem_a(to, tp + kk * 8, vd + kk * 128, kId,
+                                    (j > g.ja || kk > 0) ? 1u : 0u);
+              tc::commit(pdone(X));
+              tc::commit(empty(st));
+            }
+            __syncwarp();
+          } else if (lane == 0) {
+            mbar_arrive(empty(st));
+          }
+          if ((st += 2) > K::kStages) {
+            st = 1;
+            turn ^= 1u;
+          }
         }
-        u += 2 * (g.jb - g.ja);
       }
+      if (lane == 0) {
+        tc::commit(mdone(2 + X));
+        mbar_wait_bounded(mdone(2 + X), 0u, p.timeout_ns);
+      }
+      __syncwarp();
     }
   }
   __syncthreads();

@@ -16,8 +16,11 @@
 // (N > F) or written (F > N): no item waits for another, but lengths and the list's count are
 // written only once every reader is done.
 //
-// One CTA: the sums are a scan over the batch by its threads, kept in shared memory; each
-// item finds its sequence by bisection there.
+// The sums are a scan over the batch by a CTA's threads, kept in its shared memory; a warp finds
+// the sequence of the first of 32 tokens by a 32-way search there, a lane its own from it on.
+// Few tokens: one CTA does it all. Many: CTAs on every SM write tables, list and rows, each with
+// its own scan of the batch, and a second launch of one CTA then writes lengths, count and
+// offsets (no CTA may change what another still reads).
 #include "common.cuh"
 #include "internal.h"
 
@@ -25,14 +28,28 @@ namespace pkv {
 
 namespace {
 constexpr int kResizeThreads = 1024;
+constexpr int kResizeSmall = 256;       // threads where batch and tokens are no more
+constexpr int kResizeOneCta = 4096;     // tokens up to which one CTA does it all
+enum : int { kAll = 0, kRows = 1, kCommit = 2 };
 
-// The last of the sequences 0 .. n - 1 whose exclusive sum is at most x (0 if none is).
-__device__ __forceinline__ int owner_of(const int* sums, int n, int x) {
-  int lo = 0, hi = n;
+// The last of the sequences lo .. hi - 1 whose exclusive sum is at most x (lo if none is).
+__device__ __forceinline__ int owner_of(const int* sums, int lo, int hi, int x) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (sums[mid] <= x) lo = mid;
     else hi = mid;
+  }
+  return lo;
+}
+// The same of 0 .. n - 1, by a whole warp.
+__device__ __forceinline__ int owner_by_warp(const int* sums, int n, int x, int lane) {
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 31) / 32, at = lo + lane * step;
+    const bool ok = at < lo + len && (lane == 0 || sums[at] <= x);
+    const int k = 31 - __clz(__ballot_sync(0xffffffffu, ok));  // sums never fall
+    lo += k * step;
+    len = min(step, len - k * step);
   }
   return lo;
 }
@@ -50,8 +67,8 @@ struct ResizeWant {
 
 __device__ __forceinline__ ResizeWant resize_want(const ResizeParams& p, int s) {
   ResizeWant w;
-  w.len = __ldcg(p.lens + s);
-  w.target = __ldcg(p.targets + s);
+  w.len = p.lens[s];
+  w.target = p.targets[s];
   const long long room = (long long)p.MBS << p.bs_log2;
   w.bad = w.len < 0 || w.target < 0 || w.len > room || w.target > room;
   if (w.bad) w.target = w.len;
@@ -64,6 +81,7 @@ __device__ __forceinline__ ResizeWant resize_want(const ResizeParams& p, int s) 
   return w;
 }
 
+template <int PART>
 __global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const ResizeParams p) {
   extern __shared__ int s_sums[];  // exclusive sums: tokens, blocks taken, blocks given back
   const int B = p.B;
@@ -72,23 +90,26 @@ __global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const R
   int* s_give = s_take + B + 1;
   __shared__ long long s_warp[3][kResizeThreads / 32];
   __shared__ int s_taken;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int at = blockIdx.x * threads + tid, step = gridDim.x * threads;
   const int up = (1 << p.bs_log2) - 1;
   pdl_wait_prior_grid();
   pdl_allow_next_grid();
   if (tid == 0) s_taken = 0;
   int flags = 0;
-  int count = __ldcg(p.free_count);
+  int count = *p.free_count;
   if (count < 0 || count > p.F) {
     count = max(0, min(count, p.F));
     flags |= PKV_DEV_NO_BLOCKS;
   }
   // ---- the three sums, 64 bits wide until they are stored (wishes may exceed any list) ----
-  const int per = (B + kResizeThreads - 1) / kResizeThreads;
+  const int per = (B + threads - 1) / threads;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   long long sum[3] = {0, 0, 0};
+  ResizeWant mine = {};  // the first of the thread's sequences
   for (int s = b0; s < b1; ++s) {
     const ResizeWant w = resize_want(p, s);
+    if (s == b0) mine = w;
     if (w.bad) flags |= PKV_DEV_BAD_CONTEXT_LEN;
     sum[0] += w.tokens;
     sum[1] += w.take;
@@ -110,28 +131,28 @@ __global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const R
   for (int i = 0; i < 3; ++i) {
     run[i] = incl[i] - sum[i];
     total[i] = 0;
-    for (int w = 0; w < kResizeThreads / 32; ++w) {
+    for (int w = 0; w < threads / 32; ++w) {
       if (w < warp) run[i] += s_warp[i][w];
       total[i] += s_warp[i][w];
     }
   }
-  // blocks given back cannot outnumber the list in a consistent state
-  const int given = clamp_i32(total[2]);
+  // (B times the table row's length is below 2^30: block sums fit 32 bits)
+  const int given = int(total[2]);
   const long long avail = (long long)count + given;
   // A sequence grows if its tokens have rows and its blocks are there. Once one in order
   // lacks either, so does every later one that asks for the same: the blocks taken are the
   // first ones.
-  auto fits = [&](long long tok0, const ResizeWant& w, long long take0) {
-    return tok0 + w.tokens <= p.T && (w.take == 0 || take0 + w.take <= avail);
+  auto fits = [&](long long tok0, int tokens, int take0, int take) {
+    return tok0 + tokens <= p.T && (take == 0 || (long long)take0 + take <= avail);
   };
   for (int s = b0; s < b1; ++s) {
-    const ResizeWant w = resize_want(p, s);
+    const ResizeWant w = s == b0 ? mine : resize_want(p, s);
     s_tok[s] = clamp_i32(run[0]);
-    s_take[s] = clamp_i32(run[1]);
-    s_give[s] = clamp_i32(run[2]);
+    s_take[s] = int(run[1]);
+    s_give[s] = int(run[2]);
     if (w.tokens > 0) {
-      if (!fits(run[0], w, run[1])) flags |= PKV_DEV_NO_BLOCKS;
-      else if (w.take > 0) atomicMax(&s_taken, int(run[1] + w.take));
+      if (!fits(run[0], w.tokens, int(run[1]), w.take)) flags |= PKV_DEV_NO_BLOCKS;
+      else if (w.take > 0) atomicMax(&s_taken, int(run[1]) + w.take);
     }
     run[0] += w.tokens;
     run[1] += w.take;
@@ -139,70 +160,95 @@ __global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const R
   }
   if (tid == 0) {
     s_tok[B] = clamp_i32(total[0]);
-    s_take[B] = clamp_i32(total[1]);
+    s_take[B] = int(total[1]);
     s_give[B] = given;
   }
   __syncthreads();
   const int taken = s_taken;
-  // given-back block i: the entries that shrinking sequences no longer hold
-  auto given_block = [&](int i) {
-    const int s = owner_of(s_give, B, i);
-    const int col = ((__ldcg(p.targets + s) + up) >> p.bs_log2) + (i - s_give[s]);
-    return __ldcg(p.tables + size_t(s) * p.MBS + col);
-  };
-  auto taken_block = [&](int i) {
-    return i < given ? given_block(i) : __ldcg(p.free_list + (count - 1 - (i - given)));
-  };
-  for (int i = tid; i < taken; i += kResizeThreads) {
-    const int s = owner_of(s_take, B, i);
-    const int col = ((__ldcg(p.lens + s) + up) >> p.bs_log2) + (i - s_take[s]);
-    p.tables[size_t(s) * p.MBS + col] = taken_block(i);
-  }
-  for (int i = taken + tid; i < given; i += kResizeThreads) {
-    const long long at = (long long)count + given - 1 - i;
-    if (at < p.F) p.free_list[at] = given_block(i);
-    else flags |= PKV_DEV_NO_BLOCKS;  // more blocks than the list holds: lost
-  }
-  // ---- the new tokens ----
-  const int all = s_tok[B];
-  for (int t = tid; t < p.T; t += kResizeThreads) {
-    long long slot = -1, pos = 0;
-    if (t < all) {
-      const int s = owner_of(s_tok, B, t);
-      const ResizeWant w = resize_want(p, s);
-      if (fits(s_tok[s], w, s_take[s])) {
-        const int n = w.len + (t - s_tok[s]), col = n >> p.bs_log2;
-        const int held = (w.len + up) >> p.bs_log2;
-        const int id = col < held ? __ldcg(p.tables + size_t(s) * p.MBS + col)
-                                  : taken_block(s_take[s] + col - held);
-        slot = ((long long)id << p.bs_log2) + (n & up);
-        pos = n;
-      }
+  if constexpr (PART != kCommit) {
+    // given-back block i: the entries that shrinking sequences no longer hold
+    auto given_block = [&](int i) {
+      const int s = owner_of(s_give, 0, B, i);
+      const int col = ((p.targets[s] + up) >> p.bs_log2) + (i - s_give[s]);
+      return p.tables[size_t(s) * p.MBS + col];
+    };
+    auto taken_block = [&](int i) {
+      return i < given ? given_block(i) : p.free_list[count - 1 - (i - given)];
+    };
+    int full = 0;
+    for (int i = at; i < taken; i += step) {
+      const int s = owner_of(s_take, 0, B, i);
+      const int col = ((p.lens[s] + up) >> p.bs_log2) + (i - s_take[s]);
+      p.tables[size_t(s) * p.MBS + col] = taken_block(i);
     }
-    p.slots[t] = slot;
-    p.positions[t] = pos;
+    for (int i = taken + at; i < given; i += step) {
+      const long long to = (long long)count + given - 1 - i;
+      if (to < p.F) p.free_list[to] = given_block(i);
+      else full = PKV_DEV_NO_BLOCKS;  // more blocks than the list holds: lost
+    }
+    if (PART == kRows && full && p.status) atomicOr(p.status, full);
+    flags |= full;
+    // ---- the new tokens ----
+    const int all = s_tok[B];
+    for (long long t0 = at - lane; t0 < p.T; t0 += step) {
+      const long long t = t0 + lane;
+      int s = owner_by_warp(s_tok, B, int(t0), lane);
+      if (t >= p.T) continue;
+      long long slot = -1, pos = 0;
+      if (t < all) {
+        if (s_tok[s + 1] <= t) s = owner_of(s_tok, s, B, int(t));
+        const int tok0 = s_tok[s], take0 = s_take[s];
+        if (fits(tok0, s_tok[s + 1] - tok0, take0, s_take[s + 1] - take0)) {
+          const int len = p.lens[s];
+          const int n = len + int(t - tok0), col = n >> p.bs_log2;
+          const int held = (len + up) >> p.bs_log2;
+          const int id = col < held ? p.tables[size_t(s) * p.MBS + col]
+                                    : taken_block(take0 + col - held);
+          slot = ((long long)id << p.bs_log2) + (n & up);
+          pos = n;
+        }
+      }
+      p.slots[t] = slot;
+      p.positions[t] = pos;
+    }
   }
-  for (int s = tid; s <= B; s += kResizeThreads) p.offsets[s] = s_tok[s];
-  __syncthreads();  // every read of the lengths and the count is done
-  for (int s = tid; s < B; s += kResizeThreads) {
-    const ResizeWant w = resize_want(p, s);
-    if (!w.bad && (w.tokens == 0 || fits(s_tok[s], w, s_take[s]))) p.lens[s] = w.target;
+  if constexpr (PART != kRows) {
+    for (int s = tid; s <= B; s += threads) p.offsets[s] = s_tok[s];
+    __syncthreads();  // every read of the lengths and the count is done
+    for (int s = b0; s < b1; ++s) {
+      const ResizeWant w = s == b0 ? mine : resize_want(p, s);
+      if (!w.bad && (w.tokens == 0 || fits(s_tok[s], w.tokens, s_take[s], w.take)))
+        p.lens[s] = w.target;
+    }
+    if (tid == 0) *p.free_count = int(min((long long)p.F, avail - taken));
+    if (flags && p.status) atomicOr(p.status, flags);
   }
-  if (tid == 0) *p.free_count = clamp_i32(min((long long)p.F, avail - taken));
-  if (flags && p.status) atomicOr(p.status, flags);
 }
 
 cudaError_t launch_resize(const ResizeParams& p, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(&paged_kv_resize_kernel);
   const size_t smem = size_t(12) * (p.B + 1);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               12 * (kResizeMaxSeqs + 1));
-    if (e != cudaSuccess) return e;
-  }
   ResizeParams copy = p;
   void* args[] = {&copy};
-  return launch_pdl(fn, dim3(1), dim3(kResizeThreads), args, smem, stream);
+  auto go = [&](const void* fn, int grid, int threads) {
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 12 * (kResizeMaxSeqs + 1));
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(fn, dim3(grid), dim3(threads), args, smem, stream);
+  };
+  if (p.T <= kResizeOneCta)
+    return go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kAll>), 1,
+              p.B <= kResizeSmall && p.T <= kResizeSmall ? kResizeSmall : kResizeThreads);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int rows = (p.T - 1) / kResizeThreads + 1;  // CTAs with a token per thread
+  e = go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kRows>), rows < sms ? rows : sms,
+         kResizeThreads);
+  if (e != cudaSuccess) return e;
+  return go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kCommit>), 1, kResizeThreads);
 }
 
 }  // namespace pkv

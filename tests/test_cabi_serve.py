@@ -42,6 +42,7 @@ def test_resize_refusals(lib):
     assert resize(block_size=24) == Status.ERR_UNSUPPORTED
     assert resize(num_seqs=16385) == Status.ERR_UNSUPPORTED
     assert resize(cap=1 << 30) == Status.ERR_UNSUPPORTED
+    assert resize(n=1 << 30) == Status.ERR_UNSUPPORTED
     assert resize(num_seqs=16384, max_blocks_per_seq=1 << 16) == Status.ERR_UNSUPPORTED
     assert resize(num_seqs=0) == Status.OK
 
