@@ -45,6 +45,9 @@ constexpr int kDiffMinRange = 2;
 // in keys of a 256-row item
 constexpr int kPromptItemCost = 256;
 constexpr int kPromptMinRange = 512;
+// tree attention: the same, in tokens
+constexpr int kTreeItemCost = 128;
+constexpr int kTreeMinRange = 256;
 // cascade decode: the prefix kernel runs on about 1/kCascadePrefixShare of the SMs
 constexpr int kCascadePrefixShare = 3;
 
@@ -240,10 +243,10 @@ pkv_status check_dims(const pkv_dims* d) {
 // sets a kernel attribute, which costs tens of microseconds, so recent plans are kept.
 struct PlanKey {
   pkv_dims d;
-  int kvt, q_len, device, pair, sm_cap, tree;
+  int kvt, q_len, device, pair, sm_cap;
   bool operator==(const PlanKey& o) const {
     return std::memcmp(&d, &o.d, sizeof(d)) == 0 && kvt == o.kvt && q_len == o.q_len &&
-           device == o.device && pair == o.pair && sm_cap == o.sm_cap && tree == o.tree;
+           device == o.device && pair == o.pair && sm_cap == o.sm_cap;
   }
 };
 constexpr int kPlanCache = 16;
@@ -253,14 +256,13 @@ Plan g_plans[kPlanCache];
 int g_plan_count = 0, g_plan_next = 0;
 
 pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, int sm_cap,
-                              bool tree, Plan* pl);
+                              Plan* pl);
 
 // q_len > 1: the causal multi-query decode (bf16 caches). pair: 16-token blocks go in
 // pairs on the tensor-core paths (pairs start after a skipped prefix). sm_cap > 0: size
-// the grid for that many SMs (the rest run another kernel at the same time). tree: the new
-// tokens form a tree (q_len of any size).
+// the grid for that many SMs (the rest run another kernel at the same time).
 pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool pair = true,
-                     int sm_cap = 0, bool tree = false) {
+                     int sm_cap = 0) {
   pkv_status st = check_dims(d);
   if (st != PKV_OK) return st;
   int dev = 0;
@@ -273,14 +275,13 @@ pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool p
   key.device = dev;
   key.pair = pair ? 1 : 0;
   key.sm_cap = sm_cap;
-  key.tree = tree ? 1 : 0;
   std::lock_guard<std::mutex> lock(g_plan_mu);
   for (int i = 0; i < g_plan_count; ++i)
     if (g_plan_keys[i] == key) {
       *pl = g_plans[i];
       return PKV_OK;
     }
-  st = make_plan_uncached(d, kvt, q_len, pair, sm_cap, tree, pl);
+  st = make_plan_uncached(d, kvt, q_len, pair, sm_cap, pl);
   if (st != PKV_OK) return st;
   g_plan_keys[g_plan_next] = key;
   g_plans[g_plan_next] = *pl;
@@ -290,7 +291,7 @@ pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool p
 }
 
 pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, int sm_cap,
-                              bool tree, Plan* pl) {
+                              Plan* pl) {
   Plan P{};
   P.g = d->num_q_heads / d->num_kv_heads;
   // query rows per KV head: (new token, group member) pairs, split into work units of
@@ -309,14 +310,7 @@ pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, 
   P.HU = d->num_kv_heads * P.nsg;
   const int simt = mma ? 0 : P.g;
   bool found = false;
-  if (tree) {
-    if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
-    P.nsg = (rows + kTcTileRows - 1) / kTcTileRows;
-    P.gs = (rows + P.nsg - 1) / P.nsg;
-    P.HU = d->num_kv_heads * P.nsg;
-    found = select_tree(d->head_dim, d->block_size, rows > kTcTileRows, rows <= kTcSplitRows, kvt,
-                        &P.k);
-  } else if (q_len > 1) {
+  if (q_len > 1) {
     if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
     // KV heads with 48 or more query rows go through the tcgen05 kernel, fewer rows
     // through the mma.sync path: measured on GB300 with the spec-70b lengths, tcgen05 vs
@@ -406,8 +400,7 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
                       const int32_t* block_tables, const int32_t* context_lens, float scale,
                       const pkv_dims* d, void* workspace, size_t workspace_bytes,
                       int32_t* status, cudaStream_t stream, int q_len = 1,
-                      unsigned long long* counters = nullptr, size_t counter_words = 0,
-                      const uint64_t* tree_mask = nullptr, const int32_t* tree_lens = nullptr) {
+                      unsigned long long* counters = nullptr, size_t counter_words = 0) {
   pkv_status st = check_dims(d);
   if (st != PKV_OK) return st;
   if (q_len < 1 || q_len > kMaxQueryLen) return PKV_ERR_SHAPE;
@@ -420,7 +413,7 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
       (q8 && (!aligned16(k_scale) || !aligned16(v_scale))))
     return PKV_ERR_ALIGNMENT;
   Plan P;
-  st = make_plan(d, kvt, &P, q_len, true, 0, tree_mask != nullptr);
+  st = make_plan(d, kvt, &P, q_len);
   if (st != PKV_OK) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < P.ws_bytes)
@@ -470,9 +463,6 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
   p.unit_slot0 = -1;
   p.q_len = q_len;
   p.beta = P.k.tc ? kTcHeadCost : 0;
-  p.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
-  p.tree_lens = tree_lens;
-  p.tree_words = 2 * ((q_len + 63) / 64);
 
   // tcgen05 kernel: whole units leave through TMA tensor stores of g-row boxes when g is
   // 8, 16 or 32 and the row tiles start on tokens (each box then starts on a 1024-byte
@@ -513,7 +503,6 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
   m.W = P.k.tc ? P.W : P.W / P.nsg;  // CTAs, or workers of nsg warps
   m.beta = p.beta;
   m.wprefix = p.prefix_out + (d->num_seqs + 1);
-  m.tree_lens = tree_lens;
   if (!p.fixup) launch_merge(m, stream);  // else cut units were folded in the kernel
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   return PKV_OK;
@@ -878,6 +867,110 @@ pkv_status run_prompt(void* out, const void* q, const void* k, const void* v,
   void* args[] = {&tmq, &tmk, &tmv, &p};
   if (launch_pdl(P.k.fn, dim3(P.G), dim3(P.k.threads), args, P.k.smem, stream) != cudaSuccess ||
       launch_prompt_merge(p, P.G, stream) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  return PKV_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Tree attention
+// ---------------------------------------------------------------------------
+// workspace: [cuts (G)][records' (m, l), 2 per CTA of 2 x 128 rows][records' o]
+struct TreePlan {
+  TreeKernelInfo k;
+  int G;
+  size_t off_ml, off_o, ws_bytes;
+};
+
+pkv_status check_tree(const pkv_dims* d, int kvt, int q_len, TreeKernelInfo* k) {
+  pkv_status st = check_dims(d);
+  if (st != PKV_OK) return st;
+  if (q_len < 1 || q_len > kMaxQueryLen) return PKV_ERR_SHAPE;
+  if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
+  return select_tree(d->head_dim, d->block_size, kvt, k) ? PKV_OK : PKV_ERR_UNSUPPORTED;
+}
+
+pkv_status make_tree_plan(const pkv_dims* d, int kvt, int q_len, TreePlan* P) {
+  pkv_status st = check_tree(d, kvt, q_len, &P->k);
+  if (st != PKV_OK) return st;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PKV_ERR_CUDA;
+  P->G = sms;  // all of a CTA's TMEM and shared memory: one per SM
+  const size_t rows = size_t(2) * P->G * 256;
+  P->off_ml = align_up(size_t(P->G) * sizeof(TreeCut), 256);
+  P->off_o = align_up(P->off_ml + rows * 8, 256);
+  P->ws_bytes = align_up(P->off_o + rows * d->head_dim * 4, 256);
+  return PKV_OK;
+}
+
+pkv_status run_tree(int kvt, void* out, const void* q, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                    const int32_t* context_lens, const uint64_t* tree_mask,
+                    const int32_t* tree_lens, int q_len, float scale, const pkv_dims* d,
+                    void* workspace, size_t workspace_bytes, int32_t* status,
+                    cudaStream_t stream) {
+  TreePlan P;
+  pkv_status st = check_tree(d, kvt, q_len, &P.k);
+  if (st != PKV_OK) return st;
+  if (d->num_seqs == 0) return PKV_OK;
+  const bool q8 = kvt != PKV_KV_BF16;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !tree_mask ||
+      (q8 && (!k_scale || !v_scale)))
+    return PKV_ERR_NULL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      (q8 && (!aligned16(k_scale) || !aligned16(v_scale))) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0)
+    return PKV_ERR_ALIGNMENT;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return PKV_ERR_WORKSPACE;
+  st = make_tree_plan(d, kvt, q_len, &P);
+  if (st != PKV_OK) return st;
+  if (workspace_bytes < P.ws_bytes) return PKV_ERR_WORKSPACE;
+  const long long rows = (long long)d->num_blocks * d->num_kv_heads * d->block_size;
+  CUtensorMap tmk, tmv;
+  if (!cache_map(&tmk, k_cache, q8, d->head_dim, rows, d->block_size) ||
+      !cache_map(&tmv, v_cache, q8, d->head_dim, rows, d->block_size))
+    return PKV_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  TreeParams p{};
+  p.q = q;
+  p.out = out;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  p.tree_lens = tree_lens;
+  p.cuts = reinterpret_cast<TreeCut*>(ws);
+  p.part_ml = reinterpret_cast<float*>(ws + P.off_ml);
+  p.part_o = reinterpret_cast<float*>(ws + P.off_o);
+  p.status = status;
+  p.B = d->num_seqs;
+  p.Hq = d->num_q_heads;
+  p.Hkv = d->num_kv_heads;
+  p.MBS = d->max_blocks_per_seq;
+  p.NB = d->num_blocks;
+  p.BS = d->block_size;
+  p.D = d->head_dim;
+  p.q_len = q_len;
+  p.tree_words = 2 * ((q_len + 63) / 64);
+  const int group = d->num_q_heads / d->num_kv_heads;
+  p.parts = 1;
+  while (group % p.parts != 0 || group / p.parts > kTcTileRows) ++p.parts;
+  p.HV = d->num_kv_heads * p.parts;
+  p.g = group / p.parts;
+  p.tpt = kTcTileRows / p.g;
+  p.item_cost = kTreeItemCost;
+  p.min_range = kTreeMinRange;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.timeout_ns = kTimeoutNs;
+  if (cudaFuncSetAttribute(P.k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, P.k.smem) !=
+      cudaSuccess)
+    return PKV_ERR_CUDA;
+  void* args[] = {&tmk, &tmv, &p};
+  if (launch_pdl(P.k.fn, dim3(P.G), dim3(P.k.threads), args, P.k.smem, stream) != cudaSuccess ||
+      launch_tree_join(p, P.G, stream) != cudaSuccess)
     return PKV_ERR_CUDA;
   return PKV_OK;
 }
@@ -1464,10 +1557,8 @@ pkv_status pkv_keep_tokens(void* k_cache, void* v_cache, float* k_scale, float* 
 pkv_status pkv_decode_tree_workspace_bytes(const pkv_dims* dims, int32_t q_len,
                                            pkv_kv_dtype kv_dtype, size_t* bytes) {
   if (!bytes) return PKV_ERR_NULL;
-  if (q_len < 1 || q_len > kMaxQueryLen) return PKV_ERR_SHAPE;
-  if (kv_dtype < PKV_KV_BF16 || kv_dtype > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
-  Plan P;
-  pkv_status st = make_plan(dims, kv_dtype, &P, q_len, true, 0, true);
+  TreePlan P;
+  pkv_status st = make_tree_plan(dims, kv_dtype, q_len, &P);
   if (st != PKV_OK) return st;
   *bytes = P.ws_bytes;
   return PKV_OK;
@@ -1479,11 +1570,9 @@ pkv_status pkv_decode_tree_bf16(void* out, const void* q, const void* k_cache,
                                 const int32_t* tree_lens, int32_t q_len, float scale,
                                 const pkv_dims* dims, void* workspace, size_t workspace_bytes,
                                 int32_t* status, pkv_stream_t stream) {
-  if (!tree_mask) return PKV_ERR_NULL;
-  return run_decode(PKV_KV_BF16, out, q, k_cache, v_cache, nullptr, nullptr, block_tables,
-                    context_lens, scale, dims, workspace, workspace_bytes, status,
-                    reinterpret_cast<cudaStream_t>(stream), q_len, nullptr, 0, tree_mask,
-                    tree_lens);
+  return run_tree(PKV_KV_BF16, out, q, k_cache, v_cache, nullptr, nullptr, block_tables,
+                  context_lens, tree_mask, tree_lens, q_len, scale, dims, workspace,
+                  workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 pkv_status pkv_decode_tree_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -1494,11 +1583,9 @@ pkv_status pkv_decode_tree_q8(void* out, const void* q, const void* k_cache, con
                               void* workspace, size_t workspace_bytes, int32_t* status,
                               pkv_stream_t stream) {
   if (code_of(kv_dtype) < 0) return PKV_ERR_DTYPE;
-  if (!tree_mask) return PKV_ERR_NULL;
-  return run_decode(kv_dtype, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
-                    context_lens, scale, dims, workspace, workspace_bytes, status,
-                    reinterpret_cast<cudaStream_t>(stream), q_len, nullptr, 0, tree_mask,
-                    tree_lens);
+  return run_tree(kv_dtype, out, q, k_cache, v_cache, k_scale, v_scale, block_tables,
+                  context_lens, tree_mask, tree_lens, q_len, scale, dims, workspace,
+                  workspace_bytes, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 pkv_status pkv_prompt_workspace_bytes(const pkv_prompt_dims* dims, size_t* bytes) {

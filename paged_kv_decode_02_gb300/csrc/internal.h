@@ -41,9 +41,6 @@ struct DecodeParams {
   int HU;                      // work units per sequence (Hkv * nsg)
   float scale_log2;            // softmax scale * log2(e)
   unsigned long long timeout_ns;
-  const uint32_t* tree_mask;   // tree decode: [B, q_len, tree_words] node masks, 32 nodes a word
-  const int32_t* tree_lens;    // [B] nodes of each tree, or NULL: q_len
-  int tree_words;
 };
 
 // Parameters of the shared-prefix (cascade) kernel: for KV head h, the B*g query rows
@@ -107,7 +104,6 @@ struct MergeParams {
   int W;                       // decode workers (groups of nsg warps, or tcgen05 CTAs)
   const int32_t* wprefix;      // beta > 0: per-sequence prefix of tiles + beta * [tiles > 0]
   int beta;                    // as in DecodeParams (0: workers cut the plain order)
-  const int32_t* tree_lens;    // tree decode: [B] new tokens of each sequence, or NULL: q_len
 };
 
 void launch_merge(const MergeParams& p, cudaStream_t stream);
@@ -165,13 +161,6 @@ bool select_decode_tc(int D, int BS, bool row_tiles, bool split, int kvt,
 bool select_decode_tc_int8(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 bool select_decode_tc_e4m3(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 bool select_decode_tc_e5m2(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
-
-// The same kernels for a tree of new tokens (DecodeParams::tree_mask), one table per code in
-// tree_bf16.cu, tree_int8.cu, tree_e4m3.cu and tree_e5m2.cu.
-bool select_tree(int D, int BS, bool row_tiles, bool split, int kvt, DecodeKernelInfo* info);
-bool select_tree_int8(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
-bool select_tree_e4m3(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
-bool select_tree_e5m2(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 
 bool select_decode_int8(int D, int BS, int simt_heads, DecodeKernelInfo* info,
                         bool pair = false);
@@ -326,6 +315,46 @@ struct PromptKernelInfo {
 bool select_prompt(int D, PromptKernelInfo* info);
 // joins the records of `grid` CTAs
 cudaError_t launch_prompt_merge(const PromptParams& p, int grid, cudaStream_t stream);
+
+// Parameters of the tree attention (tree.cuh, tree_join.cu).
+struct TreeCut {               // as PromptCut; u: the item of the sequence
+  int slot, s, u, state;
+};
+struct TreeParams {
+  const void* q;               // [B, q_len, Hq, D] bf16
+  void* out;
+  const float* k_scale;        // [NB, Hkv, BS] fp32 (one-byte caches only)
+  const float* v_scale;
+  const int32_t* block_tables; // [B, MBS]
+  const int32_t* context_lens; // [B]
+  const uint32_t* tree_mask;   // [B, q_len, tree_words] node masks, 32 nodes a word
+  const int32_t* tree_lens;    // [B] nodes of each tree, or NULL: q_len
+  float* part_o;               // [2 G, 2, 128, D] fp32 records' outputs (unnormalised)
+  float* part_ml;              // [2 G, 2, 128, 2] fp32 (running max in log2 units, sum)
+  TreeCut* cuts;               // [G]
+  int32_t* status;
+  int B, Hq, Hkv, MBS, NB, BS, D, q_len, tree_words;
+  int parts;                   // equal parts that a group of more than 128 heads is cut into
+  int HV;                      // Hkv * parts
+  int g;                       // query heads per part: Hq / HV, at most 128
+  int tpt;                     // nodes per row tile: 128 / g
+  int item_cost;               // what ending an item costs, in tokens
+  int min_range;               // positions (tokens) of a CTA's stretch at least
+  float scale_log2;            // softmax scale * log2(e)
+  unsigned long long timeout_ns;
+};
+struct TreeKernelInfo {
+  const void* fn;
+  int threads, smem;
+};
+// one table per code in tree_bf16.cu, tree_int8.cu, tree_e4m3.cu and tree_e5m2.cu
+bool select_tree(int D, int BS, int kvt, TreeKernelInfo* info);
+bool select_tree_int8(int D, int BS, TreeKernelInfo* info);
+bool select_tree_e4m3(int D, int BS, TreeKernelInfo* info);
+bool select_tree_e5m2(int D, int BS, TreeKernelInfo* info);
+// joins the records of `grid` CTAs and zeroes the rows past each tree's tiles; with a status
+// word, then checks every sequence and zeroes the output of those that fail
+cudaError_t launch_tree_join(const TreeParams& p, int grid, cudaStream_t stream);
 
 // Parameters of the differential decode (decode_diff.cuh, diff_merge.cu).
 struct DiffParams {

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   auto take = [&](PromptSeg& g, bool whole_warp) {
     const uint32_t slot = heard_of % K::kQueue;
     bool ok = tc::poll_or_abort(told(slot), (heard_of / K::kQueue) & 1u, p.timeout_ns, abort_flag);
-    if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (!ok) return false;
     ++heard_of;
     const uint32_t from = base + K::kOffQueue + slot * 64;
@@ -438,39 +438,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
     if (!whole_warp || lane == 0) mbar_arrive(heard(slot));
     return g.some != 0;
   };
-  if (tid == 0) {  // for the kernel that joins the records
-    PromptCut cut = {-1, 0, 0, 0, 0};
-    if (active) {
-      PromptWalk w2 = walk;
-      PromptSeg g;
-      if (!w2.next(p, g)) {
-        cut.state = kPromptEmpty;
-      } else {
-        // the first segment, and the last one (the item that holds `stop`)
-        cut.state = (g.ja > 0 ? kPromptContinues : 0) | (g.ja > 0 && g.jb == g.n ? kPromptEnds : 0);
-        if (g.ja == 0 && g.jb < g.n) {
-          cut.state |= kPromptBegins;
-          cut.slot = 2 * c;
-          cut.s = g.s, cut.h = g.h, cut.i = g.i;
-        } else if (stop.j > 0 && stop.s < p.B && !(g.s == stop.s && g.h == stop.h && g.i == stop.i)) {
-          PromptSeq q;
-          q.load(p, stop.s);
-          if (stop.j < q.key_tiles(min(q.nq, (stop.i + 1) * per), p.keys)) {
-            cut.state |= kPromptBegins;
-            cut.slot = 2 * c + 1;
-            cut.s = stop.s, cut.h = stop.h, cut.i = stop.i;
-          }
-        }
-      }
-    }
-    p.cuts[c] = cut;
-  }
-
-  if (active && warp == 21) {
+  if (warp == 21) {
     // ---------------- the walk ----------------
     if (lane == 0) {
+      // for the kernel that joins the records: how the first segment and the last one are cut
+      PromptCut cut = {-1, 0, 0, 0, active ? kPromptEmpty : 0};
       PromptSeg g;
-      bool ok = true;
+      bool ok = active;
       for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % K::kQueue;
         g.some = walk.next(p, g) ? 1 : 0;
@@ -482,7 +456,18 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         for (int k = 0; k < 4; ++k) tc::sts128(base + K::kOffQueue + slot * 64 + 16 * k, from[k]);
         mbar_arrive(told(slot));
         if (!g.some) break;
+        if (n == 0)
+          cut.state = (g.ja > 0 ? kPromptContinues : 0) |
+                      (g.ja > 0 && g.jb == g.n ? kPromptEnds : 0);
+        if (g.ja == 0 && g.jb < g.n) {  // (the last segment)
+          cut.state |= kPromptBegins;
+          cut.slot = 2 * c + (n > 0 ? 1 : 0);
+          cut.s = g.s;
+          cut.h = g.h;
+          cut.i = g.i;
+        }
       }
+      p.cuts[c] = cut;
     }
     __syncwarp();
   } else if (warp >= 4 && warp < 20) {
@@ -502,8 +487,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       const int rt = r / p.g, rh = r % p.g;  // token of the tile, head of the group
       uint32_t step = 0;
       auto wait = [&](uint32_t b, uint32_t phase) {
-        return __all_sync(0xffffffffu,
-                          tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
+        const bool got = tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
+        return __all_sync(0xffffffffu, got && !*abort_flag) != 0;
       };
       bool ok = true, first_seg = true;
       PromptSeg g;
@@ -609,6 +594,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ofree(X));
       }
+      // One that gives up leaves no partner behind: the partner meets the flag at its next wait,
+      // and passes two of their barriers before it at most.
+      if (*abort_flag)
+        asm volatile("bar.arrive %0, 64;\n\tbar.arrive %0, 64;" ::"r"(pair.id) : "memory");
       tc::fence_before_sync();
     }
   } else {

@@ -21,6 +21,8 @@
 // Few tokens: one CTA does it all. Many: CTAs on every SM write tables, list and rows, each with
 // its own scan of the batch, and a second launch of one CTA then writes lengths, count and
 // offsets (no CTA may change what another still reads).
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -29,7 +31,7 @@ namespace pkv {
 namespace {
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeSmall = 256;       // threads where batch and tokens are no more
-constexpr int kResizeOneCta = 4096;     // tokens up to which one CTA does it all
+constexpr int kResizeOneCta = 4096;     // tokens (or blocks) up to which one CTA does it all
 enum : int { kAll = 0, kRows = 1, kCommit = 2 };
 
 // The last of the sequences lo .. hi - 1 whose exclusive sum is at most x (lo if none is).
@@ -237,14 +239,16 @@ cudaError_t launch_resize(const ResizeParams& p, cudaStream_t stream) {
     }
     return launch_pdl(fn, dim3(grid), dim3(threads), args, smem, stream);
   };
-  if (p.T <= kResizeOneCta)
+  // (a call without tokens gives blocks back, as many as the tables hold at most)
+  const long long work = p.T > 0 ? p.T : (long long)p.B * p.MBS;
+  if (work <= kResizeOneCta)
     return go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kAll>), 1,
               p.B <= kResizeSmall && p.T <= kResizeSmall ? kResizeSmall : kResizeThreads);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int rows = (p.T - 1) / kResizeThreads + 1;  // CTAs with a token per thread
+  const int rows = int(std::min(work, 1ll << 30) - 1) / kResizeThreads + 1;  // CTAs with one per thread
   e = go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kRows>), rows < sms ? rows : sms,
          kResizeThreads);
   if (e != cudaSuccess) return e;

@@ -1,0 +1,923 @@
+// tree.cuh -- attention of a tree of drafted tokens over the paged cache, on the
+// fifth-generation tensor cores (instantiated per KV dtype in tree_bf16.cu, tree_int8.cu,
+// tree_e4m3.cu and tree_e5m2.cu).
+//
+// The last t cached tokens of a sequence are the nodes of a tree ("推测解码", chenk.top page, with
+// several candidates per position); node i sees every token before them and the nodes whose
+// bits its mask has set:
+//   out[i, h] = softmax(scale * K q[i, h]) V over those tokens, reached through the block table.
+// Bound by the context's bytes, which every row of a head shares; past some 100 rows by what
+// is done with them on chip.
+//
+// Work. A query row is (node, head of the group); tpt = 128 / g nodes make a tile of 128 MMA
+// rows (g > 128: the group is cut into equal parts first). The context is walked in key tiles of
+// 64 tokens, by two pipelines X = 0 and 1. An item is one KV head with either two row tiles, one
+// per pipeline, that share each key tile, or, where only one is left, that row tile in both
+// pipelines, which take the even and the odd key tiles; their states meet at its end. (One
+// pipeline alone waits for itself: scores, softmax, P.V in turn.) Items lie on a line, each as
+// long as its context plus a constant, and every CTA takes an equal stretch of it; an item cut
+// between stretches leaves records (o, m, l) that a second kernel joins, as in the prompt
+// attention (prompt.cuh), whose pipelines these are:
+//   warp 0       TMA: the blocks of K and V tiles (lane b block b), ids read a tile ahead;
+//   warps 1, 2   S_X = Q_X K_j^T; warps 3, 12: O_X += P_X V_j (bf16 caches: after zeroing V rows
+//                past the context, which may hold anything);
+//   warps 4..7, 8..11  softmax of pipeline 0, 1: one query row per thread; also its Q rows and the
+//                end of each segment;
+//   warp 13      walks the stretch and tells the others its segments;
+//   warps 14..19 (one-byte caches) widen codes in shared memory.
+// One-byte caches: codes land in a ring of their own; K becomes fp16 exactly, V fp16 of code x
+// scale (11 bits). Q is fp16 too: a row's bf16 values times the power of two that takes its
+// largest to [2^14, 2^15), which loses nothing of a value within 2^-28 of the largest and 2^-39
+// of the largest below; the row's scale takes the power back. K's scale multiplies the fp32 score.
+// Weights are bf16 (fp16 over one-byte caches), scores, maxima and sums fp32; the reference
+// maximum moves when a tile's exceeds it by more than 8 (log2 units).
+// Every wait is bounded: on a timeout the CTA sets a status bit, lets its copies and MMAs
+// complete, frees its TMEM and leaves.
+#pragma once
+
+#include "decode.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+template <int D, int BS, int CODE>
+struct TreeCfg {
+  static constexpr bool kQ8 = CODE >= 0;
+  static constexpr int kKeys = 64;
+  static constexpr int kBlocks = kKeys / BS;     // blocks per key tile
+  static constexpr int kSlabs = D / 64;          // 128-byte column slabs of a 16-bit row
+  static constexpr int kSlabQ = 128 * 128;
+  static constexpr int kTileQ = kSlabs * kSlabQ;
+  static constexpr int kSlab = kKeys * 128;
+  static constexpr int kTile = kSlabs * kSlab;   // a K or V tile, 16 bits
+  static constexpr int kStages = kQ8 ? 4 : 6;    // of the ring K, V, K, V, ...
+  static constexpr int kCodes = kKeys * D;       // a tile of codes
+  static constexpr int kCodeStages = kQ8 ? 6 : 0;
+  static constexpr int kScaleSlots = kQ8 ? 16 : 0;  // K scales of key tile n: slot n % 16
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffKV = 2 * kTileQ;
+  static constexpr int kOffCodes = kOffKV + kStages * kTile;
+  static constexpr int kOffOut = kOffCodes + kCodeStages * kCodes;  // 32 rows of 128 bytes a warp
+  static constexpr int kOffKScale = kOffOut + 8 * 4096;
+  static constexpr int kOffVScale = kOffKScale + kScaleSlots * kKeys * 4;
+  // (m, l) of pipeline 1's rows, for pipeline 0: [2 segments][128]
+  static constexpr int kOffState = kOffVScale + kCodeStages * kKeys * 4;
+  static constexpr int kQueue = 4;
+  static constexpr int kOffQueue = kOffState + 2 * 128 * 8;
+  static constexpr int kOffBar = kOffQueue + kQueue * 64;
+  // full[stages] empty[stages] cfull[codes] cempty[codes] qfull[2] qempty[2] sfull[2] sread[2]
+  // pfull[2] pdone[2] ofree[2] mdone[4] told[queue] heard[queue]
+  static constexpr int kNumBars = 2 * kStages + 2 * kCodeStages + 18 + 2 * kQueue;
+  static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
+  static constexpr int kOffAbort = kOffTmemSlot + 4;
+  static constexpr int kOffScan = (kOffAbort + 4 + 15) / 16 * 16;
+  static constexpr int kSmem = kOffScan + 256 + 1024;
+  static constexpr int kConvWarps = kQ8 ? 6 : 0;
+  static constexpr int kThreads = (14 + kConvWarps) * 32;
+  static constexpr int kListeners = 13 + kConvWarps;  // warps that hear of segments
+  static constexpr int kColS = 0, kColP = 2 * kKeys, kColO = 3 * kKeys;
+  static_assert(kColO + 2 * D <= 512, "TMEM columns");
+  static_assert(kStages % 2 == 0 && kCodeStages % 2 == 0, "K tiles on even stages");
+  static_assert(kOffCodes % 1024 == 0 && kOffOut % 1024 == 0, "swizzle atoms");
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
+};
+
+// A sequence: its context, its tree, and its items.
+struct TreeSeq {
+  int len, nodes, tiles;  // row tiles
+  __device__ __forceinline__ void load(const TreeParams& p, int s) {
+    len = min(max(__ldg(p.context_lens + s), 0), p.MBS * p.BS);
+    nodes = p.tree_lens ? min(max(__ldg(p.tree_lens + s), 0), p.q_len) : p.q_len;
+    nodes = min(nodes, len);
+    tiles = (nodes + p.tpt - 1) / p.tpt;
+  }
+  __device__ __forceinline__ int items(const TreeParams& p) const {
+    return p.HV * ((tiles + 1) >> 1);  // (none: no nodes, the rows are zeros)
+  }
+  __device__ __forceinline__ long long length(const TreeParams& p) const {
+    return (long long)items(p) * (len + p.item_cost);
+  }
+};
+
+// What a CTA does of one item: key tiles [ja, jb) of n.
+struct alignas(16) TreeSeg {
+  int s, hv, row0, ja;   // row0: first node of tile 0
+  int jb, n, len, nodes;
+  int split;             // 1: one row tile, pipeline X takes the key tiles of parity X
+  int some;              // 0: there is none, the stretch is over
+  int pad[6];
+  __device__ __forceinline__ bool uses(int X, int j) const { return !split || (j & 1) == X; }
+  // key tiles of pipeline X in the segment
+  __device__ __forceinline__ int count(int X) const {
+    return split ? (jb + 1 - X) / 2 - (ja + 1 - X) / 2 : jb - ja;
+  }
+  __device__ __forceinline__ int first(int X) const {
+    return split ? ja + ((ja ^ X) & 1) : ja;
+  }
+};
+static_assert(sizeof(TreeSeg) == 64, "a place in the queue");
+
+struct TreePlace {
+  int s, u, j;  // sequence, item of the sequence, key tile
+};
+
+// Unnormalised state of a row in one pipeline.
+struct TreeRow {
+  float m, l;
+};
+
+struct TreeStep {
+  uint32_t ts, tp, to, sread, pdone, pfull, step;
+  int lane;
+  bool begun;
+};
+
+// One row (a thread) of a score tile: the 64 scores become weights 2^(scale s - m), 16-bit pairs
+// in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`.
+template <int D, int CODE, bool kWhole, typename Wait>
+__device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t kscale,
+                                             const uint32_t (&seen)[2], TreeRow& row,
+                                             const Wait& wait) {
+  constexpr bool kQ8 = CODE >= 0;
+  uint32_t s[64];
+  tc::tmem_ld64(at.ts, s);
+  tc::fence_before_sync();
+  __syncwarp();
+  if (at.lane == 0) mbar_arrive(at.sread);  // the next scores may come
+  if constexpr (kQ8) {  // each column times its K scale and the row's (with its sign)
+    const float2 r2 = make_float2(sl, sl);
+#pragma unroll
+    for (int t = 0; t < 64; t += 4) {
+      const uint4 k4 = lds128(kscale + 4 * t);
+      const float2 f0 = __fmul2_rn(make_float2(__uint_as_float(k4.x), __uint_as_float(k4.y)), r2);
+      const float2 f1 = __fmul2_rn(make_float2(__uint_as_float(k4.z), __uint_as_float(k4.w)), r2);
+      const float2 a = __fmul2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])), f0);
+      const float2 b =
+          __fmul2_rn(make_float2(__uint_as_float(s[t + 2]), __uint_as_float(s[t + 3])), f1);
+      s[t] = __float_as_uint(a.x);
+      s[t + 1] = __float_as_uint(a.y);
+      s[t + 2] = __float_as_uint(b.x);
+      s[t + 3] = __float_as_uint(b.y);
+    }
+  } else if (sl < 0.f) {  // a negative scale is carried by the scores' signs
+#pragma unroll
+    for (int t = 0; t < 64; ++t) s[t] ^= 0x80000000u;
+  }
+  const float asl = kQ8 ? 1.f : fabsf(sl);
+  if constexpr (!kWhole) {
+#pragma unroll
+    for (int t = 0; t < 64; ++t)
+      if (!(seen[t >> 5] >> (t & 31) & 1u)) s[t] = 0xff800000u;  // -inf
+  }
+  float mx[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) mx[t] = __uint_as_float(s[t]);
+#pragma unroll
+  for (int t = 0; t < 28; ++t)
+    mx[t & 7] = fmax3(mx[t & 7], __uint_as_float(s[8 + 2 * t]), __uint_as_float(s[9 + 2 * t]));
+  const float top = asl * fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                                fmaxf(mx[6], mx[7]));
+  float alpha = 1.f;
+  const bool up = top > row.m + 8.f;
+  if (up) {
+    alpha = fast_exp2(row.m - top);  // 0 while the row has seen nothing
+    row.m = top;
+    row.l *= alpha;
+  }
+  // (scores of -inf alone: weights 0, not 2^(-inf + inf))
+  const float m = row.m > -INFINITY ? row.m : 0.f;
+  const float2 sl2 = make_float2(asl, asl), nm2 = make_float2(-m, -m);
+  float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  uint32_t pk[32];
+#pragma unroll
+  for (int t = 0; t < 64; t += 2) {
+    const float2 x =
+        __ffma2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])), sl2, nm2);
+    float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+    if constexpr (!kWhole) {
+      w.x = seen[t >> 5] >> (t & 31) & 1u ? w.x : 0.f;
+      w.y = seen[t >> 5] >> ((t & 31) + 1) & 1u ? w.y : 0.f;
+    }
+    ls[(t >> 1) & 1] = __fadd2_rn(ls[(t >> 1) & 1], w);
+    pk[t / 2] = kQ8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+  }
+  const float2 l2 = __fadd2_rn(ls[0], ls[1]);
+  row.l += l2.x + l2.y;
+  // P.V of the tile before has completed: P's columns are free, O holds what came before
+  if (at.step > 0 && !wait(at.pdone, at.step - 1)) return false;
+  tc::fence_after_sync();
+  if (at.begun && __any_sync(0xffffffffu, up)) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      uint32_t o[16];
+      tc::tmem_ld16(at.to + c, o);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+      tc::tmem_st16(at.to + c, o);
+    }
+  }
+  tc::tmem_st32(at.tp, pk);
+  tc::fence_before_sync();
+  __syncwarp();
+  if (at.lane == 0) mbar_arrive(at.pfull);
+  return true;
+}
+
+// Sixteen codes -> two 16-byte chunks of fp16: exact, or times `sc` (rounded once).
+template <int CODE, bool kScale>
+__device__ __forceinline__ void widen16(const uint4& raw, float sc, uint4& a, uint4& b) {
+  using Codec = Code8<CODE>;
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t x = Codec::pre(w[e]);
+    o[2 * e] = Codec::lo(x);
+    o[2 * e + 1] = Codec::hi(x);
+    if constexpr (kScale) {
+      const float2 s2 = make_float2(sc, sc);
+      const float2 f = __fmul2_rn(unpack_f16x2(o[2 * e]), s2);
+      const float2 g = __fmul2_rn(unpack_f16x2(o[2 * e + 1]), s2);
+      o[2 * e] = pack_f16x2(f.x, f.y);
+      o[2 * e + 1] = pack_f16x2(g.x, g.y);
+    }
+  }
+  a = make_uint4(o[0], o[1], o[2], o[3]);
+  b = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <int D, int BS, int CODE>
+__global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tmk,
+                          const __grid_constant__ CUtensorMap tmv, const TreeParams p) {
+  using K = TreeCfg<D, BS, CODE>;
+  constexpr bool kQ8 = K::kQ8;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + K::kOffAbort);
+  long long* s_scan = reinterpret_cast<long long*>(gbase + K::kOffScan);  // [20] warps' sums
+  TreePlace* s_place = reinterpret_cast<TreePlace*>(s_scan + 20);         // [2]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [&](int i) { return base + K::kOffBar + 8 * i; };
+  auto full = [&](int st) { return bar(st); };
+  auto empty = [&](int st) { return bar(K::kStages + st); };
+  auto cfull = [&](int st) { return bar(2 * K::kStages + st); };
+  auto cempty = [&](int st) { return bar(2 * K::kStages + K::kCodeStages + st); };
+  constexpr int kB = 2 * K::kStages + 2 * K::kCodeStages;
+  auto qfull = [&](int X) { return bar(kB + X); };
+  auto qempty = [&](int X) { return bar(kB + 2 + X); };
+  auto sfull = [&](int X) { return bar(kB + 4 + X); };
+  auto sread = [&](int X) { return bar(kB + 6 + X); };
+  auto pfull = [&](int X) { return bar(kB + 8 + X); };
+  auto pdone = [&](int X) { return bar(kB + 10 + X); };
+  auto ofree = [&](int X) { return bar(kB + 12 + X); };
+  auto mdone = [&](int i) { return bar(kB + 14 + i); };
+  auto told = [&](int i) { return bar(kB + 18 + i); };
+  auto heard = [&](int i) { return bar(kB + 18 + K::kQueue + i); };
+  const uint32_t tmem_slot = base + K::kOffTmemSlot;
+
+  if (tid == 0) {
+    for (int i = 0; i < K::kNumBars; ++i) {
+      int n = 1;
+      if (i < K::kStages) n = kQ8 ? K::kConvWarps : 1;       // full: a copy, or the converters
+      else if (i < 2 * K::kStages) n = 2;                    // empty: both pipelines
+      else if (i >= 2 * K::kStages + K::kCodeStages && i < kB) n = K::kConvWarps;  // cempty
+      const int k = (i - kB) >> 1;
+      if (i >= kB && (k == 0 || k == 3 || k == 4 || k == 6)) n = 4;  // one per softmax warp
+      if (i >= kB + 18 + K::kQueue) n = K::kListeners;
+      mbar_init(bar(i), n);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  pdl_wait_prior_grid();
+
+  // ---- the line: each thread sums some sequences, the block scans, and the threads that
+  //      hold the two ends of this CTA's stretch locate them ----
+  const int chunk = (p.B + K::kThreads - 1) / K::kThreads;
+  const int b0 = min(p.B, tid * chunk), b1 = min(p.B, b0 + chunk);
+  long long sum = 0;
+  for (int s = b0; s < b1; ++s) {
+    TreeSeq q;
+    q.load(p, s);
+    sum += q.length(p);
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  if (tid < 2) s_place[tid] = TreePlace{p.B, 0, 0};
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  long long run = incl - sum, total = 0;
+  for (int w = 0; w < K::kThreads / 32; ++w) {
+    if (w < warp) run += s_scan[w];
+    total += s_scan[w];
+  }
+  const int G = int(min((long long)gridDim.x, max(1ll, total / p.min_range)));
+  const int c = blockIdx.x;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + K::kOffTmemSlot);
+  if (c < G) {
+    for (int e = 0; e < 2; ++e) {
+      const long long x = total / G * (c + e) + total % G * (c + e) / G;
+      if (x < run || x >= run + sum) continue;  // (x = total: the place past the end)
+      long long r = run;
+      for (int s = b0; s < b1; ++s) {
+        TreeSeq q;
+        q.load(p, s);
+        const long long len = q.length(p);
+        if (x < r + len) {
+          const long long one = q.len + p.item_cost, o = (x - r) % one;
+          const int n = (q.len + K::kKeys - 1) / K::kKeys;
+          s_place[e] = TreePlace{s, int((x - r) / one),
+                                 int(min((long long)n, (o + K::kKeys - 1) / K::kKeys))};
+          break;
+        }
+        r += len;
+      }
+    }
+  }
+  __syncthreads();
+  const bool active = c < G;
+  // the next segment told, to one lane or to a whole warp; false: the stretch is over
+  uint32_t heard_of = 0;
+  auto take = [&](TreeSeg& g, bool whole_warp) {
+    const uint32_t slot = heard_of % K::kQueue;
+    bool ok = tc::poll_or_abort(told(slot), (heard_of / K::kQueue) & 1u, p.timeout_ns, abort_flag);
+    if (whole_warp) ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+    if (!ok) return false;
+    ++heard_of;
+    const uint32_t from = base + K::kOffQueue + slot * 64;
+    uint4* to = reinterpret_cast<uint4*>(&g);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) to[k] = lds128(from + 16 * k);
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(heard(slot));
+    return g.some != 0;
+  };
+
+  if (warp == 13) {
+    // ---------------- the walk ----------------
+    if (lane == 0) {
+      const TreePlace first = s_place[0], stop = s_place[1];
+      // for the kernel that joins the records: how the first segment and the last one are cut
+      TreeCut cut = {-1, 0, 0, active ? kPromptEmpty : 0};
+      TreePlace at = first;
+      TreeSeq q = {0, 0, 0};
+      bool loaded = false, ok = active;
+      for (uint32_t n = 0; ok; ++n) {
+        TreeSeg g;
+        g.some = 0;
+        while (at.s < p.B && at.s <= stop.s) {
+          if (!loaded) {
+            q.load(p, at.s);
+            loaded = true;
+          }
+          if (at.u >= q.items(p)) {
+            ++at.s;
+            at.u = at.j = 0;
+            loaded = false;
+            continue;
+          }
+          const bool last = at.s == stop.s && at.u == stop.u;
+          if (at.s == stop.s && at.u > stop.u) break;
+          const int pairs = (q.tiles + 1) >> 1;
+          const int pr = at.u % pairs;
+          g.s = at.s;
+          g.hv = at.u / pairs;
+          g.row0 = 2 * pr * p.tpt;
+          g.n = (q.len + K::kKeys - 1) / K::kKeys;
+          g.ja = at.j;
+          g.jb = last ? min(stop.j, g.n) : g.n;
+          g.len = q.len;
+          g.nodes = q.nodes;
+          g.split = 2 * pr + 1 >= q.tiles ? 1 : 0;
+          at.j = 0;
+          ++at.u;
+          if (g.jb > g.ja) {
+            g.some = 1;
+            break;
+          }
+          if (last) break;
+        }
+        const uint32_t slot = n % K::kQueue;
+        if (n >= K::kQueue)
+          ok = tc::wait_or_abort(heard(slot), (n / K::kQueue - 1) & 1u, p.timeout_ns, abort_flag);
+        if (!ok) break;
+        const uint4* from = reinterpret_cast<const uint4*>(&g);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) tc::sts128(base + K::kOffQueue + slot * 64 + 16 * k, from[k]);
+        mbar_arrive(told(slot));
+        if (!g.some) break;
+        if (n == 0)
+          cut.state = (g.ja > 0 ? kPromptContinues : 0) |
+                      (g.ja > 0 && g.jb == g.n ? kPromptEnds : 0);
+        if (g.ja == 0 && g.jb < g.n) {  // (the last segment)
+          cut.state |= kPromptBegins;
+          cut.slot = 2 * c + (n > 0 ? 1 : 0);
+          cut.s = g.s;
+          cut.u = at.u - 1;
+        }
+      }
+      p.cuts[c] = cut;
+    }
+    __syncwarp();
+  } else if (active && warp >= 4 && warp < 12) {
+    // ---------------- softmax: one query row per thread ----------------
+    const int X = warp >= 8 ? 1 : 0, quarter = warp & 3;
+    const int r = quarter * 32 + lane;
+    const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
+    const uint32_t ts = trow + K::kColS + X * K::kKeys;
+    const uint32_t tp = trow + K::kColP + X * (K::kKeys / 2);
+    const uint32_t to0 = trow + K::kColO, to = to0 + X * D;
+    const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 4096;
+    const int rt = r / p.g, rh = r % p.g;  // node of the tile, head of the (part of the) group
+    auto wait = [&](uint32_t b, uint32_t phase) {
+      const bool got = tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
+      return __all_sync(0xffffffffu, got && !*abort_flag) != 0;
+    };
+    uint32_t step = 0, uses = 0, seg_no = 0, tile_no = 0;
+    float row_sl = p.scale_log2;  // of the segment whose queries were loaded last
+    // The segment's query rows -> this pipeline's Q buffer (K-major, 128-byte swizzle).
+    auto load_q = [&](const TreeSeg& g) -> bool {
+      if (g.count(X) == 0) return true;
+      if (uses > 0 && !wait(qempty(X), uses - 1)) return false;
+      ++uses;
+      const int node = g.row0 + (g.split ? 0 : X) * p.tpt + rt;
+      const bool ex = rt < p.tpt && node < p.q_len;
+      const uint4* q = reinterpret_cast<const uint4*>(p.q) +
+                       ((size_t(g.s) * p.q_len + (ex ? node : 0)) * p.Hq + g.hv * p.g + rh) *
+                           (D / 8);
+      const uint32_t qa = base + K::kOffQ + X * K::kTileQ + r * 128;
+      if constexpr (kQ8) {
+        uint4 v[D / 8];
+        uint32_t top = 0;  // the largest magnitude, as bf16 bits
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) v[k] = ex ? __ldg(q + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+        }
+        // times 2^(141 - exponent field): the largest comes to [2^14, 2^15). A factor that
+        // fp32 holds: none for rows without a finite value above 2^-112.
+        const int field = int(top >> 7);
+        const bool fit = field > 15 && field < 255;
+        const float f = fit ? __uint_as_float(uint32_t(268 - field) << 23) : 1.f;
+        row_sl = fit ? p.scale_log2 * __uint_as_float(uint32_t(field - 14) << 23) : p.scale_log2;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack_bf16x2(w[e]);
+            o[e] = pack_f16x2(x.x * f, x.y * f);
+          }
+          tc::sts128(qa + (k >> 3) * K::kSlabQ + (((k & 7) ^ (r & 7)) << 4),
+                     make_uint4(o[0], o[1], o[2], o[3]));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+          tc::sts128(qa + (k >> 3) * K::kSlabQ + (((k & 7) ^ (r & 7)) << 4),
+                     ex ? __ldg(q + k) : make_uint4(0u, 0u, 0u, 0u));
+      }
+      fence_proxy_async_smem();  // before the MMAs read them
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull(X));
+      return true;
+    };
+    TreeSeg g, nx;
+    bool have = take(g, true), first_seg = true;
+    bool ok = !have || load_q(g);
+    while (ok && have) {
+      const int node = g.row0 + (g.split ? 0 : X) * p.tpt + rt;
+      const bool stored = rt < p.tpt && node < p.q_len;  // a row of the output
+      const bool sees = stored && node < g.nodes;
+      const bool idle = !__any_sync(0xffffffffu, sees);
+      const int before = g.len - g.nodes;  // tokens before the first node
+      const uint32_t* mask = p.tree_mask + (size_t(g.s) * p.q_len + (stored ? node : 0)) * p.tree_words;
+      const float sl = row_sl;
+      // which of the 32 tokens from pos on this row sees
+      auto bits_at = [&](int pos) -> uint32_t {
+        if (!sees) return 0u;
+        const int off = pos - before;  // first token as a node
+        if (off <= -32) return 0xffffffffu;
+        auto word = [&](int i) { return i >= 0 && i < p.tree_words ? __ldg(mask + i) : 0u; };
+        const int w = off >> 5;  // (off >= -31: word -1 holds the tokens before the nodes)
+        uint32_t bits = __funnelshift_r(w < 0 ? 0xffffffffu : word(w), word(w + 1), off & 31);
+        const int left = g.nodes - off;  // bits past the last node are nobody's
+        if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
+        return bits;
+      };
+      TreeRow row = {-INFINITY, 0.f};
+      const int j0 = g.first(X), dj = g.split ? 2 : 1;
+      for (int j = j0; ok && j < g.jb; j += dj, ++step) {
+        ok = wait(sfull(X), step);
+        if (!ok) break;
+        tc::fence_after_sync();
+        const TreeStep at = {ts, tp, to, sread(X), pdone(X), pfull(X), step, lane, j > j0};
+        const uint32_t kscale = base + K::kOffKScale +
+                                ((tile_no + uint32_t(j - g.ja)) % 16u) * (K::kKeys * 4);
+        uint32_t seen[2] = {0u, 0u};
+        if (idle) {  // no row of this warp sees anything
+          ok = step == 0 || wait(pdone(X), step - 1);
+          if (ok && lane == 0) {
+            mbar_arrive(sread(X));
+            mbar_arrive(pfull(X));
+          }
+        } else if ((j + 1) * K::kKeys <= before) {
+          ok = tree_softmax<D, CODE, true>(at, sl, kscale, seen, row, wait);
+        } else {
+          seen[0] = bits_at(j * K::kKeys);
+          seen[1] = bits_at(j * K::kKeys + 32);
+          ok = tree_softmax<D, CODE, false>(at, sl, kscale, seen, row, wait);
+        }
+      }
+      if (!ok) break;
+      tile_no += uint32_t(g.jb - g.ja);
+      // the next segment's queries, so that its first scores run during this one's end
+      const bool more = take(nx, true);
+      if (more && !load_q(nx)) break;
+      const int mine = g.count(X), other = g.split ? g.count(1) : 0;
+      if (mine > 0 && !wait(pdone(X), step - 1)) break;
+      if (!sees) row = TreeRow{-INFINITY, 0.f};
+      const bool cut = g.ja > 0 || g.jb < g.n;
+      const size_t rec = (size_t(2 * c + (first_seg ? 0 : 1)) * 2 + (g.split ? 0 : X)) * 128 + r;
+      first_seg = false;
+      // ---- the segment's end: the output, or a record; of a split item by pipeline 0, once
+      //      pipeline 1's state is there ----
+      const uint32_t state = base + K::kOffState + ((seg_no++ & 1u) * 128 + r) * 8;
+      float f0 = 1.f, f1 = 0.f;
+      if (g.split) {
+        if (X == 1) {
+          tc::sts32(state, __float_as_uint(row.m));
+          tc::sts32(state + 4, __float_as_uint(row.l));
+          tc::fence_before_sync();
+        }
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+        if (X == 0) {
+          const TreeRow theirs = {__uint_as_float(lds32(state)), __uint_as_float(lds32(state + 4))};
+          const float m = fmaxf(row.m, theirs.m);
+          // (a pipeline without a tile or a sight has m = -inf and l = 0)
+          f0 = row.m > -INFINITY ? fast_exp2(row.m - m) : 1.f;
+          f1 = theirs.m > -INFINITY ? fast_exp2(theirs.m - m) : 1.f;
+          row.l = row.l * f0 + theirs.l * f1;
+          row.m = m;
+        }
+      }
+      tc::fence_after_sync();
+      if (!g.split || X == 0) {
+        if (cut) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(row.m, row.l);
+        const float inv = row.l > 0.f ? 1.f / row.l : row.l == 0.f ? 0.f : row.l;  // (NaN stays)
+        if (!cut) {
+          f0 *= inv;
+          f1 *= inv;
+        }
+        // Through shared memory, 128 bytes of each of the warp's rows at a time (chunks swizzled
+        // by the row), so that eight lanes store a row's 128 bytes.
+        uint8_t* row_out = nullptr;
+        if (stored)
+          row_out = cut ? reinterpret_cast<uint8_t*>(p.part_o + rec * D)
+                        : reinterpret_cast<uint8_t*>(
+                              reinterpret_cast<__nv_bfloat16*>(p.out) +
+                              ((size_t(g.s) * p.q_len + node) * p.Hq + g.hv * p.g + rh) * D);
+        auto put = [&](int ch, const uint4& v) {
+          tc::sts128(stage + lane * 128 + ((ch ^ (lane & 7)) << 4), v);
+        };
+        auto flush = [&](int at) {  // the staged bytes are bytes `at` .. `at` + 127 of the rows
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int from = 4 * k + (lane >> 3), ch = lane & 7;
+            uint8_t* dst = reinterpret_cast<uint8_t*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_out), from));
+            const uint4 v = lds128(stage + from * 128 + ((ch ^ (from & 7)) << 4));
+            if (dst) *reinterpret_cast<uint4*>(dst + at + ch * 16) = v;
+          }
+          __syncwarp();
+        };
+        if (__any_sync(0xffffffffu, stored)) {
+#pragma unroll 1
+          for (int c1 = 0; c1 < D; c1 += 32) {
+            uint32_t o[32];
+            if (mine > 0) {
+              tc::tmem_ld32(to + c1, o);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = sees ? __float_as_uint(__uint_as_float(o[e]) * f0) : 0u;
+            if (other > 0) {
+              uint32_t o1[32];
+              tc::tmem_ld32(to0 + D + c1, o1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (sees)
+                  o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
+            }
+            if (cut) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                put(e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+              flush(c1 * 4);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]),
+                                     __uint_as_float(o[8 * e + 2 * k + 1]));
+                put((c1 & 32) / 8 + e, make_uint4(w[0], w[1], w[2], w[3]));
+              }
+              if (c1 & 32) flush(c1 / 64 * 128);
+            }
+          }
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (mine > 0 && (!g.split || X == 0)) mbar_arrive(ofree(X));
+        if (other > 0 && X == 0) mbar_arrive(ofree(1));  // (read here)
+      }
+      g = nx;
+      have = more;
+    }
+    // one that gives up leaves no partner behind at their barrier (which meets the flag at its
+    // next wait)
+    if (*abort_flag) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");
+    tc::fence_before_sync();
+  } else if (active && warp == 0) {
+    // ---------------- TMA ----------------
+    const int rows_total = p.NB * p.Hkv * BS;  // a box at this row is all zero fill
+    constexpr int kRing = kQ8 ? K::kCodeStages : K::kStages;
+    int st = 0, u = 0;
+    uint32_t turn = 0, tile_no = 0;
+    bool ok = true;
+    TreeSeg g;
+    while (ok && take(g, true)) {
+      const int h = g.hv / p.parts;
+      // lane b: cache row of block b of key tile j (rows_total: none)
+      auto block_row = [&](int j) -> int {
+        const int blk = j * K::kBlocks + lane;
+        if (lane >= K::kBlocks || j >= g.jb || blk * BS >= g.len) return rows_total;
+        int phys = __ldg(p.block_tables + size_t(g.s) * p.MBS + blk);
+        phys = (phys < 0 || phys >= p.NB) ? 0 : phys;  // never copy outside the pool
+        return (phys * p.Hkv + h) * BS;
+      };
+      int row = block_row(g.ja);
+      for (int j = g.ja; ok && j < g.jb; ++j) {
+        const int row_next = block_row(j + 1);
+        const int row0 = __shfl_sync(0xffffffffu, row, 0);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint32_t fb = kQ8 ? cfull(st) : full(st);
+          if (u >= kRing)
+            ok = ok && __all_sync(0xffffffffu,
+                                  tc::poll_or_abort(kQ8 ? cempty(st) : empty(st), turn ^ 1u,
+                                                    p.timeout_ns, abort_flag));
+          if (!ok) break;
+          const CUtensorMap* map = kv ? &tmv : &tmk;
+          if constexpr (kQ8) {
+            if (lane == 0) mbar_arrive_expect_tx(fb, K::kCodes + K::kKeys * 4);
+            __syncwarp();
+            if (lane < K::kBlocks) {
+              tma_load_2d(base + K::kOffCodes + st * K::kCodes + lane * BS * D, map, fb, 0, row);
+              // (a block past the context: zero codes, and another block's scales)
+              const uint32_t sc = kv ? base + K::kOffVScale + st * (K::kKeys * 4)
+                                     : base + K::kOffKScale + (tile_no % 16u) * (K::kKeys * 4);
+              bulk_load(sc + lane * BS * 4,
+                        (kv ? p.v_scale : p.k_scale) + size_t(row == rows_total ? row0 : row),
+                        BS * 4, fb);
+            }
+          } else {
+            if (lane == 0) mbar_arrive_expect_tx(fb, K::kTile);
+            __syncwarp();
+            if (lane < K::kBlocks)
+#pragma unroll
+              for (int sl = 0; sl < K::kSlabs; ++sl)
+                tma_load_2d(base + K::kOffKV + st * K::kTile + sl * K::kSlab + lane * BS * 128, map,
+                            fb, sl * 64, row);
+          }
+          ++u;
+          if (++st == kRing) {
+            st = 0;
+            turn ^= 1u;
+          }
+        }
+        ++tile_no;
+        row = row_next;
+      }
+    }
+    if (lane == 0)  // every copy issued must have landed before the CTA may exit
+      for (int v = max(0, u - kRing); v < u; ++v)
+        mbar_wait_bounded(kQ8 ? cfull(v % kRing) : full(v % kRing), uint32_t(v / kRing) & 1u,
+                          p.timeout_ns);
+    __syncwarp();
+  } else if (active && (warp == 1 || warp == 2)) {
+    // ---------------- scores of pipeline X ----------------
+    if (lane == 0) {
+      const int X = warp - 1;
+      constexpr uint32_t kId =
+          kQ8 ? tc::idesc_f16<128, K::kKeys, false>() : tc::idesc_bf16<128, K::kKeys, false>();
+      const uint64_t desc_q = tc::sdesc_sw128(base + K::kOffQ + X * K::kTileQ, 16, 1024);
+      const uint64_t desc_k = tc::sdesc_sw128(base + K::kOffKV, 16, 1024);
+      const uint32_t ts = tmem + K::kColS + X * K::kKeys;
+      bool ok = true;
+      auto wait = [&](uint32_t b, uint32_t phase) {
+        ok = ok && tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
+      };
+      int st = 0;  // the ring's even stages hold K tiles
+      uint32_t turn = 0, n = 0, segs = 0;
+      TreeSeg g;
+      while (ok && take(g, false)) {
+        int left = g.count(X);
+        if (left > 0) wait(qfull(X), segs++);
+        for (int j = g.ja; ok && j < g.jb; ++j) {
+          wait(full(st), turn);
+          if (g.uses(X, j)) {
+            if (n++ > 0) wait(sread(X), n - 2);  // the scores before have been read
+            if (!ok) break;
+            tc::fence_after_sync();
+            const uint64_t kd = desc_k + uint64_t(st) * (K::kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_bf16(ts, desc_q + (kk >> 2) * (K::kSlabQ >> 4) + (kk & 3) * 2,
+                           kd + (kk >> 2) * (K::kSlab >> 4) + (kk & 3) * 2, kId, kk > 0 ? 1u : 0u);
+            tc::commit(sfull(X));
+            tc::commit(empty(st));
+            if (--left == 0) tc::commit(qempty(X));
+          } else if (ok) {  // the other pipeline's (not let go before it is there)
+            mbar_arrive(empty(st));
+          }
+          if ((st += 2) == K::kStages) {
+            st = 0;
+            turn ^= 1u;
+          }
+        }
+      }
+      tc::commit(mdone(X));  // every MMA issued must have completed before TMEM is freed
+      mbar_wait_bounded(mdone(X), 0u, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (active && (warp == 3 || warp == 12)) {
+    // ---------------- P.V of pipeline X ----------------
+    const int X = warp == 3 ? 0 : 1;
+    constexpr uint32_t kId = kQ8 ? tc::idesc_f16<128, D, true>() : tc::idesc_bf16<128, D, true>();
+    const uint64_t desc_v = tc::sdesc_sw128(base + K::kOffKV, K::kSlab, 1024);
+    const uint32_t tp = tmem + K::kColP + X * (K::kKeys / 2), to = tmem + K::kColO + X * D;
+    bool ok = true;
+    auto wait = [&](uint32_t b, uint32_t phase) {
+      ok = ok && __all_sync(0xffffffffu,
+                            tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
+    };
+    int st = 1;  // the ring's odd stages hold V tiles
+    uint32_t turn = 0, n = 0, segs = 0;
+    TreeSeg g;
+    while (ok && take(g, true)) {
+      const int j0 = g.first(X);
+      for (int j = g.ja; ok && j < g.jb; ++j) {
+        wait(full(st), turn);
+        if (!ok) break;
+        if (g.uses(X, j)) {
+          const int r0 = g.len - j * K::kKeys;  // rows of the context
+          if (!kQ8 && r0 < K::kKeys) {
+            const uint32_t vb = base + K::kOffKV + st * K::kTile + r0 * 128;
+            for (int k = lane; k < (K::kKeys - r0) * 8; k += 32)  // whole rows, swizzled or not
+#pragma unroll
+              for (int sl = 0; sl < K::kSlabs; ++sl)
+                tc::sts128(vb + sl * K::kSlab + k * 16, make_uint4(0u, 0u, 0u, 0u));
+            fence_proxy_async_smem();  // before the MMAs read them
+            __syncwarp();
+          }
+          if (j == j0 && segs++ > 0) wait(ofree(X), segs - 2);
+          wait(pfull(X), n++);
+          if (!ok) break;
+          if (lane == 0) {
+            tc::fence_after_sync();
+            const uint64_t vd = desc_v + uint64_t(st) * (K::kTile >> 4);
+#pragma unroll
+            for (int kk = 0; kk < K::kKeys / 16; ++kk)
+              tc::mma_bf16_tmem_a(to, tp + kk * 8, vd + kk * 128, kId,
+                                  (j > j0 || kk > 0) ? 1u : 0u);
+            tc::commit(pdone(X));
+            tc::commit(empty(st));
+          }
+          __syncwarp();
+        } else if (lane == 0) {
+          mbar_arrive(empty(st));
+        }
+        if ((st += 2) > K::kStages) {
+          st = 1;
+          turn ^= 1u;
+        }
+      }
+    }
+    if (lane == 0) {
+      tc::commit(mdone(2 + X));
+      mbar_wait_bounded(mdone(2 + X), 0u, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (kQ8 && active && warp >= 14) {
+    // ---------------- converters: codes -> fp16 in the MMA's layout ----------------
+    const int ct = tid - 14 * 32;
+    constexpr int kSeg = D >= 128 ? 128 : 64;    // swizzle span of a row of codes
+    int st = 0, cst = 0;
+    uint32_t turn = 0, cturn = 0, u = 0;
+    bool ok = true;
+    auto wait = [&](uint32_t b, uint32_t phase) {
+      ok = ok && __all_sync(0xffffffffu,
+                            tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
+    };
+    TreeSeg g;
+    while (ok && take(g, true)) {
+      for (int j = g.ja; ok && j < g.jb; ++j) {
+        const int valid = g.len - j * K::kKeys;  // rows of the context
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          wait(cfull(cst), cturn);
+          if (u >= uint32_t(K::kStages)) wait(empty(st), turn ^ 1u);
+          if (!ok) break;
+          const uint32_t codes = base + K::kOffCodes + cst * K::kCodes;
+          const uint32_t scales = base + K::kOffVScale + cst * (K::kKeys * 4);
+          const uint32_t tile = base + K::kOffKV + st * K::kTile;
+          // chunk idx: columns 16 (4 slab + c) .. of row t; eight lanes take two rows' halves, whose
+          // 16-bit chunks then fall on different banks
+          for (int idx = ct; idx < K::kKeys * (D / 16); idx += K::kConvWarps * 32) {
+            const int cc = idx & 3, t = idx >> 2 & 63, slab = idx >> 8;
+            const uint4 raw = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
+            uint4 a, b;
+            if constexpr (kQ8) {
+              if (kv == 0) widen16<kQ8 ? CODE : 0, false>(raw, 1.f, a, b);
+              else widen16<kQ8 ? CODE : 0, true>(raw, lds_f32(scales + 4 * t), a, b);
+            }
+            if (kv == 1 && t >= valid) a = b = make_uint4(0u, 0u, 0u, 0u);  // may hold anything
+            const uint32_t out = tile + slab * K::kSlab + t * 128;
+            tc::sts128(out + (((2 * cc) ^ (t & 7)) << 4), a);
+            tc::sts128(out + (((2 * cc + 1) ^ (t & 7)) << 4), b);
+          }
+          fence_proxy_async_smem();  // the 16-bit values, for the MMAs
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(full(st));
+            mbar_arrive(cempty(cst));
+          }
+          ++u;
+          if (++st == K::kStages) {
+            st = 0;
+            turn ^= 1u;
+          }
+          if (++cst == K::kCodeStages) {
+            cst = 0;
+            cturn ^= 1u;
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (*abort_flag && tid == 0 && p.status) atomicOr(p.status, PKV_DEV_TIMEOUT);
+  if (warp == 1) {
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int CODE>
+bool select_tree_code(int D, int BS, TreeKernelInfo* info) {
+#define PKV_TREE(DD, BB)                                                                    \
+  if (D == DD && BS == BB) {                                                                \
+    info->fn = reinterpret_cast<const void*>(&tree_attention_kernel<DD, BB, CODE>);         \
+    info->threads = TreeCfg<DD, BB, CODE>::kThreads;                                        \
+    info->smem = TreeCfg<DD, BB, CODE>::kSmem;                                              \
+    return true;                                                                            \
+  }
+  PKV_TREE(128, 16)
+  PKV_TREE(128, 32)
+  PKV_TREE(64, 16)
+  PKV_TREE(64, 32)
+#undef PKV_TREE
+  return false;
+}
+
+}  // namespace pkv
