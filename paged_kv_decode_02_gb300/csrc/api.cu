@@ -913,6 +913,7 @@ pkv_status run_tree(int kvt, void* out, const void* q, const void* k_cache, cons
   TreePlan P;
   pkv_status st = check_tree(d, kvt, q_len, &P.k);
   if (st != PKV_OK) return st;
+  if ((long long)d->num_seqs * q_len >= (1ll << 31)) return PKV_ERR_UNSUPPORTED;
   if (d->num_seqs == 0) return PKV_OK;
   const bool q8 = kvt != PKV_KV_BF16;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !tree_mask ||
@@ -968,7 +969,11 @@ pkv_status run_tree(int kvt, void* out, const void* q, const void* k_cache, cons
   if (cudaFuncSetAttribute(P.k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, P.k.smem) !=
       cudaSuccess)
     return PKV_ERR_CUDA;
-  void* args[] = {&tmk, &tmv, &p};
+  CUtensorMap tmq;
+  if (!rows_map(&tmq, RowsKey{q, (long long)d->num_q_heads * d->head_dim, d->num_seqs * q_len,
+                              d->num_q_heads, d->head_dim, p.g, p.tpt}))
+    return PKV_ERR_CUDA;
+  void* args[] = {&tmq, &tmk, &tmv, &p};
   if (launch_pdl(P.k.fn, dim3(P.G), dim3(P.k.threads), args, P.k.smem, stream) != cudaSuccess ||
       launch_tree_join(p, P.G, stream) != cudaSuccess)
     return PKV_ERR_CUDA;

@@ -216,12 +216,15 @@ __device__ __forceinline__ PromptPlace prompt_locate(const PromptParams& p, cons
 struct PromptPair {
   uint32_t mine, theirs;  // places in shared memory
   int id;                 // barrier of the two warps
-  // Gives a value to the partner and returns the partner's. A place may be written again once
-  // its reader has met the writer at another barrier since.
-  __device__ __forceinline__ float swap(float x) const {
-    tc::sts32(mine, __float_as_uint(x));
+  uint32_t turn;          // of the two places that are used in turn (0 or 128)
+  // Gives a value to the partner and returns the partner's. (A place is written again once its
+  // reader has met the writer at the next swap's barrier.)
+  __device__ __forceinline__ float swap(float x) {
+    tc::sts32(mine + turn, __float_as_uint(x));
     meet();
-    return __uint_as_float(lds32(theirs));
+    const float got = __uint_as_float(lds32(theirs + turn));
+    turn ^= 128u;
+    return got;
   }
   __device__ __forceinline__ void meet() const {
     asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
@@ -246,7 +249,7 @@ struct PromptStep {
 // kNeg: the scale is negative. Returns false on a timeout.
 template <int D, bool kWhole, bool kNeg, typename Wait>
 __device__ __forceinline__ bool prompt_softmax(const PromptStep& at, float sl, int vis,
-                                               const PromptPair& pair, PromptRow& row,
+                                               PromptPair& pair, PromptRow& row,
                                                const Wait& wait) {
   constexpr int N = PromptCfg<D>::kKeys / 2;
   uint32_t s[N];
@@ -481,8 +484,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       const uint32_t tp = trow + K::kColP + X * (K::kKeys / 2) + hp * (K::kKeys / 4);
       const uint32_t to = trow + K::kColO + X * D + hp * (D / 2);
       const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 2048;
-      const PromptPair pair = {stage + lane * 4, stage + lane * 4 + (hp ? -4 : 4) * 2048,
-                               1 + X * 4 + quarter};
+      PromptPair pair = {stage + lane * 4, stage + lane * 4 + (hp ? -4 : 4) * 2048,
+                         1 + X * 4 + quarter, 0u};
       const float sl = p.scale_log2;
       const int rt = r / p.g, rh = r % p.g;  // token of the tile, head of the group
       uint32_t step = 0;
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         const size_t rec = (size_t(2 * c + (first_seg ? 0 : 1)) * 2 + X) * K::kRows + r;
         first_seg = false;
         const float l = row.l + pair.swap(row.l);
-        pair.meet();  // the place is about to hold output
+        pair.meet();  // the places are about to hold output
         if (cut && hp == 0) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(row.m, l);
         if (je <= g.ja) continue;  // nothing of this tile here
         // ---- the segment's end: the output, or a record ----

@@ -18,13 +18,15 @@
 // long as its context plus a constant, and every CTA takes an equal stretch of it; an item cut
 // between stretches leaves records (o, m, l) that a second kernel joins, as in the prompt
 // attention (prompt.cuh), whose pipelines these are:
-//   warp 0       TMA: the blocks of K and V tiles (lane b block b), ids read a tile ahead;
-//   warps 1, 2   S_X = Q_X K_j^T; warps 3, 12: O_X += P_X V_j (bf16 caches: after zeroing V rows
+//   warp 0       TMA: the blocks of K and V tiles (lane b block b), ids read a tile ahead, and the
+//                query rows;
+//   warps 1, 2   S_X = Q_X K_j^T; warps 3, 20: O_X += P_X V_j (bf16 caches: after zeroing V rows
 //                past the context, which may hold anything);
-//   warps 4..7, 8..11  softmax of pipeline 0, 1: one query row per thread; also its Q rows and the
-//                end of each segment;
-//   warp 13      walks the stretch and tells the others its segments;
-//   warps 14..19 (one-byte caches) widen codes in shared memory.
+//   warps 4..11, 12..19  softmax of pipeline 0, 1 and the end of each segment: two threads per
+//                query row, each with half of a key tile's columns, and of O's;
+//   warp 21      walks the stretch and tells the others its segments;
+//   warps 22..27 (one-byte caches) widen codes in shared memory, three warps a tile, one trio the
+//                K tiles, one the V tiles (so that one's waits pass while the other works).
 // One-byte caches: codes land in a ring of their own; K becomes fp16 exactly, V fp16 of code x
 // scale (11 bits). Q is fp16 too: a row's bf16 values times the power of two that takes its
 // largest to [2^14, 2^15), which loses nothing of a value within 2^-28 of the largest and 2^-39
@@ -58,8 +60,8 @@ struct TreeCfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileQ;
   static constexpr int kOffCodes = kOffKV + kStages * kTile;
-  static constexpr int kOffOut = kOffCodes + kCodeStages * kCodes;  // 32 rows of 128 bytes a warp
-  static constexpr int kOffKScale = kOffOut + 8 * 4096;
+  static constexpr int kOffOut = kOffCodes + kCodeStages * kCodes;  // 32 rows of 64 bytes a warp
+  static constexpr int kOffKScale = kOffOut + 16 * 2048;
   static constexpr int kOffVScale = kOffKScale + kScaleSlots * kKeys * 4;
   // (m, l) of pipeline 1's rows, for pipeline 0: [2 segments][128]
   static constexpr int kOffState = kOffVScale + kCodeStages * kKeys * 4;
@@ -67,15 +69,15 @@ struct TreeCfg {
   static constexpr int kOffQueue = kOffState + 2 * 128 * 8;
   static constexpr int kOffBar = kOffQueue + kQueue * 64;
   // full[stages] empty[stages] cfull[codes] cempty[codes] qfull[2] qempty[2] sfull[2] sread[2]
-  // pfull[2] pdone[2] ofree[2] mdone[4] told[queue] heard[queue]
-  static constexpr int kNumBars = 2 * kStages + 2 * kCodeStages + 18 + 2 * kQueue;
+  // pfull[2] pdone[2] ofree[2] mdone[4] qland[2] told[queue] heard[queue]
+  static constexpr int kNumBars = 2 * kStages + 2 * kCodeStages + 20 + 2 * kQueue;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kOffScan = (kOffAbort + 4 + 15) / 16 * 16;
-  static constexpr int kSmem = kOffScan + 256 + 1024;
+  static constexpr int kSmem = kOffScan + 272 + 1024;
   static constexpr int kConvWarps = kQ8 ? 6 : 0;
-  static constexpr int kThreads = (14 + kConvWarps) * 32;
-  static constexpr int kListeners = 13 + kConvWarps;  // warps that hear of segments
+  static constexpr int kThreads = (22 + kConvWarps) * 32;
+  static constexpr int kListeners = 21 + kConvWarps;  // warps that hear of segments
   static constexpr int kColS = 0, kColP = 2 * kKeys, kColO = 3 * kKeys;
   static_assert(kColO + 2 * D <= 512, "TMEM columns");
   static_assert(kStages % 2 == 0 && kCodeStages % 2 == 0, "K tiles on even stages");
@@ -133,51 +135,73 @@ struct TreeStep {
   bool begun;
 };
 
-// One row (a thread) of a score tile: the 64 scores become weights 2^(scale s - m), 16-bit pairs
-// in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`.
-template <int D, int CODE, bool kWhole, typename Wait>
+// The two threads of a row (same lane of two warps, one per half of the tile's columns).
+struct TreePair {
+  uint32_t mine, theirs;  // places in shared memory
+  int id;                 // barrier of the two warps
+  __device__ __forceinline__ void meet() const {
+    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+  }
+  uint32_t turn;          // of the two places that are used in turn (0 or 128)
+  // Gives a value to the partner and returns the partner's. (A place is written again once its
+  // reader has met the writer at the next swap's barrier.)
+  __device__ __forceinline__ uint32_t swap(uint32_t x) {
+    tc::sts32(mine + turn, x);
+    meet();
+    const uint32_t got = lds32(theirs + turn);
+    turn ^= 128u;
+    return got;
+  }
+  __device__ __forceinline__ float swap(float x) {
+    return __uint_as_float(swap(__float_as_uint(x)));
+  }
+};
+
+// Half a row (a thread) of a score tile: 32 scores become weights 2^(scale s - m), 16-bit pairs
+// in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`;
+// kNeg: the scale is negative.
+template <int D, int CODE, bool kWhole, bool kNeg, typename Wait>
 __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t kscale,
-                                             const uint32_t (&seen)[2], TreeRow& row,
+                                             uint32_t seen, TreePair& pair, TreeRow& row,
                                              const Wait& wait) {
   constexpr bool kQ8 = CODE >= 0;
-  uint32_t s[64];
-  tc::tmem_ld64(at.ts, s);
+  uint32_t s[32];
+  tc::tmem_ld32(at.ts, s);
   tc::fence_before_sync();
   __syncwarp();
   if (at.lane == 0) mbar_arrive(at.sread);  // the next scores may come
-  if constexpr (kQ8) {  // each column times its K scale and the row's (with its sign)
-    const float2 r2 = make_float2(sl, sl);
+  if constexpr (kQ8) {  // each column times its K scale
 #pragma unroll
-    for (int t = 0; t < 64; t += 4) {
+    for (int t = 0; t < 32; t += 4) {
       const uint4 k4 = lds128(kscale + 4 * t);
-      const float2 f0 = __fmul2_rn(make_float2(__uint_as_float(k4.x), __uint_as_float(k4.y)), r2);
-      const float2 f1 = __fmul2_rn(make_float2(__uint_as_float(k4.z), __uint_as_float(k4.w)), r2);
-      const float2 a = __fmul2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])), f0);
+      const float2 a =
+          __fmul2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])),
+                     make_float2(__uint_as_float(k4.x), __uint_as_float(k4.y)));
       const float2 b =
-          __fmul2_rn(make_float2(__uint_as_float(s[t + 2]), __uint_as_float(s[t + 3])), f1);
+          __fmul2_rn(make_float2(__uint_as_float(s[t + 2]), __uint_as_float(s[t + 3])),
+                     make_float2(__uint_as_float(k4.z), __uint_as_float(k4.w)));
       s[t] = __float_as_uint(a.x);
       s[t + 1] = __float_as_uint(a.y);
       s[t + 2] = __float_as_uint(b.x);
       s[t + 3] = __float_as_uint(b.y);
     }
-  } else if (sl < 0.f) {  // a negative scale is carried by the scores' signs
-#pragma unroll
-    for (int t = 0; t < 64; ++t) s[t] ^= 0x80000000u;
   }
-  const float asl = kQ8 ? 1.f : fabsf(sl);
   if constexpr (!kWhole) {
 #pragma unroll
-    for (int t = 0; t < 64; ++t)
-      if (!(seen[t >> 5] >> (t & 31) & 1u)) s[t] = 0xff800000u;  // -inf
+    for (int t = 0; t < 32; ++t)
+      if (!(seen >> t & 1u)) s[t] = kNeg ? 0x7f800000u : 0xff800000u;  // the scaled score: -inf
   }
-  float mx[8];
+  auto most = [](float x, float y, float z) {
+    return kNeg ? fminf(x, fminf(y, z)) : fmax3(x, y, z);
+  };
+  float mx[4];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) mx[t] = __uint_as_float(s[t]);
+  for (int t = 0; t < 4; ++t) mx[t] = __uint_as_float(s[t]);
 #pragma unroll
-  for (int t = 0; t < 28; ++t)
-    mx[t & 7] = fmax3(mx[t & 7], __uint_as_float(s[8 + 2 * t]), __uint_as_float(s[9 + 2 * t]));
-  const float top = asl * fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                                fmaxf(mx[6], mx[7]));
+  for (int t = 0; t < 14; ++t)
+    mx[t & 3] = most(mx[t & 3], __uint_as_float(s[4 + 2 * t]), __uint_as_float(s[5 + 2 * t]));
+  const float mine = sl * most(most(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+  const float top = fmaxf(mine, pair.swap(mine));
   float alpha = 1.f;
   const bool up = top > row.m + 8.f;
   if (up) {
@@ -187,17 +211,17 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   }
   // (scores of -inf alone: weights 0, not 2^(-inf + inf))
   const float m = row.m > -INFINITY ? row.m : 0.f;
-  const float2 sl2 = make_float2(asl, asl), nm2 = make_float2(-m, -m);
+  const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(-m, -m);
   float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  uint32_t pk[32];
+  uint32_t pk[16];
 #pragma unroll
-  for (int t = 0; t < 64; t += 2) {
+  for (int t = 0; t < 32; t += 2) {
     const float2 x =
         __ffma2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])), sl2, nm2);
     float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
     if constexpr (!kWhole) {
-      w.x = seen[t >> 5] >> (t & 31) & 1u ? w.x : 0.f;
-      w.y = seen[t >> 5] >> ((t & 31) + 1) & 1u ? w.y : 0.f;
+      w.x = seen >> t & 1u ? w.x : 0.f;
+      w.y = seen >> (t + 1) & 1u ? w.y : 0.f;
     }
     ls[(t >> 1) & 1] = __fadd2_rn(ls[(t >> 1) & 1], w);
     pk[t / 2] = kQ8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
@@ -209,7 +233,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   tc::fence_after_sync();
   if (at.begun && __any_sync(0xffffffffu, up)) {
 #pragma unroll 1
-    for (int c = 0; c < D; c += 16) {
+    for (int c = 0; c < D / 2; c += 16) {
       uint32_t o[16];
       tc::tmem_ld16(at.to + c, o);
 #pragma unroll
@@ -217,7 +241,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
       tc::tmem_st16(at.to + c, o);
     }
   }
-  tc::tmem_st32(at.tp, pk);
+  tc::tmem_st16(at.tp, pk);
   tc::fence_before_sync();
   __syncwarp();
   if (at.lane == 0) mbar_arrive(at.pfull);
@@ -249,7 +273,8 @@ __device__ __forceinline__ void widen16(const uint4& raw, float sc, uint4& a, ui
 
 template <int D, int BS, int CODE>
 __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
-    tree_attention_kernel(const __grid_constant__ CUtensorMap tmk,
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tmq,
+                          const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const TreeParams p) {
   using K = TreeCfg<D, BS, CODE>;
   constexpr bool kQ8 = K::kQ8;
@@ -258,8 +283,8 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + K::kOffAbort);
-  long long* s_scan = reinterpret_cast<long long*>(gbase + K::kOffScan);  // [20] warps' sums
-  TreePlace* s_place = reinterpret_cast<TreePlace*>(s_scan + 20);         // [2]
+  long long* s_scan = reinterpret_cast<long long*>(gbase + K::kOffScan);  // [28] warps' sums
+  TreePlace* s_place = reinterpret_cast<TreePlace*>(s_scan + 28);         // [2]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return base + K::kOffBar + 8 * i; };
   auto full = [&](int st) { return bar(st); };
@@ -275,19 +300,21 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
   auto pdone = [&](int X) { return bar(kB + 10 + X); };
   auto ofree = [&](int X) { return bar(kB + 12 + X); };
   auto mdone = [&](int i) { return bar(kB + 14 + i); };
-  auto told = [&](int i) { return bar(kB + 18 + i); };
-  auto heard = [&](int i) { return bar(kB + 18 + K::kQueue + i); };
+  auto qland = [&](int X) { return bar(kB + 18 + X); };  // one-byte caches: bf16 rows are there
+  auto told = [&](int i) { return bar(kB + 20 + i); };
+  auto heard = [&](int i) { return bar(kB + 20 + K::kQueue + i); };
   const uint32_t tmem_slot = base + K::kOffTmemSlot;
 
   if (tid == 0) {
     for (int i = 0; i < K::kNumBars; ++i) {
       int n = 1;
-      if (i < K::kStages) n = kQ8 ? K::kConvWarps : 1;       // full: a copy, or the converters
+      if (i < K::kStages) n = kQ8 ? 3 : 1;                   // full: a copy, or three converters
       else if (i < 2 * K::kStages) n = 2;                    // empty: both pipelines
-      else if (i >= 2 * K::kStages + K::kCodeStages && i < kB) n = K::kConvWarps;  // cempty
+      else if (i >= 2 * K::kStages + K::kCodeStages && i < kB) n = 3;  // cempty: three converters
       const int k = (i - kB) >> 1;
-      if (i >= kB && (k == 0 || k == 3 || k == 4 || k == 6)) n = 4;  // one per softmax warp
-      if (i >= kB + 18 + K::kQueue) n = K::kListeners;
+      // one per softmax warp; qfull over bf16 caches: a copy
+      if (i >= kB && (k == 3 || k == 4 || k == 6 || (kQ8 && k == 0))) n = 8;
+      if (i >= kB + 20 + K::kQueue) n = K::kListeners;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -295,6 +322,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
   }
   if (warp == 1) tc::tmem_alloc(tmem_slot, 512);
   if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
   }
@@ -368,7 +396,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     return g.some != 0;
   };
 
-  if (warp == 13) {
+  if (warp == 21) {
     // ---------------- the walk ----------------
     if (lane == 0) {
       const TreePlace first = s_place[0], stop = s_place[1];
@@ -434,84 +462,82 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       p.cuts[c] = cut;
     }
     __syncwarp();
-  } else if (active && warp >= 4 && warp < 12) {
-    // ---------------- softmax: one query row per thread ----------------
-    const int X = warp >= 8 ? 1 : 0, quarter = warp & 3;
+  } else if (active && warp >= 4 && warp < 20) {
+    // ---------------- softmax: two threads per query row ----------------
+    const int X = warp >= 12 ? 1 : 0, quarter = warp & 3, hp = (warp >> 2 & 1) ^ 1;
     const int r = quarter * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(quarter * 32) << 16);
-    const uint32_t ts = trow + K::kColS + X * K::kKeys;
-    const uint32_t tp = trow + K::kColP + X * (K::kKeys / 2);
-    const uint32_t to0 = trow + K::kColO, to = to0 + X * D;
-    const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 4096;
+    // this thread's half of the scores, of P and of O
+    const uint32_t ts = trow + K::kColS + X * K::kKeys + hp * 32;
+    const uint32_t tp = trow + K::kColP + X * (K::kKeys / 2) + hp * 16;
+    const uint32_t to0 = trow + K::kColO + hp * (D / 2), to = to0 + X * D;
+    const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 2048;
+    TreePair pair = {stage + lane * 4, stage + lane * 4 + (hp ? -4 : 4) * 2048,
+                     1 + X * 4 + quarter, 0u};
     const int rt = r / p.g, rh = r % p.g;  // node of the tile, head of the (part of the) group
     auto wait = [&](uint32_t b, uint32_t phase) {
       const bool got = tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
       return __all_sync(0xffffffffu, got && !*abort_flag) != 0;
     };
     uint32_t step = 0, uses = 0, seg_no = 0, tile_no = 0;
-    float row_sl = p.scale_log2;  // of the segment whose queries were loaded last
-    // The segment's query rows -> this pipeline's Q buffer (K-major, 128-byte swizzle).
-    auto load_q = [&](const TreeSeg& g) -> bool {
-      if (g.count(X) == 0) return true;
-      if (uses > 0 && !wait(qempty(X), uses - 1)) return false;
-      ++uses;
-      const int node = g.row0 + (g.split ? 0 : X) * p.tpt + rt;
-      const bool ex = rt < p.tpt && node < p.q_len;
-      const uint4* q = reinterpret_cast<const uint4*>(p.q) +
-                       ((size_t(g.s) * p.q_len + (ex ? node : 0)) * p.Hq + g.hv * p.g + rh) *
-                           (D / 8);
+    const bool neg = p.scale_log2 < 0.f;
+    float row_sl = p.scale_log2;  // of the segment whose queries were taken last
+    // One-byte caches: the segment's query rows, which have landed in this pipeline's Q buffer,
+    // from bf16 to fp16 in place, each times a power of two.
+    auto take_q = [&](const TreeSeg& g) -> bool {
+      if (!kQ8 || g.count(X) == 0) return true;
+      if (!wait(qland(X), uses++)) return false;
       const uint32_t qa = base + K::kOffQ + X * K::kTileQ + r * 128;
-      if constexpr (kQ8) {
-        uint4 v[D / 8];
-        uint32_t top = 0;  // the largest magnitude, as bf16 bits
+      constexpr int kChunks = D / 16;  // of this thread's half of the row
+      auto at = [&](int k) {
+        const int ch = hp * kChunks + k;
+        return qa + (ch >> 3) * K::kSlabQ + (((ch & 7) ^ (r & 7)) << 4);
+      };
+      uint4 v[kChunks];
+      uint32_t top = 0;  // the largest magnitude, as bf16 bits
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) v[k] = ex ? __ldg(q + k) : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < kChunks; ++k) v[k] = lds128(at(k));
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      for (int k = 0; k < kChunks; ++k) {
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+      }
+      top = max(top, pair.swap(top));
+      // times 2^(141 - exponent field): the largest comes to [2^14, 2^15). A factor that fp32
+      // holds: none for rows without a finite value above 2^-112.
+      const int field = int(top >> 7);
+      const bool fit = field > 15 && field < 255;
+      const float f = fit ? __uint_as_float(uint32_t(268 - field) << 23) : 1.f;
+      row_sl = fit ? p.scale_log2 * __uint_as_float(uint32_t(field - 14) << 23) : p.scale_log2;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = unpack_bf16x2(w[e]);
+          o[e] = pack_f16x2(x.x * f, x.y * f);
         }
-        // times 2^(141 - exponent field): the largest comes to [2^14, 2^15). A factor that
-        // fp32 holds: none for rows without a finite value above 2^-112.
-        const int field = int(top >> 7);
-        const bool fit = field > 15 && field < 255;
-        const float f = fit ? __uint_as_float(uint32_t(268 - field) << 23) : 1.f;
-        row_sl = fit ? p.scale_log2 * __uint_as_float(uint32_t(field - 14) << 23) : p.scale_log2;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 x = unpack_bf16x2(w[e]);
-            o[e] = pack_f16x2(x.x * f, x.y * f);
-          }
-          tc::sts128(qa + (k >> 3) * K::kSlabQ + (((k & 7) ^ (r & 7)) << 4),
-                     make_uint4(o[0], o[1], o[2], o[3]));
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          tc::sts128(qa + (k >> 3) * K::kSlabQ + (((k & 7) ^ (r & 7)) << 4),
-                     ex ? __ldg(q + k) : make_uint4(0u, 0u, 0u, 0u));
+        tc::sts128(at(k), make_uint4(o[0], o[1], o[2], o[3]));
       }
       fence_proxy_async_smem();  // before the MMAs read them
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull(X));
       return true;
     };
-    TreeSeg g, nx;
-    bool have = take(g, true), first_seg = true;
-    bool ok = !have || load_q(g);
-    while (ok && have) {
+    TreeSeg g;
+    bool first_seg = true, ok = true;
+    while (ok && take(g, true)) {
+      ok = take_q(g);
+      if (!ok) break;
       const int node = g.row0 + (g.split ? 0 : X) * p.tpt + rt;
       const bool stored = rt < p.tpt && node < p.q_len;  // a row of the output
       const bool sees = stored && node < g.nodes;
       const bool idle = !__any_sync(0xffffffffu, sees);
       const int before = g.len - g.nodes;  // tokens before the first node
-      const uint32_t* mask = p.tree_mask + (size_t(g.s) * p.q_len + (stored ? node : 0)) * p.tree_words;
+      const uint32_t* mask =
+          p.tree_mask + (size_t(g.s) * p.q_len + (stored ? node : 0)) * p.tree_words;
       const float sl = row_sl;
       // which of the 32 tokens from pos on this row sees
       auto bits_at = [&](int pos) -> uint32_t {
@@ -527,14 +553,14 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       };
       TreeRow row = {-INFINITY, 0.f};
       const int j0 = g.first(X), dj = g.split ? 2 : 1;
-      for (int j = j0; ok && j < g.jb; j += dj, ++step) {
+      for (int j = j0; j < g.jb; j += dj, ++step) {
         ok = wait(sfull(X), step);
         if (!ok) break;
         tc::fence_after_sync();
         const TreeStep at = {ts, tp, to, sread(X), pdone(X), pfull(X), step, lane, j > j0};
-        const uint32_t kscale = base + K::kOffKScale +
-                                ((tile_no + uint32_t(j - g.ja)) % 16u) * (K::kKeys * 4);
-        uint32_t seen[2] = {0u, 0u};
+        const uint32_t kscale =
+            base + K::kOffKScale + ((tile_no + uint32_t(j - g.ja)) % 16u) * (K::kKeys * 4) +
+            hp * 128;
         if (idle) {  // no row of this warp sees anything
           ok = step == 0 || wait(pdone(X), step - 1);
           if (ok && lane == 0) {
@@ -542,20 +568,22 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
             mbar_arrive(pfull(X));
           }
         } else if ((j + 1) * K::kKeys <= before) {
-          ok = tree_softmax<D, CODE, true>(at, sl, kscale, seen, row, wait);
+          ok = neg ? tree_softmax<D, CODE, true, true>(at, sl, kscale, 0u, pair, row, wait)
+                        : tree_softmax<D, CODE, true, false>(at, sl, kscale, 0u, pair, row, wait);
         } else {
-          seen[0] = bits_at(j * K::kKeys);
-          seen[1] = bits_at(j * K::kKeys + 32);
-          ok = tree_softmax<D, CODE, false>(at, sl, kscale, seen, row, wait);
+          const uint32_t seen = bits_at(j * K::kKeys + 32 * hp);
+          ok = neg ? tree_softmax<D, CODE, false, true>(at, sl, kscale, seen, pair, row, wait)
+                        : tree_softmax<D, CODE, false, false>(at, sl, kscale, seen, pair, row, wait);
         }
+        if (!ok) break;
       }
       if (!ok) break;
       tile_no += uint32_t(g.jb - g.ja);
-      // the next segment's queries, so that its first scores run during this one's end
-      const bool more = take(nx, true);
-      if (more && !load_q(nx)) break;
+      row.l += pair.swap(row.l);
+      pair.meet();  // the places are about to hold output
       const int mine = g.count(X), other = g.split ? g.count(1) : 0;
-      if (mine > 0 && !wait(pdone(X), step - 1)) break;
+      if (mine > 0) ok = wait(pdone(X), step - 1);
+      if (!ok) break;
       if (!sees) row = TreeRow{-INFINITY, 0.f};
       const bool cut = g.ja > 0 || g.jb < g.n;
       const size_t rec = (size_t(2 * c + (first_seg ? 0 : 1)) * 2 + (g.split ? 0 : X)) * 128 + r;
@@ -565,12 +593,12 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       const uint32_t state = base + K::kOffState + ((seg_no++ & 1u) * 128 + r) * 8;
       float f0 = 1.f, f1 = 0.f;
       if (g.split) {
-        if (X == 1) {
+        if (X == 1 && hp == 0) {
           tc::sts32(state, __float_as_uint(row.m));
           tc::sts32(state + 4, __float_as_uint(row.l));
-          tc::fence_before_sync();
         }
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+        tc::fence_before_sync();
+        asm volatile("bar.sync %0, 128;" ::"r"(9 + quarter) : "memory");
         if (X == 0) {
           const TreeRow theirs = {__uint_as_float(lds32(state)), __uint_as_float(lds32(state + 4))};
           const float m = fmaxf(row.m, theirs.m);
@@ -583,72 +611,73 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       }
       tc::fence_after_sync();
       if (!g.split || X == 0) {
-        if (cut) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(row.m, row.l);
+        if (cut && hp == 0) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(row.m, row.l);
         const float inv = row.l > 0.f ? 1.f / row.l : row.l == 0.f ? 0.f : row.l;  // (NaN stays)
         if (!cut) {
           f0 *= inv;
           f1 *= inv;
         }
-        // Through shared memory, 128 bytes of each of the warp's rows at a time (chunks swizzled
-        // by the row), so that eight lanes store a row's 128 bytes.
+        // Through shared memory, 64 bytes of each of the warp's rows at a time (chunks swizzled by
+        // the row), so that four lanes store a row's 64 bytes.
         uint8_t* row_out = nullptr;
         if (stored)
-          row_out = cut ? reinterpret_cast<uint8_t*>(p.part_o + rec * D)
+          row_out = cut ? reinterpret_cast<uint8_t*>(p.part_o + rec * D + hp * (D / 2))
                         : reinterpret_cast<uint8_t*>(
                               reinterpret_cast<__nv_bfloat16*>(p.out) +
-                              ((size_t(g.s) * p.q_len + node) * p.Hq + g.hv * p.g + rh) * D);
+                              ((size_t(g.s) * p.q_len + node) * p.Hq + g.hv * p.g + rh) * D +
+                              hp * (D / 2));
         auto put = [&](int ch, const uint4& v) {
-          tc::sts128(stage + lane * 128 + ((ch ^ (lane & 7)) << 4), v);
+          tc::sts128(stage + lane * 64 + ((ch ^ (lane >> 1 & 3)) << 4), v);
         };
-        auto flush = [&](int at) {  // the staged bytes are bytes `at` .. `at` + 127 of the rows
+        auto flush = [&](int at) {  // the staged bytes are bytes `at` .. `at` + 63 of the rows
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int from = 4 * k + (lane >> 3), ch = lane & 7;
+          for (int k = 0; k < 4; ++k) {
+            const int from = 8 * k + (lane >> 2), ch = lane & 3;
             uint8_t* dst = reinterpret_cast<uint8_t*>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_out), from));
-            const uint4 v = lds128(stage + from * 128 + ((ch ^ (from & 7)) << 4));
+            const uint4 v = lds128(stage + from * 64 + ((ch ^ (from >> 1 & 3)) << 4));
             if (dst) *reinterpret_cast<uint4*>(dst + at + ch * 16) = v;
           }
           __syncwarp();
         };
         if (__any_sync(0xffffffffu, stored)) {
 #pragma unroll 1
-          for (int c1 = 0; c1 < D; c1 += 32) {
-            uint32_t o[32];
+          for (int c1 = 0; c1 < D / 2; c1 += 16) {
+            uint32_t o[16];
             if (mine > 0) {
-              tc::tmem_ld32(to + c1, o);
+              tc::tmem_ld16(to + c1, o);
             } else {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0u;
+              for (int e = 0; e < 16; ++e) o[e] = 0u;
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
               o[e] = sees ? __float_as_uint(__uint_as_float(o[e]) * f0) : 0u;
             if (other > 0) {
-              uint32_t o1[32];
-              tc::tmem_ld32(to0 + D + c1, o1);
+              uint32_t o1[16];
+              tc::tmem_ld16(to0 + D + c1, o1);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
+              for (int e = 0; e < 16; ++e)
                 if (sees)
                   o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
             }
             if (cut) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
+              for (int e = 0; e < 4; ++e)
                 put(e, make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
               flush(c1 * 4);
             } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < 2; ++e) {
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   w[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]),
                                      __uint_as_float(o[8 * e + 2 * k + 1]));
-                put((c1 & 32) / 8 + e, make_uint4(w[0], w[1], w[2], w[3]));
+                put((c1 & 16) / 8 + e, make_uint4(w[0], w[1], w[2], w[3]));
               }
-              if (c1 & 32) flush(c1 / 64 * 128);
+              if (c1 & 16) flush(c1 / 32 * 64);
             }
           }
         }
@@ -659,12 +688,13 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
         if (mine > 0 && (!g.split || X == 0)) mbar_arrive(ofree(X));
         if (other > 0 && X == 0) mbar_arrive(ofree(1));  // (read here)
       }
-      g = nx;
-      have = more;
     }
-    // one that gives up leaves no partner behind at their barrier (which meets the flag at its
-    // next wait)
-    if (*abort_flag) asm volatile("bar.arrive %0, 64;" ::"r"(1 + quarter) : "memory");
+    // One that gives up leaves no partner behind at their barriers: the others meet the flag at
+    // their next wait, and pass two of the pair's and one of the four's before it at most.
+    if (*abort_flag)
+      asm volatile("bar.arrive %0, 64;\n\tbar.arrive %0, 64;\n\tbar.arrive %1, 128;" ::"r"(pair.id),
+                   "r"(9 + quarter)
+                   : "memory");
     tc::fence_before_sync();
   } else if (active && warp == 0) {
     // ---------------- TMA ----------------
@@ -672,10 +702,46 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     constexpr int kRing = kQ8 ? K::kCodeStages : K::kStages;
     int st = 0, u = 0;
     uint32_t turn = 0, tile_no = 0;
+    uint32_t qn[2] = {0, 0};
+    int q_left = 0;  // bit X: pipeline X's query rows of the segment are still to be sent for
     bool ok = true;
     TreeSeg g;
+    // the query rows, as soon as the scores of the segment before have been computed
+    auto send_queries = [&] {
+#pragma unroll
+      for (int X = 0; X < 2; ++X) {
+        if (!(q_left >> X & 1)) continue;
+        if (qn[X] > 0 && !mbar_test_wait(qempty(X), (qn[X] - 1) & 1u)) continue;
+        const uint32_t b = kQ8 ? qland(X) : qfull(X);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b, uint32_t(p.tpt * p.g) * D * 2);
+#pragma unroll
+          for (int sl = 0; sl < K::kSlabs; ++sl)
+            tma_load_3d(base + K::kOffQ + X * K::kTileQ + sl * K::kSlabQ, &tmq, b, sl * 64,
+                        g.hv * p.g, g.s * p.q_len + g.row0 + (g.split ? 0 : X) * p.tpt);
+        }
+        __syncwarp();
+        ++qn[X];
+        q_left &= ~(1 << X);
+      }
+    };
+    // waits for a barrier, or for the queries to have been sent for (bar 0), sending meanwhile
+    auto wait = [&](uint32_t b, uint32_t phase) {
+      uint64_t t0 = 0;
+      for (uint32_t it = 1; ok; ++it) {
+        if (__all_sync(0xffffffffu, b ? mbar_test_wait(b, phase & 1u) : q_left == 0)) break;
+        if (q_left) send_queries();
+        if ((it & 127u) == 0u) {
+          const uint64_t now = global_timer_ns();
+          if (t0 == 0) t0 = now;
+          if (now - t0 > p.timeout_ns) *abort_flag = 1;
+          ok = !__any_sync(0xffffffffu, *abort_flag != 0);
+        }
+      }
+    };
     while (ok && take(g, true)) {
       const int h = g.hv / p.parts;
+      q_left = (g.count(0) > 0 ? 1 : 0) | (g.count(1) > 0 ? 2 : 0);
       // lane b: cache row of block b of key tile j (rows_total: none)
       auto block_row = [&](int j) -> int {
         const int blk = j * K::kBlocks + lane;
@@ -691,10 +757,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const uint32_t fb = kQ8 ? cfull(st) : full(st);
-          if (u >= kRing)
-            ok = ok && __all_sync(0xffffffffu,
-                                  tc::poll_or_abort(kQ8 ? cempty(st) : empty(st), turn ^ 1u,
-                                                    p.timeout_ns, abort_flag));
+          if (u >= kRing) wait(kQ8 ? cempty(st) : empty(st), turn ^ 1u);
           if (!ok) break;
           const CUtensorMap* map = kv ? &tmv : &tmk;
           if constexpr (kQ8) {
@@ -723,15 +786,21 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
             st = 0;
             turn ^= 1u;
           }
+          if (q_left) send_queries();
         }
         ++tile_no;
         row = row_next;
       }
+      if (q_left) wait(0u, 0u);
     }
-    if (lane == 0)  // every copy issued must have landed before the CTA may exit
+    if (lane == 0) {  // every copy issued must have landed before the CTA may exit
       for (int v = max(0, u - kRing); v < u; ++v)
         mbar_wait_bounded(kQ8 ? cfull(v % kRing) : full(v % kRing), uint32_t(v / kRing) & 1u,
                           p.timeout_ns);
+      for (int X = 0; X < 2; ++X)
+        if (qn[X] > 0)
+          mbar_wait_bounded(kQ8 ? qland(X) : qfull(X), (qn[X] - 1) & 1u, p.timeout_ns);
+    }
     __syncwarp();
   } else if (active && (warp == 1 || warp == 2)) {
     // ---------------- scores of pipeline X ----------------
@@ -779,7 +848,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       mbar_wait_bounded(mdone(X), 0u, p.timeout_ns);
     }
     __syncwarp();
-  } else if (active && (warp == 3 || warp == 12)) {
+  } else if (active && (warp == 3 || warp == 20)) {
     // ---------------- P.V of pipeline X ----------------
     const int X = warp == 3 ? 0 : 1;
     constexpr uint32_t kId = kQ8 ? tc::idesc_f16<128, D, true>() : tc::idesc_bf16<128, D, true>();
@@ -837,13 +906,16 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       mbar_wait_bounded(mdone(2 + X), 0u, p.timeout_ns);
     }
     __syncwarp();
-  } else if (kQ8 && active && warp >= 14) {
+  } else if (kQ8 && active && warp >= 22) {
     // ---------------- converters: codes -> fp16 in the MMA's layout ----------------
-    const int ct = tid - 14 * 32;
-    constexpr int kSeg = D >= 128 ? 128 : 64;    // swizzle span of a row of codes
-    int st = 0, cst = 0;
-    uint32_t turn = 0, cturn = 0, u = 0;
-    bool ok = true;
+    const bool kv = warp >= 25;  // V tiles
+    const int ct = tid - (kv ? 25 : 22) * 32;
+    constexpr int kSeg = D >= 128 ? 128 : 64;      // swizzle span of a row of codes
+    constexpr int kChunks = K::kKeys * (D / 16);   // of 16 codes
+    constexpr int kBatch = 3;                      // loads of a thread in flight
+    int st = kv ? 1 : 0, cst = st;  // K tiles on the rings' even stages, V tiles on the odd ones
+    uint32_t turn = 0, cturn = 0;
+    bool ok = true, begun = false;
     auto wait = [&](uint32_t b, uint32_t phase) {
       ok = ok && __all_sync(0xffffffffu,
                             tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
@@ -852,44 +924,54 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     while (ok && take(g, true)) {
       for (int j = g.ja; ok && j < g.jb; ++j) {
         const int valid = g.len - j * K::kKeys;  // rows of the context
+        wait(cfull(cst), cturn);
+        if (begun) wait(empty(st), turn ^ 1u);
+        if (!ok) break;
+        const uint32_t codes = base + K::kOffCodes + cst * K::kCodes;
+        const uint32_t scales = base + K::kOffVScale + cst * (K::kKeys * 4);
+        const uint32_t tile = base + K::kOffKV + st * K::kTile;
+        // chunk idx: columns 16 (4 slab + c) .. of row t; eight lanes take two rows' halves, whose
+        // 16-bit chunks then fall on different banks
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          wait(cfull(cst), cturn);
-          if (u >= uint32_t(K::kStages)) wait(empty(st), turn ^ 1u);
-          if (!ok) break;
-          const uint32_t codes = base + K::kOffCodes + cst * K::kCodes;
-          const uint32_t scales = base + K::kOffVScale + cst * (K::kKeys * 4);
-          const uint32_t tile = base + K::kOffKV + st * K::kTile;
-          // chunk idx: columns 16 (4 slab + c) .. of row t; eight lanes take two rows' halves, whose
-          // 16-bit chunks then fall on different banks
-          for (int idx = ct; idx < K::kKeys * (D / 16); idx += K::kConvWarps * 32) {
+        for (int i0 = 0; i0 < kChunks; i0 += kBatch * 96) {
+          uint4 raw[kBatch];
+          float sc[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int idx = ct + i0 + i * 96;
+            if (idx >= kChunks) continue;
             const int cc = idx & 3, t = idx >> 2 & 63, slab = idx >> 8;
-            const uint4 raw = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
+            raw[i] = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
+            sc[i] = kv ? lds_f32(scales + 4 * t) : 1.f;
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int idx = ct + i0 + i * 96;
+            if (idx >= kChunks) continue;
+            const int cc = idx & 3, t = idx >> 2 & 63, slab = idx >> 8;
             uint4 a, b;
-            if constexpr (kQ8) {
-              if (kv == 0) widen16<kQ8 ? CODE : 0, false>(raw, 1.f, a, b);
-              else widen16<kQ8 ? CODE : 0, true>(raw, lds_f32(scales + 4 * t), a, b);
-            }
-            if (kv == 1 && t >= valid) a = b = make_uint4(0u, 0u, 0u, 0u);  // may hold anything
+            if (!kv) widen16<kQ8 ? CODE : 0, false>(raw[i], 1.f, a, b);
+            else widen16<kQ8 ? CODE : 0, true>(raw[i], sc[i], a, b);
+            if (kv && t >= valid) a = b = make_uint4(0u, 0u, 0u, 0u);  // may hold anything
             const uint32_t out = tile + slab * K::kSlab + t * 128;
             tc::sts128(out + (((2 * cc) ^ (t & 7)) << 4), a);
             tc::sts128(out + (((2 * cc + 1) ^ (t & 7)) << 4), b);
           }
-          fence_proxy_async_smem();  // the 16-bit values, for the MMAs
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(full(st));
-            mbar_arrive(cempty(cst));
-          }
-          ++u;
-          if (++st == K::kStages) {
-            st = 0;
-            turn ^= 1u;
-          }
-          if (++cst == K::kCodeStages) {
-            cst = 0;
-            cturn ^= 1u;
-          }
+        }
+        fence_proxy_async_smem();  // the 16-bit values, for the MMAs
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full(st));
+          mbar_arrive(cempty(cst));
+        }
+        if ((st += 2) >= K::kStages) {
+          st -= K::kStages;
+          turn ^= 1u;
+          begun = true;
+        }
+        if ((cst += 2) >= K::kCodeStages) {
+          cst -= K::kCodeStages;
+          cturn ^= 1u;
         }
       }
     }
