@@ -159,8 +159,8 @@ struct TreePair {
 
 // Half a row (a thread) of a score tile: 32 scores become weights 2^(scale s - m), 16-bit pairs
 // in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`;
-// kNeg: the scale is negative.
-template <int D, int CODE, bool kWhole, bool kNeg, typename Wait>
+// sl >= 0 (the scores' MMA has changed sign for a negative scale).
+template <int D, int CODE, bool kWhole, typename Wait>
 __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t kscale,
                                              uint32_t seen, TreePair& pair, TreeRow& row,
                                              const Wait& wait) {
@@ -189,18 +189,15 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   if constexpr (!kWhole) {
 #pragma unroll
     for (int t = 0; t < 32; ++t)
-      if (!(seen >> t & 1u)) s[t] = kNeg ? 0x7f800000u : 0xff800000u;  // the scaled score: -inf
+      if (!(seen >> t & 1u)) s[t] = 0xff800000u;  // -inf
   }
-  auto most = [](float x, float y, float z) {
-    return kNeg ? fminf(x, fminf(y, z)) : fmax3(x, y, z);
-  };
   float mx[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) mx[t] = __uint_as_float(s[t]);
 #pragma unroll
   for (int t = 0; t < 14; ++t)
-    mx[t & 3] = most(mx[t & 3], __uint_as_float(s[4 + 2 * t]), __uint_as_float(s[5 + 2 * t]));
-  const float mine = sl * most(most(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+    mx[t & 3] = fmax3(mx[t & 3], __uint_as_float(s[4 + 2 * t]), __uint_as_float(s[5 + 2 * t]));
+  const float mine = sl * fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
   const float top = fmaxf(mine, pair.swap(mine));
   float alpha = 1.f;
   const bool up = top > row.m + 8.f;
@@ -383,7 +380,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
   uint32_t heard_of = 0;
   auto take = [&](TreeSeg& g, bool whole_warp) {
     const uint32_t slot = heard_of % K::kQueue;
-    bool ok = tc::poll_or_abort(told(slot), (heard_of / K::kQueue) & 1u, p.timeout_ns, abort_flag);
+    bool ok = tc::poll_or_abort<true>(told(slot), (heard_of / K::kQueue) & 1u, p.timeout_ns, abort_flag);
     if (whole_warp) ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (!ok) return false;
     ++heard_of;
@@ -476,12 +473,12 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
                      1 + X * 4 + quarter, 0u};
     const int rt = r / p.g, rh = r % p.g;  // node of the tile, head of the (part of the) group
     auto wait = [&](uint32_t b, uint32_t phase) {
-      const bool got = tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
+      const bool got = tc::poll_or_abort<true>(b, phase & 1u, p.timeout_ns, abort_flag);
       return __all_sync(0xffffffffu, got && !*abort_flag) != 0;
     };
     uint32_t step = 0, uses = 0, seg_no = 0, tile_no = 0;
-    const bool neg = p.scale_log2 < 0.f;
-    float row_sl = p.scale_log2;  // of the segment whose queries were taken last
+    const float scale = fabsf(p.scale_log2);
+    float row_sl = scale;  // of the segment whose queries were taken last
     // One-byte caches: the segment's query rows, which have landed in this pipeline's Q buffer,
     // from bf16 to fp16 in place, each times a power of two.
     auto take_q = [&](const TreeSeg& g) -> bool {
@@ -509,7 +506,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       const int field = int(top >> 7);
       const bool fit = field > 15 && field < 255;
       const float f = fit ? __uint_as_float(uint32_t(268 - field) << 23) : 1.f;
-      row_sl = fit ? p.scale_log2 * __uint_as_float(uint32_t(field - 14) << 23) : p.scale_log2;
+      row_sl = fit ? scale * __uint_as_float(uint32_t(field - 14) << 23) : scale;
 #pragma unroll
       for (int k = 0; k < kChunks; ++k) {
         const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
@@ -568,12 +565,10 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
             mbar_arrive(pfull(X));
           }
         } else if ((j + 1) * K::kKeys <= before) {
-          ok = neg ? tree_softmax<D, CODE, true, true>(at, sl, kscale, 0u, pair, row, wait)
-                        : tree_softmax<D, CODE, true, false>(at, sl, kscale, 0u, pair, row, wait);
+          ok = tree_softmax<D, CODE, true>(at, sl, kscale, 0u, pair, row, wait);
         } else {
           const uint32_t seen = bits_at(j * K::kKeys + 32 * hp);
-          ok = neg ? tree_softmax<D, CODE, false, true>(at, sl, kscale, seen, pair, row, wait)
-                        : tree_softmax<D, CODE, false, false>(at, sl, kscale, seen, pair, row, wait);
+          ok = tree_softmax<D, CODE, false>(at, sl, kscale, seen, pair, row, wait);
         }
         if (!ok) break;
       }
@@ -806,14 +801,15 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     // ---------------- scores of pipeline X ----------------
     if (lane == 0) {
       const int X = warp - 1;
-      constexpr uint32_t kId =
-          kQ8 ? tc::idesc_f16<128, K::kKeys, false>() : tc::idesc_bf16<128, K::kKeys, false>();
+      const uint32_t kId =
+          (kQ8 ? tc::idesc_f16<128, K::kKeys, false>() : tc::idesc_bf16<128, K::kKeys, false>()) |
+          (p.scale_log2 < 0.f ? tc::kIdescNegA : 0u);
       const uint64_t desc_q = tc::sdesc_sw128(base + K::kOffQ + X * K::kTileQ, 16, 1024);
       const uint64_t desc_k = tc::sdesc_sw128(base + K::kOffKV, 16, 1024);
       const uint32_t ts = tmem + K::kColS + X * K::kKeys;
       bool ok = true;
       auto wait = [&](uint32_t b, uint32_t phase) {
-        ok = ok && tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
+        ok = ok && tc::poll_or_abort<true>(b, phase & 1u, p.timeout_ns, abort_flag);
       };
       int st = 0;  // the ring's even stages hold K tiles
       uint32_t turn = 0, n = 0, segs = 0;
@@ -857,7 +853,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     bool ok = true;
     auto wait = [&](uint32_t b, uint32_t phase) {
       ok = ok && __all_sync(0xffffffffu,
-                            tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
+                            tc::poll_or_abort<true>(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
     };
     int st = 1;  // the ring's odd stages hold V tiles
     uint32_t turn = 0, n = 0, segs = 0;
@@ -912,13 +908,12 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     const int ct = tid - (kv ? 25 : 22) * 32;
     constexpr int kSeg = D >= 128 ? 128 : 64;      // swizzle span of a row of codes
     constexpr int kChunks = K::kKeys * (D / 16);   // of 16 codes
-    constexpr int kBatch = 3;                      // loads of a thread in flight
     int st = kv ? 1 : 0, cst = st;  // K tiles on the rings' even stages, V tiles on the odd ones
     uint32_t turn = 0, cturn = 0;
     bool ok = true, begun = false;
     auto wait = [&](uint32_t b, uint32_t phase) {
       ok = ok && __all_sync(0xffffffffu,
-                            tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
+                            tc::poll_or_abort<true>(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
     };
     TreeSeg g;
     while (ok && take(g, true)) {
@@ -930,33 +925,21 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
         const uint32_t codes = base + K::kOffCodes + cst * K::kCodes;
         const uint32_t scales = base + K::kOffVScale + cst * (K::kKeys * 4);
         const uint32_t tile = base + K::kOffKV + st * K::kTile;
-        // chunk idx: columns 16 (4 slab + c) .. of row t; eight lanes take two rows' halves, whose
-        // 16-bit chunks then fall on different banks
-#pragma unroll
-        for (int i0 = 0; i0 < kChunks; i0 += kBatch * 96) {
-          uint4 raw[kBatch];
-          float sc[kBatch];
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int idx = ct + i0 + i * 96;
-            if (idx >= kChunks) continue;
-            const int cc = idx & 3, t = idx >> 2 & 63, slab = idx >> 8;
-            raw[i] = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
-            sc[i] = kv ? lds_f32(scales + 4 * t) : 1.f;
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int idx = ct + i0 + i * 96;
-            if (idx >= kChunks) continue;
-            const int cc = idx & 3, t = idx >> 2 & 63, slab = idx >> 8;
-            uint4 a, b;
-            if (!kv) widen16<kQ8 ? CODE : 0, false>(raw[i], 1.f, a, b);
-            else widen16<kQ8 ? CODE : 0, true>(raw[i], sc[i], a, b);
-            if (kv && t >= valid) a = b = make_uint4(0u, 0u, 0u, 0u);  // may hold anything
-            const uint32_t out = tile + slab * K::kSlab + t * 128;
-            tc::sts128(out + (((2 * cc) ^ (t & 7)) << 4), a);
-            tc::sts128(out + (((2 * cc + 1) ^ (t & 7)) << 4), b);
-          }
+        // chunk idx: columns 16 (4 slab + c) .. of row t; eight lanes take two rows' halves (D =
+        // 128: different ones), which fall on different banks, codes and 16-bit chunks alike.
+        // (Not unrolled: the kernel's roles run side by side, and their loops are to stay in the
+        // SM's instruction caches.)
+#pragma unroll 1
+        for (int idx = ct; idx < kChunks; idx += 96) {
+          const int cc = idx & 3, t = idx >> 2 & 63, slab = (idx >> 8) ^ (t & (K::kSlabs - 1));
+          const uint4 raw = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
+          uint4 a, b;
+          if (!kv) widen16<kQ8 ? CODE : 0, false>(raw, 1.f, a, b);
+          else widen16<kQ8 ? CODE : 0, true>(raw, lds_f32(scales + 4 * t), a, b);
+          if (kv && t >= valid) a = b = make_uint4(0u, 0u, 0u, 0u);  // may hold anything
+          const uint32_t out = tile + slab * K::kSlab + t * 128;
+          tc::sts128(out + (((2 * cc) ^ (t & 7)) << 4), a);
+          tc::sts128(out + (((2 * cc + 1) ^ (t & 7)) << 4), b);
         }
         fence_proxy_async_smem();  // the 16-bit values, for the MMAs
         __syncwarp();
