@@ -212,25 +212,6 @@ __device__ __forceinline__ PromptPlace prompt_locate(const PromptParams& p, cons
   return c;
 }
 
-// The two threads of a row (same lane of two warps, one per half of the tile's columns).
-struct PromptPair {
-  uint32_t mine, theirs;  // places in shared memory
-  int id;                 // barrier of the two warps
-  uint32_t turn;          // of the two places that are used in turn (0 or 128)
-  // Gives a value to the partner and returns the partner's. (A place is written again once its
-  // reader has met the writer at the next swap's barrier.)
-  __device__ __forceinline__ float swap(float x) {
-    tc::sts32(mine + turn, __float_as_uint(x));
-    meet();
-    const float got = __uint_as_float(lds32(theirs + turn));
-    turn ^= 128u;
-    return got;
-  }
-  __device__ __forceinline__ void meet() const {
-    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
-  }
-};
-
 // A row's softmax state: the reference of its weights and of O (log2 units; the same in both
 // threads), and the sum of this thread's weights.
 struct PromptRow {
@@ -249,7 +230,7 @@ struct PromptStep {
 // kNeg: the scale is negative. Returns false on a timeout.
 template <int D, bool kWhole, bool kNeg, typename Wait>
 __device__ __forceinline__ bool prompt_softmax(const PromptStep& at, float sl, int vis,
-                                               PromptPair& pair, PromptRow& row,
+                                               tc::RowPair& pair, PromptRow& row,
                                                const Wait& wait) {
   constexpr int N = PromptCfg<D>::kKeys / 2;
   uint32_t s[N];
@@ -274,6 +255,7 @@ __device__ __forceinline__ bool prompt_softmax(const PromptStep& at, float sl, i
   const float mine = sl * most(most(mx[0], mx[1], mx[2]), most(mx[3], mx[4], mx[5]),
                                most(mx[6], mx[7], mx[7]));
   const float top = fmaxf(mine, pair.swap(mine));
+  if (pair.leaves) return false;
   float alpha = 1.f;
   const bool up = top > row.m + 8.f;
   if (up) {
@@ -484,14 +466,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       const uint32_t tp = trow + K::kColP + X * (K::kKeys / 2) + hp * (K::kKeys / 4);
       const uint32_t to = trow + K::kColO + X * D + hp * (D / 2);
       const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 2048;
-      PromptPair pair = {stage + lane * 4, stage + lane * 4 + (hp ? -4 : 4) * 2048,
-                         1 + X * 4 + quarter, 0u};
+      tc::RowPair pair = {stage + lane * 8, stage + lane * 8 + (hp ? -4 : 4) * 2048,
+                          1 + X * 4 + quarter, 0u, 0};
       const float sl = p.scale_log2;
       const int rt = r / p.g, rh = r % p.g;  // token of the tile, head of the group
       uint32_t step = 0;
       auto wait = [&](uint32_t b, uint32_t phase) {
-        const bool got = tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag);
-        return __all_sync(0xffffffffu, got && !*abort_flag) != 0;
+        return __all_sync(0xffffffffu,
+                          tc::poll_or_abort(b, phase & 1u, p.timeout_ns, abort_flag)) != 0;
       };
       bool ok = true, first_seg = true;
       PromptSeg g;
@@ -534,6 +516,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         const size_t rec = (size_t(2 * c + (first_seg ? 0 : 1)) * 2 + X) * K::kRows + r;
         first_seg = false;
         const float l = row.l + pair.swap(row.l);
+        if (pair.leaves) break;
         pair.meet();  // the places are about to hold output
         if (cut && hp == 0) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(row.m, l);
         if (je <= g.ja) continue;  // nothing of this tile here
@@ -597,10 +580,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ofree(X));
       }
-      // One that gives up leaves no partner behind: the partner meets the flag at its next wait,
-      // and passes two of their barriers before it at most.
-      if (*abort_flag)
-        asm volatile("bar.arrive %0, 64;\n\tbar.arrive %0, 64;" ::"r"(pair.id) : "memory");
+      pair.leave();
       tc::fence_before_sync();
     }
   } else {

@@ -63,14 +63,14 @@ struct TreeCfg {
   static constexpr int kOffOut = kOffCodes + kCodeStages * kCodes;  // 32 rows of 64 bytes a warp
   static constexpr int kOffKScale = kOffOut + 16 * 2048;
   static constexpr int kOffVScale = kOffKScale + kScaleSlots * kKeys * 4;
-  // (m, l) of pipeline 1's rows, for pipeline 0: [2 segments][128]
+  // (m, l) of pipeline 1's rows of a split item, for pipeline 0: [128]
   static constexpr int kOffState = kOffVScale + kCodeStages * kKeys * 4;
   static constexpr int kQueue = 4;
-  static constexpr int kOffQueue = kOffState + 2 * 128 * 8;
+  static constexpr int kOffQueue = kOffState + 128 * 8;
   static constexpr int kOffBar = kOffQueue + kQueue * 64;
   // full[stages] empty[stages] cfull[codes] cempty[codes] qfull[2] qempty[2] sfull[2] sread[2]
-  // pfull[2] pdone[2] ofree[2] mdone[4] qland[2] told[queue] heard[queue]
-  static constexpr int kNumBars = 2 * kStages + 2 * kCodeStages + 20 + 2 * kQueue;
+  // pfull[2] pdone[2] ofree[2] mdone[4] qland[2] told[queue] heard[queue] sgiven
+  static constexpr int kNumBars = 2 * kStages + 2 * kCodeStages + 21 + 2 * kQueue;
   static constexpr int kOffTmemSlot = kOffBar + kNumBars * 8;
   static constexpr int kOffAbort = kOffTmemSlot + 4;
   static constexpr int kOffScan = (kOffAbort + 4 + 15) / 16 * 16;
@@ -135,34 +135,12 @@ struct TreeStep {
   bool begun;
 };
 
-// The two threads of a row (same lane of two warps, one per half of the tile's columns).
-struct TreePair {
-  uint32_t mine, theirs;  // places in shared memory
-  int id;                 // barrier of the two warps
-  __device__ __forceinline__ void meet() const {
-    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
-  }
-  uint32_t turn;          // of the two places that are used in turn (0 or 128)
-  // Gives a value to the partner and returns the partner's. (A place is written again once its
-  // reader has met the writer at the next swap's barrier.)
-  __device__ __forceinline__ uint32_t swap(uint32_t x) {
-    tc::sts32(mine + turn, x);
-    meet();
-    const uint32_t got = lds32(theirs + turn);
-    turn ^= 128u;
-    return got;
-  }
-  __device__ __forceinline__ float swap(float x) {
-    return __uint_as_float(swap(__float_as_uint(x)));
-  }
-};
-
 // Half a row (a thread) of a score tile: 32 scores become weights 2^(scale s - m), 16-bit pairs
 // in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`;
 // sl >= 0 (the scores' MMA has changed sign for a negative scale).
 template <int D, int CODE, bool kWhole, typename Wait>
 __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t kscale,
-                                             uint32_t seen, TreePair& pair, TreeRow& row,
+                                             uint32_t seen, tc::RowPair& pair, TreeRow& row,
                                              const Wait& wait) {
   constexpr bool kQ8 = CODE >= 0;
   uint32_t s[32];
@@ -199,6 +177,7 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
     mx[t & 3] = fmax3(mx[t & 3], __uint_as_float(s[4 + 2 * t]), __uint_as_float(s[5 + 2 * t]));
   const float mine = sl * fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
   const float top = fmaxf(mine, pair.swap(mine));
+  if (pair.leaves) return false;
   float alpha = 1.f;
   const bool up = top > row.m + 8.f;
   if (up) {
@@ -300,6 +279,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
   auto qland = [&](int X) { return bar(kB + 18 + X); };  // one-byte caches: bf16 rows are there
   auto told = [&](int i) { return bar(kB + 20 + i); };
   auto heard = [&](int i) { return bar(kB + 20 + K::kQueue + i); };
+  const uint32_t sgiven = bar(kB + 20 + 2 * K::kQueue);  // pipeline 1's state is there
   const uint32_t tmem_slot = base + K::kOffTmemSlot;
 
   if (tid == 0) {
@@ -312,6 +292,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       // one per softmax warp; qfull over bf16 caches: a copy
       if (i >= kB && (k == 3 || k == 4 || k == 6 || (kQ8 && k == 0))) n = 8;
       if (i >= kB + 20 + K::kQueue) n = K::kListeners;
+      if (i == kB + 20 + 2 * K::kQueue) n = 4;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -469,14 +450,14 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     const uint32_t tp = trow + K::kColP + X * (K::kKeys / 2) + hp * 16;
     const uint32_t to0 = trow + K::kColO + hp * (D / 2), to = to0 + X * D;
     const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 2048;
-    TreePair pair = {stage + lane * 4, stage + lane * 4 + (hp ? -4 : 4) * 2048,
-                     1 + X * 4 + quarter, 0u};
+    tc::RowPair pair = {stage + lane * 8, stage + lane * 8 + (hp ? -4 : 4) * 2048,
+                        1 + X * 4 + quarter, 0u, 0};
     const int rt = r / p.g, rh = r % p.g;  // node of the tile, head of the (part of the) group
     auto wait = [&](uint32_t b, uint32_t phase) {
-      const bool got = tc::poll_or_abort<true>(b, phase & 1u, p.timeout_ns, abort_flag);
-      return __all_sync(0xffffffffu, got && !*abort_flag) != 0;
+      return __all_sync(0xffffffffu, tc::poll_or_abort<true>(b, phase & 1u, p.timeout_ns,
+                                                             abort_flag)) != 0;
     };
-    uint32_t step = 0, uses = 0, seg_no = 0, tile_no = 0;
+    uint32_t step = 0, uses = 0, given = 0, tile_no = 0;
     const float scale = fabsf(p.scale_log2);
     float row_sl = scale;  // of the segment whose queries were taken last
     // One-byte caches: the segment's query rows, which have landed in this pipeline's Q buffer,
@@ -501,6 +482,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
         for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
       }
       top = max(top, pair.swap(top));
+      if (pair.leaves) return false;
       // times 2^(141 - exponent field): the largest comes to [2^14, 2^15). A factor that fp32
       // holds: none for rows without a finite value above 2^-112.
       const int field = int(top >> 7);
@@ -575,6 +557,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       if (!ok) break;
       tile_no += uint32_t(g.jb - g.ja);
       row.l += pair.swap(row.l);
+      if (pair.leaves) break;
       pair.meet();  // the places are about to hold output
       const int mine = g.count(X), other = g.split ? g.count(1) : 0;
       if (mine > 0) ok = wait(pdone(X), step - 1);
@@ -585,16 +568,20 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
       first_seg = false;
       // ---- the segment's end: the output, or a record; of a split item by pipeline 0, once
       //      pipeline 1's state is there ----
-      const uint32_t state = base + K::kOffState + ((seg_no++ & 1u) * 128 + r) * 8;
+      const uint32_t state = base + K::kOffState + r * 8;
       float f0 = 1.f, f1 = 0.f;
       if (g.split) {
-        if (X == 1 && hp == 0) {
+        // (pipeline 1's state and O stay until pipeline 0 has read them: ofree)
+        if (X == 1 && mine > 0 && hp == 0) {
           tc::sts32(state, __float_as_uint(row.m));
           tc::sts32(state + 4, __float_as_uint(row.l));
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sgiven);
         }
-        tc::fence_before_sync();
-        asm volatile("bar.sync %0, 128;" ::"r"(9 + quarter) : "memory");
-        if (X == 0) {
+        if (X == 0 && other > 0) {
+          ok = wait(sgiven, given++);
+          if (!ok) break;
           const TreeRow theirs = {__uint_as_float(lds32(state)), __uint_as_float(lds32(state + 4))};
           const float m = fmaxf(row.m, theirs.m);
           // (a pipeline without a tile or a sight has m = -inf and l = 0)
@@ -684,12 +671,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
         if (other > 0 && X == 0) mbar_arrive(ofree(1));  // (read here)
       }
     }
-    // One that gives up leaves no partner behind at their barriers: the others meet the flag at
-    // their next wait, and pass two of the pair's and one of the four's before it at most.
-    if (*abort_flag)
-      asm volatile("bar.arrive %0, 64;\n\tbar.arrive %0, 64;\n\tbar.arrive %1, 128;" ::"r"(pair.id),
-                   "r"(9 + quarter)
-                   : "memory");
+    pair.leave();
     tc::fence_before_sync();
   } else if (active && warp == 0) {
     // ---------------- TMA ----------------
