@@ -25,7 +25,8 @@ SOURCES = ["api.cu", "append.cu", "merge.cu", "decode_bf16.cu", "decode_int8.cu"
            "decode_e4m3.cu", "decode_e5m2.cu", "noalloc.cu",
            "cascade.cu", "blocks.cu", "decode_tc.cu", "decode_tc_int8.cu", "decode_tc_e4m3.cu",
            "decode_tc_e5m2.cu", "rotate.cu", "gather.cu", "diff_bf16.cu", "diff_int8.cu",
-           "diff_e4m3.cu", "diff_e5m2.cu", "diff_merge.cu", "tree_bf16.cu", "tree_int8.cu",
+           "diff_e4m3.cu", "diff_e5m2.cu", "diff_merge.cu", "decode_tree.cu", "decode_tree_int8.cu",
+           "decode_tree_e4m3.cu", "decode_tree_e5m2.cu", "tree_bf16.cu", "tree_int8.cu",
            "tree_e4m3.cu", "tree_e5m2.cu", "tree_join.cu", "resize.cu", "keep.cu", "prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

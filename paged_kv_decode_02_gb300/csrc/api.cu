@@ -243,10 +243,10 @@ pkv_status check_dims(const pkv_dims* d) {
 // sets a kernel attribute, which costs tens of microseconds, so recent plans are kept.
 struct PlanKey {
   pkv_dims d;
-  int kvt, q_len, device, pair, sm_cap;
+  int kvt, q_len, device, pair, sm_cap, tree;
   bool operator==(const PlanKey& o) const {
     return std::memcmp(&d, &o.d, sizeof(d)) == 0 && kvt == o.kvt && q_len == o.q_len &&
-           device == o.device && pair == o.pair && sm_cap == o.sm_cap;
+           device == o.device && pair == o.pair && sm_cap == o.sm_cap && tree == o.tree;
   }
 };
 constexpr int kPlanCache = 16;
@@ -256,13 +256,14 @@ Plan g_plans[kPlanCache];
 int g_plan_count = 0, g_plan_next = 0;
 
 pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, int sm_cap,
-                              Plan* pl);
+                              bool tree, Plan* pl);
 
 // q_len > 1: the causal multi-query decode (bf16 caches). pair: 16-token blocks go in
 // pairs on the tensor-core paths (pairs start after a skipped prefix). sm_cap > 0: size
-// the grid for that many SMs (the rest run another kernel at the same time).
+// the grid for that many SMs (the rest run another kernel at the same time). tree: the new
+// tokens form a tree whose rows are one tile of a KV head.
 pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool pair = true,
-                     int sm_cap = 0) {
+                     int sm_cap = 0, bool tree = false) {
   pkv_status st = check_dims(d);
   if (st != PKV_OK) return st;
   int dev = 0;
@@ -275,13 +276,14 @@ pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool p
   key.device = dev;
   key.pair = pair ? 1 : 0;
   key.sm_cap = sm_cap;
+  key.tree = tree ? 1 : 0;
   std::lock_guard<std::mutex> lock(g_plan_mu);
   for (int i = 0; i < g_plan_count; ++i)
     if (g_plan_keys[i] == key) {
       *pl = g_plans[i];
       return PKV_OK;
     }
-  st = make_plan_uncached(d, kvt, q_len, pair, sm_cap, pl);
+  st = make_plan_uncached(d, kvt, q_len, pair, sm_cap, tree, pl);
   if (st != PKV_OK) return st;
   g_plan_keys[g_plan_next] = key;
   g_plans[g_plan_next] = *pl;
@@ -291,7 +293,7 @@ pkv_status make_plan(const pkv_dims* d, int kvt, Plan* pl, int q_len = 1, bool p
 }
 
 pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, int sm_cap,
-                              Plan* pl) {
+                              bool tree, Plan* pl) {
   Plan P{};
   P.g = d->num_q_heads / d->num_kv_heads;
   // query rows per KV head: (new token, group member) pairs, split into work units of
@@ -310,7 +312,12 @@ pkv_status make_plan_uncached(const pkv_dims* d, int kvt, int q_len, bool pair, 
   P.HU = d->num_kv_heads * P.nsg;
   const int simt = mma ? 0 : P.g;
   bool found = false;
-  if (q_len > 1) {
+  if (tree) {
+    P.nsg = 1;
+    P.gs = rows;
+    P.HU = d->num_kv_heads;
+    found = select_decode_tree(d->head_dim, d->block_size, rows <= kTcSplitRows, kvt, &P.k);
+  } else if (q_len > 1) {
     if (kvt < PKV_KV_BF16 || kvt > PKV_KV_FP8_E5M2) return PKV_ERR_DTYPE;
     // KV heads with 48 or more query rows go through the tcgen05 kernel, fewer rows
     // through the mma.sync path: measured on GB300 with the spec-70b lengths, tcgen05 vs
@@ -400,7 +407,8 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
                       const int32_t* block_tables, const int32_t* context_lens, float scale,
                       const pkv_dims* d, void* workspace, size_t workspace_bytes,
                       int32_t* status, cudaStream_t stream, int q_len = 1,
-                      unsigned long long* counters = nullptr, size_t counter_words = 0) {
+                      unsigned long long* counters = nullptr, size_t counter_words = 0,
+                      const uint64_t* tree_mask = nullptr, const int32_t* tree_lens = nullptr) {
   pkv_status st = check_dims(d);
   if (st != PKV_OK) return st;
   if (q_len < 1 || q_len > kMaxQueryLen) return PKV_ERR_SHAPE;
@@ -413,7 +421,7 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
       (q8 && (!aligned16(k_scale) || !aligned16(v_scale))))
     return PKV_ERR_ALIGNMENT;
   Plan P;
-  st = make_plan(d, kvt, &P, q_len);
+  st = make_plan(d, kvt, &P, q_len, true, 0, tree_mask != nullptr);
   if (st != PKV_OK) return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < P.ws_bytes)
@@ -463,6 +471,9 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
   p.unit_slot0 = -1;
   p.q_len = q_len;
   p.beta = P.k.tc ? kTcHeadCost : 0;
+  p.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  p.tree_lens = tree_lens;
+  p.tree_words = 2 * ((q_len + 63) / 64);
 
   // tcgen05 kernel: whole units leave through TMA tensor stores of g-row boxes when g is
   // 8, 16 or 32 and the row tiles start on tokens (each box then starts on a 1024-byte
@@ -503,6 +514,7 @@ pkv_status run_decode(int kvt, void* out, const void* q, const void* k_cache,
   m.W = P.k.tc ? P.W : P.W / P.nsg;  // CTAs, or workers of nsg warps
   m.beta = p.beta;
   m.wprefix = p.prefix_out + (d->num_seqs + 1);
+  m.tree_lens = tree_lens;
   if (!p.fixup) launch_merge(m, stream);  // else cut units were folded in the kernel
   if (cudaGetLastError() != cudaSuccess) return PKV_ERR_CUDA;
   return PKV_OK;
@@ -874,6 +886,19 @@ pkv_status run_prompt(void* out, const void* q, const void* k, const void* v,
 // ---------------------------------------------------------------------------
 // Tree attention
 // ---------------------------------------------------------------------------
+// Trees whose rows (nodes x heads of a KV head) are one tile go through the decode kernel, whose key
+// tiles are wide and whose calls are short; more rows through a kernel that reads the context once
+// for two tiles. Measured on GB300, decode kernel vs the other (us): 64 x 1733, 16 nodes, 64 / 8 heads
+// (128 rows), bf16 104 vs 134, INT8 194 vs 188, E4M3 181 vs 179; 2 x 16000, 16 nodes, 32 / 8 heads,
+// bf16 46 vs 62, INT8 55 vs 73; 4 x 40, 5 nodes, 8 / 8 heads of 64, bf16 8.5 vs 14.9; 64 x 1733, 60
+// nodes, 32 / 8 heads (240 rows), bf16 186 vs 158, INT8 425 vs 209.
+// (More sequences than the decode kernel takes go to the other as well.)
+pkv_status make_one_tile_plan(const pkv_dims* d, int kvt, int q_len, Plan* P) {
+  if ((long long)q_len * (d->num_q_heads / d->num_kv_heads) > kTcTileRows)
+    return PKV_ERR_UNSUPPORTED;
+  return make_plan(d, kvt, P, q_len, true, 0, true);
+}
+
 // workspace: [cuts (G)][records' (m, l), 2 per CTA of 2 x 128 rows][records' o]
 struct TreePlan {
   TreeKernelInfo k;
@@ -925,6 +950,13 @@ pkv_status run_tree(int kvt, void* out, const void* q, const void* k_cache, cons
     return PKV_ERR_ALIGNMENT;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PKV_ERR_WORKSPACE;
+  Plan one;
+  st = make_one_tile_plan(d, kvt, q_len, &one);
+  if (st == PKV_OK)
+    return run_decode(kvt, out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                      scale, d, workspace, workspace_bytes, status, stream, q_len, nullptr, 0,
+                      tree_mask, tree_lens);
+  if (st != PKV_ERR_UNSUPPORTED) return st;
   st = make_tree_plan(d, kvt, q_len, &P);
   if (st != PKV_OK) return st;
   if (workspace_bytes < P.ws_bytes) return PKV_ERR_WORKSPACE;
@@ -1563,7 +1595,13 @@ pkv_status pkv_decode_tree_workspace_bytes(const pkv_dims* dims, int32_t q_len,
                                            pkv_kv_dtype kv_dtype, size_t* bytes) {
   if (!bytes) return PKV_ERR_NULL;
   TreePlan P;
-  pkv_status st = make_tree_plan(dims, kv_dtype, q_len, &P);
+  pkv_status st = check_tree(dims, kv_dtype, q_len, &P.k);
+  if (st != PKV_OK) return st;
+  Plan one;
+  st = make_one_tile_plan(dims, kv_dtype, q_len, &one);
+  if (st == PKV_OK) *bytes = one.ws_bytes;
+  if (st != PKV_ERR_UNSUPPORTED) return st;
+  st = make_tree_plan(dims, kv_dtype, q_len, &P);
   if (st != PKV_OK) return st;
   *bytes = P.ws_bytes;
   return PKV_OK;

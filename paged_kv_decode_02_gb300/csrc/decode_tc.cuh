@@ -345,7 +345,11 @@ __device__ __forceinline__ void tc_tail_fixup(const DecodeParams& p, const int* 
 // instantiation keeps its own index arithmetic: measured on GB300, the general form
 // made the one-tile calls 17 % slower (spec-70b 102.4 -> 120.1 us) although it computes
 // the same values. CODE: -1 for bf16 caches, else the one-byte code format.
-template <int D, int BS, bool kTiles, int CODE = -1, int CS = 1, bool PAIR = false>
+// TREE: the new tokens are the nodes of a tree (the last t <= q_len cached tokens of the
+// sequence): a row sees every token before them and, of them, those whose bits its node's mask
+// has. Only tiles that reach past the first node take the mask's path.
+template <int D, int BS, bool kTiles, int CODE = -1, int CS = 1, bool PAIR = false,
+          bool TREE = false>
 __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 1)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv,
@@ -691,6 +695,31 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
     // token Rg / g, query head Rg % g of the group), if it exists
     auto row_of = [&](int u) { return (u % nsg) * R + r; };
     auto row_exists = [&](int u) { return r < R && row_of(u) < rows; };
+    // tree: tokens before the first node, the tree's nodes, and the row's own node (-1: none)
+    int tree_base = 0, tree_n = 0, node = -1;
+    auto tree_row = [&](const TileCursor& t) {
+      if constexpr (TREE) {
+        tree_n = p.tree_lens ? min(max(__ldg(p.tree_lens + t.s), 0), p.q_len) : p.q_len;
+        tree_n = min(tree_n, s_len[t.s]);
+        tree_base = s_len[t.s] - tree_n;
+        node = r < R && row_of(t.h) < rows ? row_of(t.h) / p.g : -1;
+        if (node >= tree_n) node = -1;
+      }
+    };
+    // tree: which of the 32 tokens from pos on this row sees
+    auto tree_bits = [&](int s, int pos) -> uint32_t {
+      if (node < 0) return 0u;
+      const int off = pos - tree_base;  // first token as a node
+      if (off <= -32) return 0xffffffffu;
+      const uint32_t* m = p.tree_mask + (size_t(s) * p.q_len + node) * p.tree_words;
+      auto word = [&](int i) { return i >= 0 && i < p.tree_words ? __ldg(m + i) : 0u; };
+      const int w = off >> 5;  // (off >= -31: word -1 holds the tokens before the nodes)
+      const uint32_t lo = w < 0 ? 0xffffffffu : word(w), hi = word(w + 1);
+      uint32_t bits = __funnelshift_r(lo, hi, off & 31);
+      const int left = tree_n - off;  // bits past the last node are nobody's
+      if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
+      return bits;
+    };
     TileCursor cur;
     tile_locate(cur, ra, s_prefix, B, U);
     // causal: new token i = Rg / g hides the last q_len - 1 - i positions of its head
@@ -703,6 +732,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
       row_ok = r < R;
       hide = row_ok ? p.q_len - 1 - r / p.g : 0;
     }
+    tree_row(cur);
     // Q rows of the KV head at cursor t -> Q buffer qb (K-major, 128-byte swizzle), as
     // asynchronous copies (padding rows zero-filled); q_ready completes and publishes them
     auto prefetch_q = [&](const TileCursor& t, int qb) {
@@ -774,6 +804,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
           row_ok = row_exists(cur.h);
           hide = row_ok ? p.q_len - 1 - row_of(cur.h) / p.g : 0;
         }
+        tree_row(cur);
       }
       if (last && i + 1 < cnt) {  // the next unit's Q rows, while this tile runs
         TileCursor nx = cur;
@@ -790,9 +821,11 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
       tc::fence_after_sync();
       // columns this row may see in the tile (context end, causal limit); padding rows
       // take the warp's largest count so that the warp runs one path
-      const int vis_row = row_ok ? min(K::kN, L - hide - t0) : -1;
+      // (tree: the columns before the nodes, a whole tile or the mask's path)
+      const int vis_row = TREE ? (node >= 0 ? min(K::kN, tree_base - t0) : -1)
+                               : row_ok ? min(K::kN, L - hide - t0) : -1;
       const int vis_w = __reduce_max_sync(0xffffffffu, vis_row);
-      const int vis = row_ok ? vis_row : vis_w;
+      const int vis = (TREE ? node >= 0 : row_ok) ? vis_row : vis_w;
       if (warp_idle) {  // no row of this warp is stored: only keep the barriers going
         if (!zero_v_tail(i, L, t0)) {
           ok = false;
@@ -854,10 +887,25 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
       // warp-uniform: every row sees the whole tile (all tiles but a head's last, and
       // the last ones of causal rows), else columns past each row's limit are masked
       const bool full = __all_sync(0xffffffffu, vis >= K::kN);
+      uint32_t seen[kNc / 32];  // tree: the columns this row sees
+      bool any = vis > 0;       // whether it sees one of the tile at all
       if (!full) {
+        if constexpr (TREE) {
+          any = false;
 #pragma unroll
-        for (int t = 0; t < kNc; ++t)
-          if (c0 + t >= vis) s[t] = 0xff800000u;  // -inf
+          for (int k = 0; k < kNc / 32; ++k) {
+            seen[k] = tree_bits(cur.s, t0 + c0 + 32 * k);
+            any = any || seen[k] != 0u;
+          }
+          if constexpr (PAIR || CS == 2) any = true;  // its other half may: the maximum tells
+#pragma unroll
+          for (int t = 0; t < kNc; ++t)
+            if (!(seen[t >> 5] >> (t & 31) & 1u)) s[t] = 0xff800000u;  // -inf
+        } else {
+#pragma unroll
+          for (int t = 0; t < kNc; ++t)
+            if (c0 + t >= vis) s[t] = 0xff800000u;  // -inf
+        }
       }
       // tile maximum: three-input max over eight independent chains (then over the
       // row's CS threads)
@@ -883,7 +931,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
       }
       float alpha = 1.f;
       bool rescale = false;
-      if (vis > 0 && mt > m_ref + 8.f) {
+      if (any && mt > m_ref + 8.f) {
         alpha = fast_exp2(m_ref - mt);  // 0 while the row has seen nothing
         m_ref = mt;
         rescale = seg_tile > 0;
@@ -906,8 +954,15 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         for (int t = 0; t < kNc; t += 2) {
           const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])),
                                       asl2, nm2);
-          const float w0 = c0 + t < vis ? fast_exp2(x.x) : 0.f,
-                      w1 = c0 + t + 1 < vis ? fast_exp2(x.y) : 0.f;
+          bool see0, see1;
+          if constexpr (TREE) {
+            see0 = seen[t >> 5] >> (t & 31) & 1u;
+            see1 = seen[t >> 5] >> ((t & 31) + 1) & 1u;
+          } else {
+            see0 = c0 + t < vis;
+            see1 = c0 + t + 1 < vis;
+          }
+          const float w0 = see0 ? fast_exp2(x.x) : 0.f, w1 = see1 ? fast_exp2(x.y) : 0.f;
           pk[t / 2] = kQ8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
         }
       }
@@ -969,7 +1024,13 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         const size_t slot = size_t(2 * c + (seg == 0 ? 0 : 1));
         // the sum of the weights (over the row's CS threads)
         const float l1 = __uint_as_float(tc::tmem_ld1(trow + K::kColL));
-        const float l = CS == 1 ? l1 : l1 + __shfl_xor_sync(0xffffffffu, l1, kRpq);
+        float l = CS == 1 ? l1 : l1 + __shfl_xor_sync(0xffffffffu, l1, kRpq);
+        // a row past the tree's last node went along with its warp: zeros
+        const bool none = TREE && node < 0;
+        if (none) {
+          l = 0.f;
+          m_ref = -INFINITY;
+        }
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if (whole) {
           // the bf16 rows go through this segment's Q buffer (its MMAs are complete),
@@ -988,6 +1049,10 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
             const int c2 = hp * kOc + c1;
             uint32_t o[32];
             tc::tmem_ld32(trow + K::kColO + c2, o);
+            if (none) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
             if constexpr (CS == 2) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -1076,6 +1141,10 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
             const int c2 = hp * kOc + c1;
             uint32_t o[32];
             tc::tmem_ld32(trow + K::kColO + c2, o);
+            if (none) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0u;
+            }
             if constexpr (CS == 2) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
@@ -1169,12 +1238,13 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
     tc_tail_fixup<D, kTiles>(p, s_prefix, s_rs, s_cut, gbase + K::kOffQ, K::kThreads);
 }
 
-template <int D, int BS, bool kTiles, int CODE, int CS = 1, bool PAIR = false>
+template <int D, int BS, bool kTiles, int CODE, int CS, bool PAIR, bool TREE>
 DecodeKernelInfo tc_info() {
   using K = TcDecode<D, BS, (CODE >= 0), PAIR>;
   DecodeKernelInfo info{};
   info.fn =
-      reinterpret_cast<const void*>(&paged_decode_tc_kernel<D, BS, kTiles, CODE, CS, PAIR>);
+      reinterpret_cast<const void*>(
+          &paged_decode_tc_kernel<D, BS, kTiles, CODE, CS, PAIR, TREE>);
   info.warps = K::kThreads / 32;
   info.stages = 2;
   info.warp_smem = K::kFixedSmem;  // per CTA, plus 12 * (B + 1)
@@ -1188,27 +1258,32 @@ DecodeKernelInfo tc_info() {
 
 // row_tiles: several row tiles per KV head; split (one tile of at most 64 rows): two
 // threads per query row, each with half of a tile's columns. Units of more than 64 rows
-// over bf16 caches with D = 128 take two softmax warps per lane quarter (paired).
-template <int CODE>
+// over bf16 caches with D = 128 take two softmax warps per lane quarter (paired). TREE: one
+// row tile only (more of them go to the tree attention's own kernel, tree.cuh).
+template <int CODE, bool TREE = false>
 bool select_tc_code(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info) {
   constexpr bool kPair = CODE < 0;
   if (row_tiles) {
-    if (D == 128 && BS == 16) *info = tc_info<128, 16, true, CODE, 1, kPair>();
-    else if (D == 128 && BS == 32) *info = tc_info<128, 32, true, CODE, 1, kPair>();
-    else if (D == 64 && BS == 16) *info = tc_info<64, 16, true, CODE>();
-    else if (D == 64 && BS == 32) *info = tc_info<64, 32, true, CODE>();
-    else return false;
+    if constexpr (TREE) {
+      return false;
+    } else {
+      if (D == 128 && BS == 16) *info = tc_info<128, 16, true, CODE, 1, kPair, TREE>();
+      else if (D == 128 && BS == 32) *info = tc_info<128, 32, true, CODE, 1, kPair, TREE>();
+      else if (D == 64 && BS == 16) *info = tc_info<64, 16, true, CODE, 1, false, TREE>();
+      else if (D == 64 && BS == 32) *info = tc_info<64, 32, true, CODE, 1, false, TREE>();
+      else return false;
+    }
   } else if (split) {
-    if (D == 128 && BS == 16) *info = tc_info<128, 16, false, CODE, 2>();
-    else if (D == 128 && BS == 32) *info = tc_info<128, 32, false, CODE, 2>();
-    else if (D == 64 && BS == 16) *info = tc_info<64, 16, false, CODE, 2>();
-    else if (D == 64 && BS == 32) *info = tc_info<64, 32, false, CODE, 2>();
+    if (D == 128 && BS == 16) *info = tc_info<128, 16, false, CODE, 2, false, TREE>();
+    else if (D == 128 && BS == 32) *info = tc_info<128, 32, false, CODE, 2, false, TREE>();
+    else if (D == 64 && BS == 16) *info = tc_info<64, 16, false, CODE, 2, false, TREE>();
+    else if (D == 64 && BS == 32) *info = tc_info<64, 32, false, CODE, 2, false, TREE>();
     else return false;
   } else {
-    if (D == 128 && BS == 16) *info = tc_info<128, 16, false, CODE, 1, kPair>();
-    else if (D == 128 && BS == 32) *info = tc_info<128, 32, false, CODE, 1, kPair>();
-    else if (D == 64 && BS == 16) *info = tc_info<64, 16, false, CODE>();
-    else if (D == 64 && BS == 32) *info = tc_info<64, 32, false, CODE>();
+    if (D == 128 && BS == 16) *info = tc_info<128, 16, false, CODE, 1, kPair, TREE>();
+    else if (D == 128 && BS == 32) *info = tc_info<128, 32, false, CODE, 1, kPair, TREE>();
+    else if (D == 64 && BS == 16) *info = tc_info<64, 16, false, CODE, 1, false, TREE>();
+    else if (D == 64 && BS == 32) *info = tc_info<64, 32, false, CODE, 1, false, TREE>();
     else return false;
   }
   return true;

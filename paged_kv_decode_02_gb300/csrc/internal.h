@@ -41,6 +41,9 @@ struct DecodeParams {
   int HU;                      // work units per sequence (Hkv * nsg)
   float scale_log2;            // softmax scale * log2(e)
   unsigned long long timeout_ns;
+  const uint32_t* tree_mask;   // tree decode: [B, q_len, tree_words] node masks, 32 nodes a word
+  const int32_t* tree_lens;    // [B] nodes of each tree, or NULL: q_len
+  int tree_words;
 };
 
 // Parameters of the shared-prefix (cascade) kernel: for KV head h, the B*g query rows
@@ -104,6 +107,7 @@ struct MergeParams {
   int W;                       // decode workers (groups of nsg warps, or tcgen05 CTAs)
   const int32_t* wprefix;      // beta > 0: per-sequence prefix of tiles + beta * [tiles > 0]
   int beta;                    // as in DecodeParams (0: workers cut the plain order)
+  const int32_t* tree_lens;    // tree decode: [B] new tokens of each sequence, or NULL: q_len
 };
 
 void launch_merge(const MergeParams& p, cudaStream_t stream);
@@ -161,6 +165,13 @@ bool select_decode_tc(int D, int BS, bool row_tiles, bool split, int kvt,
 bool select_decode_tc_int8(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 bool select_decode_tc_e4m3(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
 bool select_decode_tc_e5m2(int D, int BS, bool row_tiles, bool split, DecodeKernelInfo* info);
+
+// The same kernels for a tree of new tokens whose rows are one tile (DecodeParams::tree_mask), one
+// table per code in decode_tree.cu, decode_tree_int8.cu, _e4m3.cu and _e5m2.cu.
+bool select_decode_tree(int D, int BS, bool split, int kvt, DecodeKernelInfo* info);
+bool select_decode_tree_int8(int D, int BS, bool split, DecodeKernelInfo* info);
+bool select_decode_tree_e4m3(int D, int BS, bool split, DecodeKernelInfo* info);
+bool select_decode_tree_e5m2(int D, int BS, bool split, DecodeKernelInfo* info);
 
 bool select_decode_int8(int D, int BS, int simt_heads, DecodeKernelInfo* info,
                         bool pair = false);

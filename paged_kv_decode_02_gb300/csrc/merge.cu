@@ -53,7 +53,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) paged_decode_merge_kernel
   if (p.status != nullptr) {
     int flags = 0;
     const int L = p.context_lens[s];
-    if (lane == 0 && (L < 0 || L > p.MBS * p.BS || (L > 0 && L < p.q_len))) flags |= 0x1;
+    const int fresh = p.tree_lens ? p.tree_lens[s] : p.q_len;  // new tokens of the sequence
+    if (lane == 0 && (L < 0 || L > p.MBS * p.BS || (L > 0 && L < fresh) || fresh < 0 ||
+                      fresh > p.q_len))
+      flags |= 0x1;
     const int nblk = L <= 0 ? 0 : min((L + p.BS - 1) / p.BS, p.MBS);
     for (int j = lane; j < nblk; j += 32) {
       const int id = p.block_tables[size_t(s) * p.MBS + j];
