@@ -233,6 +233,15 @@ __device__ __forceinline__ void widen16(const uint4& raw, float sc, uint4& a, ui
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t x = Codec::pre(w[e]);
+    if constexpr (kScale && CODE == CODE_I8) {  // by way of 2^23 + 128 + code in fp32
+      const float2 s2 = make_float2(sc, sc), off = make_float2(-8388736.f, -8388736.f);
+      auto up = [&](uint32_t sel) { return __uint_as_float(prmt(x, 0x4b000000u, sel)); };
+      const float2 f = __fmul2_rn(__fadd2_rn(make_float2(up(0x7650u), up(0x7651u)), off), s2);
+      const float2 g = __fmul2_rn(__fadd2_rn(make_float2(up(0x7652u), up(0x7653u)), off), s2);
+      o[2 * e] = pack_f16x2(f.x, f.y);
+      o[2 * e + 1] = pack_f16x2(g.x, g.y);
+      continue;
+    }
     o[2 * e] = Codec::lo(x);
     o[2 * e + 1] = Codec::hi(x);
     if constexpr (kScale) {
@@ -914,11 +923,12 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
 #pragma unroll 1
         for (int idx = ct; idx < kChunks; idx += 96) {
           const int cc = idx & 3, t = idx >> 2 & 63, slab = (idx >> 8) ^ (t & (K::kSlabs - 1));
-          const uint4 raw = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
-          uint4 a, b;
-          if (!kv) widen16<kQ8 ? CODE : 0, false>(raw, 1.f, a, b);
-          else widen16<kQ8 ? CODE : 0, true>(raw, lds_f32(scales + 4 * t), a, b);
-          if (kv && t >= valid) a = b = make_uint4(0u, 0u, 0u, 0u);  // may hold anything
+          uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+          if (!kv || t < valid) {  // (past the context a V row's scale may be anything)
+            const uint4 raw = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
+            if (!kv) widen16<kQ8 ? CODE : 0, false>(raw, 1.f, a, b);
+            else widen16<kQ8 ? CODE : 0, true>(raw, lds_f32(scales + 4 * t), a, b);
+          }
           const uint32_t out = tile + slab * K::kSlab + t * 128;
           tc::sts128(out + (((2 * cc) ^ (t & 7)) << 4), a);
           tc::sts128(out + (((2 * cc + 1) ^ (t & 7)) << 4), b);
