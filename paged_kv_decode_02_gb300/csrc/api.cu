@@ -41,13 +41,18 @@ constexpr int kDiffUnitCost = 5;
 // than they save. One sequence (2 / 2 heads, bf16), at 1, 2, 3, 4: 300 tokens 7.9, 8.0, 8.3,
 // 8.6 us, 8192 tokens 11.7, 10.0, 10.0, 9.7; 3 of ~700 (32 / 8, E4M3): 11.8, 10.8, 10.6, 11.2
 constexpr int kDiffMinRange = 2;
-// prompt attention: what ending an item costs a CTA, and the least length of its stretch, both
-// in keys of a 256-row item
-constexpr int kPromptItemCost = 256;
-constexpr int kPromptMinRange = 512;
-// tree attention: the same, in tokens
-constexpr int kTreeItemCost = 128;
-constexpr int kTreeMinRange = 256;
+// prompt attention: what ending an item costs a CTA, and the least length of its stretch, both in
+// keys of a 256-row item. Measured on GB300 (us), cost 128 / 256 / 400 / 600: 8192 tokens, 32 / 8
+// heads 464, 433, 433, 435; 16 x 1024, 64 / 8 heads 354, 351, 348, 349; 1024 tokens, 32 / 32 heads
+// 40.6, 40.4, 37.7, 38.6; 32 x 100 .. 700 154, 142, 141, 147. Length 256 / 512 / 1024: three
+// prompts of 47 .. 100, 8 heads of 64, 14.4, 17.7, 21.4; the long ones alike
+constexpr int kPromptItemCost = 400;
+constexpr int kPromptMinRange = 256;
+// tree attention of several row tiles: the same, in tokens. Cost 64 / 128 / 256 / 400: 64 x 1733, 60
+// nodes, 32 / 8 heads, bf16 158, 157, 156, 156; 2 x 300, INT8 37, 34, 30, 28. Length 128 / 256 / 512:
+// the latter 28, 34, 40; 4 x 600, 40 nodes, bf16 28, 31, 33
+constexpr int kTreeItemCost = 320;
+constexpr int kTreeMinRange = 128;
 // cascade decode: the prefix kernel runs on about 1/kCascadePrefixShare of the SMs
 constexpr int kCascadePrefixShare = 3;
 
