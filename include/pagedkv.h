@@ -503,7 +503,7 @@ pkv_status pkv_decode_multi_q8(void* out, const void* q, const void* k_cache,
  * cache, whatever position its rotation used); node i attends to every token before the nodes
  * and to node j where bit j of its mask is set (its own bit included, if it is to see itself):
  *   out[s, i, h, :] = softmax(scale * K q[s, i, h]) V over those tokens.
- *   q, out     [num_seqs, q_len, num_q_heads, head_dim] bf16.
+ *   q, out     [num_seqs, q_len, num_q_heads, head_dim] bf16; out must not overlap an input.
  *   q_len      1 .. PKV_MAX_QUERY_LEN: the most nodes of a tree.
  *   tree_mask  [num_seqs, q_len, ceil(q_len / 64)] 64-bit words, device: bit j % 64 of word
  *              j / 64 of a node's row is node j's; bits of nodes at or past t are ignored.
@@ -514,8 +514,9 @@ pkv_status pkv_decode_multi_q8(void* out, const void* q, const void* k_cache,
  *   status     as for pkv_decode_multi_bf16, a tree_lens entry outside 0 .. q_len and a sequence
  *              with 0 < context_len < tree_lens[s] included. Without it, such an entry is taken
  *              as the nearest length that fits.
- * Rows are (node, head) pairs in tiles of up to 128 on the tensor cores, for every row count.
- * Cached V values a node does not see must be finite (their weight is 0).
+ * Rows are (node, head) pairs of a KV head in tiles of up to 128 on the tensor cores: one tile
+ * takes the path of pkv_decode_multi_bf16's tiles, two and more share each read of the context.
+ * Cached V values of the context must be finite, of nodes that none sees too (their weight is 0).
  */
 pkv_status pkv_decode_tree_workspace_bytes(const pkv_dims* dims, int32_t q_len,
                                            pkv_kv_dtype kv_dtype, size_t* bytes);
@@ -572,8 +573,8 @@ typedef struct pkv_prompt_dims {
  *   status        optional device int32: PKV_DEV_BAD_CONTEXT_LEN for a sequence whose offsets
  *                 fall or leave the arrays (its rows are not written); PKV_DEV_TIMEOUT.
  * fp32 scores, softmax statistics and sums; softmax weights rounded once to bf16 for P.V; bf16
- * output. Values of keys a query does not see must be finite where they share a tile of 128
- * keys with one it sees (their weight is 0); rows outside a sequence may hold anything.
+ * output. Values of keys a query does not see must be finite (their weight is 0); rows that no
+ * sequence has may hold anything.
  * num_seqs == 0 or num_q_tokens == 0 is a no-op returning PKV_OK. Token counts of 2^30 and more
  * and more than 128 query heads per KV head: PKV_ERR_UNSUPPORTED.
  */

@@ -621,8 +621,6 @@ def paged_kv_resize(block_tables, context_lens, target_lens, free_blocks, free_c
         rows.append(t)
     if token_offsets is None:
         token_offsets = torch.empty(B + 1, dtype=_I32, device=block_tables.device)
-        if B == 0:
-            token_offsets.zero_()
     else:
         _need(token_offsets, "token_offsets", _I32, 1, index)
         if token_offsets.shape[0] != B + 1:
@@ -630,6 +628,7 @@ def paged_kv_resize(block_tables, context_lens, target_lens, free_blocks, free_c
     if B == 0:
         rows[0].fill_(-1)
         rows[1].zero_()
+        token_offsets.zero_()
         return rows[0], rows[1], token_offsets
     # (heads, head_dim and num_blocks are not used: any the library takes)
     st = _run("pkv_resize_sequences", index, block_tables.data_ptr(), context_lens.data_ptr(),
@@ -714,6 +713,8 @@ def _decode_tree(kv, q, k_cache, v_cache, k_scale, v_scale, block_tables, contex
         _need(out, "out", _BF16, 4, index)
         if out.shape != shape:
             _same_shape(out, "out", shape)
+        if B and out.data_ptr() == q.data_ptr():
+            raise ValueError("out must not be q")
     dims = _pack_dims(B, Hq, hkv, d, bs, nb, block_tables.shape[1])
     status = _status_ptr(status, index)
     rows = (block_tables.data_ptr(), context_lens.data_ptr(), tree_mask.data_ptr(), lens, n,
@@ -749,8 +750,8 @@ def paged_decode_attention_tree(q, k_cache, v_cache, block_tables, context_lens,
     it; [B] int32) of the ``context_lens[s]`` cached tokens, in node order. A node sees every
     token before the nodes, and node j where bit j % 64 of ``tree_mask[s, i, j // 64]`` is set
     ([B, N, ceil(N / 64)] int64; its own bit included). Returns out [B, N, Hq, D] bf16; rows past
-    ``tree_lens[s]``, and nodes that see nothing, are zeros. ``workspace`` (uint8, at least
-    :func:`tree_workspace_bytes`) and ``status`` (int32 [1]) as for
+    ``tree_lens[s]``, and nodes that see nothing, are zeros; it must not be ``q``. ``workspace``
+    (uint8, at least :func:`tree_workspace_bytes`) and ``status`` (int32 [1]) as for
     :func:`paged_decode_attention`."""
     return _decode_tree(KV_BF16, q, k_cache, v_cache, None, None, block_tables, context_lens,
                         tree_mask, scale, tree_lens, out, workspace, status)

@@ -240,3 +240,16 @@ def test_keep_refuses_bad_paths():
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         _same(_keep(c, base, path, kept, status), want)
         assert status.item() == flag
+
+
+def test_empty_batch():
+    """No sequences: rows that the appends skip, offsets of zero."""
+    import paged_kv_decode_02_gb300 as pk
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    slots, positions = (torch.full((5,), 7, dtype=torch.int64, device="cuda") for _ in range(2))
+    offs = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    pk.paged_kv_resize(torch.empty(0, 4, dtype=torch.int32, device="cuda"), none, none.clone(),
+                       torch.zeros(3, dtype=torch.int32, device="cuda"),
+                       torch.ones(1, dtype=torch.int32, device="cuda"), 16, 5, slots, positions,
+                       offs)
+    assert (slots == -1).all() and (positions == 0).all() and offs.item() == 0

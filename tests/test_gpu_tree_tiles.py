@@ -173,3 +173,13 @@ def test_same_bits_graphs_and_a_stream(kv):
     assert torch.equal(got, first[1])
     with pytest.raises(RuntimeError):
         _call(c, q[0], masks[0], 0.09, workspace=ws[:need - 256])
+
+
+@pytest.mark.parametrize("n", [4, 40])
+def test_output_in_place_is_refused(n):
+    """A query row is read where the context is cut, after other rows have been written."""
+    c = Cache([n, 80], 2, 64, 16)
+    q = _queries(2, n, 8, 64)
+    mask, _ = random_trees([n] * 2, 3, n)
+    with pytest.raises(ValueError, match="out"):
+        _call(c, q, mask.cuda(), 0.125, out=q)
