@@ -95,8 +95,12 @@ __global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const R
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int at = blockIdx.x * threads + tid, step = gridDim.x * threads;
   const int up = (1 << p.bs_log2) - 1;
-  pdl_wait_prior_grid();
-  pdl_allow_next_grid();
+  // kCommit computes its sums while kRows runs, which started after all before it had ended, and
+  // changes nothing that the sums read
+  if constexpr (PART != kCommit) {
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
+  }
   if (tid == 0) s_taken = 0;
   int flags = 0;
   int count = *p.free_count;
@@ -213,6 +217,10 @@ __global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const R
       p.slots[t] = slot;
       p.positions[t] = pos;
     }
+  }
+  if constexpr (PART == kCommit) {
+    pdl_wait_prior_grid();
+    pdl_allow_next_grid();
   }
   if constexpr (PART != kRows) {
     for (int s = tid; s <= B; s += threads) p.offsets[s] = s_tok[s];

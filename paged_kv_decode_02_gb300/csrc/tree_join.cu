@@ -1,13 +1,12 @@
 // tree_join.cu -- what follows the tree attention (tree.cuh): records of items cut between two
 // CTAs' stretches are joined, rows past each tree's tiles become zeros, and, with a status word,
 // every sequence is checked.
+#include "join.cuh"
 #include "tree.cuh"
 
 namespace pkv {
 
 namespace {
-constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 32;   // rows per CTA
 constexpr int kZeroCtas = 152;  // CTAs that zero rows, sequence after sequence
 }  // namespace
 
@@ -20,9 +19,8 @@ __device__ __forceinline__ void zero_rows(const TreeParams& p, int s, int first,
     o[k] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// CTA (c, y), c < G: rows 32 y .. of the item that CTA c's stretch begins and does not end. Its
-// parts are that record and the first records of the CTAs after it, up to the one that ends the
-// item; they meet at the largest of their maxima. A row takes D / 4 lanes, a quad of columns each.
+// CTA (c, y), c < G: rows 32 y .. of the item that CTA c's stretch begins and does not end. A row
+// takes D / 4 lanes, a quad of columns each. The CTAs after those zero what no tile covers.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParams p, int G) {
   constexpr int Q = D / 4;
@@ -42,39 +40,26 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const TreeParam
   q.load(p, cut.s);
   const int pairs = (q.tiles + 1) >> 1, pr = cut.u % pairs, hv = cut.u / pairs;
   const int rows = 2 * pr + 1 >= q.tiles ? 128 : 256;
+  constexpr int R = kJoinRows * Q / kJoinThreads;  // rows of a thread
   const int dq = threadIdx.x % Q;
-  for (int r0 = threadIdx.x / Q; r0 < kJoinRows; r0 += kJoinThreads / Q) {
-    const int row = blockIdx.y * kJoinRows + r0, X = row >> 7, r = row & 127;
+  int row[R];
+  float4 o[R];
+  float L[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    row[i] = blockIdx.y * kJoinRows + threadIdx.x / Q + i * (kJoinThreads / Q);
+  join_parts<D>(p.cuts, p.part_ml, p.part_o, blockIdx.x, G, cut.slot, row, dq, o, L);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int X = row[i] >> 7, r = row[i] & 127;
     const int rt = r / p.g, node = (2 * pr + X) * p.tpt + rt;
-    if (row >= rows || rt >= p.tpt || node >= p.q_len) continue;
-    float M = -INFINITY, L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](int slot) {
-      const size_t rec = size_t(slot) * 256 + row;
-      const float2 ml = reinterpret_cast<const float2*>(p.part_ml)[rec];
-      // a part that saw nothing has no output; a NaN sum goes on
-      if (!(ml.x > -INFINITY) && ml.y == 0.f) return;
-      const float4 v = reinterpret_cast<const float4*>(p.part_o)[rec * Q + dq];
-      const float m = fmaxf(M, ml.x);
-      const float a = M > -INFINITY ? fast_exp2(M - m) : 0.f;
-      const float b = ml.x > -INFINITY ? fast_exp2(ml.x - m) : 1.f;
-      L = L * a + ml.y * b;
-      o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
-      M = m;
-    };
-    add(cut.slot);
-    for (int c = blockIdx.x + 1; c < G; ++c) {
-      const int state = p.cuts[c].state;
-      if (state & kPromptEmpty) continue;
-      if (!(state & kPromptContinues)) break;
-      add(2 * c);
-      if (state & kPromptEnds) break;
-    }
-    const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // (NaN stays)
+    if (row[i] >= rows || rt >= p.tpt || node >= p.q_len) continue;
+    const float inv = L[i] > 0.f ? 1.f / L[i] : L[i] == 0.f ? 0.f : L[i];  // (NaN stays)
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) +
                          ((size_t(cut.s) * p.q_len + node) * p.Hq + hv * p.g + r % p.g) * D;
     reinterpret_cast<uint2*>(out)[dq] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv),
+                   pack_bf16x2(o[i].z * inv, o[i].w * inv));
   }
 }
 
