@@ -133,14 +133,22 @@ __global__ void __launch_bounds__(kResizeThreads) paged_kv_resize_kernel(const R
   if (lane == 31)
     for (int i = 0; i < 3; ++i) s_warp[i][warp] = incl[i];
   __syncthreads();
-  long long run[3], total[3];
-  for (int i = 0; i < 3; ++i) {
-    run[i] = incl[i] - sum[i];
-    total[i] = 0;
-    for (int w = 0; w < threads / 32; ++w) {
-      if (w < warp) run[i] += s_warp[i][w];
-      total[i] += s_warp[i][w];
+  const int warps = threads / 32;
+  if (warp < 3) {  // warp i: the warps' sums i, inclusive
+    long long x = lane < warps ? s_warp[warp][lane] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
     }
+    s_warp[warp][lane] = x;
+  }
+  __syncthreads();
+  long long run[3], total[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    run[i] = incl[i] - sum[i] + (warp > 0 ? s_warp[i][warp - 1] : 0);
+    total[i] = s_warp[i][warps - 1];
   }
   // (B times the table row's length is below 2^30: block sums fit 32 bits)
   const int given = int(total[2]);
@@ -260,7 +268,8 @@ cudaError_t launch_resize(const ResizeParams& p, cudaStream_t stream) {
   e = go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kRows>), rows < sms ? rows : sms,
          kResizeThreads);
   if (e != cudaSuccess) return e;
-  return go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kCommit>), 1, kResizeThreads);
+  return go(reinterpret_cast<const void*>(&paged_kv_resize_kernel<kCommit>), 1,
+            p.B <= kResizeSmall ? kResizeSmall : kResizeThreads);
 }
 
 }  // namespace pkv
