@@ -19,7 +19,7 @@
 // short ones fill the SMs alike, without host knowledge of the lengths, and no order of
 // atomics touches a result.
 //
-// A CTA (704 threads):
+// A CTA (704 threads, 80 registers):
 //   warp 0      TMA: Q of both tiles, K and V tiles through one ring of stages;
 //   warps 1, 2  one thread each issues S_X = Q_X K_j^T into the score columns of tile 0, tile 1;
 //   warps 3, 20 one thread each issues O_X += P_X V_j with P_X (bf16) read from TMEM, after the
@@ -39,6 +39,14 @@
 // (89 %), 96 813 (94 %), 128 1025 (100 %; Q and K come from shared memory, whose bandwidth bounds
 // small N); with 128 keys, P over the scores it came from and so every step of a tile in
 // sequence, a step took 3500 cycles for two tiles, where the MMAs take 2050.
+// Whole calls on GB300: 32768 tokens, 32 / 8 heads, 6.1 to 6.3 ms (1400 to 1430 TFLOP/s, by the
+// power the part is given); 8192 tokens 432 us (1270); 16 x 1024, 64 / 8 heads, 340 us (810); chunks of
+// 256 over 1500, 187 us (990). What is left is the end of an item, some 7000 cycles of a tile's
+// softmax warps where a step of 80 keys takes 2050: the last P.V, O through shared memory to its
+// rows, the next segment. Tried, and slower: the end put off behind the next item's first softmax
+// (340 -> 413 us at 16 x 1024: longer live ranges in the loop), the next segment taken before it
+// (377), both P.V by one thread and the walk by the TMA thread (393, with 91 registers in place of
+// 80), waits by try_wait (8192 tokens: 437 -> 503).
 // The softmax keeps a reference maximum per row that moves only when a tile's maximum exceeds
 // it by more than 8 (log2 units; weights then reach 2^8 and keep their relative precision), so
 // O is rescaled in TMEM a few times per item at most. Scores, maxima and sums are fp32; a

@@ -20,7 +20,11 @@
 // the sequence of the first of 32 tokens by a 32-way search there, a lane its own from it on.
 // Few tokens: one CTA does it all. Many: CTAs on every SM write tables, list and rows, each with
 // its own scan of the batch, and a second launch of one CTA then writes lengths, count and
-// offsets (no CTA may change what another still reads).
+// offsets (no CTA may change what another still reads); it computes its sums beside the first.
+// Bound by the chain of length, scan, search, table entry (1.8 MB of rows take 0.3 us). Measured
+// on GB300, GPU time of two calls, in and out: 256 prompts of 1 .. 900 tokens 9.4 us (all by one
+// CTA some 470; sums of warps added up by each thread 14.3; the commit's sums after the rows
+// 22.0); 4096 of 1 .. 200 tokens 23.9; 64 sequences that grow by a token 6.4.
 #include <algorithm>
 
 #include "common.cuh"
