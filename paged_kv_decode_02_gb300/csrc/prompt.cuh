@@ -46,7 +46,8 @@
 // rows, the next segment. Tried, and slower: the end put off behind the next item's first softmax
 // (340 -> 413 us at 16 x 1024: longer live ranges in the loop), the next segment taken before it
 // (377), both P.V by one thread and the walk by the TMA thread (393, with 91 registers in place of
-// 80), waits by try_wait (8192 tokens: 437 -> 503).
+// 80), rows stored as whole lines, half a warp's at a time (430), segments read again at their end
+// (fewer spills: 339), waits by try_wait (8192 tokens: 437 -> 503).
 // The softmax keeps a reference maximum per row that moves only when a tile's maximum exceeds
 // it by more than 8 (log2 units; weights then reach 2^8 and keep their relative precision), so
 // O is rescaled in TMEM a few times per item at most. Scores, maxima and sums are fp32; a
