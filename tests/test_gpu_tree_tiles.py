@@ -183,3 +183,22 @@ def test_output_in_place_is_refused(n):
     mask, _ = random_trees([n] * 2, 3, n)
     with pytest.raises(ValueError, match="out"):
         _call(c, q, mask.cuda(), 0.125, out=q)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("b", [1500, 20000])
+def test_large_batches(b, kv):
+    """More sequences than the decode kernel takes, of few rows each; every one of three lengths."""
+    n, hq, hkv, d, bs = 2, 4, 2, 64, 16
+    lens = [2, 17, 0][:3]
+    c = Cache(lens, hkv, d, bs, kv, seed=7)
+    pick = torch.arange(b, device="cuda") % 3
+    q3 = _queries(3, n, hq, d, seed=8)
+    mask = torch.tensor([[[1], [3]]] * 3)
+    seen = [torch.tensor([[True, False], [True, True]])] * 3
+    sizes = [2, 2, 0]
+    out, bound = tree_reference(c, q3, seen, sizes, 0.125)
+    c.tables, c.context_lens = c.tables[pick].contiguous(), c.context_lens[pick].contiguous()
+    got = _call(c, q3[pick].contiguous(), mask.cuda()[pick].contiguous(), 0.125,
+                tree_lens=_sizes(sizes)[pick].contiguous())
+    check(got, out[pick], bound[pick])
