@@ -514,8 +514,8 @@ pkv_status pkv_decode_multi_q8(void* out, const void* q, const void* k_cache,
  *   status     as for pkv_decode_multi_bf16, a tree_lens entry outside 0 .. q_len and a sequence
  *              with 0 < context_len < tree_lens[s] included. Without it, such an entry is taken
  *              as the nearest length that fits.
- * Rows are (node, head) pairs of a KV head in tiles of up to 128 on the tensor cores: one tile
- * takes the path of pkv_decode_multi_bf16's tiles, two and more share each read of the context.
+ * Rows are (node, head) pairs of a KV head in tiles of up to 128 on the tensor cores; two tiles
+ * share each read of the context.
  * Cached V values of the context must be finite, of nodes that none sees too (their weight is 0).
  */
 pkv_status pkv_decode_tree_workspace_bytes(const pkv_dims* dims, int32_t q_len,

@@ -893,14 +893,22 @@ pkv_status run_prompt(void* out, const void* q, const void* k, const void* v,
 // ---------------------------------------------------------------------------
 // Trees whose rows (nodes x heads of a KV head) are one tile go through the decode kernel, whose key
 // tiles are wide and whose calls are short; more rows through a kernel that reads the context once
-// for two tiles. Measured on GB300, decode kernel vs the other (us): 64 x 1733, 16 nodes, 64 / 8 heads
-// (128 rows), bf16 104 vs 134, INT8 194 vs 188, E4M3 181 vs 179; 2 x 16000, 16 nodes, 32 / 8 heads,
-// bf16 46 vs 62, INT8 55 vs 73; 4 x 40, 5 nodes, 8 / 8 heads of 64, bf16 8.5 vs 14.9; 64 x 1733, 60
-// nodes, 32 / 8 heads (240 rows), bf16 186 vs 158, INT8 425 vs 209.
+// for two tiles. Over one-byte caches that kernel, which widens with six warps, also has the better
+// of one tile of more than 64 rows, unless contexts are short; their lengths are the device's, so
+// the table's row decides. Measured on GB300, decode kernel vs the other (us): bf16, 64 x 1733, 16
+// nodes, 64 / 8 heads (128 rows) 104 vs 134, 2 x 16000, 16 nodes, 32 / 8 heads 46 vs 62, 4 x 40, 5
+// nodes, 8 / 8 heads of 64, 8.5 vs 14.9, 64 x 1733, 60 nodes, 32 / 8 heads (240 rows) 186 vs 155; one-byte
+// (INT8, E4M3), 64 x 1733, 20 nodes, 32 / 8 heads (80 rows) 223 vs 182, 207 vs 175, 128 x 4096, 12
+// nodes, 64 / 8 heads 796 vs 663, 734 vs 643, 64 x 500, 32 nodes, 32 / 8 heads 85 vs 84, 81 vs 84, 256
+// x 100, 20 nodes 108 vs 149, 107 vs 152; 64 rows: 64 x 500, 16 nodes 78 vs 82, 72 vs 84, 2 x 16000
+// 56 vs 55, 50 vs 56; 240 rows, 64 x 1733 425 vs 200.
 // (More sequences than the decode kernel takes go to the other as well.)
+constexpr int kTreeLongTable = 512;  // tokens of a table's row
 pkv_status make_one_tile_plan(const pkv_dims* d, int kvt, int q_len, Plan* P) {
-  if ((long long)q_len * (d->num_q_heads / d->num_kv_heads) > kTcTileRows)
-    return PKV_ERR_UNSUPPORTED;
+  const long long rows = (long long)q_len * (d->num_q_heads / d->num_kv_heads);
+  const bool wide = kvt != PKV_KV_BF16 && rows > kTcSplitRows &&
+                    (long long)d->max_blocks_per_seq * d->block_size >= kTreeLongTable;
+  if (rows > kTcTileRows || wide) return PKV_ERR_UNSUPPORTED;
   return make_plan(d, kvt, P, q_len, true, 0, true);
 }
 

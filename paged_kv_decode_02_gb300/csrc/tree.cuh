@@ -6,8 +6,9 @@
 // several candidates per position); node i sees every token before them and the nodes whose
 // bits its mask has set:
 //   out[i, h] = softmax(scale * K q[i, h]) V over those tokens, reached through the block table.
-// The context's bytes, which every row of a head shares, are the floor; more than 128 rows per head
-// (fewer: decode_tc.cuh) are bound by what is done with a tile on chip.
+// The context's bytes, which every row of a head shares, are the floor; more than 128 rows per head,
+// and more than 64 over one-byte caches (fewer: decode_tc.cuh, chosen in api.cu), are bound by what is
+// done with a tile on chip.
 //
 // Work. A query row is (node, head of the group); tpt = 128 / g nodes make a tile of 128 MMA
 // rows (g > 128: the group is cut into equal parts first). The context is walked in key tiles of
