@@ -543,14 +543,16 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
                                      (long long)(g.q.q0 + tok) * p.out_stride +
                                      (long long)(g.h * p.g + rh) * D + hp * (D / 2));
         if (!row_ok) row_out = nullptr;
+        int ln;  // (the lane, read anew: what is made from it holds no registers in the loop above)
+        asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln));
         auto put = [&](int ch, const uint4& v) {
-          tc::sts128(stage + lane * 64 + ((ch ^ (lane >> 1 & 3)) << 4), v);
+          tc::sts128(stage + ln * 64 + ((ch ^ (ln >> 1 & 3)) << 4), v);
         };
         auto flush = [&](int at) {  // the staged bytes are bytes `at` .. `at` + 63 of the rows
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int from = 8 * k + (lane >> 2), ch = lane & 3;
+            const int from = 8 * k + (ln >> 2), ch = ln & 3;
             uint8_t* dst = reinterpret_cast<uint8_t*>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_out), from));
             const uint4 v = lds128(stage + from * 64 + ((ch ^ (from >> 1 & 3)) << 4));

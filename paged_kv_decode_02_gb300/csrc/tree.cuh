@@ -484,6 +484,9 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     auto take_q = [&](const TreeSeg& g) -> bool {
       if (!kQ8 || g.count(X) == 0) return true;
       if (!wait(qland(X), uses++)) return false;
+      int ln;
+      asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln));
+      const int r = quarter * 32 + ln;
       const uint32_t qa = base + K::kOffQ + X * K::kTileQ + r * 128;
       constexpr int kChunks = D / 16;  // of this thread's half of the row
       auto at = [&](int k) {
@@ -627,14 +630,16 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
                               reinterpret_cast<__nv_bfloat16*>(p.out) +
                               ((size_t(g.s) * p.q_len + node) * p.Hq + g.hv * p.g + rh) * D +
                               hp * (D / 2));
+        int ln;  // (the lane, read anew: what is made from it holds no registers in the loop above)
+        asm volatile("mov.u32 %0, %%laneid;" : "=r"(ln));
         auto put = [&](int ch, const uint4& v) {
-          tc::sts128(stage + lane * 64 + ((ch ^ (lane >> 1 & 3)) << 4), v);
+          tc::sts128(stage + ln * 64 + ((ch ^ (ln >> 1 & 3)) << 4), v);
         };
         auto flush = [&](int at) {  // the staged bytes are bytes `at` .. `at` + 63 of the rows
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int from = 8 * k + (lane >> 2), ch = lane & 3;
+            const int from = 8 * k + (ln >> 2), ch = ln & 3;
             uint8_t* dst = reinterpret_cast<uint8_t*>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row_out), from));
             const uint4 v = lds128(stage + from * 64 + ((ch ^ (from >> 1 & 3)) << 4));
