@@ -239,7 +239,7 @@ struct PromptStep {
 // kNeg: the scale is negative. Returns false on a timeout.
 template <int D, bool kWhole, bool kNeg, typename Wait>
 __device__ __forceinline__ bool prompt_softmax(const PromptStep& at, float sl, int vis,
-                                               tc::RowPair& pair, PromptRow& row,
+                                               tc::RowPair& pair, PromptRow& row, bool& gone,
                                                const Wait& wait) {
   constexpr int N = PromptCfg<D>::kKeys / 2;
   uint32_t s[N];
@@ -263,8 +263,8 @@ __device__ __forceinline__ bool prompt_softmax(const PromptStep& at, float sl, i
     mx[t & 7] = most(mx[t & 7], __uint_as_float(s[8 + 2 * t]), __uint_as_float(s[9 + 2 * t]));
   const float mine = sl * most(most(mx[0], mx[1], mx[2]), most(mx[3], mx[4], mx[5]),
                                most(mx[6], mx[7], mx[7]));
-  const float top = fmaxf(mine, pair.swap(mine));
-  if (pair.leaves) return false;
+  const float top = fmaxf(mine, pair.swap(mine, gone));
+  if (gone) return false;
   float alpha = 1.f;
   const bool up = top > row.m + 8.f;
   if (up) {
@@ -477,7 +477,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       const uint32_t to = trow + K::kColO + X * D + hp * (D / 2);
       const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 2048;
       tc::RowPair pair = {stage + lane * 8, stage + lane * 8 + (hp ? -4 : 4) * 2048,
-                          1 + X * 4 + quarter, 0u, 0};
+                          1 + X * 4 + quarter};
+      bool gone = false;
       const float sl = p.scale_log2;
       const int rt = r / p.g, rh = r % p.g;  // token of the tile, head of the group
       uint32_t step = 0;
@@ -513,11 +514,11 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
               mbar_arrive(pfull(X));
             }
           } else if (whole) {
-            ok = sl < 0.f ? prompt_softmax<D, true, true>(at, sl, vis, pair, row, wait)
-                          : prompt_softmax<D, true, false>(at, sl, vis, pair, row, wait);
+            ok = sl < 0.f ? prompt_softmax<D, true, true>(at, sl, vis, pair, row, gone, wait)
+                          : prompt_softmax<D, true, false>(at, sl, vis, pair, row, gone, wait);
           } else {
-            ok = sl < 0.f ? prompt_softmax<D, false, true>(at, sl, vis, pair, row, wait)
-                          : prompt_softmax<D, false, false>(at, sl, vis, pair, row, wait);
+            ok = sl < 0.f ? prompt_softmax<D, false, true>(at, sl, vis, pair, row, gone, wait)
+                          : prompt_softmax<D, false, false>(at, sl, vis, pair, row, gone, wait);
           }
           if (!ok) break;
         }
@@ -525,8 +526,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         const bool cut = g.ja > 0 || g.jb < g.n;
         const size_t rec = (size_t(2 * c + (first_seg ? 0 : 1)) * 2 + X) * K::kRows + r;
         first_seg = false;
-        const float l = row.l + pair.swap(row.l);
-        if (pair.leaves) break;
+        const float l = row.l + pair.swap(row.l, gone);
+        if (gone) break;
         pair.meet();  // the places are about to hold output
         if (cut && hp == 0) reinterpret_cast<float2*>(p.part_ml)[rec] = make_float2(row.m, l);
         if (je <= g.ja) continue;  // nothing of this tile here
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ofree(X));
       }
-      pair.leave();
+      if (!gone) pair.leave();
       tc::fence_before_sync();
     }
   } else {

@@ -253,36 +253,35 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[20])
 }
 // Two warps whose threads of the same lane share a row, each with half of a tile's columns: they
 // exchange values, and leave together. A named barrier waits without a limit, so a warp that gives
-// up (a wait that ran out) says so at the pair's next exchange, wherever the partner comes to it,
-// and each leaves only behind an exchange at which one of the two has said that it does.
+// up (a wait that ran out), or is through, says so at the pair's next exchange, wherever the partner
+// comes to it, and each leaves only behind an exchange at which one of the two has said that it
+// does.
 struct RowPair {
-  uint32_t mine, theirs;  // places in shared memory: 8 bytes a lane, two in turn
+  uint32_t mine, theirs;  // places in shared memory: 8 bytes a lane, two (256 bytes apart) in turn
   int id;                 // barrier of the two warps
-  uint32_t turn;          // 0 or 256
-  int leaves;             // 1: this warp goes on to the next exchange only; 2: both leave
   __device__ __forceinline__ void meet() const {
     asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
   }
-  // Gives a value to the partner and returns the partner's. (A place is written again once its
-  // reader has met the writer at the next exchange.)
-  __device__ __forceinline__ uint32_t swap(uint32_t x) {
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(mine + turn), "r"(x), "r"(leaves)
-                 : "memory");
+  // Gives a value to the partner and returns the partner's; `gone`: the partner leaves, and so must
+  // this warp, with nothing more to say. (A place is written again once its reader has met the
+  // writer at the next exchange.)
+  __device__ __forceinline__ uint32_t swap(uint32_t x, bool& gone) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(mine), "r"(x), "r"(0) : "memory");
     meet();
     uint32_t y, z;
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(y), "=r"(z) : "r"(theirs + turn) : "memory");
-    turn ^= 256u;
-    if ((uint32_t(leaves) | z) != 0u) leaves = 2;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(y), "=r"(z) : "r"(theirs) : "memory");
+    mine ^= 256u;
+    theirs ^= 256u;
+    if (z != 0u) gone = true;
     return y;
   }
-  __device__ __forceinline__ float swap(float x) {
-    return __uint_as_float(swap(__float_as_uint(x)));
+  __device__ __forceinline__ float swap(float x, bool& gone) {
+    return __uint_as_float(swap(__float_as_uint(x), gone));
   }
-  // The end, or a wait that ran out: returns once the partner need not be met again.
-  __device__ __forceinline__ void leave() {
-    if (leaves == 2) return;
-    leaves = 1;
-    swap(0u);
+  // This warp leaves (not after a swap with `gone`).
+  __device__ __forceinline__ void leave() const {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(mine), "r"(0), "r"(1) : "memory");
+    meet();
   }
 };
 

@@ -151,7 +151,7 @@ struct TreeStep {
 template <int D, int CODE, bool kWhole, typename Wait>
 __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t kscale,
                                              uint32_t seen, tc::RowPair& pair, TreeRow& row,
-                                             const Wait& wait) {
+                                             bool& gone, const Wait& wait) {
   constexpr bool kQ8 = CODE >= 0;
   uint32_t s[32];
   tc::tmem_ld32(at.ts, s);
@@ -186,8 +186,8 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   for (int t = 0; t < 14; ++t)
     mx[t & 3] = fmax3(mx[t & 3], __uint_as_float(s[4 + 2 * t]), __uint_as_float(s[5 + 2 * t]));
   const float mine = sl * fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-  const float top = fmaxf(mine, pair.swap(mine));
-  if (pair.leaves) return false;
+  const float top = fmaxf(mine, pair.swap(mine, gone));
+  if (gone) return false;
   float alpha = 1.f;
   const bool up = top > row.m + 8.f;
   if (up) {
@@ -470,7 +470,8 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     const uint32_t to0 = trow + K::kColO + hp * (D / 2), to = to0 + X * D;
     const uint32_t stage = base + K::kOffOut + uint32_t(warp - 4) * 2048;
     tc::RowPair pair = {stage + lane * 8, stage + lane * 8 + (hp ? -4 : 4) * 2048,
-                        1 + X * 4 + quarter, 0u, 0};
+                        1 + X * 4 + quarter};
+    bool gone = false;
     const int rt = r / p.g, rh = r % p.g;  // node of the tile, head of the (part of the) group
     auto wait = [&](uint32_t b, uint32_t phase) {
       return __all_sync(0xffffffffu, tc::poll_or_abort<true>(b, phase & 1u, p.timeout_ns,
@@ -503,8 +504,8 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
       }
-      top = max(top, pair.swap(top));
-      if (pair.leaves) return false;
+      top = max(top, pair.swap(top, gone));
+      if (gone) return false;
       // times 2^(141 - exponent field): the largest comes to [2^14, 2^15). A factor that fp32
       // holds: none for rows without a finite value above 2^-112.
       const int field = int(top >> 7);
@@ -569,17 +570,17 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
             mbar_arrive(pfull(X));
           }
         } else if ((j + 1) * K::kKeys <= before) {
-          ok = tree_softmax<D, CODE, true>(at, sl, kscale, 0u, pair, row, wait);
+          ok = tree_softmax<D, CODE, true>(at, sl, kscale, 0u, pair, row, gone, wait);
         } else {
           const uint32_t seen = bits_at(j * K::kKeys + 32 * hp);
-          ok = tree_softmax<D, CODE, false>(at, sl, kscale, seen, pair, row, wait);
+          ok = tree_softmax<D, CODE, false>(at, sl, kscale, seen, pair, row, gone, wait);
         }
         if (!ok) break;
       }
       if (!ok) break;
       tile_no += uint32_t(g.jb - g.ja);
-      row.l += pair.swap(row.l);
-      if (pair.leaves) break;
+      row.l += pair.swap(row.l, gone);
+      if (gone) break;
       pair.meet();  // the places are about to hold output
       const int mine = g.count(X), other = g.split ? g.count(1) : 0;
       if (mine > 0) ok = wait(pdone(X), step - 1);
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
         if (other > 0 && X == 0) mbar_arrive(ofree(1));  // (read here)
       }
     }
-    pair.leave();
+    if (!gone) pair.leave();
     tc::fence_before_sync();
   } else if (active && warp == 0) {
     // ---------------- TMA ----------------
