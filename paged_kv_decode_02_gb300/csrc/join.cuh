@@ -9,10 +9,10 @@
 // The records are some MB that were just written, so the time is that of the loads' chain: all of
 // a thread's rows are loaded at once, and a warp reads 32 CTAs' cuts to see which continue.
 // Measured on GB300, whole calls, rows and cuts one after the other -> at once (us): a tree of 33
-// nodes over 131071 tokens, E4M3 (19 parts) 207 -> 179; prompts of 1024 tokens, 32 / 32 heads, 37.9
-// -> 35.5, of 600, 8 / 8, 27.7 -> 21.4, 16 x 1024, 64 / 8, 349 -> 345. Two parts at once: 176 for the
-// tree, 1 to 4 % more for the others (registers). 16 rows a CTA: within 1 %, three short prompts
-// 14.5 -> 16.0.
+// nodes over 131071 tokens, E4M3 (19 parts) 207 -> 179; prompts of 1024 tokens, 32 / 32 heads,
+// 37.9 -> 35.5, of 600, 8 / 8, 27.7 -> 21.4, 16 x 1024, 64 / 8, 349 -> 345. Two parts at once: 176
+// for the tree, 1 to 4 % more for the others (registers). 16 rows a CTA: within 1 %, three short
+// prompts 14.5 -> 16.0.
 #pragma once
 
 #include "common.cuh"

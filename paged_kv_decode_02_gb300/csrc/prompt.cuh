@@ -39,9 +39,9 @@
 // (89 %), 96 813 (94 %), 128 1025 (100 %; Q and K come from shared memory, whose bandwidth bounds
 // small N); with 128 keys, P over the scores it came from and so every step of a tile in
 // sequence, a step took 3500 cycles for two tiles, where the MMAs take 2050.
-// Whole calls on GB300: 32768 tokens, 32 / 8 heads, 6.1 to 6.3 ms (1400 to 1430 TFLOP/s, by the
-// power the part is given); 8192 tokens 432 us (1270); 16 x 1024, 64 / 8 heads, 340 us (810); chunks of
-// 256 over 1500, 187 us (990). What is left is the end of an item, some 7000 cycles of a tile's
+// Whole calls on GB300: 32768 tokens, 32 / 8 heads, 6.0 to 6.2 ms (1410 to 1460 TFLOP/s, by the
+// power the part is given); 8192 tokens 423 us (1300); 16 x 1024, 64 / 8 heads, 332 us (830);
+// chunks of 256 over 1500, 184 us (1000). What is left is the end of an item, some 7000 cycles of a tile's
 // softmax warps where a step of 80 keys takes 2050: the last P.V, O through shared memory to its
 // rows, the next segment. Tried, and slower: the end put off behind the next item's first softmax
 // (340 -> 413 us at 16 x 1024: longer live ranges in the loop), the next segment taken before it
@@ -347,7 +347,10 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
       // sread, pfull, ofree: one arrival per softmax warp; empty: one per tile
       const bool soft = i >= kB && (k == 3 || k == 4 || k == 6);
       // heard: one per warp that listens
-      mbar_init(bar(i), soft ? 8 : i >= K::kStages && i < kB ? 2 : i >= kB + 18 + K::kQueue ? 21 : 1);
+      mbar_init(bar(i), soft                            ? 8
+                        : i >= K::kStages && i < kB     ? 2
+                        : i >= kB + 18 + K::kQueue      ? 21
+                                                        : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -413,7 +416,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
   }
   __syncthreads();
   const bool active = c < G;
-  pdl_allow_next_grid();  // the join's CTAs come early and wait (16 x 1024, 64 / 8 heads: 345 -> 341 us)
+  // the join's CTAs come early and wait (16 x 1024, 64 / 8 heads: 345 -> 341 us)
+  pdl_allow_next_grid();
   const PromptPlace first = s_place[0], stop = s_place[1];
   PromptWalk walk;
   walk.begin(first, stop);
@@ -605,12 +609,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
         PromptSeg g;
         auto load_tile = [&](const CUtensorMap* map, int h, int row) {
           const int st = u % K::kStages, n = u / K::kStages;
-          if (n > 0) ok = ok && tc::wait_or_abort(empty(st), uint32_t(n - 1) & 1u, p.timeout_ns, abort_flag);
+          if (n > 0)
+            ok = ok && tc::wait_or_abort(empty(st), uint32_t(n - 1) & 1u, p.timeout_ns, abort_flag);
           if (!ok) return;
           mbar_arrive_expect_tx(full(st), K::kTile);
-  #pragma unroll
+#pragma unroll
           for (int sl = 0; sl < K::kSlabs; ++sl)
-            tma_load_3d(base + K::kOffKV + st * K::kTile + sl * K::kSlab, map, full(st), sl * 64, h, row);
+            tma_load_3d(base + K::kOffKV + st * K::kTile + sl * K::kSlab, map, full(st), sl * 64,
+                        h, row);
           ++u;
         };
         while (ok && take(g, false)) {
@@ -621,7 +627,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::kThreads, 1)
               ok = tc::wait_or_abort(qempty(X), uint32_t(qn[X] - 1) & 1u, p.timeout_ns, abort_flag);
             if (!ok) break;
             mbar_arrive_expect_tx(qfull(X), uint32_t(p.tpt * p.g) * D * 2);
-  #pragma unroll
+#pragma unroll
             for (int sl = 0; sl < K::kSlabs; ++sl)
               tma_load_3d(base + K::kOffQ + X * K::kTileQ + sl * K::kSlabQ, &tmq, qfull(X), sl * 64,
                           g.h * p.g, g.q.q0 + g.i * per + X * p.tpt);

@@ -6,9 +6,9 @@
 // several candidates per position); node i sees every token before them and the nodes whose
 // bits its mask has set:
 //   out[i, h] = softmax(scale * K q[i, h]) V over those tokens, reached through the block table.
-// The context's bytes, which every row of a head shares, are the floor; more than 128 rows per head,
-// and more than 64 over one-byte caches (fewer: decode_tc.cuh, chosen in api.cu), are bound by what is
-// done with a tile on chip.
+// The context's bytes, which every row of a head shares, are the floor; more than 128 rows per
+// head, and more than 64 over one-byte caches (fewer: decode_tc.cuh, chosen in api.cu), are bound
+// by what is done with a tile on chip.
 //
 // Work. A query row is (node, head of the group); tpt = 128 / g nodes make a tile of 128 MMA
 // rows (g > 128: the group is cut into equal parts first). The context is walked in key tiles of
@@ -34,11 +34,11 @@
 // of the largest below; the row's scale takes the power back. K's scale multiplies the fp32 score.
 // Weights are bf16 (fp16 over one-byte caches), scores, maxima and sums fp32; the reference
 // maximum moves when a tile's exceeds it by more than 8 (log2 units).
-// Measured on GB300, whole calls: 64 x 1733 tokens, 60 nodes, 32 / 8 heads, bf16 155 us (2400 to
-// 2900 cycles per key tile of two row tiles, of which the MMAs take 1300: scores, softmax and P.V of a
-// tile wait for each other, and an item's end takes some 8000), INT8 200; 16 x 8192, INT8 197 us
+// Measured on GB300, whole calls: 64 x 1733 tokens, 60 nodes, 32 / 8 heads, bf16 150 us (2400 to
+// 2900 cycles per key tile of two row tiles, of which the MMAs take 1300: scores, softmax and P.V
+// of a tile wait for each other, and an item's end takes some 8000), INT8 200; 16 x 8192, INT8 195
 // (3300 cycles: the V trio is busy throughout, its instructions among those of 16 softmax warps;
-// without widening 170); 1 x 131071, 33 nodes, E4M3 179. The roles' loops are kept small: with the
+// without widening 170); 1 x 131071, 33 nodes, E4M3 177. The roles' loops are kept small: with the
 // widening unrolled the kernel waited for instructions (4 of 12 warps per issue) and took 248.
 // Slower: four V and two K warps with fp16 products (INT8 205 -> 221), converters on low warps
 // (207 -> 221), lighter polling (205 -> 212: the barriers' unit is shared), both pipelines at a
@@ -380,7 +380,8 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
   uint32_t heard_of = 0;
   auto take = [&](TreeSeg& g, bool whole_warp) {
     const uint32_t slot = heard_of % K::kQueue;
-    bool ok = tc::poll_or_abort<true>(told(slot), (heard_of / K::kQueue) & 1u, p.timeout_ns, abort_flag);
+    bool ok = tc::poll_or_abort<true>(told(slot), (heard_of / K::kQueue) & 1u, p.timeout_ns,
+                                      abort_flag);
     if (whole_warp) ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (!ok) return false;
     ++heard_of;
