@@ -709,12 +709,15 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     int q_left = 0;  // bit X: pipeline X's query rows of the segment are still to be sent for
     bool ok = true;
     TreeSeg g;
-    // the query rows, as soon as the scores of the segment before have been computed
+    // the query rows, as soon as the scores of the segment before have been computed (each lane's
+    // look at the barrier is its own: the warp goes by all of them, or its lanes could part here)
     auto send_queries = [&] {
 #pragma unroll
       for (int X = 0; X < 2; ++X) {
         if (!(q_left >> X & 1)) continue;
-        if (qn[X] > 0 && !mbar_test_wait(qempty(X), (qn[X] - 1) & 1u)) continue;
+        if (qn[X] > 0 &&
+            !__all_sync(0xffffffffu, mbar_test_wait(qempty(X), (qn[X] - 1) & 1u)))
+          continue;
         const uint32_t b = kQ8 ? qland(X) : qfull(X);
         if (lane == 0) {
           mbar_arrive_expect_tx(b, uint32_t(p.tpt * p.g) * D * 2);
