@@ -252,7 +252,8 @@ cudaError_t launch_resize(const ResizeParams& p, cudaStream_t stream) {
   ResizeParams copy = p;
   void* args[] = {&copy};
   auto go = [&](const void* fn, int grid, int threads) {
-    if (smem > 48 * 1024) {
+    // (a CTA has 48 KB without asking, static arrays among them: some 800 bytes here)
+    if (smem > 40 * 1024) {
       const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  12 * (kResizeMaxSeqs + 1));
       if (e != cudaSuccess) return e;
