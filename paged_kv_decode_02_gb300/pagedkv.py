@@ -787,9 +787,10 @@ def prompt_attention(q, k, v, q_offsets, scale, kv_offsets=None, out=None, works
     and those of ``kv_offsets`` (``q_offsets`` without it; both [B + 1] int32) of k and v. Its
     queries are its last tokens: query i sees keys j <= nk - nq + i. Returns out [Tq, Hq, D]
     bf16: the tensor given, whose rows outside every sequence stay as they were, or a new one.
-    A query without keys gets zeros. ``workspace`` (uint8, at least
-    :func:`prompt_workspace_bytes`); ``status`` (int32 [1]) flags offsets that fall or leave the
-    arrays, whose sequences are not computed."""
+    A query without keys gets zeros. ``out`` must not overlap an input (one that begins where an
+    input begins is refused). ``workspace`` (uint8, at least :func:`prompt_workspace_bytes`);
+    ``status`` (int32 [1]) flags offsets that fall or leave the arrays, whose sequences are not
+    computed."""
     if not isinstance(q, _Tensor):
         raise TypeError("q must be a torch.Tensor")
     index = q.get_device()
@@ -818,6 +819,8 @@ def prompt_attention(q, k, v, q_offsets, scale, kv_offsets=None, out=None, works
         out_shape, out_stride = _token_rows(out, "out", index)
         if out_shape != q_shape:
             _same_shape(out, "out", q_shape)
+        if tq and out.data_ptr() in (q.data_ptr(), k.data_ptr(), v.data_ptr()):
+            raise ValueError("out must not be an input")
     dims = _pack_prompt(B, hq, hkv, d, tq, tk, out_stride, q_stride, k_stride, v_stride)
     if workspace is None:
         with torch.cuda.device(index):
