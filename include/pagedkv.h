@@ -531,7 +531,8 @@ pkv_status pkv_decode_tree_bf16(void* out, const void* q, const void* k_cache,
  * pkv_decode_tree_q8 -- pkv_decode_tree_bf16 over a one-byte cache (kv_dtype PKV_KV_INT8,
  * PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2, else PKV_ERR_DTYPE): codes widened exactly, the K scale
  * on the fp32 score, V rounded once to fp16 (code x scale: V rows' absmax below 65504, and
- * above 1e-3 or so for their small values to keep their precision), fp16 softmax weights.
+ * above 1e-3 or so for their small values to keep their precision), softmax weights of fp16,
+ * within 2^-11 of themselves down to 2^-21 of a row's largest, within 2^-32 of it below.
  */
 pkv_status pkv_decode_tree_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale,

@@ -940,7 +940,8 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
       // caches); their row sums come from the tensor cores (P times a ones tile, beside
       // P.V)
       uint32_t pk[kNc / 2];
-      const float2 asl2 = make_float2(asl, asl), nm2 = make_float2(-m_ref, -m_ref);
+      const float nm = (TREE && kQ8 ? tc::kLift16 : 0.f) - m_ref;
+      const float2 asl2 = make_float2(asl, asl), nm2 = make_float2(nm, nm);
       if (full) {
 #pragma unroll
         for (int t = 0; t < kNc; t += 2) {

@@ -145,8 +145,8 @@ struct TreeStep {
   bool begun;
 };
 
-// Half a row (a thread) of a score tile: 32 scores become weights 2^(scale s - m), 16-bit pairs
-// in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`;
+// Half a row (a thread) of a score tile: 32 scores become weights 2^(scale s - m) (fp16: times
+// 2^kLift16), 16-bit pairs in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`;
 // sl >= 0 (the scores' MMA has changed sign for a negative scale).
 template <int D, int CODE, bool kWhole, typename Wait>
 __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t kscale,
@@ -197,7 +197,8 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   }
   // (scores of -inf alone: weights 0, not 2^(-inf + inf))
   const float m = row.m > -INFINITY ? row.m : 0.f;
-  const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(-m, -m);
+  const float nm = (kQ8 ? tc::kLift16 : 0.f) - m;
+  const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(nm, nm);
   float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   uint32_t pk[16];
 #pragma unroll
