@@ -530,9 +530,9 @@ pkv_status pkv_decode_tree_bf16(void* out, const void* q, const void* k_cache,
 /*
  * pkv_decode_tree_q8 -- pkv_decode_tree_bf16 over a one-byte cache (kv_dtype PKV_KV_INT8,
  * PKV_KV_FP8_E4M3 or PKV_KV_FP8_E5M2, else PKV_ERR_DTYPE): codes widened exactly, the K scale
- * on the fp32 score, V rounded once to fp16 (code x scale: V rows' absmax below 65504, and
- * above 1e-3 or so for their small values to keep their precision), softmax weights of fp16,
- * within 2^-11 of themselves down to 2^-21 of a row's largest, within 2^-32 of it below.
+ * on the fp32 score, the V scale on the fp32 softmax weight, whose product is rounded once to
+ * fp16: to 2^-11 of itself down to 2^-21 of a row's largest product, to 2^-32 of that one below.
+ * V scales up to 2^100; rows of any size beside each other.
  */
 pkv_status pkv_decode_tree_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const float* k_scale, const float* v_scale,

@@ -898,12 +898,13 @@ pkv_status run_prompt(void* out, const void* q, const void* k, const void* v,
 // the table's row decides. Measured on GB300, decode kernel vs the other (us): bf16, 64 x 1733, 16
 // nodes, 64 / 8 heads (128 rows) 104 vs 134, 2 x 16000, 16 nodes, 32 / 8 heads 46 vs 62, 4 x 40, 5
 // nodes, 8 / 8 heads of 64, 8.5 vs 14.9, 64 x 1733, 60 nodes, 32 / 8 heads (240 rows) 186 vs 155; one-byte
-// (INT8, E4M3), 64 x 1733, 20 nodes, 32 / 8 heads (80 rows) 223 vs 182, 207 vs 175, 128 x 4096, 12
-// nodes, 64 / 8 heads 796 vs 663, 734 vs 643, 64 x 500, 32 nodes, 32 / 8 heads 85 vs 84, 81 vs 84, 256
-// x 100, 20 nodes 108 vs 149, 107 vs 152; 64 rows: 64 x 500, 16 nodes 78 vs 82, 72 vs 84, 2 x 16000
-// 56 vs 55, 50 vs 56; 240 rows, 64 x 1733 425 vs 200.
+// (INT8, E4M3), 64 x 1733, 20 nodes, 32 / 8 heads (80 rows) 242 vs 177, 231 vs 177, 128 x 4096, 12
+// nodes, 64 / 8 heads 884 vs 659, 843 vs 657, 128 x 300, 32 nodes, 32 / 8 heads 148 vs 128, 144 vs 127,
+// 256 x 200, 20 nodes 204 vs 206, 204 vs 198, 256 x 100 121 vs 159, 122 vs 159 (what a server with
+// such contexts in tables of 256 tokens and more loses); 64 rows: 64 x 500, 16 nodes 77 vs 85, 74 vs
+// 84, 2 x 16000 54 vs 57, 51 vs 56, and 64 x 1733, 8 nodes, 64 / 8 heads 175 vs 176, 161 vs 175.
 // (More sequences than the decode kernel takes go to the other as well.)
-constexpr int kTreeLongTable = 512;  // tokens of a table's row
+constexpr int kTreeLongTable = 256;  // tokens of a table's row
 pkv_status make_one_tile_plan(const pkv_dims* d, int kvt, int q_len, Plan* P) {
   const long long rows = (long long)q_len * (d->num_q_heads / d->num_kv_heads);
   const bool wide = kvt != PKV_KV_BF16 && rows > kTcSplitRows &&

@@ -129,6 +129,11 @@ __device__ __forceinline__ float lds_f32(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
+// The exponent lg of a V scale, |scale| < 2^lg, for the references of weights that carry their V
+// scales (trees over one-byte caches, tcgen05.cuh). Its range keeps sums of 2^20 weights within fp32.
+__device__ __forceinline__ float value_log(uint32_t scale_bits) {
+  return float(min(max(int(scale_bits >> 23 & 255u) - 126, -80), 100));
+}
 __device__ __forceinline__ void sts128_zero(uint32_t addr) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
 }

@@ -80,7 +80,7 @@ __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <int D, int BS, bool Q8 = false, bool PAIR = false>
+template <int D, int BS, bool Q8 = false, bool PAIR = false, bool TREE = false>
 struct TcDecode {
   static constexpr int kM = 128;               // query rows per MMA (rows of a KV head, padded)
   static constexpr int kN = 128;               // tokens per tile
@@ -96,7 +96,8 @@ struct TcDecode {
   // one-byte caches: a tile's codes land in the last kCodeTile bytes of its 16-bit
   // buffer; its scales in kN fp32 slots: K scales in four (tile i in slot i % 4: the
   // softmax of tile i reads them, and tile i + 4's copy only starts once it has), then V
-  // scales in two (the stage's, read by the converters only)
+  // scales in two (the stage's, read by the converters only). Trees: V scales with the K
+  // tile and in four slots like its scales, then their exponents (value_log)
   static constexpr int kCodeTile = kN * D;
   static constexpr int kCodeOff = kTile - kCodeTile;
   static constexpr int kScaleBytes = kN * 4;
@@ -104,7 +105,8 @@ struct TcDecode {
   // paired softmax warps (bf16 caches, so no scales): the halves of each row's tile
   // maximum, [2 tiles][2 halves][128 rows] fp32
   static constexpr int kOffXmax = kOffScales;
-  static constexpr int kOffBar = kOffScales + (Q8 ? 6 * kScaleBytes : PAIR ? 2048 : 0);
+  static constexpr int kOffBar =
+      kOffScales + (Q8 ? (TREE ? 12 : 6) * kScaleBytes : PAIR ? 2048 : 0);
   // mbarriers: kfull[2] kempty[2] vfull[2] vempty[2] sfull[2] pfull ofull mdone qfull[2] ofree
   // (+ one-byte caches: kstage[2] vstage[2], the copies of the codes; kscale[4], the K
   // scales of slot i % 4 ready for the softmax; paired softmax warps: xmax[4], both
@@ -350,12 +352,13 @@ __device__ __forceinline__ void tc_tail_fixup(const DecodeParams& p, const int* 
 // has. Only tiles that reach past the first node take the mask's path.
 template <int D, int BS, bool kTiles, int CODE = -1, int CS = 1, bool PAIR = false,
           bool TREE = false>
-__global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 1)
+__global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR, TREE>::kThreads, 1)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                            const __grid_constant__ CUtensorMap tmv,
                            const __grid_constant__ CUtensorMap tmo, const DecodeParams p) {
   constexpr bool kQ8 = CODE >= 0;
-  using K = TcDecode<D, BS, kQ8, PAIR>;
+  constexpr bool kLift = TREE && kQ8;  // weights carry V scales (tcgen05.cuh: kLift16)
+  using K = TcDecode<D, BS, kQ8, PAIR, TREE>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -383,9 +386,11 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
   // complete when the converters have written the bf16 values
   auto kstage = [&](int st) { return bar(16 + st); };
   auto vstage = [&](int st) { return bar(18 + st); };
-  // K scales of tile i: slot i % 4; V scales of tile i: slot 4 + i % 2
+  // K scales of tile i: slot i % 4; V scales of tile i: slot 4 + i % 2 (kLift: 4 + i % 4, and
+  // their exponents in 8 + i % 4)
   auto scale_area = [&](bool is_k, int i) {
-    return base + K::kOffScales + uint32_t(is_k ? (i & 3) : 4 + (i & 1)) * K::kScaleBytes;
+    return base + K::kOffScales +
+           uint32_t(is_k ? (i & 3) : 4 + (i & (kLift ? 3 : 1))) * K::kScaleBytes;
   };
   auto kscale = [&](int i) { return bar(20 + (i & 3)); };
   // paired softmax: both warps of lane quarter q have written their tile maxima
@@ -522,16 +527,20 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
                                                      abort_flag)))
         break;
       if constexpr (kQ8) {
-        if (lane == 0) mbar_arrive_expect_tx(fb, K::kCodeTile + K::kScaleBytes);
+        if (lane == 0)
+          mbar_arrive_expect_tx(fb, K::kCodeTile + (!kLift ? 1 : is_k ? 2 : 0) * K::kScaleBytes);
         __syncwarp();
         // a block past the context copies zero-filled codes and block 0's scales (its
         // rows become zeros in the conversion; the scales only have to be readable)
         const int row0 = __shfl_sync(0xffffffffu, row, 0);
         if (lane < K::kBlocks) {
           tma_load_2d(region + st * K::kTile + K::kCodeOff + lane * BS * D, map, fb, 0, row);
-          const float* sc = is_k ? p.k_scale : p.v_scale;
-          bulk_load(scale_area(is_k, i) + lane * BS * 4,
-                    sc + size_t(row == rows_total ? row0 : row), BS * 4, fb);
+          const size_t at = size_t(row == rows_total ? row0 : row);
+          if (!kLift || is_k)
+            bulk_load(scale_area(is_k, i) + lane * BS * 4, (is_k ? p.k_scale : p.v_scale) + at,
+                      BS * 4, fb);
+          if (kLift && is_k)
+            bulk_load(scale_area(false, i) + lane * BS * 4, p.v_scale + at, BS * 4, fb);
         }
       } else {
         if (lane == 0) mbar_arrive_expect_tx(fb, K::kTile);
@@ -593,10 +602,12 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         for (int kk = 0; kk < K::kN / 16; ++kk) {
           tc::mma_bf16_tmem_a(tmem + K::kColO, tmem + K::kColP + kk * 8, vd + kk * 128, kIdO,
                               (!seg_first || kk > 0) ? 1u : 0u);
-          // the row sums of the bf16 weights this P.V used, next to O (same rescaling)
-          tc::mma_bf16_tmem_a(tmem + K::kColL, tmem + K::kColP + kk * 8,
-                              desc_ones + (kk >> 2) * 128 + (kk & 3) * 2, kIdL,
-                              (!seg_first || kk > 0) ? 1u : 0u);
+          // the row sums of the bf16 weights this P.V used, next to O (same rescaling; kLift:
+          // the softmax's own)
+          if constexpr (!kLift)
+            tc::mma_bf16_tmem_a(tmem + K::kColL, tmem + K::kColP + kk * 8,
+                                desc_ones + (kk >> 2) * 128 + (kk & 3) * 2, kIdL,
+                                (!seg_first || kk > 0) ? 1u : 0u);
         }
         tc::commit(vempty(st));
         tc::commit(ofull);
@@ -789,6 +800,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
       return true;
     };
     float m_ref = -INFINITY;
+    float l_own = 0.f;  // kLift: the sum of this thread's weights
     int seg = 0, seg_j0 = cur.j, seg_tile = 0;
     bool ok = true;
     prefetch_q(cur, 0);
@@ -908,15 +920,35 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         }
       }
       // tile maximum: three-input max over eight independent chains (then over the
-      // row's CS threads)
+      // row's CS threads); kLift: of the scaled scores plus their V scales' exponents
+      const float2 asl2 = make_float2(asl, asl);
+      const uint32_t vs = scale_area(false, i) + 4 * c0;
       float mx[8];
+      if constexpr (kLift) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) mx[j] = __uint_as_float(s[j]);
+        for (int t = 0; t < kNc; t += 4) {
+          const uint4 g4 = lds128(vs + 4 * K::kScaleBytes + 4 * t);
+          const float2 a = __ffma2_rn(
+              make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])), asl2,
+              make_float2(__uint_as_float(g4.x), __uint_as_float(g4.y)));
+          const float2 b = __ffma2_rn(
+              make_float2(__uint_as_float(s[t + 2]), __uint_as_float(s[t + 3])), asl2,
+              make_float2(__uint_as_float(g4.z), __uint_as_float(g4.w)));
+          const int k = t >> 1 & 6;
+          mx[k] = t < 16 ? fmaxf(a.x, a.y) : fmax3(mx[k], a.x, a.y);
+          mx[k + 1] = t < 16 ? fmaxf(b.x, b.y) : fmax3(mx[k + 1], b.x, b.y);
+        }
+      } else {
 #pragma unroll
-      for (int u = 0; u < (kNc - 8) / 2; ++u)
-        mx[u & 7] = fmax3(mx[u & 7], __uint_as_float(s[8 + 2 * u]), __uint_as_float(s[9 + 2 * u]));
-      float mt = asl * fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
-                             fmaxf(mx[6], mx[7]));
+        for (int j = 0; j < 8; ++j) mx[j] = __uint_as_float(s[j]);
+#pragma unroll
+        for (int u = 0; u < (kNc - 8) / 2; ++u)
+          mx[u & 7] =
+              fmax3(mx[u & 7], __uint_as_float(s[8 + 2 * u]), __uint_as_float(s[9 + 2 * u]));
+      }
+      float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]),
+                       fmaxf(mx[6], mx[7]));
+      if constexpr (!kLift) mt *= asl;
       if constexpr (CS == 2) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, kRpq));
       if constexpr (PAIR) {  // the partner warp's half: [tile % 2][half][row] fp32
         const uint32_t xa = base + K::kOffXmax + uint32_t(i & 1) * 1024 + uint32_t(ar) * 4;
@@ -935,20 +967,32 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         alpha = fast_exp2(m_ref - mt);  // 0 while the row has seen nothing
         m_ref = mt;
         rescale = seg_tile > 0;
+        if constexpr (kLift) l_own *= alpha;
       }
       // weights 2^(scale * s - m) (packed fp32x2 FMAs), bf16 pairs (fp16 over one-byte
       // caches); their row sums come from the tensor cores (P times a ones tile, beside
       // P.V)
       uint32_t pk[kNc / 2];
-      const float nm = (TREE && kQ8 ? tc::kLift16 : 0.f) - m_ref;
-      const float2 asl2 = make_float2(asl, asl), nm2 = make_float2(nm, nm);
+      const float nm = (kLift ? tc::kLift16 : 0.f) - m_ref;
+      const float2 nm2 = make_float2(nm, nm);
+      float2 ls = make_float2(0.f, 0.f);
+      uint4 v4 = make_uint4(0u, 0u, 0u, 0u);  // kLift: V scales of columns t & ~3 ..
+      // the weights of columns t, t + 1
+      auto put = [&](int t, float2 w) {
+        if constexpr (kLift) {
+          ls = __fadd2_rn(ls, w);
+          if ((t & 2) == 0) v4 = lds128(vs + 4 * t);
+          w = __fmul2_rn(w, make_float2(__uint_as_float(t & 2 ? v4.z : v4.x),
+                                        __uint_as_float(t & 2 ? v4.w : v4.y)));
+        }
+        pk[t / 2] = kQ8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
+      };
       if (full) {
 #pragma unroll
         for (int t = 0; t < kNc; t += 2) {
           const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])),
                                       asl2, nm2);
-          pk[t / 2] = kQ8 ? pack_f16x2(fast_exp2(x.x), fast_exp2(x.y))
-                          : pack_bf16x2(fast_exp2(x.x), fast_exp2(x.y));
+          put(t, make_float2(fast_exp2(x.x), fast_exp2(x.y)));
         }
       } else {
 #pragma unroll
@@ -963,10 +1007,10 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
             see0 = c0 + t < vis;
             see1 = c0 + t + 1 < vis;
           }
-          const float w0 = see0 ? fast_exp2(x.x) : 0.f, w1 = see1 ? fast_exp2(x.y) : 0.f;
-          pk[t / 2] = kQ8 ? pack_f16x2(w0, w1) : pack_bf16x2(w0, w1);
+          put(t, make_float2(see0 ? fast_exp2(x.x) : 0.f, see1 ? fast_exp2(x.y) : 0.f));
         }
       }
+      if constexpr (kLift) l_own += ls.x + ls.y;
       if (!zero_v_tail(i, L, t0)) {
         ok = false;
         break;
@@ -988,7 +1032,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
           tc::tmem_st32(trow + K::kColO + c2, o);
         }
-        if (hp == 0)
+        if (!kLift && hp == 0)
           tc::tmem_st1(trow + K::kColL,
                        __float_as_uint(__uint_as_float(tc::tmem_ld1(trow + K::kColL)) * alpha));
       }
@@ -1024,7 +1068,8 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         const bool whole = seg_j0 == 0 && cur.j == cur.n - 1;
         const size_t slot = size_t(2 * c + (seg == 0 ? 0 : 1));
         // the sum of the weights (over the row's CS threads)
-        const float l1 = __uint_as_float(tc::tmem_ld1(trow + K::kColL));
+        float l1 = l_own;
+        if constexpr (!kLift) l1 = __uint_as_float(tc::tmem_ld1(trow + K::kColL));
         float l = CS == 1 ? l1 : l1 + __shfl_xor_sync(0xffffffffu, l1, kRpq);
         // a row past the tree's last node went along with its warp: zeros
         const bool none = TREE && node < 0;
@@ -1175,6 +1220,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         mbar_arrive(ofree);
         ++seg;
         m_ref = -INFINITY;
+        l_own = 0.f;
       }
       tile_next(cur, s_prefix, B, U);
     }
@@ -1203,7 +1249,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
         // K: the codes themselves as bf16 (exact), the score MMA's other operand being
         // the bf16 q, and the softmax multiplies each score column by its K scale (fp32);
         // V: code x scale as fp16, whose 11-bit significand keeps it within 2^-12 of its
-        // value (P.V then runs on fp16 weights)
+        // value (P.V then runs on fp16 weights); trees: the codes themselves
         if constexpr (kQ8) {
           const uint32_t tile = base + (kv == 0 ? K::kOffK : K::kOffV) + st * K::kTile;
           if (kv == 0) {
@@ -1211,9 +1257,15 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
                                                              ct);
             // scales of rows past the context may hold anything: zero for the softmax
             if (ct >= valid) tc::sts32(scale_area(true, i) + 4 * ct, 0u);
+            if constexpr (kLift) {  // (and the V scales, and their exponents)
+              const uint32_t vs = scale_area(false, i) + 4 * ct;
+              if (ct >= valid) tc::sts32(vs, 0u);
+              tc::sts32(vs + 4 * K::kScaleBytes,
+                        __float_as_uint(value_log(ct < valid ? lds32(vs) : 0u)));
+            }
           } else {
-            convert_codes<D, (kQ8 ? CODE : 0), true, true>(tile, scale_area(false, i), valid,
-                                                           ct);
+            convert_codes<D, (kQ8 ? CODE : 0), true, !kLift>(tile, scale_area(false, i), valid,
+                                                             ct);
           }
         }
         fence_proxy_async_smem();  // the 16-bit values, for the MMAs (async proxy)
@@ -1241,7 +1293,7 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR>::kThreads, 
 
 template <int D, int BS, bool kTiles, int CODE, int CS, bool PAIR, bool TREE>
 DecodeKernelInfo tc_info() {
-  using K = TcDecode<D, BS, (CODE >= 0), PAIR>;
+  using K = TcDecode<D, BS, (CODE >= 0), PAIR, TREE>;
   DecodeKernelInfo info{};
   info.fn =
       reinterpret_cast<const void*>(

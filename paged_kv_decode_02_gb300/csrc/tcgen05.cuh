@@ -251,11 +251,15 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[20])
       : "r"(taddr + 0u), "r"(taddr + 16u), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19])
       : "memory");
 }
-// fp16 softmax weights of a tree over one-byte caches are 2^(x - m + kLift16). The reference m lies
-// at most 8 below the largest score so far, so weights reach 2^15, below 65504, and one of 2^-21 of
-// the largest is still a normal number; without the lift a token of 2^-25 of the largest weight was
-// lost, and many of them (2^17 tokens: 0.4 % of a result, times how much larger their values are) with
-// it. The factor is in O and in the sum of the weights alike, so it leaves with their quotient.
+// Trees over one-byte caches: the MMA's weights are P = w vs, fp16, w = 2^(x - m + kLift16) the
+// softmax weight of a token and vs the scale of its V row, whose codes are the other operand. The
+// row's reference m follows the largest x + lg (|vs| < 2^lg) among the tokens that it sees and lies at
+// most 8 below, so P reaches 2^15, below 65504, and a product of 2^-21 of the largest is still a normal
+// number, whatever the size of the V rows and however it changes along the context. The sum of the
+// weights takes w in fp32, before vs and the rounding. (Weights without the lift: a token of 2^-25 of
+// the largest weight was lost, and a long tail with it. fp16 values of code x scale: V rows above 65504
+// became infinite, those far below 1e-3 lost their bits.) The factor 2^(kLift16 - m) is in O and in the
+// sum alike, so it leaves with their quotient.
 constexpr float kLift16 = 7.f;
 
 // Two warps whose threads of the same lane share a row, each with half of a tile's columns: they

@@ -28,21 +28,22 @@
 //   warp 21      walks the stretch and tells the others its segments;
 //   warps 22..27 (one-byte caches) widen codes in shared memory, three warps a tile, one trio the
 //                K tiles, one the V tiles (so that one's waits pass while the other works).
-// One-byte caches: codes land in a ring of their own; K becomes fp16 exactly, V fp16 of code x
-// scale (11 bits). Q is fp16 too: a row's bf16 values times the power of two that takes its
+// One-byte caches: codes land in a ring of their own and become fp16 exactly, K and V; K's scale
+// multiplies the fp32 score, V's scale the weight (tcgen05.cuh: kLift16). Q is fp16 too: a row's bf16 values times the power of two that takes its
 // largest to [2^14, 2^15), which loses nothing of a value within 2^-28 of the largest and 2^-39
-// of the largest below; the row's scale takes the power back. K's scale multiplies the fp32 score.
+// of the largest below; the row's scale takes the power back.
 // Weights are bf16 (fp16 over one-byte caches), scores, maxima and sums fp32; the reference
 // maximum moves when a tile's exceeds it by more than 8 (log2 units).
 // Measured on GB300, whole calls: 64 x 1733 tokens, 60 nodes, 32 / 8 heads, bf16 150 us (2400 to
 // 2900 cycles per key tile of two row tiles, of which the MMAs take 1300: scores, softmax and P.V
-// of a tile wait for each other, and an item's end takes some 8000), INT8 200; 16 x 8192, INT8 195
-// (3300 cycles: the V trio is busy throughout, its instructions among those of 16 softmax warps;
-// without widening 170); 1 x 131071, 33 nodes, E4M3 177. The roles' loops are kept small: with the
-// widening unrolled the kernel waited for instructions (4 of 12 warps per issue) and took 248.
-// Slower: four V and two K warps with fp16 products (INT8 205 -> 221), converters on low warps
-// (207 -> 221), lighter polling (205 -> 212: the barriers' unit is shared), both pipelines at a
-// split item's end (bf16 129 -> 135).
+// of a tile wait for each other, and an item's end takes some 8000), INT8 210; 16 x 8192, INT8 204
+// (3500 cycles: the widening and 16 softmax warps share the issue slots; with fp16 values of code x
+// scale, which V rows of some sizes do not survive, 195, and without widening 170); 1 x 131071, 33
+// nodes, E4M3 184. The roles' loops are kept small: with the widening unrolled the kernel waited for
+// instructions (4 of 12 warps per issue: 248 for 215), and with a second way to the reference for
+// tiles whose V scales are alike it took 208 for 204. Slower: four V and two K warps (INT8 205 -> 221),
+// converters on low warps (207 -> 221), lighter polling (205 -> 212: the barriers' unit is shared),
+// both pipelines at a split item's end (bf16 129 -> 135).
 // Every wait is bounded: on a timeout the CTA sets a status bit, lets its copies and MMAs
 // complete, frees its TMEM and leaves.
 #pragma once
@@ -66,15 +67,16 @@ struct TreeCfg {
   static constexpr int kStages = kQ8 ? 4 : 6;    // of the ring K, V, K, V, ...
   static constexpr int kCodes = kKeys * D;       // a tile of codes
   static constexpr int kCodeStages = kQ8 ? 6 : 0;
-  static constexpr int kScaleSlots = kQ8 ? 16 : 0;  // K scales of key tile n: slot n % 16
+  // key tile n: slot n % 16, K scales, V scales and V scales' exponents (value_log)
+  static constexpr int kScaleSlots = kQ8 ? 16 : 0;
+  static constexpr int kSlot = 3 * kKeys * 4;
   static constexpr int kOffQ = 0;
   static constexpr int kOffKV = 2 * kTileQ;
   static constexpr int kOffCodes = kOffKV + kStages * kTile;
   static constexpr int kOffOut = kOffCodes + kCodeStages * kCodes;  // 32 rows of 64 bytes a warp
-  static constexpr int kOffKScale = kOffOut + 16 * 2048;
-  static constexpr int kOffVScale = kOffKScale + kScaleSlots * kKeys * 4;
+  static constexpr int kOffScales = kOffOut + 16 * 2048;
   // (m, l) of pipeline 1's rows of a split item, for pipeline 0: [128]
-  static constexpr int kOffState = kOffVScale + kCodeStages * kKeys * 4;
+  static constexpr int kOffState = kOffScales + kScaleSlots * kSlot;
   static constexpr int kQueue = 4;
   static constexpr int kOffQueue = kOffState + 128 * 8;
   static constexpr int kOffBar = kOffQueue + kQueue * 64;
@@ -145,14 +147,20 @@ struct TreeStep {
   bool begun;
 };
 
-// Half a row (a thread) of a score tile: 32 scores become weights 2^(scale s - m) (fp16: times
-// 2^kLift16), 16-bit pairs in P's columns. kWhole: the row sees all columns, else those whose bits are set in `seen`;
+// Half a row (a thread) of a score tile: 32 scores become weights 2^(scale s - m) (one-byte caches:
+// times 2^kLift16 and V scales; `scales`: this half's in the tile's slot), 16-bit pairs in P's columns.
+// kWhole: the row sees all columns, else those whose bits are set in `seen`;
 // sl >= 0 (the scores' MMA has changed sign for a negative scale).
 template <int D, int CODE, bool kWhole, typename Wait>
-__device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t kscale,
+__device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint32_t scales,
                                              uint32_t seen, tc::RowPair& pair, TreeRow& row,
                                              bool& gone, const Wait& wait) {
   constexpr bool kQ8 = CODE >= 0;
+  constexpr uint32_t kV = TreeCfg<D, 16, CODE>::kKeys * 4;  // bytes from K scales to V scales
+  auto pair_of = [](uint32_t a, uint32_t b) {
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
+  };
+  const float2 sl2 = make_float2(sl, sl);
   uint32_t s[32];
   tc::tmem_ld32(at.ts, s);
   tc::fence_before_sync();
@@ -161,13 +169,9 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   if constexpr (kQ8) {  // each column times its K scale
 #pragma unroll
     for (int t = 0; t < 32; t += 4) {
-      const uint4 k4 = lds128(kscale + 4 * t);
-      const float2 a =
-          __fmul2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])),
-                     make_float2(__uint_as_float(k4.x), __uint_as_float(k4.y)));
-      const float2 b =
-          __fmul2_rn(make_float2(__uint_as_float(s[t + 2]), __uint_as_float(s[t + 3])),
-                     make_float2(__uint_as_float(k4.z), __uint_as_float(k4.w)));
+      const uint4 k4 = lds128(scales + 4 * t);
+      const float2 a = __fmul2_rn(pair_of(s[t], s[t + 1]), pair_of(k4.x, k4.y));
+      const float2 b = __fmul2_rn(pair_of(s[t + 2], s[t + 3]), pair_of(k4.z, k4.w));
       s[t] = __float_as_uint(a.x);
       s[t + 1] = __float_as_uint(a.y);
       s[t + 2] = __float_as_uint(b.x);
@@ -179,13 +183,26 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
     for (int t = 0; t < 32; ++t)
       if (!(seen >> t & 1u)) s[t] = 0xff800000u;  // -inf
   }
-  float mx[4];
+  float mx[4], mine;
+  if constexpr (kQ8) {  // the largest scaled score plus exponent of the V scale
 #pragma unroll
-  for (int t = 0; t < 4; ++t) mx[t] = __uint_as_float(s[t]);
+    for (int t = 0; t < 32; t += 4) {
+      const uint4 g4 = lds128(scales + 2 * kV + 4 * t);
+      const float2 a = __ffma2_rn(pair_of(s[t], s[t + 1]), sl2, pair_of(g4.x, g4.y));
+      const float2 b = __ffma2_rn(pair_of(s[t + 2], s[t + 3]), sl2, pair_of(g4.z, g4.w));
+      const int i = t >> 1 & 2;
+      mx[i] = t < 8 ? fmaxf(a.x, a.y) : fmax3(mx[i], a.x, a.y);
+      mx[i + 1] = t < 8 ? fmaxf(b.x, b.y) : fmax3(mx[i + 1], b.x, b.y);
+    }
+    mine = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+  } else {
 #pragma unroll
-  for (int t = 0; t < 14; ++t)
-    mx[t & 3] = fmax3(mx[t & 3], __uint_as_float(s[4 + 2 * t]), __uint_as_float(s[5 + 2 * t]));
-  const float mine = sl * fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+    for (int t = 0; t < 4; ++t) mx[t] = __uint_as_float(s[t]);
+#pragma unroll
+    for (int t = 0; t < 14; ++t)
+      mx[t & 3] = fmax3(mx[t & 3], __uint_as_float(s[4 + 2 * t]), __uint_as_float(s[5 + 2 * t]));
+    mine = sl * fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+  }
   const float top = fmaxf(mine, pair.swap(mine, gone));
   if (gone) return false;
   float alpha = 1.f;
@@ -198,20 +215,30 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   // (scores of -inf alone: weights 0, not 2^(-inf + inf))
   const float m = row.m > -INFINITY ? row.m : 0.f;
   const float nm = (kQ8 ? tc::kLift16 : 0.f) - m;
-  const float2 sl2 = make_float2(sl, sl), nm2 = make_float2(nm, nm);
+  const float2 nm2 = make_float2(nm, nm);
   float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   uint32_t pk[16];
 #pragma unroll
-  for (int t = 0; t < 32; t += 2) {
-    const float2 x =
-        __ffma2_rn(make_float2(__uint_as_float(s[t]), __uint_as_float(s[t + 1])), sl2, nm2);
-    float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-    if constexpr (!kWhole) {
-      w.x = seen >> t & 1u ? w.x : 0.f;
-      w.y = seen >> (t + 1) & 1u ? w.y : 0.f;
+  for (int t = 0; t < 32; t += 4) {
+    uint4 v4;
+    if constexpr (kQ8) v4 = lds128(scales + kV + 4 * t);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int u = t + 2 * i;
+      const float2 x = __ffma2_rn(pair_of(s[u], s[u + 1]), sl2, nm2);
+      float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      if constexpr (!kWhole) {
+        w.x = seen >> u & 1u ? w.x : 0.f;
+        w.y = seen >> (u + 1) & 1u ? w.y : 0.f;
+      }
+      ls[i] = __fadd2_rn(ls[i], w);
+      if constexpr (kQ8) {
+        const float2 pv = __fmul2_rn(w, i ? pair_of(v4.z, v4.w) : pair_of(v4.x, v4.y));
+        pk[u / 2] = pack_f16x2(pv.x, pv.y);
+      } else {
+        pk[u / 2] = pack_bf16x2(w.x, w.y);
+      }
     }
-    ls[(t >> 1) & 1] = __fadd2_rn(ls[(t >> 1) & 1], w);
-    pk[t / 2] = kQ8 ? pack_f16x2(w.x, w.y) : pack_bf16x2(w.x, w.y);
   }
   const float2 l2 = __fadd2_rn(ls[0], ls[1]);
   row.l += l2.x + l2.y;
@@ -235,33 +262,17 @@ __device__ __forceinline__ bool tree_softmax(const TreeStep& at, float sl, uint3
   return true;
 }
 
-// Sixteen codes -> two 16-byte chunks of fp16: exact, or times `sc` (rounded once).
-template <int CODE, bool kScale>
-__device__ __forceinline__ void widen16(const uint4& raw, float sc, uint4& a, uint4& b) {
+// Sixteen codes -> two 16-byte chunks of fp16, exact.
+template <int CODE>
+__device__ __forceinline__ void widen16(const uint4& raw, uint4& a, uint4& b) {
   using Codec = Code8<CODE>;
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   uint32_t o[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t x = Codec::pre(w[e]);
-    if constexpr (kScale && CODE == CODE_I8) {  // by way of 2^23 + 128 + code in fp32
-      const float2 s2 = make_float2(sc, sc), off = make_float2(-8388736.f, -8388736.f);
-      auto up = [&](uint32_t sel) { return __uint_as_float(prmt(x, 0x4b000000u, sel)); };
-      const float2 f = __fmul2_rn(__fadd2_rn(make_float2(up(0x7650u), up(0x7651u)), off), s2);
-      const float2 g = __fmul2_rn(__fadd2_rn(make_float2(up(0x7652u), up(0x7653u)), off), s2);
-      o[2 * e] = pack_f16x2(f.x, f.y);
-      o[2 * e + 1] = pack_f16x2(g.x, g.y);
-      continue;
-    }
     o[2 * e] = Codec::lo(x);
     o[2 * e + 1] = Codec::hi(x);
-    if constexpr (kScale) {
-      const float2 s2 = make_float2(sc, sc);
-      const float2 f = __fmul2_rn(unpack_f16x2(o[2 * e]), s2);
-      const float2 g = __fmul2_rn(unpack_f16x2(o[2 * e + 1]), s2);
-      o[2 * e] = pack_f16x2(f.x, f.y);
-      o[2 * e + 1] = pack_f16x2(g.x, g.y);
-    }
   }
   a = make_uint4(o[0], o[1], o[2], o[3]);
   b = make_uint4(o[4], o[5], o[6], o[7]);
@@ -562,9 +573,8 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
         if (!ok) break;
         tc::fence_after_sync();
         const TreeStep at = {ts, tp, to, sread(X), pdone(X), pfull(X), step, lane, j > j0};
-        const uint32_t kscale =
-            base + K::kOffKScale + ((tile_no + uint32_t(j - g.ja)) % 16u) * (K::kKeys * 4) +
-            hp * 128;
+        const uint32_t scales =
+            base + K::kOffScales + ((tile_no + uint32_t(j - g.ja)) % 16u) * K::kSlot + hp * 128;
         if (idle) {  // no row of this warp sees anything
           ok = step == 0 || wait(pdone(X), step - 1);
           if (ok && lane == 0) {
@@ -572,10 +582,10 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
             mbar_arrive(pfull(X));
           }
         } else if ((j + 1) * K::kKeys <= before) {
-          ok = tree_softmax<D, CODE, true>(at, sl, kscale, 0u, pair, row, gone, wait);
+          ok = tree_softmax<D, CODE, true>(at, sl, scales, 0u, pair, row, gone, wait);
         } else {
           const uint32_t seen = bits_at(j * K::kKeys + 32 * hp);
-          ok = tree_softmax<D, CODE, false>(at, sl, kscale, seen, pair, row, gone, wait);
+          ok = tree_softmax<D, CODE, false>(at, sl, scales, seen, pair, row, gone, wait);
         }
         if (!ok) break;
       }
@@ -768,16 +778,17 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
           if (!ok) break;
           const CUtensorMap* map = kv ? &tmv : &tmk;
           if constexpr (kQ8) {
-            if (lane == 0) mbar_arrive_expect_tx(fb, K::kCodes + K::kKeys * 4);
+            // (with the K tile the scales of both)
+            if (lane == 0) mbar_arrive_expect_tx(fb, K::kCodes + (kv ? 0 : 2 * K::kKeys * 4));
             __syncwarp();
             if (lane < K::kBlocks) {
               tma_load_2d(base + K::kOffCodes + st * K::kCodes + lane * BS * D, map, fb, 0, row);
-              // (a block past the context: zero codes, and another block's scales)
-              const uint32_t sc = kv ? base + K::kOffVScale + st * (K::kKeys * 4)
-                                     : base + K::kOffKScale + (tile_no % 16u) * (K::kKeys * 4);
-              bulk_load(sc + lane * BS * 4,
-                        (kv ? p.v_scale : p.k_scale) + size_t(row == rows_total ? row0 : row),
-                        BS * 4, fb);
+              if (kv == 0) {  // (a block past the context: zero codes, and another block's scales)
+                const uint32_t sc = base + K::kOffScales + (tile_no % 16u) * K::kSlot;
+                const size_t at = size_t(row == rows_total ? row0 : row);
+                bulk_load(sc + lane * BS * 4, p.k_scale + at, BS * 4, fb);
+                bulk_load(sc + K::kKeys * 4 + lane * BS * 4, p.v_scale + at, BS * 4, fb);
+              }
             }
           } else {
             if (lane == 0) mbar_arrive_expect_tx(fb, K::kTile);
@@ -921,7 +932,7 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     constexpr int kSeg = D >= 128 ? 128 : 64;      // swizzle span of a row of codes
     constexpr int kChunks = K::kKeys * (D / 16);   // of 16 codes
     int st = kv ? 1 : 0, cst = st;  // K tiles on the rings' even stages, V tiles on the odd ones
-    uint32_t turn = 0, cturn = 0;
+    uint32_t turn = 0, cturn = 0, tile_no = 0;
     bool ok = true, begun = false;
     auto wait = [&](uint32_t b, uint32_t phase) {
       ok = ok && __all_sync(0xffffffffu,
@@ -929,14 +940,20 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
     };
     TreeSeg g;
     while (ok && take(g, true)) {
-      for (int j = g.ja; ok && j < g.jb; ++j) {
+      for (int j = g.ja; ok && j < g.jb; ++j, ++tile_no) {
         const int valid = g.len - j * K::kKeys;  // rows of the context
         wait(cfull(cst), cturn);
         if (begun) wait(empty(st), turn ^ 1u);
         if (!ok) break;
         const uint32_t codes = base + K::kOffCodes + cst * K::kCodes;
-        const uint32_t scales = base + K::kOffVScale + cst * (K::kKeys * 4);
         const uint32_t tile = base + K::kOffKV + st * K::kTile;
+        if (!kv && ct < K::kKeys) {  // the V scales' exponents, for the softmax
+          const uint32_t vs =
+              base + K::kOffScales + (tile_no % 16u) * K::kSlot + (K::kKeys + ct) * 4;
+          if (ct >= valid) tc::sts32(vs, 0u);  // (past the context a scale may be anything)
+          tc::sts32(vs + K::kKeys * 4,
+                    __float_as_uint(value_log(ct < valid ? lds32(vs) : 0u)));
+        }
         // chunk idx: columns 16 (4 slab + c) .. of row t; eight lanes take two rows' halves (D =
         // 128: different ones), which fall on different banks, codes and 16-bit chunks alike.
         // (Not unrolled: the kernel's roles run side by side, and their loops are to stay in the
@@ -945,11 +962,9 @@ __global__ void __launch_bounds__(TreeCfg<D, BS, CODE>::kThreads, 1)
         for (int idx = ct; idx < kChunks; idx += 96) {
           const int cc = idx & 3, t = idx >> 2 & 63, slab = (idx >> 8) ^ (t & (K::kSlabs - 1));
           uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-          if (!kv || t < valid) {  // (past the context a V row's scale may be anything)
-            const uint4 raw = lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16)));
-            if (!kv) widen16<kQ8 ? CODE : 0, false>(raw, 1.f, a, b);
-            else widen16<kQ8 ? CODE : 0, true>(raw, lds_f32(scales + 4 * t), a, b);
-          }
+          if (!kv || t < valid)  // (past the context a V row may be anything, its weights are 0)
+            widen16<kQ8 ? CODE : 0>(
+                lds128(codes + swz<kSeg>(uint32_t(t * D + (4 * slab + cc) * 16))), a, b);
           const uint32_t out = tile + slab * K::kSlab + t * 128;
           tc::sts128(out + (((2 * cc) ^ (t & 7)) << 4), a);
           tc::sts128(out + (((2 * cc + 1) ^ (t & 7)) << 4), b);

@@ -11,12 +11,12 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("d,bs", [(128, 16), (128, 32), (64, 16), (64, 32)])
 @pytest.mark.parametrize("kv", ["bf16", "int8", "e4m3", "e5m2"])
-@pytest.mark.parametrize("n", [9, 16])
-def test_one_tile_of_65_to_128_rows(d, bs, kv, n):
-    """Rows of one whole tile in tables of less than 512 tokens: every type, head size and block,
-    with context ends inside a tile, at its end and past it; joined by the merge kernel and by the
-    last CTA."""
-    lens = [n, 128, 129, 300, 479]
+@pytest.mark.parametrize("n,longest", [(9, 222), (16, 222), (9, 479), (16, 479)])
+def test_one_tile_of_65_to_128_rows(d, bs, kv, n, longest):
+    """Rows of one whole tile in tables of less than 256 and of 512 tokens: every type, head size
+    and block, with context ends inside a tile, at its end and past it; joined by the merge kernel
+    and by the last CTA."""
+    lens = [n, 128, 129, longest - 99, longest]
     c = Cache(lens, 2, d, bs, kv, seed=n)
     assert c.tables.shape[1] * bs < 512
     q = _queries(len(lens), n, 16, d, seed=n)
