@@ -39,11 +39,12 @@
 // (89 %), 96 813 (94 %), 128 1025 (100 %; Q and K come from shared memory, whose bandwidth bounds
 // small N); with 128 keys, P over the scores it came from and so every step of a tile in
 // sequence, a step took 3500 cycles for two tiles, where the MMAs take 2050.
-// Whole calls on GB300: 32768 tokens, 32 / 8 heads, 6.0 to 6.2 ms (1410 to 1460 TFLOP/s, by the
-// power the part is given); 8192 tokens 423 us (1300); 16 x 1024, 64 / 8 heads, 332 us (830);
-// chunks of 256 over 1500, 184 us (1000). What is left is the end of an item, some 7000 cycles of a tile's
+// GPU time on GB300, calls of a graph: 32768 tokens, 32 / 8 heads, 6.1 ms (1440 TFLOP/s; 6.3 to 6.7
+// where inputs change from call to call, by the power the part is given); 8192 tokens 427 us (1290);
+// 16 x 1024, 64 / 8 heads, 333 us (820); chunks of 256 over 1500, 184 us (1000). What is left is the end of an item, some 7000 cycles of a tile's
 // softmax warps where a step of 80 keys takes 2050: the last P.V, O through shared memory to its
-// rows, the next segment. Tried, and slower: the end put off behind the next item's first softmax
+// rows, the next segment; and the softmax does not fit its registers (80 a thread: 60 to 64 bytes of
+// spill stores, 72 to 80 of loads). Tried, and slower: the end put off behind the next item's first softmax
 // (340 -> 413 us at 16 x 1024: longer live ranges in the loop), the next segment taken before it
 // (377), both P.V by one thread and the walk by the TMA thread (393, with 91 registers in place of
 // 80), rows stored as whole lines, half a warp's at a time (430), segments read again at their end
@@ -51,7 +52,12 @@
 // The softmax keeps a reference maximum per row that moves only when a tile's maximum exceeds
 // it by more than 8 (log2 units; weights then reach 2^8 and keep their relative precision), so
 // O is rescaled in TMEM a few times per item at most. Scores, maxima and sums are fp32; a
-// weight is rounded once to bf16 as the MMA's operand, the sum takes it before that.
+// weight is rounded once to bf16 as the MMA's operand, the sum takes it before that: results are
+// within 0.0018 to 0.0022 (relative, all elements) of those in 64 bits, of which the rounding of the
+// output alone makes 0.0016. Weights as two bf16 terms, whose second P.V adds the rest, leave only
+// that rounding, and cost 25 % (16 x 1024, 64 / 8 heads: 333 -> 418 us) to 44 % (32768 tokens): P of
+// both terms leaves TMEM columns for 64 keys a tile, and P.V doubles. One term, as in the multi-query
+// decode of the same rows.
 // Every wait is bounded: on a timeout the CTA sets a status bit, lets its copies and MMAs
 // complete, frees its TMEM and leaves.
 #pragma once

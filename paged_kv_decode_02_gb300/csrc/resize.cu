@@ -18,13 +18,16 @@
 //
 // The sums are a scan over the batch by a CTA's threads, kept in its shared memory; a warp finds
 // the sequence of the first of 32 tokens by a 32-way search there, a lane its own from it on.
-// Few tokens: one CTA does it all. Many: CTAs on every SM write tables, list and rows, each with
-// its own scan of the batch, and a second launch of one CTA then writes lengths, count and
-// offsets (no CTA may change what another still reads); it computes its sums beside the first.
+// Few tokens: one CTA does it all, and hands back what comes back in the same call, however many
+// blocks. Many, or none: CTAs on every SM write tables, list and rows, each with its own scan of the
+// batch, and a second launch of one CTA then writes lengths, count and offsets (no CTA may change
+// what another still reads); it computes its sums beside the first.
 // Bound by the chain of length, scan, search, table entry (1.8 MB of rows take 0.3 us). Measured
 // on GB300, GPU time of two calls, in and out: 256 prompts of 1 .. 900 tokens 9.4 us (all by one
 // CTA some 470; sums of warps added up by each thread 14.3; the commit's sums after the rows
-// 22.0); 4096 of 1 .. 200 tokens 23.9; 64 sequences that grow by a token 6.4.
+// 22.0); 4096 of 1 .. 200 tokens 23.9; 64 sequences that grow by a token 6.4. Of one call in which 256
+// sequences grow by a token 3.5; with one of 2000 tokens that leaves meanwhile 4.2, with 56 of 8000
+// (28000 blocks, by the one CTA) 65: such a step is better two calls, the leaving ones first.
 #include <algorithm>
 
 #include "common.cuh"
