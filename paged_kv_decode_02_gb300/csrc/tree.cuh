@@ -29,25 +29,24 @@
 //   warps 22..27 (one-byte caches) widen codes in shared memory, three warps a tile, one trio the
 //                K tiles, one the V tiles (so that one's waits pass while the other works).
 // One-byte caches: codes land in a ring of their own and become fp16 exactly, K and V; K's scale
-// multiplies the fp32 score, V's scale the weight (tcgen05.cuh: kLift16). Q is fp16 too: a row's bf16 values times the power of two that takes its
-// largest to [2^14, 2^15), which loses nothing of a value within 2^-28 of the largest and 2^-39
-// of the largest below; the row's scale takes the power back.
+// multiplies the fp32 score, V's scale the weight (tcgen05.cuh: kLift16). Q is fp16 too: a row's bf16
+// values times the power of two that takes its largest to [2^14, 2^15), which loses nothing of a value
+// within 2^-28 of the largest and 2^-39 of the largest below; the row's scale takes the power back.
 // Weights are rounded once, to bf16 (fp16 over one-byte caches), scores, maxima and sums are fp32; the
 // reference maximum moves when a tile's exceeds it by more than 8 (log2 units). Results are within
 // 0.0020 to 0.0024 (bf16) and 0.0017 (one-byte) of those in 64 bits, of which the rounding of the
 // output makes 0.0017; bf16 weights as two terms, with a second P.V, would leave only that and cost 10
 // to 15 % (64 x 1733, trees of 60: 151 -> 169 us), so they are one, as in the multi-query decode.
-// Measured on GB300, whole calls: 64 x 1733 tokens, 60 nodes, 32 / 8 heads, bf16 150 us (2400 to
+// Measured on GB300, whole calls: 64 x 1733 tokens, 60 nodes, 32 / 8 heads, bf16 151 us (2400 to
 // 2900 cycles per key tile of two row tiles, of which the MMAs take 1300: scores, softmax and P.V
-// of a tile wait for each other, and an item's end takes some 8000; registers: 36 to 60 bytes of spill
-// stores), INT8 210; 16 x 8192, INT8 204
-// (3500 cycles: the widening and 16 softmax warps share the issue slots; with fp16 values of code x
-// scale, which V rows of some sizes do not survive, 195, and without widening 170); 1 x 131071, 33
-// nodes, E4M3 184. The roles' loops are kept small: with the widening unrolled the kernel waited for
-// instructions (4 of 12 warps per issue: 248 for 215), and with a second way to the reference for
-// tiles whose V scales are alike it took 208 for 204. Slower: four V and two K warps (INT8 205 -> 221),
-// converters on low warps (207 -> 221), lighter polling (205 -> 212: the barriers' unit is shared),
-// both pipelines at a split item's end (bf16 129 -> 135).
+// of a tile wait for each other, and an item's end takes some 8000; 36 to 60 bytes of registers are
+// spilled), INT8 209; 16 x 8192, INT8 204 (3500 cycles: the widening and 16 softmax warps share the
+// issue slots; with fp16 values of code x scale, which V rows of some sizes do not survive, 195, and
+// without widening 170); 1 x 131071, 33 nodes, E4M3 184. The roles' loops are kept small: with the
+// widening unrolled the kernel waited for instructions (4 of 12 warps per issue: 248 for 215), and with
+// a second way to the reference for tiles whose V scales are alike it took 208 for 204. Slower: four V
+// and two K warps (INT8 205 -> 221), converters on low warps (207 -> 221), lighter polling (205 -> 212:
+// the barriers' unit is shared), both pipelines at a split item's end (bf16 129 -> 135).
 // Every wait is bounded: on a timeout the CTA sets a status bit, lets its copies and MMAs
 // complete, frees its TMEM and leaves.
 #pragma once
