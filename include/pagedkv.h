@@ -508,7 +508,8 @@ pkv_status pkv_decode_multi_q8(void* out, const void* q, const void* k_cache,
  *   tree_mask  [num_seqs, q_len, ceil(q_len / 64)] 64-bit words, device: bit j % 64 of word
  *              j / 64 of a node's row is node j's; bits of nodes at or past t are ignored.
  *   tree_lens  [num_seqs] int32, device: nodes of each tree, 0 .. q_len; NULL: q_len for all.
- *              Rows i >= tree_lens[s] of out get zeros, as does a node that sees no token.
+ *              Rows i >= tree_lens[s] of out get zeros, as does a node that sees no token, or
+ *              none with a score above -inf.
  *   workspace  at least pkv_decode_tree_workspace_bytes(dims, q_len, kv_dtype) bytes, as for
  *              pkv_decode_bf16.
  *   status     as for pkv_decode_multi_bf16, a tree_lens entry outside 0 .. q_len and a sequence
@@ -562,8 +563,9 @@ typedef struct pkv_prompt_dims {
  * q_offsets[s] query rows and the nk = kv_offsets[s + 1] - kv_offsets[s] key and value rows
  * from its offsets on; the queries are its last tokens: query i sees keys j <= nk - nq + i.
  *   out[q_offsets[s] + i, h, :] = softmax(scale * K q[.., i, h]) V over those keys
- * (zeros where there is none). nk == nq: whole prompts. nk > nq: a chunk of chunked prefill
- * ("Orca 的迭代级调度", same page) over keys and values that pkv_gather_tokens read back.
+ * (zeros where there is none, or none with a score above -inf). nk == nq: whole prompts. nk > nq:
+ * a chunk of chunked prefill ("Orca 的迭代级调度", same page) over keys and values that
+ * pkv_gather_tokens read back.
  *   q, out        [num_q_tokens, Hq, D] bf16; out must not overlap an input.
  *   k, v          [num_kv_tokens, Hkv, D] bf16.
  *   q_offsets, kv_offsets  [num_seqs + 1] int32, device, never falling (they may be the same

@@ -973,7 +973,9 @@ __global__ void __launch_bounds__(TcDecode<D, BS, (CODE >= 0), PAIR, TREE>::kThr
       // caches); their row sums come from the tensor cores (P times a ones tile, beside
       // P.V)
       uint32_t pk[kNc / 2];
-      const float nm = (kLift ? tc::kLift16 : 0.f) - m_ref;
+      // (trees, scores of -inf alone so far: weights 0, not 2^(-inf + inf))
+      const float nm =
+          (kLift ? tc::kLift16 : 0.f) - (TREE && !(m_ref > -INFINITY) ? 0.f : m_ref);
       const float2 nm2 = make_float2(nm, nm);
       float2 ls = make_float2(0.f, 0.f);
       uint4 v4 = make_uint4(0u, 0u, 0u, 0u);  // kLift: V scales of columns t & ~3 ..
